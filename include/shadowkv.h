@@ -281,6 +281,164 @@ skv_status shadowkv_check(shadowkv_ctx* ctx);
 skv_status shadowkv_attention_noalloc(const shadowkv_params* p, const void* q, const void* K,
                                       const void* V, int n_tokens, void* out, void* stream);
 
+/* -------------------------------------------- queries and keys for a step
+ * A b x h x s x d tensor given by strides: element (i, g, t, j) lies at
+ * ptr + i sb + g sh + t ss + j (strides in elements, not negative; the d
+ * elements of a row are adjacent).  A projection's output b x s x (h d) read
+ * in place has sh = d. */
+typedef struct shadowkv_rows {
+  void* ptr;
+  long long sb, sh, ss;
+} shadowkv_rows;
+
+typedef struct shadowkv_norm_rope_params {
+  int b, s;           /* sequences, tokens of each */
+  int h_q, h_kv;      /* query heads, key heads */
+  int d;              /* head dimension: 64 or 128 */
+  int rot;            /* rotated dimensions, the first of each head: a multiple of 8, 0..d */
+  int dtype;          /* SKV_DTYPE_F32 or SKV_DTYPE_BF16: rows and weights */
+  int norm;           /* 1: normalise each head's row before the rotation; 0: rotate only */
+  int pos_per_token;  /* 0: pos holds b first positions, token t at pos[i] + t; 1: b x s positions */
+  float eps;          /* added to the mean square (norm); > 0 */
+  float theta;        /* base of the rotation's frequencies; > 0 */
+} shadowkv_norm_rope_params;
+
+/*
+ * Norm of every query and key head, with the rotation to the token's
+ * position in the same pass:
+ *   y = x / sqrt(mean_j x_j^2 + eps) * w        (norm = 1; w = 1 where the weight is NULL)
+ *   (y_i, y_{i + rot/2}) turned by the angle pos theta^(-2i/rot), i < rot/2,
+ * the rotate-half pairing the rest of the library uses.  rot = 0 leaves the
+ * rows normed but not turned: the pre-RoPE keys shadowkv_prefill takes.
+ *   q, k           : device rows b x h_q x s x d and b x h_kv x s x d; either may be
+ *                    NULL (then its weight and output are too).
+ *   q_weight, k_weight : device, d elements each, or NULL.
+ *   pos            : device int32, b or b x s (pos_per_token), any value;
+ *                    NULL: token t at position t.
+ *   q_out, k_out   : device rows.  An output may be its own input (same pointer and
+ *                    strides); otherwise no output overlaps an input or the other output.
+ * Everything is computed in fp32 and rounded once; the angle is reduced in
+ * 64-bit integers and is exact to 2^-30 of a turn at any position.  Row
+ * pointers and strides must be multiples of 4 elements, and pointers aligned
+ * to 4 elements (SKV_ERR_INVALID_ARG).  b = 0 or s = 0 does nothing.
+ * Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, const shadowkv_rows* q,
+                                 const shadowkv_rows* k, const void* q_weight, const void* k_weight,
+                                 const int32_t* pos, const shadowkv_rows* q_out,
+                                 const shadowkv_rows* k_out, void* stream);
+
+/* ------------------------------------------------ 8-bit block cache
+ * A dense key/value cache for the sequences and layers a caller does not
+ * compress: post-RoPE keys and values held in 8 bits (e4m3: sign, 4 exponent
+ * and 3 mantissa bits), with one scale per block of `block` tokens of one KV
+ * head.  All memory is the caller's and stays the caller's; the struct only
+ * names it, and the calls allocate nothing.
+ *
+ * Blocks live in a pool.  Pair (i, g) = sequence i, KV head g holds
+ * n_tok[i, g] tokens: token t is row t % block of the pool block
+ * table[i, g, t / block].  Every table entry, also past the tokens held, must
+ * name a pool block (0 <= id < n_pool) and no pool block that a pair appends to may be
+ * named twice; entry c of pair p = p max_blocks + c does for a pool of
+ * b h_kv max_blocks blocks.  Codes inside a pool block:
+ *   k_codes : row t, dimension j at byte (t/8) 8 d + (j/16) 128 + (t%8) 16 + j%16
+ *   v_codes : row t, dimension j at byte (t/16) 16 d + j 16 + t%16
+ * (the tensor core's K-major operand order for K, and for V transposed).  The
+ * value of a code is the e4m3 number times the block's k_scale or v_scale.
+ * A scale written by the library is 2^e with the smallest e >= -100 for which
+ * max |x| <= 448 2^e over the block's finite entries.
+ *
+ * A kernel that meets a table entry outside the pool or a token count outside
+ * 0..max_blocks block records it in *status (see shadowkv_cache_check) and reads
+ * block 0, or the nearest count, in its place.  Calls that touch the same
+ * cache must be ordered (one stream, or events), except that attention calls
+ * that do not gather weights may overlap each other. */
+typedef struct shadowkv_cache {
+  int b, h_kv;        /* sequences, KV heads */
+  int d;              /* head dimension: 64 or 128 */
+  int block;          /* tokens per block: 16, 32, 64 or 128 */
+  int max_blocks;     /* table entries per pair, 1..16384 */
+  int n_pool;         /* blocks in the pool */
+  void* k_codes;      /* n_pool x block x d bytes, 16-byte aligned */
+  void* v_codes;
+  float* k_scale;     /* n_pool */
+  float* v_scale;
+  int32_t* table;     /* b x h_kv x max_blocks */
+  int32_t* n_tok;     /* b x h_kv */
+  float* weight;      /* b x h_kv x max_blocks: attention weight gathered per block; NULL: none kept */
+  int32_t* status;    /* 1 int, 0 at the start */
+} shadowkv_cache;
+
+/* Checks the cache's sizes and pointers without touching the GPU. */
+skv_status shadowkv_cache_validate(const shadowkv_cache* c);
+
+/*
+ * Appends tokens to every pair, quantising them.
+ *   dtype : SKV_DTYPE_F32 or SKV_DTYPE_BF16, of k and v.
+ *   k, v  : device rows b x h_kv x s x d (post-RoPE keys, values); pointers and
+ *           strides multiples of 16 bytes.
+ *   lens  : device int32, b: tokens of each sequence, 0..s (k and v are not read
+ *           past them); NULL: s each.
+ * A block's scale covers its tokens; where a later append needs a larger one, the
+ * codes held are rescaled by the power of two between them (exact unless
+ * they leave e4m3's normal range).  Infinities become the largest code, NaN
+ * stays NaN.  Bytes of a block past its tokens are left as they were.  The weight of a
+ * block that gets its first token is set to 0.  Tokens past max_blocks block are dropped and
+ * recorded in *status, as is a length outside 0..s (clamped).
+ * s = 0 does nothing.  Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_cache_append(const shadowkv_cache* c, int dtype, const shadowkv_rows* k,
+                                 const shadowkv_rows* v, int s, const int32_t* lens, void* stream);
+
+/* Bytes of workspace shadowkv_cache_attend needs for h_q query heads on the
+ * current device (0 if the arguments are not valid). */
+size_t shadowkv_cache_attend_workspace(const shadowkv_cache* c, int h_q);
+
+/*
+ * Attention of one new token per sequence over the cache:
+ *   out = sum_t p_t V_t,  p = softmax_t(scale q . K_t)  over the pair's tokens,
+ * query head g reading KV head g / (h_q / h_kv); h_q / h_kv in {1, 2, 4, 8}.
+ *   dtype : SKV_DTYPE_F32 or SKV_DTYPE_BF16, of q and out.
+ *   q, out: device rows b x h_q x 1 x d (ss is not used), aligned to their elements.
+ *   lse   : device f32, b x h_q: log sum_t exp(scale q . K_t), or NULL.
+ *   gather, decay : with gather = 1 every block i that holds tokens gets
+ *           weight[i] = decay weight[i] + sum over its tokens and the pair's query
+ *           heads of p (decay = 0: the old weight is not read); needs weight.
+ *   work  : device, 256-byte aligned, at least shadowkv_cache_attend_workspace bytes; its
+ *           contents before and after the call mean nothing.  Calls that may run
+ *           at the same time need workspaces of their own.
+ * A pair without tokens gives zeros, an lse of -inf and no weight.
+ * The products run on e4m3 operands: q and p are split exactly into sums of e4m3
+ * terms (bf16: 2 for q, 3 for p, which keeps 12 bits of p; f32: 6 each), all
+ * accumulated in fp32.
+ * Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_cache_attend(const shadowkv_cache* c, int dtype, int h_q, const shadowkv_rows* q,
+                                 float scale, int gather, float decay, const shadowkv_rows* out,
+                                 float* lse, void* work, size_t work_bytes, void* stream);
+
+/*
+ * Evicts whole blocks by gathered weight.  A pair with more than `keep`
+ * blocks (its last, partly filled one counts) keeps its first `sink`, its
+ * last `recent`, and of the others those of largest weight (ties to the lower index, NaN
+ * below everything), `keep` in all, in their order; n_tok falls accordingly.
+ * The freed blocks' ids follow the kept ones in the table, so that
+ * later appends reuse them; weights past the kept blocks become 0.
+ * Other pairs stay as they are (their weights past the blocks held become 0).
+ *   dst  : gets table, n_tok and weight; NULL or the same memory: in place.
+ *          Its sizes must be src's; its pool is not used.
+ *   kept : device int32, b x h_kv x keep: the old index of every block that is still held, -1 behind
+ *          the last; or NULL.
+ * Needs 1 <= keep <= max_blocks, sink, recent >= 0, sink + recent <= keep, and weights.
+ * Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_cache_evict(const shadowkv_cache* src, const shadowkv_cache* dst, int keep, int sink,
+                                int recent, int32_t* kept, void* stream);
+
+/* Synchronizes the current device and reads the cache's status word;
+ * SKV_ERR_DEVICE_CHECK if a kernel recorded an id, a length or a token count out of range. */
+skv_status shadowkv_cache_check(const shadowkv_cache* c);
+
 /* ------------------------------------------------------ timing / counting */
 /* Kernels are numbered 0..shadowkv_num_kernels()-1 with stable names. */
 int shadowkv_num_kernels(void);

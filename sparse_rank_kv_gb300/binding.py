@@ -56,6 +56,25 @@ class StateIn(ctypes.Structure):
                 ("V_loc", ctypes.c_void_p), ("V", ctypes.c_void_p), ("v_on_host", ctypes.c_int)]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("sb", ctypes.c_longlong), ("sh", ctypes.c_longlong),
+                ("ss", ctypes.c_longlong)]
+
+
+class NormRopeParams(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int), ("s", ctypes.c_int), ("h_q", ctypes.c_int), ("h_kv", ctypes.c_int),
+                ("d", ctypes.c_int), ("rot", ctypes.c_int), ("dtype", ctypes.c_int), ("norm", ctypes.c_int),
+                ("pos_per_token", ctypes.c_int), ("eps", ctypes.c_float), ("theta", ctypes.c_float)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int), ("h_kv", ctypes.c_int), ("d", ctypes.c_int), ("block", ctypes.c_int),
+                ("max_blocks", ctypes.c_int), ("n_pool", ctypes.c_int), ("k_codes", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("n_tok", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
 class Layout(ctypes.Structure):
     _fields_ = [("kv_records", ctypes.c_int), ("a_tiled", ctypes.c_int), ("tc_score", ctypes.c_int),
                 ("tc_rebuild", ctypes.c_int), ("tc_attention", ctypes.c_int),
@@ -103,6 +122,14 @@ def lib() -> ctypes.CDLL:
             "shadowkv_field_bytes": (I, [V, I, P(S)]),
             "shadowkv_export": (I, [V, I, V, S]),
             "shadowkv_attention_noalloc": (I, [P(Params), V, V, V, I, V, V]),
+            "shadowkv_qk_norm_rope": (I, [P(NormRopeParams), P(Rows), P(Rows), V, V, V, P(Rows), P(Rows), V]),
+            "shadowkv_cache_validate": (I, [P(CacheDesc)]),
+            "shadowkv_cache_append": (I, [P(CacheDesc), I, P(Rows), P(Rows), I, V, V]),
+            "shadowkv_cache_attend_workspace": (S, [P(CacheDesc), I]),
+            "shadowkv_cache_attend": (I, [P(CacheDesc), I, I, P(Rows), ctypes.c_float, I, ctypes.c_float,
+                                          P(Rows), V, V, S, V]),
+            "shadowkv_cache_evict": (I, [P(CacheDesc), P(CacheDesc), I, I, I, V, V]),
+            "shadowkv_cache_check": (I, [P(CacheDesc)]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -281,3 +308,218 @@ def load_state(p: Params, st: dict, stream=None) -> Context:
     _check(lib().shadowkv_load_state(ctypes.byref(p), ctypes.byref(s), _stream(stream),
                                      ctypes.byref(h)))
     return Context(h, p)
+
+
+# ------------------------------------------------------ dense decode path
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> Rows:
+    """A b x h x s x d (or b x h x d) tensor as strided rows."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return Rows(t.data_ptr(), st[0], st[1], st[2] if len(st) == 4 else 0)
+
+
+def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, device):
+    """Data pointer of a contiguous tensor of a given shape, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return dt
+
+
+def _on(device, call, stream):
+    """Runs call(cudaStream_t) with the tensors' device current."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+    if device.index == torch.cuda.current_device():
+        _check(call(_stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(_stream(stream)))
+
+
+def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6, norm: bool = True,
+                 theta: float = 1e4, rot: Optional[int] = None, pos: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Norm of every query and key head and its rotation to the token's position.
+
+    q (b, h_q, s, d) and k (b, h_kv, s, d), float32 or bfloat16, of any strides
+    with d contiguous; either may be None.  The weights have d elements.  pos: int32, (b,)
+    first positions or (b, s), or None for 0..s-1.  rot: rotated dimensions
+    (default d; 0: none).  The outputs are made like the inputs, contiguous,
+    unless given; returns (q_out, k_out)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    if x.dim() != 4:
+        raise ValueError("q and k must be (b, h, s, d)")
+    (b, _, s, d), dev = x.shape, x.device
+    dt = _dtype(x, "q" if q is not None else "k")
+    rows = {}
+    for name, t, w, out in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
+        if t is None:
+            if w is not None or out is not None:
+                raise ValueError(f"{name} is None, its weight or output is not")
+            rows[name] = (0, None, None, None, None)
+            continue
+        if t.dim() != 4:
+            raise ValueError("q and k must be (b, h, s, d)")
+        shape = (b, t.shape[1], s, d)
+        if out is None:
+            out = torch.empty(shape, dtype=t.dtype, device=dev)
+        rows[name] = (shape[1], _rows(t, name, shape, x.dtype, dev), _rows(out, name + "_out", shape, x.dtype, dev),
+                      _dense(w, name + "_weight", (d,), x.dtype, dev), out)
+    per_token = pos is not None and pos.dim() == 2
+    pp = _dense(pos, "pos", (b, s) if per_token else (b,), torch.int32, dev)
+    p = NormRopeParams(b, s, rows["q"][0], rows["k"][0], d, d if rot is None else rot, dt, int(norm),
+                       int(per_token), eps, theta)
+    _on(dev, lambda st: lib().shadowkv_qk_norm_rope(p, rows["q"][1], rows["k"][1], rows["q"][3], rows["k"][3], pp,
+                                                    rows["q"][2], rows["k"][2], st), stream)
+    return rows["q"][4], rows["k"][4]
+
+
+class BlockCache:
+    """A dense key/value cache in e4m3 with a scale per block of tokens and head
+    (shadowkv_cache), on tensors it only names:
+
+      k_codes (n_pool, block/8, d/16, 8, 16), v_codes (n_pool, block/16, d, 16)
+                                    8-bit (float8_e4m3fn or uint8)
+      k_scale, v_scale (n_pool,)    float32
+      table (b, h_kv, max_blocks)   int32: the pool block of each pair's blocks
+      n_tok (b, h_kv)               int32: tokens held
+      weight (b, h_kv, max_blocks)  float32: attention weight gathered per block, or None
+
+    Copies and checkpoints are copies of these tensors.  Calls on one cache
+    must be ordered on one stream (or by events)."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, table, n_tok, weight=None):
+        if k_codes.dim() != 5 or v_codes.dim() != 4 or table.dim() != 3:
+            raise ValueError("k_codes must have 5 dimensions, v_codes 4 and table 3")
+        n_pool, b8, d16, _, _ = k_codes.shape
+        block, d = 8 * b8, 16 * d16
+        b, h, mb = table.shape
+        dev = table.device
+        for name, t, shape in (("k_codes", k_codes, (n_pool, b8, d16, 8, 16)),
+                               ("v_codes", v_codes, (n_pool, block // 16, d, 16))):
+            if t.element_size() != 1:
+                raise ValueError(f"{name} must hold 8-bit codes, got {t.dtype}")
+            _dense(t, name, shape, t.dtype, dev)
+        for name, t, shape, dt in (("k_scale", k_scale, (n_pool,), torch.float32),
+                                   ("v_scale", v_scale, (n_pool,), torch.float32),
+                                   ("table", table, (b, h, mb), torch.int32), ("n_tok", n_tok, (b, h), torch.int32),
+                                   ("weight", weight, (b, h, mb), torch.float32)):
+            _dense(t, name, shape, dt, dev)
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.table, self.n_tok, self.weight = table, n_tok, weight
+        self.b, self.h_kv, self.d, self.block, self.max_blocks, self.device = b, h, d, block, mb, dev
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._desc = CacheDesc(b, h, d, block, mb, n_pool, k_codes.data_ptr(), v_codes.data_ptr(),
+                               k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), n_tok.data_ptr(),
+                               weight.data_ptr() if weight is not None else None, self.status.data_ptr())
+        self._work_bytes = {}
+        _check(lib().shadowkv_cache_validate(self._desc))
+
+    @classmethod
+    def empty(cls, b: int, h_kv: int, d: int, max_blocks: int, block: int = 64, device="cuda"):
+        """A cache without tokens, every pair with max_blocks pool blocks of its own."""
+        dev = torch.device(device)
+        n = b * h_kv * max_blocks
+        z = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype, device=dev)  # noqa: E731
+        return cls(z(n, block // 8, d // 16, 8, 16, dtype=torch.uint8), z(n, block // 16, d, 16, dtype=torch.uint8),
+                   z(n), z(n), torch.arange(n, dtype=torch.int32, device=dev).view(b, h_kv, max_blocks),
+                   z(b, h_kv, dtype=torch.int32), z(b, h_kv, max_blocks))
+
+    def fork(self) -> "BlockCache":
+        """A cache with tables, counts and weights of its own over the same pool.
+        Blocks the two share must not be appended to."""
+        return BlockCache(self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.table.clone(),
+                          self.n_tok.clone(), None if self.weight is None else self.weight.clone())
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, lens: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Appends s tokens to every pair: k, v (b, h_kv, s, d), any strides with
+        d contiguous; lens (b,) int32: tokens of each sequence (default all s)."""
+        if k.dim() != 4:
+            raise ValueError("k and v must be (b, h_kv, s, d)")
+        s = k.shape[2]
+        dt = _dtype(k, "k")
+        shape = (self.b, self.h_kv, s, self.d)
+        rk, rv = _rows(k, "k", shape, k.dtype, self.device), _rows(v, "v", shape, k.dtype, self.device)
+        lp = _dense(lens, "lens", (self.b,), torch.int32, self.device)
+        _on(self.device, lambda st: lib().shadowkv_cache_append(self._desc, dt, rk, rv, s, lp, st), stream)
+
+    def attend(self, q: torch.Tensor, *, scale: Optional[float] = None, decay: Optional[float] = None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """softmax(scale q K^T) V over the tokens held; q (b, h_q, d), scale 1/sqrt(d)
+        by default.  decay: gather block weights, weight = decay weight + this
+        call's (None: weights stay as they are).  lse (b, h_q) float32 receives the log sums.
+        The workspace comes from torch's allocator, on the call's stream."""
+        if q.dim() != 3:
+            raise ValueError("q must be (b, h_q, d)")
+        hq = q.shape[1]
+        dt = _dtype(q, "q")
+        shape = (self.b, hq, self.d)
+        rq = _rows(q, "q", shape, q.dtype, self.device)
+        lp = _dense(lse, "lse", (self.b, hq), torch.float32, self.device)
+        made = []
+
+        def call(st):
+            nb = self._work_bytes.get(hq)
+            if nb is None:
+                nb = lib().shadowkv_cache_attend_workspace(self._desc, hq)
+                if nb == 0:
+                    _check(7)
+                self._work_bytes[hq] = nb
+            work = torch.empty(nb, dtype=torch.uint8, device=self.device)
+            o = out if out is not None else torch.empty(shape, dtype=q.dtype, device=self.device)
+            made.append(o)
+            return lib().shadowkv_cache_attend(
+                self._desc, dt, hq, rq, self.d ** -0.5 if scale is None else scale, int(decay is not None),
+                0.0 if decay is None else decay, _rows(o, "out", shape, q.dtype, self.device), lp, work.data_ptr(),
+                nb, st)
+
+        if stream is None:
+            _on(self.device, call, None)
+        else:
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
+            with torch.cuda.stream(s):
+                _on(self.device, call, s)
+        return made[0]
+
+    def evict(self, keep: int, *, sink: int = 0, recent: int = 1, into: Optional["BlockCache"] = None,
+              kept: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Keeps at most `keep` blocks of every pair: the first `sink`, the last
+        `recent` and those of largest weight.  into: a cache of the same sizes
+        that takes the table, counts and weights (default: in place).  kept (b, h_kv, keep) int32
+        receives the old index of each block still held, then -1."""
+        kp = _dense(kept, "kept", (self.b, self.h_kv, keep), torch.int32, self.device)
+        dst = None if into is None else into._desc
+        if into is not None and into.device != self.device:
+            raise ValueError(f"into is on {into.device}, expected {self.device}")
+        _on(self.device, lambda st: lib().shadowkv_cache_evict(self._desc, dst, keep, sink, recent, kp, st), stream)
+
+    def reset(self) -> None:
+        """Drops every token (on torch's current stream)."""
+        self.n_tok.zero_()
+
+    def check(self) -> None:
+        """Waits for the device; raises if a call met a bad block id, length or count."""
+        _on(self.device, lambda st: lib().shadowkv_cache_check(self._desc), None)

@@ -236,5 +236,7 @@ cudaError_t launch_random_basis(Ctx& c, float* X, cudaStream_t st);
 bool svd_tc_supported(const shadowkv_params& p);
 size_t svd_tc_workspace_bytes(const shadowkv_params& p, int nsm);
 cudaError_t svd_tc_basis(Ctx& c, const void* K, void* ws, cudaStream_t st);   // K: bf16 keys
+// cache.cu: the 8-bit block cache's sizes and pointers (sets the error text)
+skv_status cache_checked(const shadowkv_cache* c);
 
 }  // namespace skv

@@ -1,0 +1,226 @@
+// Norm of query and key heads with the rotation to the token's position
+// (shadowkv_qk_norm_rope): y = x / sqrt(mean x^2 + eps) w, then rotate-half
+// over the first `rot` dimensions by pos theta^(-2i/rot).
+//
+// D/8 lanes hold a row, each with two 4-element pieces: a rotated lane the
+// pieces at 4l and 4l + rot/2, so that a pair's two elements are in one
+// thread; the other lanes two adjacent pieces.
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace skv {
+
+struct RopeFreq {
+  unsigned long long f[64];   // theta^(-2i/rot) / (2 pi), in units of 2^-64 turns
+};
+
+struct NormRopeArgs {
+  const void *x[2], *w[2];                 // q, k
+  void* y[2];
+  long long xb[2], xh[2], xs[2], yb[2], yh[2], ys[2];
+  const int32_t* pos;
+  int s, h_q, heads, rot, norm, per_token;
+  float eps;
+};
+
+// Sine and cosine of pos f turns (f in units of 2^-64).  The product's low 64
+// bits are the fraction of a turn, exact up to f's own rounding at any
+// position; its top 32 bits are split into the nearest quarter and a rest
+// within an eighth of a turn, which fp32 holds to 2^-28.
+template <bool kFast>
+__device__ __forceinline__ void rope_turn(long long pos, unsigned long long f, float* sn, float* cs) {
+  const uint32_t u = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * f + 0x80000000ull) >> 32);
+  const uint32_t quarter = (u + 0x20000000u) >> 30;
+  const float r = static_cast<float>(static_cast<int32_t>(u - (quarter << 30)));
+  float s, c;
+  // the hardware sine and cosine are within 2^-21 here: enough for results
+  // that are rounded to bf16
+  if (kFast) __sincosf(r * (6.283185307179586f / 4294967296.f), &s, &c);
+  else sincospif(r * (2.f / 4294967296.f), &s, &c);
+  const float a = quarter & 1 ? c : s, b = quarter & 1 ? s : c;
+  *sn = quarter & 2 ? -a : a;
+  *cs = (quarter + 1) & 2 ? -b : b;
+}
+
+template <typename T> struct Quad;
+template <> struct Quad<float> {
+  __device__ __forceinline__ static void load(const float* p, float* o) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+  }
+  __device__ __forceinline__ static void store(float* p, const float* o) {
+    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+  }
+};
+template <> struct Quad<bf16> {
+  __device__ __forceinline__ static void load(const bf16* p, float* o) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
+    o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+  __device__ __forceinline__ static void store(bf16* p, const float* o) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+  }
+};
+
+constexpr int kNrThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kNrThreads)
+k_norm_rope(const __grid_constant__ NormRopeArgs a, const __grid_constant__ RopeFreq freq) {
+  constexpr int LPR = D / 8, RPC = kNrThreads / LPR;
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
+  const int l = threadIdx.x % LPR;
+  const long long token = blockIdx.x;
+  const int i = static_cast<int>(token / a.s), t = static_cast<int>(token - static_cast<long long>(i) * a.s);
+  const int head = blockIdx.y * RPC + threadIdx.x / LPR;
+  const bool live = head < a.heads;
+  const int which = head >= a.h_q ? 1 : 0, hh = which ? head - a.h_q : head;
+  const int nrot = a.rot >> 3;
+  const bool turned = l < nrot;
+  const int o0 = turned ? 4 * l : a.rot + 8 * (l - nrot);
+  const int o1 = turned ? 4 * l + (a.rot >> 1) : o0 + 4;
+  float x[8] = {};
+  if (live) {
+    const T* row = static_cast<const T*>(a.x[which]) + i * a.xb[which] + hh * a.xh[which] + t * a.xs[which];
+    Quad<T>::load(row + o0, x);
+    Quad<T>::load(row + o1, x + 4);
+  }
+  if (a.norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(ss * (1.f / D) + a.eps);
+    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (live && a.w[which]) {
+      Quad<T>::load(static_cast<const T*>(a.w[which]) + o0, w);
+      Quad<T>::load(static_cast<const T*>(a.w[which]) + o1, w + 4);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+  }
+  if (!live) return;
+  if (turned) {
+    const long long pos = !a.pos ? t : a.per_token ? a.pos[token] : static_cast<long long>(a.pos[i]) + t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float sn, cs;
+      rope_turn<sizeof(T) == 2>(pos, freq.f[4 * l + e], &sn, &cs);
+      const float x1 = x[e], x2 = x[4 + e];
+      x[e] = x1 * cs - x2 * sn;
+      x[4 + e] = x2 * cs + x1 * sn;
+    }
+  }
+  T* out = static_cast<T*>(a.y[which]) + i * a.yb[which] + hh * a.yh[which] + t * a.ys[which];
+  Quad<T>::store(out + o0, x);
+  Quad<T>::store(out + o1, x + 4);
+}
+
+static cudaError_t launch_norm_rope(const shadowkv_norm_rope_params& p, const NormRopeArgs& a, const RopeFreq& f,
+                                    cudaStream_t st) {
+  const int rpc = kNrThreads / (p.d / 8);
+  const dim3 grid(static_cast<unsigned>(static_cast<long long>(p.b) * p.s), (a.heads + rpc - 1) / rpc);
+  const bool bf = p.dtype == SKV_DTYPE_BF16;
+  auto k = bf ? (p.d == 128 ? k_norm_rope<bf16, 128> : k_norm_rope<bf16, 64>)
+              : (p.d == 128 ? k_norm_rope<float, 128> : k_norm_rope<float, 64>);
+  return launch_pdl(k, grid, dim3(kNrThreads), 0, st, a, f);
+}
+
+// The frequencies of one (theta, rot), kept for the thread's next call with the
+// same ones (64 extended-precision powers take longer than the kernel).
+static const RopeFreq& rope_freq(float theta, int rot) {
+  thread_local RopeFreq f;
+  thread_local float have_theta = -1.f;
+  thread_local int have_rot = -1;
+  if (have_theta != theta || have_rot != rot) {
+    const long double two_pi = 6.283185307179586476925286766559005768L;
+    for (int i = 0; i < rot / 2; ++i) {
+      const long double turns = powl(static_cast<long double>(theta), -2.0L * i / rot) / two_pi;
+      const long double frac = turns - floorl(turns);
+      f.f[i] = static_cast<unsigned long long>(ldexpl(frac, 63)) << 1;
+    }
+    have_theta = theta;
+    have_rot = rot;
+  }
+  return f;
+}
+
+// b x heads x s x d rows of E-byte elements: pointer and strides in whole
+// 4-element pieces; an output's tokens must not share rows.
+static const char* rows_fault(const shadowkv_rows& r, int b, int h, int s, int E, bool out) {
+  if (!r.ptr) return "a row pointer is NULL";
+  if (reinterpret_cast<uintptr_t>(r.ptr) % (4 * E)) return "row pointers must be aligned to 4 elements";
+  if (r.sb < 0 || r.sh < 0 || r.ss < 0) return "row strides must not be negative";
+  if (r.sb % 4 || r.sh % 4 || r.ss % 4) return "row strides must be multiples of 4 elements";
+  if (out && ((b > 1 && !r.sb) || (h > 1 && !r.sh) || (s > 1 && !r.ss))) return "an output stride is 0";
+  return nullptr;
+}
+
+}  // namespace skv
+
+extern "C" skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, const shadowkv_rows* q,
+                                            const shadowkv_rows* k, const void* q_weight, const void* k_weight,
+                                            const int32_t* pos, const shadowkv_rows* q_out,
+                                            const shadowkv_rows* k_out, void* stream) {
+  using skv::set_error;
+  if (!p) return set_error(SKV_ERR_INVALID_ARG, "params is NULL");
+  if (!q && !k) return set_error(SKV_ERR_INVALID_ARG, "q and k are both NULL");
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr))
+    return set_error(SKV_ERR_INVALID_ARG, "q and q_out, k and k_out must be given together");
+  if ((!q && q_weight) || (!k && k_weight)) return set_error(SKV_ERR_INVALID_ARG, "a weight without its rows");
+  const int hq = q ? p->h_q : 0, hk = k ? p->h_kv : 0;
+  if (p->b < 0 || p->s < 0 || (q && hq < 1) || (k && hk < 1))
+    return set_error(SKV_ERR_INVALID_ARG, "need b, s >= 0 and h_q, h_kv >= 1");
+  if (hq > 65536 || hk > 65536) return set_error(SKV_ERR_UNSUPPORTED, "more than 65536 heads");
+  if (static_cast<long long>(p->b) * p->s >= (1LL << 31))
+    return set_error(SKV_ERR_UNSUPPORTED, "b * s must be < 2^31");
+  if (p->d != 64 && p->d != 128) return set_error(SKV_ERR_UNSUPPORTED, "d must be 64 or 128");
+  if (p->rot < 0 || p->rot > p->d || p->rot % 8)
+    return set_error(SKV_ERR_INVALID_ARG, "rot must be a multiple of 8 in 0..d");
+  if (p->dtype != SKV_DTYPE_F32 && p->dtype != SKV_DTYPE_BF16) return set_error(SKV_ERR_INVALID_ARG, "bad dtype");
+  if (p->norm != 0 && p->norm != 1) return set_error(SKV_ERR_INVALID_ARG, "norm must be 0 or 1");
+  if (p->pos_per_token != 0 && p->pos_per_token != 1)
+    return set_error(SKV_ERR_INVALID_ARG, "pos_per_token must be 0 or 1");
+  if (p->norm && (!(p->eps > 0.f) || !std::isfinite(p->eps)))
+    return set_error(SKV_ERR_INVALID_ARG, "eps must be > 0 and finite");
+  if (p->rot && (!(p->theta > 0.f) || !std::isfinite(p->theta)))
+    return set_error(SKV_ERR_INVALID_ARG, "theta must be > 0 and finite");
+  const int E = p->dtype == SKV_DTYPE_BF16 ? 2 : 4;
+  const shadowkv_rows* in[2] = {q, k};
+  const shadowkv_rows* out[2] = {q_out, k_out};
+  const void* w[2] = {q_weight, k_weight};
+  skv::NormRopeArgs a{};
+  for (int i = 0; i < 2; ++i) {
+    if (!in[i]) continue;
+    const char* f = skv::rows_fault(*in[i], p->b, i ? hk : hq, p->s, E, false);
+    if (!f) f = skv::rows_fault(*out[i], p->b, i ? hk : hq, p->s, E, true);
+    if (!f && reinterpret_cast<uintptr_t>(w[i]) % (4 * E)) f = "weights must be aligned to 4 elements";
+    if (f) return set_error(SKV_ERR_INVALID_ARG, f);
+    a.x[i] = in[i]->ptr;
+    a.xb[i] = in[i]->sb; a.xh[i] = in[i]->sh; a.xs[i] = in[i]->ss;
+    a.y[i] = out[i]->ptr;
+    a.yb[i] = out[i]->sb; a.yh[i] = out[i]->sh; a.ys[i] = out[i]->ss;
+    a.w[i] = w[i];
+  }
+  if (reinterpret_cast<uintptr_t>(pos) % 4) return set_error(SKV_ERR_INVALID_ARG, "pos must be 4-byte aligned");
+  if (p->b == 0 || p->s == 0) return SKV_OK;
+  a.pos = pos;
+  a.s = p->s;
+  a.h_q = hq;
+  a.heads = hq + hk;
+  a.rot = p->rot;
+  a.norm = p->norm;
+  a.per_token = p->pos_per_token;
+  a.eps = p->eps;
+  const cudaError_t e = skv::launch_norm_rope(*p, a, skv::rope_freq(p->theta, p->rot), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
+  return SKV_OK;
+}
