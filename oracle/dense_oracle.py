@@ -91,11 +91,12 @@ class Cache:
         return cat(0), cat(2)
 
     def attend(self, q, scale, decay=None):
-        """q (b, h_q, d): out, lse, mag (sum p |v|), logit magnitude (max sum |q k| scale) per head."""
+        """q (b, h_q, d): out, lse, mag (sum p |v|), logit magnitude (max sum |q k| scale) per
+        head, and the sum over 128-token tiles of the tile's largest p times its largest 448 V scale."""
         b, hq, d = q.shape
         G = hq // self.h
         out, mag = np.zeros((b, hq, d)), np.zeros((b, hq, d))
-        lse, lm = np.full((b, hq), -np.inf), np.zeros((b, hq))
+        lse, lm, top = np.full((b, hq), -np.inf), np.zeros((b, hq)), np.zeros((b, hq))
         for i in range(b):
             for g in range(self.h):
                 k, v = self.values(i, g)
@@ -111,12 +112,16 @@ class Cache:
                     p /= p.sum()
                     out[i, h], mag[i, h] = p @ v, p @ np.abs(v)
                     lm[i, h] = (abs(scale) * (np.abs(k) @ np.abs(q[i, h]))).max()
+                    per = 128 // self.block
+                    for t in range(0, n, 128):
+                        vs = max(abs(x[3]) for x in self.blocks[i, g][t // self.block:t // self.block + per])
+                        top[i, h] += p[t:t + 128].max() * 448 * vs
                     full = np.zeros(len(w) * self.block)
                     full[:n] = p
                     w += full.reshape(len(w), self.block).sum(1)
                 if decay is not None:
                     self.weight[i, g] = list(decay * np.asarray(self.weight[i, g]) + w if decay else w)
-        return out, lse, mag, lm
+        return out, lse, mag, lm, top
 
 
 def evict(weight, n_tok, block, keep, sink, recent):

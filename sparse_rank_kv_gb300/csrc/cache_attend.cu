@@ -113,122 +113,473 @@ __device__ __forceinline__ void share_find(const AttendArgs& a, int cta, int nct
   __syncthreads();
 }
 
-// ------------------------------------------------------------ CUDA cores
+// ------------------------------------------------------------ tensor cores
+// The codes go to the tensor core as they are (tcgen05 kind::f8f6f4, one
+// K-major tile per 128 tokens, straight from bulk copies of whole blocks):
+//   S = K Q^T   (M = 128 tokens, K = d),        Q: QP rows per query head
+//   O = V^T P^T (M = d, K = 128 tokens),        P: PP rows per query head
+// q and p are not e4m3 numbers but sums of them: x = x0 + x1/16 + x2/256 + ...,
+// each term the e4m3 rounding of what the ones before leave, 4 bits each.
+// Two terms hold a bf16 query exactly (8 bits), four hold p to 16 bits, six an
+// fp32 value; e4m3's range ends them at 2^-18 16^(1-terms) of the largest entry (of
+// a tile's p V-scale, of a q row): 2^-30 for bf16's p, 2^-38 for fp32.  Decoding has
+// G <= 8 query rows for a tile of at least 16, so the terms fill rows that
+// would be padding, and no code is ever converted.  Products of e4m3 numbers accumulate in fp32 (measured: within
+// 2^-22 of the sum of magnitudes, as an fp32 matrix product).
+constexpr int kCaSoft = 128;                  // softmax threads: warps 0..3, thread = token, then dimension
+constexpr int kCaThreads = kCaSoft + 64;      // warp 4: copies, warp 5: tcgen05.mma
+constexpr int kCaSmemMax = 113 * 1024;        // two CTAs per SM
+
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kCaT) k_attend(const __grid_constant__ AttendArgs a) {
-  __shared__ int s_where[3], s_scan[32];
-  __shared__ float sq[G][D], sp[G][kCaT], red[4][G];
+struct Ca {
+  static constexpr int QP = sizeof(T) == 2 ? 2 : 6, PP = sizeof(T) == 2 ? 4 : 6;
+  static constexpr int N1 = (G * QP + 15) / 16 * 16, N2 = (G * PP + 15) / 16 * 16;
+  static constexpr int KB = kCaT * D, Stage = 2 * KB;       // K tile, V tile
+  static constexpr int QB = N1 * D, PB = N2 * kCaT;
+  static constexpr int Misc = 2048;
+  static constexpr int NST = (kCaSmemMax - 128 - QB - 2 * PB - Misc) / Stage;
+  static constexpr int Smem = 128 + NST * Stage + QB + 2 * PB + Misc;
+  static constexpr int Cols0 = 2 * N1 + 2 * N2;
+  static constexpr int Cols = Cols0 <= 32 ? 32 : Cols0 <= 64 ? 64 : Cols0 <= 128 ? 128 : 256;
+  static_assert(NST >= 2 && Cols0 <= 256, "attention tile");
+};
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// kind::f8f6f4, e4m3 A and B (format 0), fp32 D, both K-major, M = 128
+constexpr uint32_t idesc_e4m3(int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A CTA's tiles in order: `left` tiles from tile `tile` of pair `pair`.
+struct TileCursor {
+  int pair, tile, left, ntok, nt;
+  __device__ __forceinline__ void begin(const CacheDev& c, int p, int t, int n) {
+    pair = p;
+    tile = t;
+    left = n;
+    ntok = cache_tokens(c, p);
+    nt = (ntok + kCaT - 1) / kCaT;
+  }
+  // to the next tile; true when it is another pair's
+  __device__ __forceinline__ bool next(const CacheDev& c) {
+    if (--left <= 0) return false;
+    if (++tile < nt) return false;
+    tile = 0;
+    do {
+      if (++pair >= c.pairs) { left = 0; return false; }
+      ntok = cache_tokens(c, pair);
+      nt = (ntok + kCaT - 1) / kCaT;
+    } while (nt == 0);
+    return true;
+  }
+  __device__ __forceinline__ int run() const { return min(nt - tile, left); }   // tiles left in this pair
+};
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant__ AttendArgs a) {
+  using C = Ca<T, D, G>;
+  constexpr int N1 = C::N1, N2 = C::N2, NST = C::NST;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  unsigned char* stages = smem;
+  unsigned char* qbuf = stages + NST * C::Stage;
+  unsigned char* pbuf = qbuf + C::QB;
+  unsigned char* misc = pbuf + 2 * C::PB;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc);   // [NST <= 7]
+  uint64_t* empty = full + 8;                           // [NST]
+  uint64_t* sfull = empty + 8;                          // [2]
+  uint64_t* pfull = sfull + 2;
+  uint64_t* ofull = pfull + 2;
+  uint64_t* qfull = ofull + 2;                          // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 192);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 196);
+  int* s_where = reinterpret_cast<int*>(misc + 200);    // [3]
+  float* sqs = reinterpret_cast<float*>(misc + 224);    // [G] q scales
+  float* red = reinterpret_cast<float*>(misc + 256);    // [2][4][G]
+  int* s_scan = reinterpret_cast<int*>(misc + 512);     // [32]
+  float* ssc = reinterpret_cast<float*>(misc + 640);    // [NST][20]: K scales, V factors, V reference
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   tc::grid_dep_launch();
+
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sfull[i], 1);
+      tc::mbar_init(&pfull[i], kCaSoft / 32);
+      tc::mbar_init(&ofull[i], 1);
+    }
+    tc::mbar_init(qfull, kCaSoft / 32);
+    tc::fence_mbar_init();
+    *s_abort = 0;
+  }
+  if (warp == 5) {
+    tc::tmem_alloc(tmem_slot, C::Cols);
+    tc::tmem_relinquish();
+  }
+  // operand rows past the terms stay zero
+  for (int i = tid; i < (C::QB + 2 * C::PB) / 16; i += kCaThreads)
+    reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async_smem();
+  tc::fence_before();
   tc::grid_dep_wait();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
   const int cta = blockIdx.x;
-  share_find<kCaT>(a, cta, gridDim.x, s_where, s_scan);
+  share_find<kCaThreads>(a, cta, gridDim.x, s_where, s_scan);
   const int total = s_where[2], n = min(static_cast<int>(gridDim.x), total);
-  if (cta >= n) return;
-  const int t0 = share_begin(cta, n, total), t1 = share_begin(cta + 1, n, total);
-  const int gran = min(1 << a.c.shift, 32);
-  int pair = s_where[0], tile = s_where[1], left = t1 - t0, at = t0;
-  while (left > 0) {
-    const int ntok = cache_tokens(a.c, pair), nt = (ntok + kCaT - 1) / kCaT;
-    if (tile >= nt) {   // the next pair (one without tokens has no tile)
-      if (pair + 1 >= a.c.pairs) break;
-      ++pair;
-      tile = 0;
-      continue;
+  const int t0 = cta < n ? share_begin(cta, n, total) : 0, ntile = cta < n ? share_begin(cta + 1, n, total) - t0 : 0;
+  const int shift = a.c.shift, B = 1 << shift;
+  auto abort_now = [&]() {
+    *s_abort = 1;
+    flag_error(a.c.status, DEV_TIMEOUT);
+  };
+
+  if (ntile > 0 && warp == 4) {
+    // ------------------------------------------------------------ copies
+    // lane = block of the tile; block ids are loaded two tiles ahead, the
+    // blocks' scales one ahead
+    TileCursor cur, nx1, nx2;
+    cur.begin(a.c, s_where[0], s_where[1], ntile);
+    auto blocks = [&](const TileCursor& c) { return c.left > 0 ? (min(kCaT, c.ntok - c.tile * kCaT) + B - 1) >> shift : 0; };
+    auto id_of = [&](const TileCursor& c) {
+      return lane < blocks(c) ? cache_block(a.c, c.pair, ((c.tile * kCaT) >> shift) + lane) : 0;
+    };
+    int id = id_of(cur);
+    nx1 = cur;
+    nx1.next(a.c);
+    int id1 = id_of(nx1);
+    float ks = a.c.ks[id], vs = a.c.vs[id];
+    int it = 0;
+    for (;; ++it) {
+      nx2 = nx1;
+      if (nx2.left > 0) nx2.next(a.c);
+      const int id2 = id_of(nx2);
+      const float ks1 = a.c.ks[id1], vs1 = a.c.vs[id1];
+      const int st = it % NST, use = it / NST;
+      bool ok = true;
+      if (lane == 0) ok = !*s_abort && tc::mbar_wait(&empty[st], (use & 1) ^ 1, kWaitLimit);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        if (lane == 0) abort_now();
+        break;
+      }
+      const int nb = blocks(cur);
+      float* sc = ssc + st * 20;
+      // V's scales relative to the tile's largest, which O is multiplied by
+      float vref = lane < nb ? fabsf(vs) : 0.f;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, o));
+      if (lane < nb) {
+        sc[lane] = ks;
+        sc[8 + lane] = vref > 0.f ? vs / vref * 256.f : vs == vs ? 0.f : vs;
+      }
+      if (lane == 0) sc[16] = vref * (1.f / 256.f);
+      __syncwarp();
+      if (lane == 0) tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb) * 2u * (B * D));
+      __syncwarp();
+      if (lane < nb) {
+        unsigned char* dst = stages + st * C::Stage + lane * (B * D);
+        const size_t src = static_cast<size_t>(id) * (B * D);
+        tc::bulk_load(dst, a.c.kc + src, B * D, &full[st]);
+        tc::bulk_load(dst + C::KB, a.c.vc + src, B * D, &full[st]);
+      }
+      if (nx1.left <= 0) { ++it; break; }
+      cur = nx1;
+      nx1 = nx2;
+      id = id1;
+      id1 = id2;
+      ks = ks1;
+      vs = vs1;
     }
-    if (tile == 0 && tid == 0) a.w.first[pair] = at;
-    const int seq = pair / a.c.h_kv, head = pair - seq * a.c.h_kv;
-    __syncthreads();
-    for (int i = tid; i < G * D; i += kCaT) {
-      const int g = i / D, j = i - g * D;
-      sq[g][j] = Ty<T>::to_f(static_cast<const T*>(a.q)[seq * a.qb + (static_cast<long long>(head) * G + g) * a.qh + j]);
+    // after an abort, no copy may still be on its way when the CTA ends
+    if (lane == 0 && *s_abort)
+      for (int u = max(0, it - NST); u < it; ++u) tc::mbar_wait(&full[u % NST], (u / NST) & 1, kWaitLimit);
+    __syncwarp();
+  } else if (ntile > 0 && warp == 5) {
+    // ------------------------------------------------------------ tensor core
+    if (lane == 0) {
+      TileCursor cur;
+      cur.begin(a.c, s_where[0], s_where[1], ntile);
+      const uint32_t tS = tmem, tO = tmem + 2 * N1;
+      int it = 0, runs = 0;
+      bool ok = true;
+      auto scores = [&](bool first) {
+        const int st = it % NST;
+        if (first) ok = ok && tc::mbar_wait(qfull, (runs++) & 1, kWaitLimit);
+        ok = ok && tc::mbar_wait(&full[st], (it / NST) & 1, kWaitLimit);
+        if (!ok) return;
+        tc::fence_after();
+        const uint32_t k0 = tc::smem_u32(stages + st * C::Stage), q0 = tc::smem_u32(qbuf);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          mma_e4m3(tS + (it & 1) * N1, tc::desc_k_none(k0 + k * 256, 128, 8 * D),
+                   tc::desc_k_none(q0 + k * (2 * N1 * 16), N1 * 16, 128), idesc_e4m3(N1), k > 0);
+        tc::mma_commit(&sfull[it & 1]);
+      };
+      auto values = [&](int j) {
+        const int st = j % NST;
+        ok = ok && tc::mbar_wait(&pfull[j & 1], (j >> 1) & 1, kWaitLimit);
+        if (!ok) return;
+        tc::fence_after();
+        const uint32_t v0 = tc::smem_u32(stages + st * C::Stage + C::KB), p0 = tc::smem_u32(pbuf + (j & 1) * C::PB);
+#pragma unroll
+        for (int k = 0; k < kCaT / 32; ++k)
+          mma_e4m3(tO + (j & 1) * N2, tc::desc_k_none(v0 + k * (2 * D * 16), D * 16, 128),
+                   tc::desc_k_none(p0 + k * (2 * N2 * 16), N2 * 16, 128), idesc_e4m3(N2), k > 0);
+        tc::mma_commit(&ofull[j & 1]);
+        tc::mma_commit(&empty[st]);
+      };
+      // S of the next tile is issued before O of this one, so that the
+      // softmax never waits for it; at a new pair, whose q the softmax
+      // warps lay out after their last tile of the old one, after it
+      bool first = true;
+      for (;;) {
+        if (first && it > 0) {
+          values(it - 1);
+          scores(true);
+        } else {
+          scores(first);
+          if (it > 0) values(it - 1);
+        }
+        if (!ok) break;
+        first = cur.next(a.c);
+        ++it;
+        if (cur.left <= 0) break;
+      }
+      if (ok) values(it - 1);
+      if (!ok) abort_now();
     }
-    __syncthreads();
-    const int end = min(nt, tile + left);
-    float m[G], l[G], acc[G];
+    __syncwarp();
+  } else if (ntile > 0) {
+    // ------------------------------------------------------------ softmax
+    TileCursor cur;
+    cur.begin(a.c, s_where[0], s_where[1], ntile);
+    const uint32_t tS = tmem + (static_cast<uint32_t>(warp) << 21), tO = tS + 2 * N1;
+    const int gran = min(B, 32);
+    bool ok = true;
+    // q's terms, each head scaled by a power of two so that the largest
+    // entry is at most 448; an entry that is not finite makes the head NaN
+    auto lay_q = [&](int pair) {
+      const int seq = pair / a.c.h_kv, kvh = pair - seq * a.c.h_kv;
+      for (int g = warp; g < G; g += 4) {
+        const T* row = static_cast<const T*>(a.q) + seq * a.qb + (static_cast<long long>(kvh) * G + g) * a.qh;
+        float x[D / 32], m = 0.f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) { m[g] = -INFINITY; l[g] = 0.f; acc[g] = 0.f; }
-    for (int t = tile; t < end; ++t) {
-      const int tok0 = t * kCaT, cnt = min(kCaT, ntok - tok0);
-      float s[G];
-      const int tok = tok0 + tid;
-      if (tid < cnt) {
-        const int id = cache_block(a.c, pair, tok >> a.c.shift), r = tok & ((1 << a.c.shift) - 1);
-        const uint8_t* row = a.c.kc + static_cast<size_t>(id) * (D << a.c.shift) + (r >> 3) * (8 * D) + (r & 7) * 16;
+        for (int e = 0; e < D / 32; ++e) {
+          x[e] = Ty<T>::to_f(row[lane + 32 * e]);
+          const float ax = fabsf(x[e]);
+          m = fmaxf(m, ax < INFINITY ? ax : 0.f);
+          if (!(ax < INFINITY)) x[e] = __int_as_float(0x7fffffff);
+        }
+        m = warp_max(m);
+        const float s = cache_scale_of(m), inv = 1.f / s;
 #pragma unroll
-        for (int g = 0; g < G; ++g) s[g] = 0.f;
-        for (int p = 0; p < D / 16; ++p) {
-          const uint4 v = *reinterpret_cast<const uint4*>(row + p * 128);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int e = 0; e < D / 32; e += 2) {
+          float u = x[e] * inv, v = x[e + 1] * inv;
+          const int j = lane + 32 * e;
+          unsigned char* dst = qbuf + (j >> 4) * (N1 * 16) + (j & 15);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 f = e4m3_unpack2(w[e >> 1] >> (16 * (e & 1)));
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-              s[g] = fmaf(f.x, sq[g][p * 16 + 2 * e], fmaf(f.y, sq[g][p * 16 + 2 * e + 1], s[g]));
+          for (int i = 0; i < C::QP; ++i) {
+            const uint32_t c2 = e4m3_pack2(u, v);
+            dst[(i * G + g) * 16] = static_cast<unsigned char>(c2);
+            dst[(i * G + g) * 16 + 2 * N1 * 16] = static_cast<unsigned char>(c2 >> 8);
+            const float2 f = e4m3_unpack2(c2);
+            u = (u - f.x) * 16.f;
+            v = (v - f.y) * 16.f;
           }
         }
-        const float ks = a.c.ks[id] * a.scale_log2;
-#pragma unroll
-        for (int g = 0; g < G; ++g) s[g] *= ks;
-      } else {
-#pragma unroll
-        for (int g = 0; g < G; ++g) s[g] = -INFINITY;
+        if (lane == 0) sqs[g] = s * a.scale_log2;
       }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(qfull);
+      ok = tc::named_sync_and(1, kCaSoft, ok);
+    };
+    lay_q(cur.pair);
+    int it = 0, at = t0;
+    while (cur.left > 0 && ok) {
+      const int pair = cur.pair, ntok = cur.ntok, nrun = cur.run();
+      if (cur.tile == 0 && tid == 0) a.w.first[pair] = at;
+      // running maximum, sum and output of the run; p is relative to its own
+      // tile's maximum, whatever larger one came before (a token with most of
+      // the weight and little value must not push the others' terms out)
+      float m[G], l[G], acc[G], al[G], be[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float x = warp_max(s[g]);
-        if (lane == 0) red[warp][g] = x;
+        m[g] = -INFINITY;
+        l[g] = acc[g] = al[g] = be[g] = 0.f;
       }
-      __syncthreads();
+      // adds tile j's O to the run's sums
+      auto take_o = [&](int j) {
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&ofull[j & 1], (j >> 1) & 1, kWaitLimit));
+        if (!ok) return;
+        tc::fence_after();
+        float o[N2];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float mn = fmaxf(fmaxf(fmaxf(red[0][g], red[1][g]), fmaxf(red[2][g], red[3][g])), m[g]);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float al = exp2f(m[g] - ref);
-        m[g] = mn;
-        const float p = exp2f(s[g] - ref);
-        l[g] = l[g] * al + p;
-        acc[g] *= al;
-        sp[g][tid] = p;
+        for (int c = 0; c < N2; c += 16) tc::tmem_ld16(tO + (j & 1) * N2 + c, o + c);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float x = o[(C::PP - 1) * G + g];
+#pragma unroll
+          for (int i = C::PP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, o[i * G + g]);
+          acc[g] = fmaf(acc[g], al[g], x * be[g]);
+        }
+      };
+      for (int r = 0; r < nrun; ++r, ++it) {
+        const int t = cur.tile + r, st = it % NST, cnt = min(kCaT, ntok - t * kCaT);
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&full[st], (it / NST) & 1, kWaitLimit) &&
+                                         tc::mbar_wait(&sfull[it & 1], (it >> 1) & 1, kWaitLimit));
+        float s[G];
+        const float* sc = ssc + st * 20;
+        const int blk = tid >> shift;
+        if (ok) {
+          tc::fence_after();
+          float v[N1];
+#pragma unroll
+          for (int c = 0; c < N1; c += 16) tc::tmem_ld16(tS + (it & 1) * N1 + c, v + c);
+          const float ks = sc[blk];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            float x = v[(C::QP - 1) * G + g];
+#pragma unroll
+            for (int i = C::QP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, v[i * G + g]);
+            s[g] = tid < cnt ? x * (sqs[g] * ks) : -INFINITY;
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float x = redux_max(s[g]);
+            if (lane == 0) red[(it & 1) * 32 + warp * G + g] = x;
+          }
+        }
+        ok = tc::named_sync_and(1, kCaSoft, ok);
+        if (!ok) break;
+        float al_new[G], be_new[G];
+        unsigned char* pb = pbuf + (it & 1) * C::PB + (tid >> 4) * (N2 * 16) + (tid & 15);
+        const float vf = tid < cnt ? sc[8 + blk] : 0.f, vref = sc[16];
+        float p[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float* rd = red + (it & 1) * 32 + g;
+          const float mt = fmaxf(fmaxf(rd[0], rd[G]), fmaxf(rd[2 * G], rd[3 * G]));
+          const float tref = mt == -INFINITY ? 0.f : mt, mn = fmaxf(mt, m[g]), ref = mn == -INFINITY ? 0.f : mn;
+          al_new[g] = exp2f(m[g] - ref);
+          be_new[g] = exp2f(mt - ref);
+          m[g] = mn;
+          p[g] = exp2f(s[g] - tref);
+          l[g] = fmaf(l[g], al_new[g], p[g] * be_new[g]);
+          be_new[g] *= vref;
+          if (a.gather && tid == 0) a.w.tmax[(static_cast<size_t>(pair) * a.w.tiles + t) * G + g] = tref;
+        }
         if (a.gather) {
-          float z = p;
-          for (int o = 1; o < gran; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-          if ((tid & (gran - 1)) == 0)
-            a.w.psum[(static_cast<size_t>(pair) * a.w.granules + (tok0 + tid) / gran) * G + g] = z;
-          if (tid == 0) a.w.tmax[(static_cast<size_t>(pair) * a.w.tiles + t) * G + g] = ref;
+          float z[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            z[g] = p[g];
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) z[g] += __shfl_xor_sync(0xffffffffu, z[g], o);
+            if (gran == 32) z[g] += __shfl_xor_sync(0xffffffffu, z[g], 16);
+          }
+          if ((lane & (gran - 1)) == 0) {
+            float* dst = a.w.psum + (static_cast<size_t>(pair) * a.w.granules + (t * kCaT + tid) / gran) * G;
+#pragma unroll
+            for (int g = 0; g < G; ++g) dst[g] = z[g];
+          }
+        }
+        // p's terms, times the token's V scale; rows term G + head
+#pragma unroll
+        for (int g = 0; g < G; g += 2) {
+          float u = p[g] * vf, v = G > 1 ? p[g + (G > 1)] * vf : 0.f;
+#pragma unroll
+          for (int i = 0; i < C::PP; ++i) {
+            const uint32_t c2 = e4m3_pack2(u, v);
+            pb[(i * G + g) * 16] = static_cast<unsigned char>(c2);
+            if (G > 1) pb[(i * G + g + 1) * 16] = static_cast<unsigned char>(c2 >> 8);
+            const float2 f = e4m3_unpack2(c2);
+            u = (u - f.x) * 16.f;
+            v = (v - f.y) * 16.f;
+          }
+        }
+        // V past the tokens may be any bytes, NaN too: zero under zero weights
+        if (cnt < kCaT && tid < D) {
+          unsigned char* vb = stages + st * C::Stage + C::KB + tid * 16;
+          for (int u = cnt >> 4; u < kCaT / 16; ++u) {
+            uint4* w = reinterpret_cast<uint4*>(vb + u * (D * 16));
+            const int keep = cnt - u * 16;   // bytes kept, if any
+            if (keep <= 0) {
+              *w = make_uint4(0, 0, 0, 0);
+            } else {
+              uint4 x = *w;
+              uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int kb = keep - 4 * e;
+                xw[e] = kb >= 4 ? xw[e] : kb <= 0 ? 0u : xw[e] & ((1u << (8 * kb)) - 1u);
+              }
+              *w = x;
+            }
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&pfull[it & 1]);
+        if (r > 0) take_o(it - 1);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          al[g] = al_new[g];
+          be[g] = be_new[g];
         }
       }
-      __syncthreads();
-      if (tid < D) {
-        for (int u = 0; u < cnt; ++u) {
-          const int tk = tok0 + u, id = cache_block(a.c, pair, tk >> a.c.shift), r = tk & ((1 << a.c.shift) - 1);
-          const uint8_t c8 = a.c.vc[static_cast<size_t>(id) * (D << a.c.shift) + (r >> 4) * (16 * D) + tid * 16 + (r & 15)];
-          const float v = e4m3_unpack2(c8).x * a.c.vs[id];
-#pragma unroll
-          for (int g = 0; g < G; ++g) acc[g] = fmaf(sp[g][u], v, acc[g]);
-        }
-      }
-      __syncthreads();
-    }
-    // the partial of (this CTA, pair)
-    float* part = a.w.part + static_cast<size_t>(cta + pair) * G * (D + 2);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const float z = warp_sum(l[g]);
-      if (lane == 0) red[warp][g] = z;
-      if (tid < D) part[g * (D + 2) + tid] = acc[g];
-    }
-    __syncthreads();
-    if (tid == 0)
+      if (!ok) break;
+      cur.tile += nrun - 1;
+      cur.left -= nrun - 1;
+      cur.next(a.c);
+      at += nrun;
+      if (cur.left > 0) lay_q(cur.pair);   // S of the next pair can start
+      take_o(it - 1);
+      tc::fence_before();
+      // the partial of (this CTA, pair)
+      float* part = a.w.part + static_cast<size_t>(cta + pair) * G * (D + 2);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        part[g * (D + 2) + D] = m[g];
-        part[g * (D + 2) + D + 1] = red[0][g] + red[1][g] + red[2][g] + red[3][g];
+        const float z = warp_sum(l[g]);
+        if (lane == 0) red[64 + warp * G + g] = z;
+        if (tid < D) part[g * (D + 2) + tid] = acc[g];
       }
-    at += end - tile;
-    left -= end - tile;
-    tile = end;
+      ok = tc::named_sync_and(1, kCaSoft, ok);
+      if (tid < G) {
+        const float* rd = red + 64 + tid;
+        float mm = m[0];
+#pragma unroll
+        for (int g = 1; g < G; ++g) mm = tid == g ? m[g] : mm;
+        part[tid * (D + 2) + D] = mm;
+        part[tid * (D + 2) + D + 1] = rd[0] + rd[G] + rd[2 * G] + rd[3 * G];
+      }
+    }
+    if (!ok && tid == 0) abort_now();
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, C::Cols);
   }
 }
 
@@ -312,7 +663,9 @@ k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int chunk, int nc
 
 template <typename T, int D, int G>
 static cudaError_t attend_t(const AttendArgs& a, int ncta, cudaStream_t st) {
-  cudaError_t e = launch_pdl(k_attend<T, D, G>, dim3(ncta), dim3(kCaT), 0, st, a);
+  const auto kern = k_attend<T, D, G>;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), Ca<T, D, G>::Smem);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ncta), dim3(kCaThreads), Ca<T, D, G>::Smem, st, a);
   if (e != cudaSuccess) return e;
   const int chunk = 512;
   const int nchunk = a.gather ? (a.c.max_blocks + chunk - 1) / chunk : 0;
