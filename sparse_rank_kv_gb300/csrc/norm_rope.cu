@@ -23,7 +23,8 @@ struct NormRopeArgs {
   void* y[2];
   long long xb[2], xh[2], xs[2], yb[2], yh[2], ys[2];
   const int32_t* pos;
-  int s, h_q, heads, rot, norm, per_token;
+  uint32_t tokens;                         // b s
+  int s, h_q, heads, chunk, rot, norm, per_token;
   float eps;
 };
 
@@ -46,88 +47,133 @@ __device__ __forceinline__ void rope_turn(long long pos, unsigned long long f, f
   *cs = (quarter + 1) & 2 ? -b : b;
 }
 
+// 4 elements of a row, as loaded and as floats.
 template <typename T> struct Quad;
 template <> struct Quad<float> {
-  __device__ __forceinline__ static void load(const float* p, float* o) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-  }
-  __device__ __forceinline__ static void store(float* p, const float* o) {
-    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
-  }
+  typedef float4 Raw;
+  __device__ __forceinline__ static void get(Raw v, float* o) { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
+  __device__ __forceinline__ static Raw put(const float* o) { return make_float4(o[0], o[1], o[2], o[3]); }
 };
 template <> struct Quad<bf16> {
-  __device__ __forceinline__ static void load(const bf16* p, float* o) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
+  typedef uint2 Raw;
+  __device__ __forceinline__ static void get(Raw v, float* o) {
     o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
     o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
   }
-  __device__ __forceinline__ static void store(bf16* p, const float* o) {
+  __device__ __forceinline__ static Raw put(const float* o) {
     __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+    return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
   }
 };
 
 constexpr int kNrThreads = 256;
+constexpr int kNrTokens = 4;    // tokens per CTA
 
+// CTA = 4 tokens x `chunk` heads.  The tokens' sines and cosines are formed
+// once, a pair per thread, and every D/8-lane group keeps its token's in
+// registers over its heads, which it loads kNrRows at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(kNrThreads)
 k_norm_rope(const __grid_constant__ NormRopeArgs a, const __grid_constant__ RopeFreq freq) {
-  constexpr int LPR = D / 8, RPC = kNrThreads / LPR;
+  constexpr int LPR = D / 8, Sub = kNrThreads / LPR / kNrTokens;   // row groups per token
+  constexpr int Rows = 16 / sizeof(T) / 2;                         // rows in flight per group
+  typedef typename Quad<T>::Raw Raw;
+  __shared__ float2 s_cs[kNrTokens][D / 2];
   tc::grid_dep_launch();
+  const int half = a.rot >> 1;
+  const uint32_t tok0 = blockIdx.x * kNrTokens;
   tc::grid_dep_wait();
-  const int l = threadIdx.x % LPR;
-  const long long token = blockIdx.x;
-  const int i = static_cast<int>(token / a.s), t = static_cast<int>(token - static_cast<long long>(i) * a.s);
-  const int head = blockIdx.y * RPC + threadIdx.x / LPR;
-  const bool live = head < a.heads;
-  const int which = head >= a.h_q ? 1 : 0, hh = which ? head - a.h_q : head;
+  auto place = [&](uint32_t token, int* i, int* t) {
+    *i = static_cast<int>(token / static_cast<uint32_t>(a.s));
+    *t = static_cast<int>(token - static_cast<uint32_t>(*i) * static_cast<uint32_t>(a.s));
+  };
+  for (int e = threadIdx.x; e < kNrTokens * half; e += kNrThreads) {
+    const int u = e / half, p = e - u * half;
+    const uint32_t token = tok0 + u;
+    if (token >= a.tokens) break;
+    int i, t;
+    place(token, &i, &t);
+    const long long pos = !a.pos ? t : a.per_token ? a.pos[token] : static_cast<long long>(a.pos[i]) + t;
+    float sn, cs;
+    rope_turn<sizeof(T) == 2>(pos, freq.f[p], &sn, &cs);
+    s_cs[u][p] = make_float2(cs, sn);
+  }
+  __syncthreads();
+  const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR, u = grp / Sub, sub = grp % Sub;
+  const uint32_t token = tok0 + u;
+  const bool live = token < a.tokens;
   const int nrot = a.rot >> 3;
   const bool turned = l < nrot;
   const int o0 = turned ? 4 * l : a.rot + 8 * (l - nrot);
-  const int o1 = turned ? 4 * l + (a.rot >> 1) : o0 + 4;
-  float x[8] = {};
-  if (live) {
-    const T* row = static_cast<const T*>(a.x[which]) + i * a.xb[which] + hh * a.xh[which] + t * a.xs[which];
-    Quad<T>::load(row + o0, x);
-    Quad<T>::load(row + o1, x + 4);
-  }
-  if (a.norm) {
-    float ss = 0.f;
+  const int o1 = turned ? 4 * l + half : o0 + 4;
+  float2 cs[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+  for (int e = 0; e < 4; ++e) cs[e] = turned ? s_cs[u][4 * l + e] : make_float2(1.f, 0.f);
+  int i = 0, t = 0;
+  if (live) place(token, &i, &t);
+  const int c0 = blockIdx.y * a.chunk, c1 = min(a.heads, c0 + a.chunk);
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(ss * (1.f / D) + a.eps);
+  for (int which = 0; which < 2; ++which) {
+    // this part's heads of the chunk, as indexes into q or k
+    const int base = which ? a.h_q : 0;
+    const int h0 = max(c0, base) - base, h1 = min(c1, which ? a.heads : a.h_q) - base;
+    if (h0 >= h1) continue;
+    const T* src = static_cast<const T*>(a.x[which]) + i * a.xb[which] + t * a.xs[which];
+    T* dst = static_cast<T*>(a.y[which]) + i * a.yb[which] + t * a.ys[which];
     float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-    if (live && a.w[which]) {
-      Quad<T>::load(static_cast<const T*>(a.w[which]) + o0, w);
-      Quad<T>::load(static_cast<const T*>(a.w[which]) + o1, w + 4);
+    if (a.norm && a.w[which]) {
+      Quad<T>::get(*reinterpret_cast<const Raw*>(static_cast<const T*>(a.w[which]) + o0), w);
+      Quad<T>::get(*reinterpret_cast<const Raw*>(static_cast<const T*>(a.w[which]) + o1), w + 4);
     }
+    for (int hb = h0; hb < h1; hb += Rows * Sub) {   // the same count for every lane of the warp
+      Raw r0[Rows] = {}, r1[Rows] = {};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
-  }
-  if (!live) return;
-  if (turned) {
-    const long long pos = !a.pos ? t : a.per_token ? a.pos[token] : static_cast<long long>(a.pos[i]) + t;
+      for (int v = 0; v < Rows; ++v) {
+        const int h = hb + v * Sub + sub;
+        if (live && h < h1) {
+          r0[v] = *reinterpret_cast<const Raw*>(src + h * a.xh[which] + o0);
+          r1[v] = *reinterpret_cast<const Raw*>(src + h * a.xh[which] + o1);
+        }
+      }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float sn, cs;
-      rope_turn<sizeof(T) == 2>(pos, freq.f[4 * l + e], &sn, &cs);
-      const float x1 = x[e], x2 = x[4 + e];
-      x[e] = x1 * cs - x2 * sn;
-      x[4 + e] = x2 * cs + x1 * sn;
+      for (int v = 0; v < Rows; ++v) {
+        const int h = hb + v * Sub + sub;
+        float x[8];
+        Quad<T>::get(r0[v], x);
+        Quad<T>::get(r1[v], x + 4);
+        if (a.norm) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float r = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+        }
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = x[e] * cs[e].x - x[4 + e] * cs[e].y;
+          y[4 + e] = x[4 + e] * cs[e].x + x[e] * cs[e].y;
+        }
+        if (live && h < h1) {
+          *reinterpret_cast<Raw*>(dst + h * a.yh[which] + o0) = Quad<T>::put(turned ? y : x);
+          *reinterpret_cast<Raw*>(dst + h * a.yh[which] + o1) = Quad<T>::put(turned ? y + 4 : x + 4);
+        }
+      }
     }
   }
-  T* out = static_cast<T*>(a.y[which]) + i * a.yb[which] + hh * a.yh[which] + t * a.ys[which];
-  Quad<T>::store(out + o0, x);
-  Quad<T>::store(out + o1, x + 4);
 }
 
-static cudaError_t launch_norm_rope(const shadowkv_norm_rope_params& p, const NormRopeArgs& a, const RopeFreq& f,
+static cudaError_t launch_norm_rope(const shadowkv_norm_rope_params& p, NormRopeArgs& a, const RopeFreq& f,
                                     cudaStream_t st) {
-  const int rpc = kNrThreads / (p.d / 8);
-  const dim3 grid(static_cast<unsigned>(static_cast<long long>(p.b) * p.s), (a.heads + rpc - 1) / rpc);
+  const long long groups = (static_cast<long long>(a.tokens) + kNrTokens - 1) / kNrTokens;
+  // few tokens: one head per row group, spread over CTAs; many: all heads in
+  // one CTA, which then forms its angles once (measured at 32 + 8 heads of 128)
+  const int sub = kNrThreads / (p.d / 8) / kNrTokens;
+  a.chunk = groups < 512 ? sub : a.heads;
+  const dim3 grid(static_cast<unsigned>(groups), (a.heads + a.chunk - 1) / a.chunk);
   const bool bf = p.dtype == SKV_DTYPE_BF16;
   auto k = bf ? (p.d == 128 ? k_norm_rope<bf16, 128> : k_norm_rope<bf16, 64>)
               : (p.d == 128 ? k_norm_rope<float, 128> : k_norm_rope<float, 64>);
@@ -214,6 +260,7 @@ extern "C" skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, 
   if (p->b == 0 || p->s == 0) return SKV_OK;
   a.pos = pos;
   a.s = p->s;
+  a.tokens = static_cast<uint32_t>(p->b) * static_cast<uint32_t>(p->s);
   a.h_q = hq;
   a.heads = hq + hk;
   a.rot = p->rot;
