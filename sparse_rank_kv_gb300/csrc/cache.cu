@@ -26,11 +26,16 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= FLT_MAX ? a : 0.f;   // infinities and NaN do not count
 }
 
-// x / s: by the reciprocal where s is a power of two (then the exact
-// quotient), else (a partly filled block the caller made with a scale of its
-// own) by division.
 __device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0u; }
-__device__ __forceinline__ float quotient(float x, float s, float inv, bool pow2) { return pow2 ? x * inv : x / s; }
+
+// Two held codes (low 16 bits) under a scale larger by 1 / ratio.
+__device__ __forceinline__ uint32_t rescale2(uint32_t c2, float ratio) {
+  const float2 f = e4m3_unpack2(c2);
+  return e4m3_pack2(f.x * ratio, f.y * ratio);
+}
+__device__ __forceinline__ uint32_t rescale4(uint32_t c4, float ratio) {
+  return rescale2(c4, ratio) | (rescale2(c4 >> 16, ratio) << 16);
+}
 
 // The tokens a pair's append covers: [n0, end) of the pair.
 __device__ __forceinline__ void append_range(const AppendArgs& a, int pair, int* n0, int* end) {
@@ -52,143 +57,231 @@ __device__ __forceinline__ void append_range(const AppendArgs& a, int pair, int*
   *end = n + cnt;
 }
 
-// Quantises the new tokens [n0, end) that fall into the pair's block blk, for
-// K (which = 0) or V (1).  Two passes over the tokens' rows: the largest
-// magnitude, then the codes (the second pass hits L1).
-template <typename T, int D>
-__device__ __forceinline__ void append_block(const AppendArgs& a, int pair, int blk, int n0, int end, int which,
-                                             float* red) {
-  constexpr int VE = 16 / sizeof(T);        // elements per 16-byte load
+// Bytes t of w0, w1 (t < 4) replaced by the low and the high code of c2.
+__device__ __forceinline__ void put_codes(uint32_t* w0, uint32_t* w1, int t, uint32_t c2) {
+  const int sh = t * 8;
+  *w0 = (*w0 & ~(0xffu << sh)) | ((c2 & 0xffu) << sh);
+  *w1 = (*w1 & ~(0xffu << sh)) | (((c2 >> 8) & 0xffu) << sh);
+}
+
+// One block's K or V in the hands of TPJ threads: 16 code bytes of K per unit
+// (16 dimensions of a row), 2 x 16 of V (16 tokens of two dimensions), so that
+// every store is 16 bytes and the loads of a unit's elements are all in
+// flight together.  Elements are loaded once and wait in registers while the
+// block's largest magnitude is found.
+template <typename T, int D, int B>
+struct Ap {
+  static constexpr int TPJ = B * D / 32 < kApThreads ? B * D / 32 : kApThreads;
+  static constexpr int UV = B * D / 32 / TPJ, UK = 2 * UV;   // units per thread
+  static constexpr int E = sizeof(T) / 2;                    // 32-bit words per two elements
+  static constexpr int Words = 16 * UV * E;                  // raw words per thread
+  // unit u of K: 8 consecutive threads take a group's 8 rows (128 adjacent code bytes)
+  __device__ __forceinline__ static int k_row(int u) { return (u / (D / 2) << 3) + (u & 7); }
+  __device__ __forceinline__ static int k_piece(int u) { return (u >> 3) % (D / 16); }
+  __device__ __forceinline__ static int v_tok(int u) { return u / (D / 2) << 4; }
+  __device__ __forceinline__ static int v_dim(int u) { return u % (D / 2) * 2; }
+  // the two elements at pair index p of the raw words
+  __device__ __forceinline__ static float2 pair(const uint32_t* w, int p) {
+    if constexpr (E == 1) return make_float2(__uint_as_float(w[p] << 16), __uint_as_float(w[p] & 0xffff0000u));
+    else return make_float2(__uint_as_float(w[2 * p]), __uint_as_float(w[2 * p + 1]));
+  }
+
+  // rows [e0, e1) of the block from src (row 0's address; rows outside are not read)
+  __device__ __forceinline__ static void load(uint32_t* w, const T* src, long long ss, int which, int e0, int e1, int tid) {
+    if (which == 0) {
+#pragma unroll
+      for (int i = 0; i < UK; ++i) {
+        const int u = tid + i * TPJ, r = k_row(u);
+        const bool on = r >= e0 && r < e1;
+        const uint4* p = reinterpret_cast<const uint4*>(src + r * ss + k_piece(u) * 16);
+#pragma unroll
+        for (int e = 0; e < 2 * E; ++e) {
+          const uint4 x = on ? p[e] : make_uint4(0, 0, 0, 0);
+          uint32_t* o = w + i * 8 * E + 4 * e;
+          o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < UV; ++i) {
+        const int u = tid + i * TPJ, t0 = v_tok(u), j = v_dim(u);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const bool on = t0 + t >= e0 && t0 + t < e1;
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(src + (t0 + t) * ss + j);
+          uint32_t* o = w + (i * 16 + t) * E;
+          if constexpr (E == 1) {
+            o[0] = on ? *p : 0u;
+          } else {
+            const uint2 x = on ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
+            o[0] = x.x; o[1] = x.y;
+          }
+        }
+      }
+    }
+  }
+
+  // the largest magnitude, as fp32 bits (integer order is magnitude order);
+  // 0x7f800000 and above: something is infinite or NaN
+  __device__ __forceinline__ static uint32_t top(const uint32_t* w) {
+    uint32_t m = 0;
+    if constexpr (E == 1) {
+#pragma unroll
+      for (int i = 0; i < Words; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+      return max(m & 0xffff0000u, m << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < Words; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
+    }
+  }
+  __device__ __forceinline__ static uint32_t top_finite(const uint32_t* w) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < Words / E; ++p) {
+      const float2 f = pair(w, p);
+      const uint32_t a = __float_as_uint(f.x) & 0x7fffffffu, b = __float_as_uint(f.y) & 0x7fffffffu;
+      m = max(m, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+    }
+    return m;
+  }
+
+  // codes of the rows in w under scale sc; with grow, of the rows [0, e0)
+  // held, too, whose scale was smaller by ratio
+  __device__ __forceinline__ static void store(const uint32_t* w, uint8_t* dst, float sc, bool grow, float ratio,
+                                               int which, int e0, int e1, int tid) {
+    const float inv = 1.f / sc;   // exact for a power of two
+    const bool pow2 = is_pow2(sc);
+    auto code2 = [&](float2 f) {
+      // a partly filled block the caller made may have another scale: divide
+      return pow2 ? e4m3_pack2(f.x * inv, f.y * inv) : e4m3_pack2(f.x / sc, f.y / sc);
+    };
+    if (which == 0) {
+#pragma unroll
+      for (int i = 0; i < UK; ++i) {
+        const int u = tid + i * TPJ, r = k_row(u);
+        if (r >= e1 || (r < e0 && !grow)) continue;
+        uint4* d = reinterpret_cast<uint4*>(dst + (r >> 3) * (8 * D) + k_piece(u) * 128 + (r & 7) * 16);
+        if (r < e0) {
+          const uint4 o = *d;
+          *d = make_uint4(rescale4(o.x, ratio), rescale4(o.y, ratio), rescale4(o.z, ratio), rescale4(o.w, ratio));
+        } else {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = __byte_perm(code2(pair(w + i * 8 * E, 2 * e)), code2(pair(w + i * 8 * E, 2 * e + 1)), 0x5410);
+          *d = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < UV; ++i) {
+        const int u = tid + i * TPJ, t0 = v_tok(u), j = v_dim(u);
+        if (t0 >= e1 || (t0 + 16 <= e0 && !grow)) continue;
+        uint4* d = reinterpret_cast<uint4*>(dst + (t0 >> 4) * (16 * D) + j * 16);
+        uint32_t a[4], b[4];
+        if (t0 >= e0 && t0 + 16 <= e1) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t* x = w + (i * 16 + 4 * t) * E;
+            const uint32_t p = __byte_perm(code2(pair(x, 0)), code2(pair(x, 1)), 0x5140);   // t0 t1 of j, of j + 1
+            const uint32_t q = __byte_perm(code2(pair(x, 2)), code2(pair(x, 3)), 0x5140);
+            a[t] = __byte_perm(p, q, 0x5410);
+            b[t] = __byte_perm(p, q, 0x7632);
+          }
+        } else {
+          // bytes of tokens that are neither held nor new stay as they are
+          const uint4 oa = d[0], ob = d[1];
+          a[0] = oa.x; a[1] = oa.y; a[2] = oa.z; a[3] = oa.w;
+          b[0] = ob.x; b[1] = ob.y; b[2] = ob.z; b[3] = ob.w;
+#pragma unroll
+          for (int t = 0; t < 16; ++t) {
+            const int r = t0 + t;
+            if (r >= e0 && r < e1) {
+              put_codes(&a[t >> 2], &b[t >> 2], t & 3, code2(pair(w + (i * 16 + t) * E, 0)));
+            } else if (r < e0 && grow) {
+              const uint32_t old = ((a[t >> 2] >> (8 * (t & 3))) & 0xffu) | (((b[t >> 2] >> (8 * (t & 3))) & 0xffu) << 8);
+              put_codes(&a[t >> 2], &b[t >> 2], t & 3, rescale2(old, ratio));
+            }
+          }
+        }
+        d[0] = make_uint4(a[0], a[1], a[2], a[3]);
+        d[1] = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+    }
+  }
+};
+
+// Group of TPJ threads = a run of `per` blocks of a pair's K or V, the next
+// block's rows loading while the current block is quantised (without that
+// every block pays its loads' latency, which bounds a CTA per block).
+// k_append_count moves the token counts after.
+template <typename T, int D, int B>
+__global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constant__ AppendArgs a, int per, int nrun) {
+  typedef Ap<T, D, B> A;
+  constexpr int NW = (A::TPJ + 31) / 32;
+  __shared__ uint32_t red[2][kApThreads / 32];
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
+  const int grp = threadIdx.x / A::TPJ, tid = threadIdx.x % A::TPJ, warp = threadIdx.x >> 5;
+  const long long job = static_cast<long long>(blockIdx.x) * (kApThreads / A::TPJ) + grp;
+  const int run = static_cast<int>(job % nrun);
+  const long long pw = job / nrun;
+  const int which = static_cast<int>(pw & 1);
+  if ((pw >> 1) >= a.c.pairs) return;
+  const int pair = static_cast<int>(pw >> 1);
   const CacheDev& c = a.c;
-  const int B = 1 << c.shift, tid = threadIdx.x;
-  const int b0 = blk << c.shift;
-  const int e0 = max(n0 - b0, 0), e1 = min(end - b0, B);   // new rows of the block
-  if (e0 >= e1) return;
-  const int id = cache_block(c, pair, blk);
+  int n0, end;
+  append_range(a, pair, &n0, &end);
+  int blk = (n0 / B) + run * per;
+  const int last = min(blk + per, (end + B - 1) / B);   // blocks [blk, last)
+  if (blk >= last) return;
   const int seq = pair / c.h_kv, head = pair - seq * c.h_kv;
   const T* src = which ? static_cast<const T*>(a.v) + seq * a.vb + head * a.vh
                        : static_cast<const T*>(a.k) + seq * a.kb + head * a.kh;
   const long long ss = which ? a.vs : a.ks;
-  src += (static_cast<long long>(b0) + e0 - n0) * ss;       // row e0 of the block
-  uint8_t* dst = (which ? c.vc : c.kc) + static_cast<size_t>(id) * (D << c.shift);
-  float* scale = (which ? c.vs : c.ks) + id;
-
-  float m = 0.f;
-  for (int u = tid; u < (e1 - e0) * (D / VE); u += kApThreads) {
-    const int r = u / (D / VE), p = u % (D / VE);
-    float x[VE];
-    Ty<T>::load16(src + r * ss + p * VE, x);
-#pragma unroll
-    for (int e = 0; e < VE; ++e) m = fmaxf(m, finite_abs(x[e]));
-  }
-  m = warp_max(m);
-  __syncthreads();
-  if ((tid & 31) == 0) red[tid >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kApThreads / 32; ++w) m = fmaxf(m, red[w]);
-  const float fresh = cache_scale_of(m);
-  const float was = e0 > 0 ? *scale : 0.f;
-  const float sc = fmaxf(fresh, was);
-  const bool grow = e0 > 0 && sc > was;
-  const float ratio = e0 > 0 ? was / sc : 1.f;
-  const float inv = 1.f / sc;
-  const bool pow2 = is_pow2(sc);
-  auto dv = [&](float x) { return quotient(x, sc, inv, pow2); };
-  auto rescale2 = [&](uint32_t c2) {
-    const float2 f = e4m3_unpack2(c2);
-    return e4m3_pack2(f.x * ratio, f.y * ratio);
+  src -= static_cast<long long>(n0) * ss;               // the pair's token 0
+  auto all_max = [&](uint32_t m, int turn) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (NW > 1) {
+      if ((tid & 31) == 0) red[turn][warp] = m;
+      tc::named_sync(1 + grp, A::TPJ);
+      for (int w = 0; w < NW; ++w) m = max(m, red[turn][grp * NW + w]);
+    }
+    return m;
   };
-
-  if (which == 0) {
-    // K: unit = 16 dimensions of a row (16 bytes); 8 consecutive threads take
-    // 8 rows, whose units are adjacent in the block
-    const int r0 = grow ? 0 : e0 & ~7;
-    for (int u = tid; u < (((e1 + 7) & ~7) - r0) * (D / 16); u += kApThreads) {
-      const int r = r0 + ((u / (8 * (D / 16))) << 3) + (u & 7), p = (u >> 3) % (D / 16);
-      if (r >= e1 || (r < e0 && !grow)) continue;
-      uint4* w = reinterpret_cast<uint4*>(dst + (r >> 3) * (8 * D) + p * 128 + (r & 7) * 16);
-      uint32_t o[4];
-      if (r < e0) {
-        const uint4 old = *w;
-        const uint32_t in[4] = {old.x, old.y, old.z, old.w};
+  uint32_t w[A::Words], nx[A::Words];
+  int id = cache_block(c, pair, blk);
+  A::load(nx, src + static_cast<long long>(blk) * B * ss, ss, which, max(n0 - blk * B, 0), min(end - blk * B, B), tid);
+  for (int turn = 0; blk < last; ++blk, turn ^= 1) {
+    const int e0 = max(n0 - blk * B, 0), e1 = min(end - blk * B, B);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = rescale2(in[e]) | (rescale2(in[e] >> 16) << 16);
-      } else {
-        float x[16];
-#pragma unroll
-        for (int e = 0; e < 16; e += VE) Ty<T>::load16(src + (r - e0) * ss + p * 16 + e, x + e);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = e4m3_pack2(dv(x[4 * e]), dv(x[4 * e + 1])) | (e4m3_pack2(dv(x[4 * e + 2]), dv(x[4 * e + 3])) << 16);
-      }
-      *w = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int i = 0; i < A::Words; ++i) w[i] = nx[i];
+    int id_next = 0;
+    if (blk + 1 < last) {
+      id_next = cache_block(c, pair, blk + 1);
+      A::load(nx, src + static_cast<long long>(blk + 1) * B * ss, ss, which, 0, min(end - (blk + 1) * B, B), tid);
     }
-  } else {
-    // V: unit = 16 tokens of two dimensions (32 bytes); bytes of tokens
-    // that are neither held nor new stay as they are
-    const int g0 = grow ? 0 : e0 >> 4, g1 = (e1 + 15) >> 4;
-    for (int u = tid; u < (g1 - g0) * (D / 2); u += kApThreads) {
-      const int t0 = (g0 + u / (D / 2)) << 4, j = (u % (D / 2)) * 2;
-      uint4* w = reinterpret_cast<uint4*>(dst + (t0 >> 4) * (16 * D) + j * 16);
-      uint32_t o[2][4] = {};
-      if (t0 < e0 || t0 + 16 > e1) {
-        const uint4 a0 = w[0], a1 = w[1];
-        o[0][0] = a0.x; o[0][1] = a0.y; o[0][2] = a0.z; o[0][3] = a0.w;
-        o[1][0] = a1.x; o[1][1] = a1.y; o[1][2] = a1.z; o[1][3] = a1.w;
-      }
-#pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        const int r = t0 + t, sh = (t & 3) * 8;
-        uint32_t c2;
-        if (r >= e0 && r < e1) {
-          const T* p = src + (r - e0) * ss + j;
-          c2 = e4m3_pack2(dv(Ty<T>::to_f(p[0])), dv(Ty<T>::to_f(p[1])));
-        } else if (r < e0 && grow) {
-          c2 = rescale2(((o[0][t >> 2] >> sh) & 0xffu) | (((o[1][t >> 2] >> sh) & 0xffu) << 8));
-        } else {
-          continue;
-        }
-        o[0][t >> 2] = (o[0][t >> 2] & ~(0xffu << sh)) | ((c2 & 0xffu) << sh);
-        o[1][t >> 2] = (o[1][t >> 2] & ~(0xffu << sh)) | ((c2 >> 8) << sh);
-      }
-      w[0] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-      w[1] = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+    float* scale = (which ? c.vs : c.ks) + id;
+    const float was = e0 > 0 ? *scale : 0.f;
+    // two reductions of one block use both halves of red; the next block's
+    // first one, `turn` later, is behind another barrier of the group
+    uint32_t m = all_max(A::top(w), turn);
+    if (m >= 0x7f800000u) {
+      tc::named_sync(1 + grp, A::TPJ);
+      m = all_max(A::top_finite(w), turn ^ 1);
+      tc::named_sync(1 + grp, A::TPJ);
     }
+    const float sc = fmaxf(cache_scale_of(__uint_as_float(m)), was);
+    const bool grow = e0 > 0 && sc > was;
+    if (NW == 1) __syncwarp();   // every lane has read the old scale
+    if (tid == 0) {
+      *scale = sc;
+      if (which == 0 && e0 == 0 && c.weight) c.weight[static_cast<size_t>(pair) * c.max_blocks + blk] = 0.f;
+    }
+    A::store(w, (which ? c.vc : c.kc) + static_cast<size_t>(id) * (D * B), sc, grow, was / sc, which, e0, e1, tid);
+    id = id_next;
   }
-  __syncthreads();   // every thread has read the old scale
-  if (tid == 0) {
-    *scale = sc;
-    if (which == 0 && e0 == 0 && c.weight) c.weight[static_cast<size_t>(pair) * c.max_blocks + blk] = 0.f;
-  }
-}
-
-// Few new tokens (s <= block): one CTA per pair covers the at most two
-// blocks they touch and moves the pair's count.
-template <typename T, int D>
-__global__ void __launch_bounds__(kApThreads) k_append_few(const __grid_constant__ AppendArgs a) {
-  __shared__ float red[kApThreads / 32];
-  tc::grid_dep_launch();
-  tc::grid_dep_wait();
-  const int pair = blockIdx.x;
-  int n0, end;
-  append_range(a, pair, &n0, &end);
-  for (int blk = n0 >> a.c.shift; blk << a.c.shift < end; ++blk)
-    for (int which = 0; which < 2; ++which) append_block<T, D>(a, pair, blk, n0, end, which, red);
-  __syncthreads();
-  if (threadIdx.x == 0) a.c.n_tok[pair] = end;
-}
-
-// Many: CTA (block, pair) for K and V; k_append_count moves the counts after.
-template <typename T, int D>
-__global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constant__ AppendArgs a, int nblk) {
-  __shared__ float red[kApThreads / 32];
-  tc::grid_dep_launch();
-  tc::grid_dep_wait();
-  const int pair = blockIdx.x / nblk, bi = blockIdx.x - pair * nblk;
-  int n0, end;
-  append_range(a, pair, &n0, &end);
-  append_block<T, D>(a, pair, (n0 >> a.c.shift) + bi, n0, end, blockIdx.y, red);
 }
 
 __global__ void __launch_bounds__(kApThreads) k_append_count(const __grid_constant__ AppendArgs a) {
@@ -201,18 +294,119 @@ __global__ void __launch_bounds__(kApThreads) k_append_count(const __grid_consta
   a.c.n_tok[pair] = end;
 }
 
+// One new token: a warp for a pair's K, one for its V, lane = D/32 adjacent
+// dimensions.  Only where the token needs a larger scale does the warp pass over
+// the block's codes.
 template <typename T, int D>
-static cudaError_t append_t(const AppendArgs& a, cudaStream_t st) {
-  const int B = 1 << a.c.shift;
-  if (a.s <= B)
-    return launch_pdl(k_append_few<T, D>, dim3(a.c.pairs), dim3(kApThreads), 0, st, a);
+__global__ void __launch_bounds__(kApThreads) k_append_one(const __grid_constant__ AppendArgs a) {
+  constexpr int N = D / 32;
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
+  const CacheDev& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, which = warp & 1;
+  const int pair = blockIdx.x * (kApThreads / 64) + (warp >> 1);
+  int n0 = 0, end = 0;
+  if (pair < c.pairs) {
+    const int seq = pair / c.h_kv, head = pair - seq * c.h_kv;
+    const T* src = which ? static_cast<const T*>(a.v) + seq * a.vb + head * a.vh
+                         : static_cast<const T*>(a.k) + seq * a.kb + head * a.kh;
+    // the row is there whatever the counts say, except where lens gives the
+    // sequence no token
+    float x[N] = {};
+    const bool any = !a.lens || a.lens[seq] > 0;
+    if (any) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] = Ty<T>::to_f(src[lane * N + e]);
+    }
+    append_range(a, pair, &n0, &end);
+    if (end > n0) {
+      const int blk = n0 >> c.shift, e0 = n0 - (blk << c.shift);
+      const int id = cache_block(c, pair, blk);
+      uint8_t* dst = (which ? c.vc : c.kc) + static_cast<size_t>(id) * (D << c.shift);
+      float* scale = (which ? c.vs : c.ks) + id;
+      const float was = e0 > 0 ? *scale : 0.f;
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) m = max(m, __float_as_uint(finite_abs(x[e])));
+      m = __reduce_max_sync(0xffffffffu, m);
+      const float sc = fmaxf(cache_scale_of(__uint_as_float(m)), was);
+      if (e0 > 0 && sc > was) {
+        const float ratio = was / sc;
+        for (int u = lane; u < (D << c.shift) / 16; u += 32) {
+          // 16 bytes: one row of K, 16 tokens of V
+          const int r = which ? (u / D) << 4 : (u / (D / 2) << 3) + (u & 7);
+          if (r >= e0) continue;
+          uint4* w = reinterpret_cast<uint4*>(dst) + u;
+          const uint4 o = *w;
+          const uint32_t in[4] = {o.x, o.y, o.z, o.w};
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = rescale4(in[e], ratio);
+            const int left = which ? e0 - r - 4 * e : 4;   // tokens of this word that are held
+            if (left < 4) {
+              const uint32_t keep = left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+              y[e] = (y[e] & keep) | (in[e] & ~keep);
+            }
+          }
+          *w = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      __syncwarp();
+      const float inv = 1.f / sc;
+      const bool pow2 = is_pow2(sc);
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        const uint32_t c2 = pow2 ? e4m3_pack2(x[e] * inv, x[e + 1] * inv) : e4m3_pack2(x[e] / sc, x[e + 1] / sc);
+        const int j = lane * N + e;
+        if (which == 0) {
+          *reinterpret_cast<uint16_t*>(dst + (e0 >> 3) * (8 * D) + (j >> 4) * 128 + (e0 & 7) * 16 + (j & 15)) =
+              static_cast<uint16_t>(c2);
+        } else {
+          uint8_t* w = dst + (e0 >> 4) * (16 * D) + j * 16 + (e0 & 15);
+          w[0] = static_cast<uint8_t>(c2);
+          w[16] = static_cast<uint8_t>(c2 >> 8);
+        }
+      }
+      if (lane == 0) {
+        *scale = sc;
+        if (which == 0 && e0 == 0 && c.weight) c.weight[static_cast<size_t>(pair) * c.max_blocks + blk] = 0.f;
+      }
+    }
+  }
+  __syncthreads();   // both warps of a pair have read its count
+  if (pair < c.pairs && which == 0 && lane == 0) c.n_tok[pair] = end;
+}
+
+template <typename T, int D, int B>
+static cudaError_t append_many(const AppendArgs& a, cudaStream_t st) {
+  typedef Ap<T, D, B> A;
   const long long touched = (static_cast<long long>(a.s) + B - 1) / B + 1;
   const int nblk = static_cast<int>(touched < a.c.max_blocks ? touched : a.c.max_blocks);
-  cudaError_t e = launch_pdl(k_append_many<T, D>, dim3(static_cast<unsigned>(a.c.pairs) * nblk, 2), dim3(kApThreads), 0, st,
-                             a, nblk);
+  // runs of up to 8 blocks as long as about 4096 groups are left
+  const long long jobs = 2LL * a.c.pairs * nblk;
+  const int per = static_cast<int>(jobs / 4096 < 1 ? 1 : jobs / 4096 > 8 ? 8 : jobs / 4096);
+  const int nrun = (nblk + per - 1) / per;
+  const long long groups = 2LL * a.c.pairs * nrun, gpc = kApThreads / A::TPJ;
+  cudaError_t e = launch_pdl(k_append_many<T, D, B>, dim3(static_cast<unsigned>((groups + gpc - 1) / gpc)),
+                             dim3(kApThreads), 0, st, a, per, nrun);
   if (e == cudaSuccess)
     e = launch_pdl(k_append_count, dim3((a.c.pairs + kApThreads - 1) / kApThreads), dim3(kApThreads), 0, st, a);
   return e;
+}
+
+template <typename T, int D>
+static cudaError_t append_t(const AppendArgs& a, cudaStream_t st) {
+  if (a.s == 1) {
+    constexpr int ppc = kApThreads / 64;   // pairs per CTA
+    return launch_pdl(k_append_one<T, D>, dim3((a.c.pairs + ppc - 1) / ppc), dim3(kApThreads), 0, st, a);
+  }
+  switch (a.c.shift) {
+    case 4: return append_many<T, D, 16>(a, st);
+    case 5: return append_many<T, D, 32>(a, st);
+    case 6: return append_many<T, D, 64>(a, st);
+    default: return append_many<T, D, 128>(a, st);
+  }
 }
 
 // ------------------------------------------------------------------ evict
