@@ -316,14 +316,11 @@ _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> Rows:
     """A b x h x s x d (or b x h x d) tensor as strided rows."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {tuple(shape)} on "
+                         f"{device} (shape, type and device)")
     st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return Rows(t.data_ptr(), st[0], st[1], st[2] if len(st) == 4 else 0)
 
@@ -332,7 +329,7 @@ def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, device):
     """Data pointer of a contiguous tensor of a given shape, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -345,15 +342,23 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return dt
 
 
-def _on(device, call, stream):
-    """Runs call(cudaStream_t) with the tensors' device current."""
+def _call(fn, device, stream, *args) -> None:
+    """fn(*args, cudaStream_t) with the tensors' device current; stream None:
+    torch's current stream of that device."""
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, got {device}")
-    if device.index == torch.cuda.current_device():
-        _check(call(_stream(stream)))
+    i = device.index
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(i)
     else:
-        with torch.cuda.device(device):
-            _check(call(_stream(stream)))
+        st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if i == torch._C._cuda_getDevice():
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, st)
+    if rc:
+        _check(rc)
 
 
 def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
@@ -370,31 +375,28 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight:
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
-    if x.dim() != 4:
+    if x.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be (b, h, s, d)")
-    (b, _, s, d), dev = x.shape, x.device
+    (b, _, s, d), dev, dtype = x.shape, x.device, x.dtype
     dt = _dtype(x, "q" if q is not None else "k")
-    rows = {}
-    for name, t, w, out in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
+    heads, rows, outs, ws = [0, 0], [None, None], [None, None], [None, None]
+    made = [q_out, k_out]
+    for i, (name, t, w) in enumerate((("q", q, q_weight), ("k", k, k_weight))):
         if t is None:
-            if w is not None or out is not None:
+            if w is not None or made[i] is not None:
                 raise ValueError(f"{name} is None, its weight or output is not")
-            rows[name] = (0, None, None, None, None)
             continue
-        if t.dim() != 4:
-            raise ValueError("q and k must be (b, h, s, d)")
-        shape = (b, t.shape[1], s, d)
-        if out is None:
-            out = torch.empty(shape, dtype=t.dtype, device=dev)
-        rows[name] = (shape[1], _rows(t, name, shape, x.dtype, dev), _rows(out, name + "_out", shape, x.dtype, dev),
-                      _dense(w, name + "_weight", (d,), x.dtype, dev), out)
+        heads[i] = t.shape[1]
+        shape = (b, heads[i], s, d)
+        if made[i] is None:
+            made[i] = torch.empty(shape, dtype=dtype, device=dev)
+        rows[i], outs[i] = _rows(t, name, shape, dtype, dev), _rows(made[i], name + "_out", shape, dtype, dev)
+        ws[i] = _dense(w, name + "_weight", (d,), dtype, dev)
     per_token = pos is not None and pos.dim() == 2
     pp = _dense(pos, "pos", (b, s) if per_token else (b,), torch.int32, dev)
-    p = NormRopeParams(b, s, rows["q"][0], rows["k"][0], d, d if rot is None else rot, dt, int(norm),
-                       int(per_token), eps, theta)
-    _on(dev, lambda st: lib().shadowkv_qk_norm_rope(p, rows["q"][1], rows["k"][1], rows["q"][3], rows["k"][3], pp,
-                                                    rows["q"][2], rows["k"][2], st), stream)
-    return rows["q"][4], rows["k"][4]
+    p = NormRopeParams(b, s, heads[0], heads[1], d, d if rot is None else rot, dt, int(norm), int(per_token), eps, theta)
+    _call(lib().shadowkv_qk_norm_rope, dev, stream, p, rows[0], rows[1], ws[0], ws[1], pp, outs[0], outs[1])
+    return made[0], made[1]
 
 
 class BlockCache:
@@ -464,7 +466,7 @@ class BlockCache:
         shape = (self.b, self.h_kv, s, self.d)
         rk, rv = _rows(k, "k", shape, k.dtype, self.device), _rows(v, "v", shape, k.dtype, self.device)
         lp = _dense(lens, "lens", (self.b,), torch.int32, self.device)
-        _on(self.device, lambda st: lib().shadowkv_cache_append(self._desc, dt, rk, rv, s, lp, st), stream)
+        _call(lib().shadowkv_cache_append, self.device, stream, self._desc, dt, rk, rv, s, lp)
 
     def attend(self, q: torch.Tensor, *, scale: Optional[float] = None, decay: Optional[float] = None,
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -474,35 +476,36 @@ class BlockCache:
         The workspace comes from torch's allocator, on the call's stream."""
         if q.dim() != 3:
             raise ValueError("q must be (b, h_q, d)")
-        hq = q.shape[1]
+        dev, hq = self.device, q.shape[1]
         dt = _dtype(q, "q")
         shape = (self.b, hq, self.d)
-        rq = _rows(q, "q", shape, q.dtype, self.device)
-        lp = _dense(lse, "lse", (self.b, hq), torch.float32, self.device)
-        made = []
-
-        def call(st):
-            nb = self._work_bytes.get(hq)
-            if nb is None:
-                nb = lib().shadowkv_cache_attend_workspace(self._desc, hq)
-                if nb == 0:
-                    _check(7)
-                self._work_bytes[hq] = nb
-            work = torch.empty(nb, dtype=torch.uint8, device=self.device)
-            o = out if out is not None else torch.empty(shape, dtype=q.dtype, device=self.device)
-            made.append(o)
-            return lib().shadowkv_cache_attend(
-                self._desc, dt, hq, rq, self.d ** -0.5 if scale is None else scale, int(decay is not None),
-                0.0 if decay is None else decay, _rows(o, "out", shape, q.dtype, self.device), lp, work.data_ptr(),
-                nb, st)
-
-        if stream is None:
-            _on(self.device, call, None)
-        else:
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
+        rq = _rows(q, "q", shape, q.dtype, dev)
+        lp = _dense(lse, "lse", (self.b, hq), torch.float32, dev)
+        if stream is not None:
+            # the output and the workspace are allocated on the stream that uses them
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), dev)
             with torch.cuda.stream(s):
-                _on(self.device, call, s)
-        return made[0]
+                return self.attend(q, scale=scale, decay=decay, out=out, lse=lse)
+        nb = self._work_bytes.get(hq)
+        if nb is None:
+            nb = self._workspace(hq)
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
+        work = torch.empty(nb, dtype=torch.uint8, device=dev)
+        _call(lib().shadowkv_cache_attend, dev, None, self._desc, dt, hq, rq,
+              self.d ** -0.5 if scale is None else scale, decay is not None, 0.0 if decay is None else decay,
+              _rows(out, "out", shape, q.dtype, dev), lp, work.data_ptr(), nb)
+        return out
+
+    def _workspace(self, hq: int) -> int:
+        if self.device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {self.device}")
+        with torch.cuda.device(self.device):
+            nb = lib().shadowkv_cache_attend_workspace(self._desc, hq)
+        if nb == 0:
+            _check(7)
+        self._work_bytes[hq] = nb
+        return nb
 
     def evict(self, keep: int, *, sink: int = 0, recent: int = 1, into: Optional["BlockCache"] = None,
               kept: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -514,7 +517,7 @@ class BlockCache:
         dst = None if into is None else into._desc
         if into is not None and into.device != self.device:
             raise ValueError(f"into is on {into.device}, expected {self.device}")
-        _on(self.device, lambda st: lib().shadowkv_cache_evict(self._desc, dst, keep, sink, recent, kp, st), stream)
+        _call(lib().shadowkv_cache_evict, self.device, stream, self._desc, dst, keep, sink, recent, kp)
 
     def reset(self) -> None:
         """Drops every token (on torch's current stream)."""
@@ -522,4 +525,5 @@ class BlockCache:
 
     def check(self) -> None:
         """Waits for the device; raises if a call met a bad block id, length or count."""
-        _on(self.device, lambda st: lib().shadowkv_cache_check(self._desc), None)
+        with torch.cuda.device(self.device):
+            _check(lib().shadowkv_cache_check(self._desc))
