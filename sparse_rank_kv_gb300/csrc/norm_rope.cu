@@ -47,36 +47,45 @@ __device__ __forceinline__ void rope_turn(long long pos, unsigned long long f, f
   *cs = (quarter + 1) & 2 ? -b : b;
 }
 
-// 4 elements of a row, as loaded and as floats.
+// 4 elements of a row, as loaded and as two float pairs.
 template <typename T> struct Quad;
 template <> struct Quad<float> {
   typedef float4 Raw;
-  __device__ __forceinline__ static void get(Raw v, float* o) { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
-  __device__ __forceinline__ static Raw put(const float* o) { return make_float4(o[0], o[1], o[2], o[3]); }
+  __device__ __forceinline__ static void get(Raw v, float2* o) {
+    o[0] = make_float2(v.x, v.y);
+    o[1] = make_float2(v.z, v.w);
+  }
+  __device__ __forceinline__ static Raw put(const float2* o) { return make_float4(o[0].x, o[0].y, o[1].x, o[1].y); }
 };
 template <> struct Quad<bf16> {
   typedef uint2 Raw;
-  __device__ __forceinline__ static void get(Raw v, float* o) {
-    o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
-    o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
+  __device__ __forceinline__ static void get(Raw v, float2* o) {
+    o[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    o[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
   }
-  __device__ __forceinline__ static Raw put(const float* o) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
+  __device__ __forceinline__ static Raw put(const float2* o) {
+    __nv_bfloat162 a = __float22bfloat162_rn(o[0]), b = __float22bfloat162_rn(o[1]);
     return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
   }
 };
 
 constexpr int kNrThreads = 256;
 constexpr int kNrTokens = 4;    // tokens per CTA
+constexpr int kNrCtas = 5;      // per SM (48 registers)
 
 // CTA = 4 tokens x `chunk` heads.  The tokens' sines and cosines are formed
 // once, a pair per thread, and every D/8-lane group keeps its token's in
-// registers over its heads, which it loads kNrRows at a time.
+// registers over its heads, which it loads two (fp32: one) at a time; the other
+// CTAs of the SM cover its loads.  The arithmetic is on pairs (fma.f32x2).
+// Measured at 32768 tokens of 32 + 8 heads of 128 in bf16 (671 MB): 116 us, 5.8
+// TB/s; 141 us with scalar arithmetic (bound by its instructions), 122 us with
+// four CTAs per SM, 147 us with four rows at a time, 144 us with the next rows
+// prefetched into registers.
 template <typename T, int D>
-__global__ void __launch_bounds__(kNrThreads)
+__global__ void __launch_bounds__(kNrThreads, kNrCtas)
 k_norm_rope(const __grid_constant__ NormRopeArgs a, const __grid_constant__ RopeFreq freq) {
   constexpr int LPR = D / 8, Sub = kNrThreads / LPR / kNrTokens;   // row groups per token
-  constexpr int Rows = 16 / sizeof(T) / 2;                         // rows in flight per group
+  constexpr int Rows = 4 / sizeof(T);                              // rows in flight per group
   typedef typename Quad<T>::Raw Raw;
   __shared__ float2 s_cs[kNrTokens][D / 2];
   tc::grid_dep_launch();
@@ -106,62 +115,79 @@ k_norm_rope(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Rope
   const bool turned = l < nrot;
   const int o0 = turned ? 4 * l : a.rot + 8 * (l - nrot);
   const int o1 = turned ? 4 * l + half : o0 + 4;
-  float2 cs[4];
+  float2 cs[2], sn[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) cs[e] = turned ? s_cs[u][4 * l + e] : make_float2(1.f, 0.f);
+  for (int e = 0; e < 2; ++e) {
+    const float2 x = turned ? s_cs[u][4 * l + 2 * e] : make_float2(1.f, 0.f);
+    const float2 y = turned ? s_cs[u][4 * l + 2 * e + 1] : make_float2(1.f, 0.f);
+    cs[e] = make_float2(x.x, y.x);
+    sn[e] = make_float2(x.y, y.y);
+  }
   int i = 0, t = 0;
   if (live) place(token, &i, &t);
   const int c0 = blockIdx.y * a.chunk, c1 = min(a.heads, c0 + a.chunk);
-#pragma unroll
+#pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     // this part's heads of the chunk, as indexes into q or k
     const int base = which ? a.h_q : 0;
     const int h0 = max(c0, base) - base, h1 = min(c1, which ? a.heads : a.h_q) - base;
     if (h0 >= h1) continue;
-    const T* src = static_cast<const T*>(a.x[which]) + i * a.xb[which] + t * a.xs[which];
-    T* dst = static_cast<T*>(a.y[which]) + i * a.yb[which] + t * a.ys[which];
-    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    const long long xh = a.xh[which], yh = a.yh[which];
+    const int first = h0 + sub;
+    const int mine = live && first < h1 ? (h1 - first + Sub - 1) / Sub : 0;   // rows of this group
+    const T* src = static_cast<const T*>(a.x[which]) + i * a.xb[which] + t * a.xs[which] + first * xh;
+    T* dst = static_cast<T*>(a.y[which]) + i * a.yb[which] + t * a.ys[which] + first * yh;
+    float2 w[4] = {{1.f, 1.f}, {1.f, 1.f}, {1.f, 1.f}, {1.f, 1.f}};
     if (a.norm && a.w[which]) {
       Quad<T>::get(*reinterpret_cast<const Raw*>(static_cast<const T*>(a.w[which]) + o0), w);
-      Quad<T>::get(*reinterpret_cast<const Raw*>(static_cast<const T*>(a.w[which]) + o1), w + 4);
+      Quad<T>::get(*reinterpret_cast<const Raw*>(static_cast<const T*>(a.w[which]) + o1), w + 2);
     }
-    for (int hb = h0; hb < h1; hb += Rows * Sub) {   // the same count for every lane of the warp
-      Raw r0[Rows] = {}, r1[Rows] = {};
+    const int most = (h1 - h0 + Sub - 1) / Sub;   // the same count for every lane of the warp
+    for (int n = 0; n < most; n += Rows) {
+      Raw r0[Rows], r1[Rows];
 #pragma unroll
       for (int v = 0; v < Rows; ++v) {
-        const int h = hb + v * Sub + sub;
-        if (live && h < h1) {
-          r0[v] = *reinterpret_cast<const Raw*>(src + h * a.xh[which] + o0);
-          r1[v] = *reinterpret_cast<const Raw*>(src + h * a.xh[which] + o1);
+        r0[v] = Raw{};
+        r1[v] = Raw{};
+        if (n + v < mine) {
+          const T* p = src + v * Sub * xh;
+          r0[v] = *reinterpret_cast<const Raw*>(p + o0);
+          r1[v] = *reinterpret_cast<const Raw*>(p + o1);
         }
       }
+      src += Rows * Sub * xh;
 #pragma unroll
       for (int v = 0; v < Rows; ++v) {
-        const int h = hb + v * Sub + sub;
-        float x[8];
+        float2 x[4];
         Quad<T>::get(r0[v], x);
-        Quad<T>::get(r1[v], x + 4);
+        Quad<T>::get(r1[v], x + 2);
         if (a.norm) {
-          float ss = 0.f;
+          float2 s2 = __fmul2_rn(x[0], x[0]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+          for (int e = 1; e < 4; ++e) s2 = __ffma2_rn(x[e], x[e], s2);
+          float ss = s2.x + s2.y;
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
+          const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+          const float2 rr = make_float2(r, r);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+          for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(__fmul2_rn(x[e], rr), w[e]);
         }
-        float y[8];
+        if (turned) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = x[e] * cs[e].x - x[4 + e] * cs[e].y;
-          y[4 + e] = x[4 + e] * cs[e].x + x[e] * cs[e].y;
+          for (int e = 0; e < 2; ++e) {
+            const float2 x1 = x[e], x2 = x[2 + e], m = __fmul2_rn(x2, sn[e]);
+            x[e] = __ffma2_rn(x1, cs[e], make_float2(-m.x, -m.y));
+            x[2 + e] = __ffma2_rn(x2, cs[e], __fmul2_rn(x1, sn[e]));
+          }
         }
-        if (live && h < h1) {
-          *reinterpret_cast<Raw*>(dst + h * a.yh[which] + o0) = Quad<T>::put(turned ? y : x);
-          *reinterpret_cast<Raw*>(dst + h * a.yh[which] + o1) = Quad<T>::put(turned ? y + 4 : x + 4);
+        if (n + v < mine) {
+          T* p = dst + v * Sub * yh;
+          *reinterpret_cast<Raw*>(p + o0) = Quad<T>::put(x);
+          *reinterpret_cast<Raw*>(p + o1) = Quad<T>::put(x + 2);
         }
       }
+      dst += Rows * Sub * yh;
     }
   }
 }
