@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -314,22 +315,47 @@ def load_state(p: Params, st: dict, stream=None) -> Context:
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> Rows:
-    """A b x h x s x d (or b x h x d) tensor as strided rows."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
+# The packed forms of Rows and NormRopeParams: the calls of a decode step are
+# made every few microseconds, and a ctypes structure takes one to fill.
+_PACK_ROWS = struct.Struct("Pqqq").pack
+_PACK_NORM_ROPE = struct.Struct("9i2f").pack
+_step = None
+
+
+def _step_calls():
+    """The per-step entry points, taking packed structures and raw pointers."""
+    global _step
+    if _step is None:
+        L = lib()
+        V, I, S, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+        C = ctypes.POINTER(CacheDesc)
+        fns = {}
+        for name, args in (("qk_norm_rope", [V] * 9), ("cache_append", [C, I, V, V, I, V, V]),
+                           ("cache_attend", [C, I, I, V, F, I, F, V, V, V, S, V]),
+                           ("cache_evict", [C, C, I, I, I, V, V])):
+            fn = L["shadowkv_" + name]      # a function object of its own, beside lib()'s
+            fn.restype, fn.argtypes = I, args
+            fns[name] = fn
+        _step = fns
+    return _step
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> bytes:
+    """A b x h x s x d (or b x h x d) tensor as strided rows (a packed Rows)."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {tuple(shape)} on "
                          f"{device} (shape, type and device)")
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return Rows(t.data_ptr(), st[0], st[1], st[2] if len(st) == 4 else 0)
+    return _PACK_ROWS(t.data_ptr(), st[0], st[1], st[2] if len(st) == 4 else 0)
 
 
 def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, device):
     """Data pointer of a contiguous tensor of a given shape, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -394,8 +420,8 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight:
         ws[i] = _dense(w, name + "_weight", (d,), dtype, dev)
     per_token = pos is not None and pos.dim() == 2
     pp = _dense(pos, "pos", (b, s) if per_token else (b,), torch.int32, dev)
-    p = NormRopeParams(b, s, heads[0], heads[1], d, d if rot is None else rot, dt, int(norm), int(per_token), eps, theta)
-    _call(lib().shadowkv_qk_norm_rope, dev, stream, p, rows[0], rows[1], ws[0], ws[1], pp, outs[0], outs[1])
+    p = _PACK_NORM_ROPE(b, s, heads[0], heads[1], d, d if rot is None else rot, dt, norm, per_token, eps, theta)
+    _call(_step_calls()["qk_norm_rope"], dev, stream, p, rows[0], rows[1], ws[0], ws[1], pp, outs[0], outs[1])
     return made[0], made[1]
 
 
@@ -437,7 +463,7 @@ class BlockCache:
         self._desc = CacheDesc(b, h, d, block, mb, n_pool, k_codes.data_ptr(), v_codes.data_ptr(),
                                k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), n_tok.data_ptr(),
                                weight.data_ptr() if weight is not None else None, self.status.data_ptr())
-        self._work_bytes = {}
+        self._work = {}
         _check(lib().shadowkv_cache_validate(self._desc))
 
     @classmethod
@@ -466,14 +492,16 @@ class BlockCache:
         shape = (self.b, self.h_kv, s, self.d)
         rk, rv = _rows(k, "k", shape, k.dtype, self.device), _rows(v, "v", shape, k.dtype, self.device)
         lp = _dense(lens, "lens", (self.b,), torch.int32, self.device)
-        _call(lib().shadowkv_cache_append, self.device, stream, self._desc, dt, rk, rv, s, lp)
+        _call(_step_calls()["cache_append"], self.device, stream, self._desc, dt, rk, rv, s, lp)
 
     def attend(self, q: torch.Tensor, *, scale: Optional[float] = None, decay: Optional[float] = None,
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """softmax(scale q K^T) V over the tokens held; q (b, h_q, d), scale 1/sqrt(d)
         by default.  decay: gather block weights, weight = decay weight + this
         call's (None: weights stay as they are).  lse (b, h_q) float32 receives the log sums.
-        The workspace comes from torch's allocator, on the call's stream."""
+        The workspace comes from torch's allocator and is kept per stream; a call
+        under capture takes one of its own from the graph's memory, so that
+        graphs share none."""
         if q.dim() != 3:
             raise ValueError("q must be (b, h_q, d)")
         dev, hq = self.device, q.shape[1]
@@ -486,26 +514,36 @@ class BlockCache:
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), dev)
             with torch.cuda.stream(s):
                 return self.attend(q, scale=scale, decay=decay, out=out, lse=lse)
-        nb = self._work_bytes.get(hq)
-        if nb is None:
-            nb = self._workspace(hq)
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=dev)
-        work = torch.empty(nb, dtype=torch.uint8, device=dev)
-        _call(lib().shadowkv_cache_attend, dev, None, self._desc, dt, hq, rq,
+        ro = _rows(out, "out", shape, q.dtype, dev)
+        if dev.type == "cuda" and torch._C._cuda_getDevice() != dev.index:
+            with torch.cuda.device(dev):
+                return self.attend(q, scale=scale, decay=decay, out=out, lse=lse)
+        work, ptr, nb = self._workspace(hq)
+        _call(_step_calls()["cache_attend"], dev, None, self._desc, dt, hq, rq,
               self.d ** -0.5 if scale is None else scale, decay is not None, 0.0 if decay is None else decay,
-              _rows(out, "out", shape, q.dtype, dev), lp, work.data_ptr(), nb)
+              ro, lp, ptr, nb)
         return out
 
-    def _workspace(self, hq: int) -> int:
+    def _workspace(self, hq: int):
+        """(tensor, pointer, bytes) of attend's workspace on the current stream."""
         if self.device.type != "cuda":
             raise ValueError(f"tensors must be on a CUDA device, got {self.device}")
-        with torch.cuda.device(self.device):
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
+        key = (hq, torch._C._cuda_getCurrentRawStream(self.device.index))
+        have = None if capturing else self._work.get(key)
+        if have is None:
             nb = lib().shadowkv_cache_attend_workspace(self._desc, hq)
-        if nb == 0:
-            _check(7)
-        self._work_bytes[hq] = nb
-        return nb
+            if nb == 0:
+                _check(7)
+            t = torch.empty(nb, dtype=torch.uint8, device=self.device)
+            have = (t, t.data_ptr(), nb)
+            if not capturing:
+                if len(self._work) >= 8:
+                    self._work.pop(next(iter(self._work)))
+                self._work[key] = have
+        return have
 
     def evict(self, keep: int, *, sink: int = 0, recent: int = 1, into: Optional["BlockCache"] = None,
               kept: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -517,7 +555,7 @@ class BlockCache:
         dst = None if into is None else into._desc
         if into is not None and into.device != self.device:
             raise ValueError(f"into is on {into.device}, expected {self.device}")
-        _call(lib().shadowkv_cache_evict, self.device, stream, self._desc, dst, keep, sink, recent, kp)
+        _call(_step_calls()["cache_evict"], self.device, stream, self._desc, dst, keep, sink, recent, kp)
 
     def reset(self) -> None:
         """Drops every token (on torch's current stream)."""

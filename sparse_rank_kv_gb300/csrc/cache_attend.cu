@@ -137,8 +137,8 @@ struct Ca {
   static constexpr int KB = kCaT * D, Stage = 2 * KB;       // K tile, V tile
   static constexpr int QB = N1 * D, PB = N2 * kCaT;
   static constexpr int Misc = 2048;
-  static constexpr int NST = (kCaSmemMax - 128 - QB - 2 * PB - Misc) / Stage;
-  static constexpr int Smem = 128 + NST * Stage + QB + 2 * PB + Misc;
+  static constexpr int NST = (kCaSmemMax - 128 - 2 * QB - 2 * PB - Misc) / Stage;
+  static constexpr int Smem = 128 + NST * Stage + 2 * QB + 2 * PB + Misc;
   static constexpr int Cols0 = 2 * N1 + 2 * N2;
   static constexpr int Cols = Cols0 <= 32 ? 32 : Cols0 <= 64 ? 64 : Cols0 <= 128 ? 128 : 256;
   static_assert(NST >= 2 && Cols0 <= 256, "attention tile");
@@ -156,6 +156,12 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
 // kind::f8f6f4, e4m3 A and B (format 0), fp32 D, both K-major, M = 128
 constexpr uint32_t idesc_e4m3(int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+// 2^x by the special function unit (2^-22 relative); results below 2^-126 are 0
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 __device__ __forceinline__ float redux_max(float x) {
   float r;
@@ -195,22 +201,22 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   unsigned char* stages = smem;
-  unsigned char* qbuf = stages + NST * C::Stage;
-  unsigned char* pbuf = qbuf + C::QB;
+  unsigned char* qbuf = stages + NST * C::Stage;        // [2], by the pair's turn in this CTA
+  unsigned char* pbuf = qbuf + 2 * C::QB;               // [2], by tile
   unsigned char* misc = pbuf + 2 * C::PB;
   uint64_t* full = reinterpret_cast<uint64_t*>(misc);   // [NST <= 7]
   uint64_t* empty = full + 8;                           // [NST]
   uint64_t* sfull = empty + 8;                          // [2]
   uint64_t* pfull = sfull + 2;
   uint64_t* ofull = pfull + 2;
-  uint64_t* qfull = ofull + 2;                          // [1]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 192);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 196);
-  int* s_where = reinterpret_cast<int*>(misc + 200);    // [3]
-  float* sqs = reinterpret_cast<float*>(misc + 224);    // [G] q scales
-  float* red = reinterpret_cast<float*>(misc + 256);    // [2][4][G]
-  int* s_scan = reinterpret_cast<int*>(misc + 512);     // [32]
-  float* ssc = reinterpret_cast<float*>(misc + 640);    // [NST][20]: K scales, V factors, V reference
+  uint64_t* qfull = ofull + 2;                          // [2]
+  float* sqs = reinterpret_cast<float*>(misc + 192);    // [2][8] q scales
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 640);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 644);
+  int* s_where = reinterpret_cast<int*>(misc + 648);    // [3]
+  float* red = reinterpret_cast<float*>(misc + 256);    // [2][4][G] maxima, [4][G] sums
+  int* s_scan = reinterpret_cast<int*>(misc + 512);     // [32], before the sums are used
+  float* ssc = reinterpret_cast<float*>(misc + 672);    // [NST][20]: K scales, V factors, V reference
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   tc::grid_dep_launch();
 
@@ -223,8 +229,8 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       tc::mbar_init(&sfull[i], 1);
       tc::mbar_init(&pfull[i], kCaSoft / 32);
       tc::mbar_init(&ofull[i], 1);
+      tc::mbar_init(&qfull[i], kCaSoft / 32);
     }
-    tc::mbar_init(qfull, kCaSoft / 32);
     tc::fence_mbar_init();
     *s_abort = 0;
   }
@@ -233,7 +239,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
     tc::tmem_relinquish();
   }
   // operand rows past the terms stay zero
-  for (int i = tid; i < (C::QB + 2 * C::PB) / 16; i += kCaThreads)
+  for (int i = tid; i < (2 * C::QB + 2 * C::PB) / 16; i += kCaThreads)
     reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0, 0, 0, 0);
   tc::fence_proxy_async_smem();
   tc::fence_before();
@@ -318,15 +324,18 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       TileCursor cur;
       cur.begin(a.c, s_where[0], s_where[1], ntile);
       const uint32_t tS = tmem, tO = tmem + 2 * N1;
-      int it = 0, runs = 0;
+      int it = 0, runs = -1;
       bool ok = true;
       auto scores = [&](bool first) {
         const int st = it % NST;
-        if (first) ok = ok && tc::mbar_wait(qfull, (runs++) & 1, kWaitLimit);
+        if (first) {
+          ++runs;
+          ok = ok && tc::mbar_wait(&qfull[runs & 1], (runs >> 1) & 1, kWaitLimit);
+        }
         ok = ok && tc::mbar_wait(&full[st], (it / NST) & 1, kWaitLimit);
         if (!ok) return;
         tc::fence_after();
-        const uint32_t k0 = tc::smem_u32(stages + st * C::Stage), q0 = tc::smem_u32(qbuf);
+        const uint32_t k0 = tc::smem_u32(stages + st * C::Stage), q0 = tc::smem_u32(qbuf + (runs & 1) * C::QB);
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
           mma_e4m3(tS + (it & 1) * N1, tc::desc_k_none(k0 + k * 256, 128, 8 * D),
@@ -347,11 +356,11 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
         tc::mma_commit(&empty[st]);
       };
       // S of the next tile is issued before O of this one, so that the
-      // softmax never waits for it; at a new pair, whose q the softmax
-      // warps lay out after their last tile of the old one, after it
+      // softmax never waits for it; at a new pair whose q is not laid out
+      // yet (pairs of one tile), after it
       bool first = true;
       for (;;) {
-        if (first && it > 0) {
+        if (first && it > 0 && !tc::mbar_test(&qfull[(runs + 1) & 1], ((runs + 1) >> 1) & 1)) {
           values(it - 1);
           scores(true);
         } else {
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
     bool ok = true;
     // q's terms, each head scaled by a power of two so that the largest
     // entry is at most 448; an entry that is not finite makes the head NaN
-    auto lay_q = [&](int pair) {
+    auto lay_q = [&](int pair, int turn) {
       const int seq = pair / a.c.h_kv, kvh = pair - seq * a.c.h_kv;
       for (int g = warp; g < G; g += 4) {
         const T* row = static_cast<const T*>(a.q) + seq * a.qb + (static_cast<long long>(kvh) * G + g) * a.qh;
@@ -394,7 +403,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
         for (int e = 0; e < D / 32; e += 2) {
           float u = x[e] * inv, v = x[e + 1] * inv;
           const int j = lane + 32 * e;
-          unsigned char* dst = qbuf + (j >> 4) * (N1 * 16) + (j & 15);
+          unsigned char* dst = qbuf + (turn & 1) * C::QB + (j >> 4) * (N1 * 16) + (j & 15);
 #pragma unroll
           for (int i = 0; i < C::QP; ++i) {
             const uint32_t c2 = e4m3_pack2(u, v);
@@ -405,15 +414,15 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
             v = (v - f.y) * 16.f;
           }
         }
-        if (lane == 0) sqs[g] = s * a.scale_log2;
+        if (lane == 0) sqs[(turn & 1) * 8 + g] = s * a.scale_log2;
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(qfull);
+      if (lane == 0) tc::mbar_arrive(&qfull[turn & 1]);
       ok = tc::named_sync_and(1, kCaSoft, ok);
     };
-    lay_q(cur.pair);
-    int it = 0, at = t0;
+    lay_q(cur.pair, 0);
+    int it = 0, at = t0, turn = 0;
     while (cur.left > 0 && ok) {
       const int pair = cur.pair, ntok = cur.ntok, nrun = cur.run();
       if (cur.tile == 0 && tid == 0) a.w.first[pair] = at;
@@ -442,6 +451,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
           acc[g] = fmaf(acc[g], al[g], x * be[g]);
         }
       };
+      TileCursor after;
       for (int r = 0; r < nrun; ++r, ++it) {
         const int t = cur.tile + r, st = it % NST, cnt = min(kCaT, ntok - t * kCaT);
         ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&full[st], (it / NST) & 1, kWaitLimit) &&
@@ -460,7 +470,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
             float x = v[(C::QP - 1) * G + g];
 #pragma unroll
             for (int i = C::QP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, v[i * G + g]);
-            s[g] = tid < cnt ? x * (sqs[g] * ks) : -INFINITY;
+            s[g] = tid < cnt ? x * (sqs[(turn & 1) * 8 + g] * ks) : -INFINITY;
           }
 #pragma unroll
           for (int g = 0; g < G; ++g) {
@@ -479,10 +489,10 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
           const float* rd = red + (it & 1) * 32 + g;
           const float mt = fmaxf(fmaxf(rd[0], rd[G]), fmaxf(rd[2 * G], rd[3 * G]));
           const float tref = mt == -INFINITY ? 0.f : mt, mn = fmaxf(mt, m[g]), ref = mn == -INFINITY ? 0.f : mn;
-          al_new[g] = exp2f(m[g] - ref);
-          be_new[g] = exp2f(mt - ref);
+          al_new[g] = ex2(m[g] - ref);
+          be_new[g] = ex2(mt - ref);
           m[g] = mn;
-          p[g] = exp2f(s[g] - tref);
+          p[g] = ex2(s[g] - tref);
           l[g] = fmaf(l[g], al_new[g], p[g] * be_new[g]);
           be_new[g] *= vref;
           if (a.gather && tid == 0) a.w.tmax[(static_cast<size_t>(pair) * a.w.tiles + t) * G + g] = tref;
@@ -540,6 +550,15 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&pfull[it & 1]);
+        if (r == 0) {
+          // the next pair's q, so that its S can start while this one ends
+          // (the buffer's last reader was the S of the pair before)
+          after = cur;
+          after.tile += nrun - 1;
+          after.left -= nrun - 1;
+          after.next(a.c);
+          if (after.left > 0) lay_q(after.pair, turn + 1);
+        }
         if (r > 0) take_o(it - 1);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -548,11 +567,9 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
         }
       }
       if (!ok) break;
-      cur.tile += nrun - 1;
-      cur.left -= nrun - 1;
-      cur.next(a.c);
+      cur = after;
       at += nrun;
-      if (cur.left > 0) lay_q(cur.pair);   // S of the next pair can start
+      ++turn;
       take_o(it - 1);
       tc::fence_before();
       // the partial of (this CTA, pair)
@@ -591,13 +608,15 @@ constexpr int kCmThreads = 256;
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kCmThreads)
 k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int chunk, int nchunk) {
-  __shared__ float s_M[G], s_L[G], s_acc[kCmThreads / D][D];
+  constexpr int SL = kCmThreads / D, Pre = 4;   // partials per pass; rows held while the maxima are formed
+  __shared__ float s_M[G], s_L[G], s_acc[SL][D];
   const int tid = threadIdx.x;
   tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int P = a.c.pairs, bx = blockIdx.x;
   const bool head_role = bx < P * G;
   const int pair = head_role ? bx / G : (bx - P * G) / nchunk;
+  const int total = a.w.first[P], f = a.w.first[pair];   // (f is not written for a pair without tokens)
   const int ntok = cache_tokens(a.c, pair), nt = (ntok + kCaT - 1) / kCaT;
   const int seq = pair / a.c.h_kv, kvh = pair - seq * a.c.h_kv;
   if (nt == 0) {
@@ -608,10 +627,22 @@ k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int chunk, int nc
     }
     return;
   }
-  const int T_all = a.w.first[P], n = min(ncta, T_all), f = a.w.first[pair];
-  const int c0 = share_owner(f, n, T_all), c1 = share_owner(f + nt - 1, n, T_all);
+  const int n = min(ncta, total);
+  const int c0 = share_owner(f, n, total), c1 = share_owner(f + nt - 1, n, total);
+  const int g_out = bx % G, j = tid % D, sl = tid / D;
+  const float* rows = a.w.part + (static_cast<size_t>(c0 + pair) * G + g_out) * (D + 2);   // partial c0 + u: + u G (D + 2)
+  float pre[Pre], pm[Pre];
+  if (head_role) {
+#pragma unroll
+    for (int u = 0; u < Pre; ++u) {
+      const bool on = c0 + sl + u * SL <= c1;
+      const float* p = rows + static_cast<size_t>(sl + u * SL) * G * (D + 2);
+      pre[u] = on ? p[j] : 0.f;
+      pm[u] = on ? p[D] : -INFINITY;
+    }
+  }
   // the heads' largest maximum and total sum over the pair's partials
-  if (tid < 32 * G && tid / 32 < G) {
+  if (tid < 32 * G) {
     const int g = tid / 32, lane = tid & 31;
     float M = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32)
@@ -621,27 +652,29 @@ k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int chunk, int nc
     float L = 0.f;
     for (int c = c0 + lane; c <= c1; c += 32) {
       const float* p = a.w.part + (static_cast<size_t>(c + pair) * G + g) * (D + 2) + D;
-      L = fmaf(p[1], exp2f(p[0] - ref), L);
+      L = fmaf(p[1], ex2(p[0] - ref), L);
     }
     L = warp_sum(L);
     if (lane == 0) { s_M[g] = ref; s_L[g] = L; }
   }
   __syncthreads();
   if (head_role) {
-    const int g = bx % G, j = tid % D, sl = tid / D;
     float acc = 0.f;
-    for (int c = c0 + sl; c <= c1; c += kCmThreads / D) {
-      const float* p = a.w.part + (static_cast<size_t>(c + pair) * G + g) * (D + 2);
-      acc = fmaf(p[j], exp2f(p[D] - s_M[g]), acc);
+#pragma unroll
+    for (int u = 0; u < Pre; ++u) acc = fmaf(pre[u], ex2(pm[u] - s_M[g_out]), acc);
+    for (int c = c0 + sl + Pre * SL; c <= c1; c += SL) {
+      const float* p = rows + static_cast<size_t>(c - c0) * G * (D + 2);
+      acc = fmaf(p[j], ex2(p[D] - s_M[g_out]), acc);
     }
     s_acc[sl][j] = acc;
     __syncthreads();
     if (sl == 0) {
-      for (int u = 1; u < kCmThreads / D; ++u) acc += s_acc[u][j];
-      const int h = kvh * G + g;
-      static_cast<T*>(a.out)[seq * a.ob + h * a.oh + j] = Ty<T>::from_f(acc / s_L[g]);
+#pragma unroll
+      for (int u = 1; u < SL; ++u) acc += s_acc[u][j];
+      const int h = kvh * G + g_out;
+      static_cast<T*>(a.out)[seq * a.ob + h * a.oh + j] = Ty<T>::from_f(acc / s_L[g_out]);
       if (a.lse && j == 0)
-        a.lse[static_cast<size_t>(seq) * a.c.h_kv * G + h] = (s_M[g] + log2f(s_L[g])) * 0.6931471805599453f;
+        a.lse[static_cast<size_t>(seq) * a.c.h_kv * G + h] = (s_M[g_out] + log2f(s_L[g_out])) * 0.6931471805599453f;
     }
     return;
   }
@@ -654,7 +687,7 @@ k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int chunk, int nc
       float z = 0.f;
       for (int u = 0; u < B / gran; ++u)
         z += a.w.psum[(static_cast<size_t>(pair) * a.w.granules + i * (B / gran) + u) * G + g];
-      w += z * exp2f(a.w.tmax[(static_cast<size_t>(pair) * a.w.tiles + tile) * G + g] - s_M[g]) / s_L[g];
+      w += z * ex2(a.w.tmax[(static_cast<size_t>(pair) * a.w.tiles + tile) * G + g] - s_M[g]) / s_L[g];
     }
     float* dst = a.c.weight + static_cast<size_t>(pair) * a.c.max_blocks + i;
     *dst = a.decay == 0.f ? w : fmaf(a.decay, *dst, w);
