@@ -86,13 +86,15 @@ struct Ap {
     else return make_float2(__uint_as_float(w[2 * p]), __uint_as_float(w[2 * p + 1]));
   }
 
-  // rows [e0, e1) of the block from src (row 0's address; rows outside are not read)
-  __device__ __forceinline__ static void load(uint32_t* w, const T* src, long long ss, int which, int e0, int e1, int tid) {
+  // rows [e0, e1) of the block from src (row 0's address; rows outside are
+  // not read).  Full: all of them.
+  template <bool Full>
+  __device__ __forceinline__ static void load_rows(uint32_t* w, const T* src, long long ss, int which, int e0, int e1, int tid) {
     if (which == 0) {
 #pragma unroll
       for (int i = 0; i < UK; ++i) {
         const int u = tid + i * TPJ, r = k_row(u);
-        const bool on = r >= e0 && r < e1;
+        const bool on = Full || (r >= e0 && r < e1);
         const uint4* p = reinterpret_cast<const uint4*>(src + r * ss + k_piece(u) * 16);
 #pragma unroll
         for (int e = 0; e < 2 * E; ++e) {
@@ -104,14 +106,14 @@ struct Ap {
     } else {
 #pragma unroll
       for (int i = 0; i < UV; ++i) {
-        const int u = tid + i * TPJ, t0 = v_tok(u), j = v_dim(u);
+        const int u = tid + i * TPJ, t0 = v_tok(u);
+        const T* p = src + t0 * ss + v_dim(u);
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          const bool on = t0 + t >= e0 && t0 + t < e1;
-          const uint32_t* p = reinterpret_cast<const uint32_t*>(src + (t0 + t) * ss + j);
+        for (int t = 0; t < 16; ++t, p += ss) {
+          const bool on = Full || (t0 + t >= e0 && t0 + t < e1);
           uint32_t* o = w + (i * 16 + t) * E;
           if constexpr (E == 1) {
-            o[0] = on ? *p : 0u;
+            o[0] = on ? *reinterpret_cast<const uint32_t*>(p) : 0u;
           } else {
             const uint2 x = on ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
             o[0] = x.x; o[1] = x.y;
@@ -119,6 +121,10 @@ struct Ap {
         }
       }
     }
+  }
+  __device__ __forceinline__ static void load(uint32_t* w, const T* src, long long ss, int which, int e0, int e1, int tid) {
+    if (e0 == 0 && e1 == B) load_rows<true>(w, src, ss, which, e0, e1, tid);
+    else load_rows<false>(w, src, ss, which, e0, e1, tid);
   }
 
   // the largest magnitude, as fp32 bits (integer order is magnitude order);
@@ -146,67 +152,93 @@ struct Ap {
     return m;
   }
 
-  // codes of the rows in w under scale sc; with grow, of the rows [0, e0)
-  // held, too, whose scale was smaller by ratio
-  __device__ __forceinline__ static void store(const uint32_t* w, uint8_t* dst, float sc, bool grow, float ratio,
-                                               int which, int e0, int e1, int tid) {
+  // four K codes, or two tokens' codes of V's two dimensions, of whole rows
+  // under a power-of-two scale
+  __device__ __forceinline__ static uint32_t code2(const uint32_t* w, int p, float inv) {
+    const float2 f = __fmul2_rn(pair(w, p), make_float2(inv, inv));
+    return e4m3_pack2(f.x, f.y);
+  }
+  // codes of a block that is all new
+  __device__ __forceinline__ static void store_full(const uint32_t* w, uint8_t* dst, float sc, int which, int tid) {
     const float inv = 1.f / sc;   // exact for a power of two
-    const bool pow2 = is_pow2(sc);
-    auto code2 = [&](float2 f) {
-      // a partly filled block the caller made may have another scale: divide
-      return pow2 ? e4m3_pack2(f.x * inv, f.y * inv) : e4m3_pack2(f.x / sc, f.y / sc);
-    };
     if (which == 0) {
 #pragma unroll
       for (int i = 0; i < UK; ++i) {
-        const int u = tid + i * TPJ, r = k_row(u);
-        if (r >= e1 || (r < e0 && !grow)) continue;
-        uint4* d = reinterpret_cast<uint4*>(dst + (r >> 3) * (8 * D) + k_piece(u) * 128 + (r & 7) * 16);
-        if (r < e0) {
-          const uint4 o = *d;
-          *d = make_uint4(rescale4(o.x, ratio), rescale4(o.y, ratio), rescale4(o.z, ratio), rescale4(o.w, ratio));
-        } else {
-          uint32_t o[4];
+        const int u = tid + i * TPJ;
+        uint32_t o[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = __byte_perm(code2(pair(w + i * 8 * E, 2 * e)), code2(pair(w + i * 8 * E, 2 * e + 1)), 0x5410);
-          *d = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        for (int e = 0; e < 4; ++e)
+          o[e] = __byte_perm(code2(w + i * 8 * E, 2 * e, inv), code2(w + i * 8 * E, 2 * e + 1, inv), 0x5410);
+        reinterpret_cast<uint4*>(dst)[u] = make_uint4(o[0], o[1], o[2], o[3]);   // units lie in the block's order
       }
     } else {
 #pragma unroll
       for (int i = 0; i < UV; ++i) {
-        const int u = tid + i * TPJ, t0 = v_tok(u), j = v_dim(u);
-        if (t0 >= e1 || (t0 + 16 <= e0 && !grow)) continue;
-        uint4* d = reinterpret_cast<uint4*>(dst + (t0 >> 4) * (16 * D) + j * 16);
+        const int u = tid + i * TPJ;
         uint32_t a[4], b[4];
-        if (t0 >= e0 && t0 + 16 <= e1) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t* x = w + (i * 16 + 4 * t) * E;
-            const uint32_t p = __byte_perm(code2(pair(x, 0)), code2(pair(x, 1)), 0x5140);   // t0 t1 of j, of j + 1
-            const uint32_t q = __byte_perm(code2(pair(x, 2)), code2(pair(x, 3)), 0x5140);
-            a[t] = __byte_perm(p, q, 0x5410);
-            b[t] = __byte_perm(p, q, 0x7632);
-          }
-        } else {
-          // bytes of tokens that are neither held nor new stay as they are
-          const uint4 oa = d[0], ob = d[1];
-          a[0] = oa.x; a[1] = oa.y; a[2] = oa.z; a[3] = oa.w;
-          b[0] = ob.x; b[1] = ob.y; b[2] = ob.z; b[3] = ob.w;
-#pragma unroll
-          for (int t = 0; t < 16; ++t) {
-            const int r = t0 + t;
-            if (r >= e0 && r < e1) {
-              put_codes(&a[t >> 2], &b[t >> 2], t & 3, code2(pair(w + (i * 16 + t) * E, 0)));
-            } else if (r < e0 && grow) {
-              const uint32_t old = ((a[t >> 2] >> (8 * (t & 3))) & 0xffu) | (((b[t >> 2] >> (8 * (t & 3))) & 0xffu) << 8);
-              put_codes(&a[t >> 2], &b[t >> 2], t & 3, rescale2(old, ratio));
-            }
-          }
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t* x = w + (i * 16 + 4 * t) * E;
+          const uint32_t p = __byte_perm(code2(x, 0, inv), code2(x, 1, inv), 0x5140);   // t0 t1 of j, of j + 1
+          const uint32_t q = __byte_perm(code2(x, 2, inv), code2(x, 3, inv), 0x5140);
+          a[t] = __byte_perm(p, q, 0x5410);
+          b[t] = __byte_perm(p, q, 0x7632);
         }
+        uint4* d = reinterpret_cast<uint4*>(dst) + 2 * u;
         d[0] = make_uint4(a[0], a[1], a[2], a[3]);
         d[1] = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+    }
+  }
+  // codes of rows [e0, e1) read again from src, under any scale sc; with
+  // grow, the rows [0, e0) held, too, whose scale was smaller by ratio.  At
+  // most two blocks of an append go here: kept out of the other path's way.
+  __device__ __noinline__ static void store_part(const T* src, long long ss, uint8_t* dst, float sc, bool grow, float ratio,
+                                                 int which, int e0, int e1, int tid) {
+    const float inv = 1.f / sc;
+    const bool pow2 = is_pow2(sc);
+    auto one = [&](const T* p) {
+      const float x = Ty<T>::to_f(p[0]), y = Ty<T>::to_f(p[1]);
+      // a partly filled block the caller made may have another scale: divide
+      return pow2 ? e4m3_pack2(x * inv, y * inv) : e4m3_pack2(x / sc, y / sc);
+    };
+    if (which == 0) {
+      for (int u = tid; u < B * D / 16; u += TPJ) {
+        const int r = k_row(u);
+        if (r >= e1 || (r < e0 && !grow)) continue;
+        uint4* d = reinterpret_cast<uint4*>(dst) + u;
+        if (r < e0) {
+          const uint4 o = *d;
+          *d = make_uint4(rescale4(o.x, ratio), rescale4(o.y, ratio), rescale4(o.z, ratio), rescale4(o.w, ratio));
+        } else {
+          const T* p = src + r * ss + k_piece(u) * 16;
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = one(p + 4 * e) | (one(p + 4 * e + 2) << 16);
+          *d = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    } else {
+      // bytes of tokens that are neither held nor new stay as they are
+      for (int u = tid; u < B * D / 32; u += TPJ) {
+        const int t0 = v_tok(u), j = v_dim(u);
+        if (t0 >= e1 || (t0 + 16 <= e0 && !grow)) continue;
+        uint4* d = reinterpret_cast<uint4*>(dst) + 2 * u;
+        uint4 oa = d[0], ob = d[1];
+        uint32_t* a = reinterpret_cast<uint32_t*>(&oa);
+        uint32_t* b = reinterpret_cast<uint32_t*>(&ob);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const int r = t0 + t, sh = (t & 3) * 8;
+          if (r >= e0 && r < e1) {
+            put_codes(&a[t >> 2], &b[t >> 2], t & 3, one(src + r * ss + j));
+          } else if (r < e0 && grow) {
+            const uint32_t old = ((a[t >> 2] >> sh) & 0xffu) | (((b[t >> 2] >> sh) & 0xffu) << 8);
+            put_codes(&a[t >> 2], &b[t >> 2], t & 3, rescale2(old, ratio));
+          }
+        }
+        d[0] = oa;
+        d[1] = ob;
       }
     }
   }
@@ -279,7 +311,9 @@ __global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constan
       *scale = sc;
       if (which == 0 && e0 == 0 && c.weight) c.weight[static_cast<size_t>(pair) * c.max_blocks + blk] = 0.f;
     }
-    A::store(w, (which ? c.vc : c.kc) + static_cast<size_t>(id) * (D * B), sc, grow, was / sc, which, e0, e1, tid);
+    uint8_t* dst = (which ? c.vc : c.kc) + static_cast<size_t>(id) * (D * B);
+    if (e0 == 0 && e1 == B) A::store_full(w, dst, sc, which, tid);
+    else A::store_part(src + static_cast<long long>(blk) * B * ss, ss, dst, sc, grow, was / sc, which, e0, e1, tid);
     id = id_next;
   }
 }
