@@ -444,79 +444,154 @@ static cudaError_t append_t(const AppendArgs& a, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ evict
-constexpr int kEvThreads = 512;
 constexpr int kEvMax = 16384;   // blocks per pair
-constexpr int kEvRegs = kEvMax / kEvThreads;
 
-static size_t evict_smem(int mb) {
-  const size_t nw = (mb + 31) / 32;
-  return 4 * (2 * static_cast<size_t>(mb) + 2 * nw + topk_scratch_ints(kEvThreads));
-}
-
-// CTA = pair.  The blocks' weights become order-preserving keys (protected
-// blocks the largest), block_topk marks the `keep` largest, and a block's new
-// place follows from the marked blocks before it.  Entries pass through
-// registers, so that the tables may be rewritten in place.
-__global__ void __launch_bounds__(kEvThreads)
+// CTA = pair; thread t holds the table entries and weights t, t + NT, ... in
+// registers (so the tables may be rewritten in place).  Weights become
+// order-preserving keys, protected blocks the largest; the `keep`-th largest
+// key is found two bits at a time by counting over the block (one barrier a step, ending
+// as soon as some prefix has exactly `keep` keys above it), and every block's
+// new place from ballots.  A few microseconds of latency bound it, whatever the size:
+// measured against a radix select in shared memory, 8.8 -> 2.5 us for 63 blocks, 13.3
+// -> 7.7 us for 2049.
+template <int NT, int R>
+__global__ void __launch_bounds__(NT)
 k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, float* weight, int32_t* kept, int keep,
         int sink, int recent) {
-  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int NW = NT / 32;
+  __shared__ uint2 s_cnt[2][NW];
+  __shared__ int s_pre[R * NW];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
-  const int mb = c.max_blocks, nw_max = (mb + 31) >> 5, tid = threadIdx.x;
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem);   // [mb]
-  int* order = reinterpret_cast<int*>(keys + mb);       // [mb] old index of every new place
-  uint32_t* bits = reinterpret_cast<uint32_t*>(order + mb);
-  int* wpref = reinterpret_cast<int*>(bits + nw_max);
-  int* scratch = wpref + nw_max;
+  const int mb = c.max_blocks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pair = blockIdx.x;
   const size_t row = static_cast<size_t>(pair) * mb;
+  int32_t id[R];
+  float w[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = tid + r * NT;
+    id[r] = i < mb ? c.table[row + i] : 0;
+    w[r] = i < mb ? c.weight[row + i] : 0.f;
+  }
   const int tok = cache_tokens(c, pair);
   const int B = 1 << c.shift, n = (tok + B - 1) >> c.shift;
-  const bool over = n > keep;
-  const int nk = over ? keep : n;
-  if (over) {
-    for (int i = tid; i < n; i += kEvThreads) {
-      const float w = c.weight[row + i];
-      keys[i] = i < sink || i >= n - recent ? 0xffffffffu : w == w ? order_key(w + 0.f) : 1u;   // -0 as 0, NaN last
+  const int nk = min(n, keep);
+  // 0: no block (never chosen); 1: NaN, below every number; -0 as 0
+  auto key = [&](int r) -> uint32_t {
+    const int i = tid + r * NT;
+    if (i >= n) return 0u;
+    if (i < sink || i >= n - recent) return 0xffffffffu;
+    return w[r] == w[r] ? order_key(w[r] + 0.f) : 1u;
+  };
+  // sums over the block of three counts of at most 16384 each
+  int turn = 0;
+  auto count3 = [&](uint32_t c1, uint32_t c2, uint32_t c3) {
+    const uint32_t a = __reduce_add_sync(0xffffffffu, c1 | (c2 << 16)), b = __reduce_add_sync(0xffffffffu, c3);
+    if (lane == 0) s_cnt[turn][warp] = make_uint2(a, b);
+    __syncthreads();
+    const uint2 v = lane < NW ? s_cnt[turn][lane] : make_uint2(0, 0);
+    turn ^= 1;
+    const uint32_t t = __reduce_add_sync(0xffffffffu, v.x);
+    return make_int3(t & 0xffffu, t >> 16, __reduce_add_sync(0xffffffffu, v.y));
+  };
+  // exclusive prefix, in index order, of one flag per block
+  auto prefix = [&](uint32_t flags, int* out) {
+    uint32_t bal[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      bal[r] = __ballot_sync(0xffffffffu, (flags >> r) & 1u);
+      if (lane == 0) s_pre[r * NW + warp] = __popc(bal[r]);
     }
     __syncthreads();
-    block_topk(keys, n, keep, order, scratch, bits, wpref);   // order[0, keep): the kept, ascending
-    for (int i = tid; i < n; i += kEvThreads) {
-      const uint32_t b = bits[i >> 5], bit = 1u << (i & 31);
-      if (!(b & bit)) order[keep + i - wpref[i >> 5] - __popc(b & (bit - 1u))] = i;
+    if (warp == 0) {
+      int run = 0;
+      for (int e0 = 0; e0 < R * NW; e0 += 32) {
+        const int v = e0 + lane < R * NW ? s_pre[e0 + lane] : 0;
+        int x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (e0 + lane < R * NW) s_pre[e0 + lane] = run + x - v;
+        run += __shfl_sync(0xffffffffu, x, 31);
+      }
     }
-    for (int i = n + tid; i < mb; i += kEvThreads) order[i] = i;
     __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) out[r] = s_pre[r * NW + warp] + __popc(bal[r] & ((1u << lane) - 1u));
+    __syncthreads();   // s_pre may be written again
+  };
+
+  uint32_t stay = 0;   // bit r: block tid + r NT is kept
+  if (n > keep) {
+    uint32_t T = 0;
+    int ge = n;   // keys >= T
+    for (int sh = 30; sh >= 0 && ge != keep; sh -= 2) {
+      uint32_t c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint32_t k = key(r);
+        c1 += k >= (T | (1u << sh));
+        c2 += k >= (T | (2u << sh));
+        c3 += k >= (T | (3u << sh));
+      }
+      const int3 s = count3(c1, c2, c3);
+      if (s.z >= keep) { T |= 3u << sh; ge = s.z; }
+      else if (s.y >= keep) { T |= 2u << sh; ge = s.y; }
+      else if (s.x >= keep) { T |= 1u << sh; ge = s.x; }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) stay |= (key(r) >= T && key(r) != 0u ? 1u : 0u) << r;
+    if (ge != keep) {
+      // more keys equal T than fit: those of the lowest index
+      uint32_t eq = 0, gt = 0;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        eq |= (key(r) == T ? 1u : 0u) << r;
+        gt += key(r) > T;
+      }
+      const int need = keep - count3(gt, 0, 0).x;
+      int at[R];
+      prefix(eq, at);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (((eq >> r) & 1u) && at[r] >= need) stay &= ~(1u << r);
+    }
   } else {
-    for (int i = tid; i < mb; i += kEvThreads) order[i] = i;
-    __syncthreads();
-  }
-  int32_t id[kEvRegs];
-  float wt[kEvRegs];
 #pragma unroll
-  for (int r = 0; r < kEvRegs; ++r) {
-    const int i = tid + r * kEvThreads;
-    if (i < mb) {
-      id[r] = c.table[row + order[i]];
-      wt[r] = i < nk ? c.weight[row + order[i]] : 0.f;
-    }
+    for (int r = 0; r < R; ++r) stay |= (tid + r * NT < n ? 1u : 0u) << r;
   }
-  __syncthreads();
+  int at[R];
+  prefix(stay, at);   // its barriers also stand between every read and write of the tables
 #pragma unroll
-  for (int r = 0; r < kEvRegs; ++r) {
-    const int i = tid + r * kEvThreads;
-    if (i < mb) {
-      table[row + i] = id[r];
-      weight[row + i] = wt[r];
-    }
+  for (int r = 0; r < R; ++r) {
+    const int i = tid + r * NT;
+    if (i >= mb) continue;
+    const bool s = (stay >> r) & 1u;
+    const int to = i >= n ? i : s ? at[r] : nk + i - at[r];   // kept, then freed, then the rest
+    table[row + to] = id[r];
+    weight[row + to] = s ? w[r] : 0.f;
+    if (s && kept) kept[static_cast<size_t>(pair) * keep + to] = i;
+    if (i == n - 1) n_tok[pair] = s ? (nk - 1) * B + tok - (n - 1) * B : nk * B;
   }
+  if (n == 0 && tid == 0) n_tok[pair] = 0;
   if (kept)
-    for (int i = tid; i < keep; i += kEvThreads) kept[static_cast<size_t>(pair) * keep + i] = i < nk ? order[i] : -1;
-  if (tid == 0) {
-    const bool last = nk > 0 && order[nk - 1] == n - 1;   // the newest block is still held
-    n_tok[pair] = last ? (nk - 1) * B + tok - (n - 1) * B : nk * B;
-  }
+    for (int i = nk + tid; i < keep; i += NT) kept[static_cast<size_t>(pair) * keep + i] = -1;
+}
+
+static cudaError_t launch_evict(const shadowkv_cache& src, const shadowkv_cache& dst, int keep, int sink, int recent,
+                                int32_t* kept, cudaStream_t st) {
+  auto go = [&](auto kern, int nt) {
+    return launch_pdl(kern, dim3(src.b * src.h_kv), dim3(nt), 0, st, cache_dev(src), dst.table, dst.n_tok, dst.weight, kept,
+                      keep, sink, recent);
+  };
+  const int mb = src.max_blocks;
+  if (mb <= 256) return go(k_evict<256, 1>, 256);
+  if (mb <= 1024) return go(k_evict<1024, 1>, 1024);
+  if (mb <= 4096) return go(k_evict<1024, 4>, 1024);
+  return go(k_evict<1024, 16>, 1024);
 }
 
 }  // namespace skv
@@ -614,12 +689,7 @@ skv_status shadowkv_cache_evict(const shadowkv_cache* src, const shadowkv_cache*
   if (sink < 0 || recent < 0 || sink > keep || recent > keep - sink)
     return set_error(SKV_ERR_INVALID_ARG, "need sink, recent >= 0 and sink + recent <= keep");
   if (reinterpret_cast<uintptr_t>(kept) % 4) return set_error(SKV_ERR_INVALID_ARG, "kept must be 4-byte aligned");
-  const size_t smem = skv::evict_smem(src->max_blocks);
-  cudaError_t e = skv::set_smem_once(reinterpret_cast<const void*>(skv::k_evict), static_cast<int>(smem));
-  if (e == cudaSuccess)
-    e = skv::launch_pdl(skv::k_evict, dim3(src->b * src->h_kv), dim3(skv::kEvThreads), smem,
-                        static_cast<cudaStream_t>(stream), skv::cache_dev(*src), dst->table, dst->n_tok, dst->weight,
-                        kept, keep, sink, recent);
+  const cudaError_t e = skv::launch_evict(*src, *dst, keep, sink, recent, kept, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SKV_OK : set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
 }
 
