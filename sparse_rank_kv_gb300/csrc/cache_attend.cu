@@ -324,56 +324,47 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       TileCursor cur;
       cur.begin(a.c, s_where[0], s_where[1], ntile);
       const uint32_t tS = tmem, tO = tmem + 2 * N1;
-      int it = 0, runs = -1;
-      bool ok = true;
-      auto scores = [&](bool first) {
-        const int st = it % NST;
-        if (first) {
-          ++runs;
-          ok = ok && tc::mbar_wait(&qfull[runs & 1], (runs >> 1) & 1, kWaitLimit);
-        }
-        ok = ok && tc::mbar_wait(&full[st], (it / NST) & 1, kWaitLimit);
-        if (!ok) return;
-        tc::fence_after();
-        const uint32_t k0 = tc::smem_u32(stages + st * C::Stage), q0 = tc::smem_u32(qbuf + (runs & 1) * C::QB);
+      // S(i) needs its K, its pair's q, and the softmax to be done with S(i - 2)
+      // (P(i - 2) is there); O(j) needs P(j).  Whichever is ready goes, O
+      // first: it frees a stage for the next copy
+      int i = 0, j = 0, runs = 0;      // next S, next O; runs: pair's turn of tile i
+      bool more = true;
+      uint64_t t_last = tc::globaltimer_ns();
+      while (more || j < i) {
+        bool did = false;
+        if (j < i && tc::mbar_test(&pfull[j & 1], (j >> 1) & 1)) {
+          tc::fence_after();
+          const int st = j % NST;
+          const uint32_t v0 = tc::smem_u32(stages + st * C::Stage + C::KB), p0 = tc::smem_u32(pbuf + (j & 1) * C::PB);
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          mma_e4m3(tS + (it & 1) * N1, tc::desc_k_none(k0 + k * 256, 128, 8 * D),
-                   tc::desc_k_none(q0 + k * (2 * N1 * 16), N1 * 16, 128), idesc_e4m3(N1), k > 0);
-        tc::mma_commit(&sfull[it & 1]);
-      };
-      auto values = [&](int j) {
-        const int st = j % NST;
-        ok = ok && tc::mbar_wait(&pfull[j & 1], (j >> 1) & 1, kWaitLimit);
-        if (!ok) return;
-        tc::fence_after();
-        const uint32_t v0 = tc::smem_u32(stages + st * C::Stage + C::KB), p0 = tc::smem_u32(pbuf + (j & 1) * C::PB);
-#pragma unroll
-        for (int k = 0; k < kCaT / 32; ++k)
-          mma_e4m3(tO + (j & 1) * N2, tc::desc_k_none(v0 + k * (2 * D * 16), D * 16, 128),
-                   tc::desc_k_none(p0 + k * (2 * N2 * 16), N2 * 16, 128), idesc_e4m3(N2), k > 0);
-        tc::mma_commit(&ofull[j & 1]);
-        tc::mma_commit(&empty[st]);
-      };
-      // S of the next tile is issued before O of this one, so that the
-      // softmax never waits for it; at a new pair whose q is not laid out
-      // yet (pairs of one tile), after it
-      bool first = true;
-      for (;;) {
-        if (first && it > 0 && !tc::mbar_test(&qfull[(runs + 1) & 1], ((runs + 1) >> 1) & 1)) {
-          values(it - 1);
-          scores(true);
-        } else {
-          scores(first);
-          if (it > 0) values(it - 1);
+          for (int k = 0; k < kCaT / 32; ++k)
+            mma_e4m3(tO + (j & 1) * N2, tc::desc_k_none(v0 + k * (2 * D * 16), D * 16, 128),
+                     tc::desc_k_none(p0 + k * (2 * N2 * 16), N2 * 16, 128), idesc_e4m3(N2), k > 0);
+          tc::mma_commit(&ofull[j & 1]);
+          tc::mma_commit(&empty[st]);
+          ++j;
+          did = true;
         }
-        if (!ok) break;
-        first = cur.next(a.c);
-        ++it;
-        if (cur.left <= 0) break;
+        if (more && j >= i - 1 && tc::mbar_test(&full[i % NST], (i / NST) & 1) &&
+            tc::mbar_test(&qfull[runs & 1], (runs >> 1) & 1)) {
+          tc::fence_after();
+          const uint32_t k0 = tc::smem_u32(stages + (i % NST) * C::Stage), q0 = tc::smem_u32(qbuf + (runs & 1) * C::QB);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            mma_e4m3(tS + (i & 1) * N1, tc::desc_k_none(k0 + k * 256, 128, 8 * D),
+                     tc::desc_k_none(q0 + k * (2 * N1 * 16), N1 * 16, 128), idesc_e4m3(N1), k > 0);
+          tc::mma_commit(&sfull[i & 1]);
+          ++i;
+          if (cur.next(a.c)) ++runs;
+          more = cur.left > 0;
+          did = true;
+        }
+        if (did) t_last = tc::globaltimer_ns();
+        else if (*s_abort || tc::globaltimer_ns() - t_last > kWaitLimit) {
+          abort_now();
+          break;
+        }
       }
-      if (ok) values(it - 1);
-      if (!ok) abort_now();
     }
     __syncwarp();
   } else if (ntile > 0) {
