@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
     auto id_of = [&](const TileCursor& c) {
       return lane < blocks(c) ? cache_block(a.c, c.pair, ((c.tile * kCaT) >> shift) + lane) : 0;
     };
+    const uint64_t once = tc::l2_evict_first_policy();
     int id = id_of(cur);
     nx1 = cur;
     nx1.next(a.c);
@@ -303,8 +304,8 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       if (lane < nb) {
         unsigned char* dst = stages + st * C::Stage + lane * (B * D);
         const size_t src = static_cast<size_t>(id) * (B * D);
-        tc::bulk_load(dst, a.c.kc + src, B * D, &full[st]);
-        tc::bulk_load(dst + C::KB, a.c.vc + src, B * D, &full[st]);
+        tc::bulk_load_hint(dst, a.c.kc + src, B * D, &full[st], once);
+        tc::bulk_load_hint(dst + C::KB, a.c.vc + src, B * D, &full[st], once);
       }
       if (nx1.left <= 0) { ++it; break; }
       cur = nx1;
