@@ -256,17 +256,17 @@ __global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constan
   tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int grp = threadIdx.x / A::TPJ, tid = threadIdx.x % A::TPJ, warp = threadIdx.x >> 5;
-  const long long job = static_cast<long long>(blockIdx.x) * (kApThreads / A::TPJ) + grp;
-  const int run = static_cast<int>(job % nrun);
-  const long long pw = job / nrun;
-  const int which = static_cast<int>(pw & 1);
-  if ((pw >> 1) >= a.c.pairs) return;
-  const int pair = static_cast<int>(pw >> 1);
+  const uint32_t job = blockIdx.x * (kApThreads / A::TPJ) + grp;   // 2 pairs nrun < 2^32
+  const uint32_t pw = job / static_cast<uint32_t>(nrun);
+  const int run = static_cast<int>(job - pw * static_cast<uint32_t>(nrun));
+  const int which = static_cast<int>(pw & 1u), pair = static_cast<int>(pw >> 1);
+  if (pair >= a.c.pairs) return;
   const CacheDev& c = a.c;
   int n0, end;
   append_range(a, pair, &n0, &end);
-  int blk = (n0 / B) + run * per;
-  const int last = min(blk + per, (end + B - 1) / B);   // blocks [blk, last)
+  constexpr int S = B == 16 ? 4 : B == 32 ? 5 : B == 64 ? 6 : 7;
+  int blk = (n0 >> S) + run * per;
+  const int last = min(blk + per, (end + B - 1) >> S);   // blocks [blk, last)
   if (blk >= last) return;
   const int seq = pair / c.h_kv, head = pair - seq * c.h_kv;
   const T* src = which ? static_cast<const T*>(a.v) + seq * a.vb + head * a.vh
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constan
     if (NW > 1) {
       if ((tid & 31) == 0) red[turn][warp] = m;
       tc::named_sync(1 + grp, A::TPJ);
-      for (int w = 0; w < NW; ++w) m = max(m, red[turn][grp * NW + w]);
+      m = __reduce_max_sync(0xffffffffu, red[turn][grp * NW + (tid & (NW - 1))]);
     }
     return m;
   };

@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&full[i], 2);   // the copies, and the scales
       tc::mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -268,17 +268,10 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       return lane < blocks(c) ? cache_block(a.c, c.pair, ((c.tile * kCaT) >> shift) + lane) : 0;
     };
     const uint64_t once = tc::l2_evict_first_policy();
-    int id = id_of(cur);
-    nx1 = cur;
-    nx1.next(a.c);
-    int id1 = id_of(nx1);
-    float ks = a.c.ks[id], vs = a.c.vs[id];
+    int id = id_of(cur), id1 = 0;
+    float ks = 0.f, vs = 0.f;
     int it = 0;
     for (;; ++it) {
-      nx2 = nx1;
-      if (nx2.left > 0) nx2.next(a.c);
-      const int id2 = id_of(nx2);
-      const float ks1 = a.c.ks[id1], vs1 = a.c.vs[id1];
       const int st = it % NST, use = it / NST;
       bool ok = true;
       if (lane == 0) ok = !*s_abort && tc::mbar_wait(&empty[st], (use & 1) ^ 1, kWaitLimit);
@@ -288,6 +281,25 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
         break;
       }
       const int nb = blocks(cur);
+      if (lane == 0) tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb) * 2u * (B * D));
+      __syncwarp();
+      if (lane < nb) {
+        unsigned char* dst = stages + st * C::Stage + lane * (B * D);
+        const size_t src = static_cast<size_t>(id) * (B * D);
+        tc::bulk_load_hint(dst, a.c.kc + src, B * D, &full[st], once);
+        tc::bulk_load_hint(dst + C::KB, a.c.vc + src, B * D, &full[st], once);
+      }
+      if (it == 0) {
+        ks = a.c.ks[id];
+        vs = a.c.vs[id];
+        nx1 = cur;
+        nx1.next(a.c);
+        id1 = id_of(nx1);
+      }
+      nx2 = nx1;
+      if (nx2.left > 0) nx2.next(a.c);
+      const int id2 = id_of(nx2);
+      const float ks1 = a.c.ks[id1], vs1 = a.c.vs[id1];
       float* sc = ssc + st * 20;
       // V's scales relative to the tile's largest, which O is multiplied by
       float vref = lane < nb ? fabsf(vs) : 0.f;
@@ -299,14 +311,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       }
       if (lane == 0) sc[16] = vref * (1.f / 256.f);
       __syncwarp();
-      if (lane == 0) tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb) * 2u * (B * D));
-      __syncwarp();
-      if (lane < nb) {
-        unsigned char* dst = stages + st * C::Stage + lane * (B * D);
-        const size_t src = static_cast<size_t>(id) * (B * D);
-        tc::bulk_load_hint(dst, a.c.kc + src, B * D, &full[st], once);
-        tc::bulk_load_hint(dst + C::KB, a.c.vc + src, B * D, &full[st], once);
-      }
+      if (lane == 0) tc::mbar_arrive(&full[st]);
       if (nx1.left <= 0) { ++it; break; }
       cur = nx1;
       nx1 = nx2;
