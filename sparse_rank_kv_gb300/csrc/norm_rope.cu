@@ -77,10 +77,10 @@ constexpr int kNrCtas = 5;      // per SM (48 registers)
 // once, a pair per thread, and every D/8-lane group keeps its token's in
 // registers over its heads, which it loads two (fp32: one) at a time; the other
 // CTAs of the SM cover its loads.  The arithmetic is on pairs (fma.f32x2).
-// Measured at 32768 tokens of 32 + 8 heads of 128 in bf16 (671 MB): 116 us, 5.8
-// TB/s; 141 us with scalar arithmetic (bound by its instructions), 122 us with
-// four CTAs per SM, 147 us with four rows at a time, 144 us with the next rows
-// prefetched into registers.
+// Measured at 32768 tokens of 32 + 8 heads of 128 in bf16 (671 MB): 101 us, 6.6
+// TB/s, bound by DRAM; without the L2 prefetch 116 us, then with scalar
+// arithmetic 141 us (bound by its instructions), with four CTAs per SM 122 us, with four rows at
+// a time 147 us, with the next rows prefetched into registers 144 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(kNrThreads, kNrCtas)
 k_norm_rope(const __grid_constant__ NormRopeArgs a, const __grid_constant__ RopeFreq freq) {
@@ -96,21 +96,32 @@ k_norm_rope(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Rope
     *i = static_cast<int>(token / static_cast<uint32_t>(a.s));
     *t = static_cast<int>(token - static_cast<uint32_t>(*i) * static_cast<uint32_t>(a.s));
   };
+  const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR, u = grp / Sub, sub = grp % Sub;
+  const uint32_t token = tok0 + u;
+  const bool live = token < a.tokens;
+  int i = 0, t = 0;
+  if (live) place(token, &i, &t);
+  const int c0 = blockIdx.y * a.chunk, c1 = min(a.heads, c0 + a.chunk);
+  // with several rounds of rows ahead, all of them go to L2 while the angles are formed
+  for (int h = c0 + sub + l * Sub; live && a.chunk > Sub * Rows && h < c1; h += Sub * LPR) {
+    const int w = h < a.h_q ? 0 : 1;
+    const char* p = reinterpret_cast<const char*>(static_cast<const T*>(a.x[w]) + i * a.xb[w] + t * a.xs[w] +
+                                                  (w ? h - a.h_q : h) * a.xh[w]);
+#pragma unroll
+    for (int e = 0; e < D * static_cast<int>(sizeof(T)); e += 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + e));
+  }
   for (int e = threadIdx.x; e < kNrTokens * half; e += kNrThreads) {
     const int u = e / half, p = e - u * half;
-    const uint32_t token = tok0 + u;
-    if (token >= a.tokens) break;
+    if (tok0 + u >= a.tokens) break;
     int i, t;
-    place(token, &i, &t);
-    const long long pos = !a.pos ? t : a.per_token ? a.pos[token] : static_cast<long long>(a.pos[i]) + t;
+    place(tok0 + u, &i, &t);
+    const long long pos = !a.pos ? t : a.per_token ? a.pos[tok0 + u] : static_cast<long long>(a.pos[i]) + t;
     float sn, cs;
     rope_turn<sizeof(T) == 2>(pos, freq.f[p], &sn, &cs);
     s_cs[u][p] = make_float2(cs, sn);
   }
   __syncthreads();
-  const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR, u = grp / Sub, sub = grp % Sub;
-  const uint32_t token = tok0 + u;
-  const bool live = token < a.tokens;
   const int nrot = a.rot >> 3;
   const bool turned = l < nrot;
   const int o0 = turned ? 4 * l : a.rot + 8 * (l - nrot);
@@ -123,9 +134,6 @@ k_norm_rope(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Rope
     cs[e] = make_float2(x.x, y.x);
     sn[e] = make_float2(x.y, y.y);
   }
-  int i = 0, t = 0;
-  if (live) place(token, &i, &t);
-  const int c0 = blockIdx.y * a.chunk, c1 = min(a.heads, c0 + a.chunk);
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     // this part's heads of the chunk, as indexes into q or k
