@@ -359,7 +359,7 @@ typedef struct shadowkv_cache {
   int block;          /* tokens per block: 16, 32, 64 or 128 */
   int max_blocks;     /* table entries per pair, 1..16384 */
   int n_pool;         /* blocks in the pool */
-  void* k_codes;      /* n_pool x block x d bytes, 16-byte aligned */
+  void* k_codes;      /* n_pool x block x d bytes, 32-byte aligned */
   void* v_codes;
   float* k_scale;     /* n_pool */
   float* v_scale;

@@ -1,6 +1,11 @@
 // The 8-bit block cache (include/shadowkv.h): its checks, the append that
 // quantises new tokens into it, and the eviction of whole blocks by gathered
 // attention weight.
+//
+// Every kernel waits for its stream's previous kernel before it touches
+// memory.  Only a call's inner kernels let their dependents start early: a
+// call's last kernel does not, since kernels of the library read some of
+// their inputs before their own grid-dependency wait.
 #include <cfloat>
 #include <cstdint>
 
@@ -64,6 +69,17 @@ __device__ __forceinline__ void put_codes(uint32_t* w0, uint32_t* w1, int t, uin
   *w1 = (*w1 & ~(0xffu << sh)) | (((c2 >> 8) & 0xffu) << sh);
 }
 
+__device__ __forceinline__ void load32(uint32_t* w, const void* p) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t* a, const uint32_t* b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]),
+               "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3])
+               : "memory");
+}
+
 // One block's K or V in the hands of TPJ threads: 16 code bytes of K per unit
 // (16 dimensions of a row), 2 x 16 of V (16 tokens of two dimensions), so that
 // every store is 16 bytes and the loads of a unit's elements are all in
@@ -90,17 +106,24 @@ struct Ap {
   // not read).  Full: all of them.
   template <bool Full>
   __device__ __forceinline__ static void load_rows(uint32_t* w, const T* src, long long ss, int which, int e0, int e1, int tid) {
+    // 32-byte loads where the rows are 32-byte aligned
+    const bool wide = ((reinterpret_cast<uintptr_t>(src) | static_cast<uintptr_t>(ss * static_cast<long long>(sizeof(T)))) & 31u) == 0;
     if (which == 0) {
 #pragma unroll
       for (int i = 0; i < UK; ++i) {
         const int u = tid + i * TPJ, r = k_row(u);
         const bool on = Full || (r >= e0 && r < e1);
-        const uint4* p = reinterpret_cast<const uint4*>(src + r * ss + k_piece(u) * 16);
+        const T* p = src + r * ss + k_piece(u) * 16;
+        if (Full && wide) {
 #pragma unroll
-        for (int e = 0; e < 2 * E; ++e) {
-          const uint4 x = on ? p[e] : make_uint4(0, 0, 0, 0);
-          uint32_t* o = w + i * 8 * E + 4 * e;
-          o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+          for (int e = 0; e < E; ++e) load32(w + (i * E + e) * 8, p + e * (16 / E));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2 * E; ++e) {
+            const uint4 x = on ? reinterpret_cast<const uint4*>(p)[e] : make_uint4(0, 0, 0, 0);
+            uint32_t* o = w + i * 8 * E + 4 * e;
+            o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+          }
         }
       }
     } else {
@@ -133,7 +156,8 @@ struct Ap {
     uint32_t m = 0;
     if constexpr (E == 1) {
 #pragma unroll
-      for (int i = 0; i < Words; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+      for (int i = 0; i < Words; ++i)
+        asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %1;\n\tmax.NaN.bf16x2 %0, %0, t;\n\t}" : "+r"(m) : "r"(w[i]));
       return max(m & 0xffff0000u, m << 16);
     } else {
 #pragma unroll
@@ -184,9 +208,7 @@ struct Ap {
           a[t] = __byte_perm(p, q, 0x5410);
           b[t] = __byte_perm(p, q, 0x7632);
         }
-        uint4* d = reinterpret_cast<uint4*>(dst) + 2 * u;
-        d[0] = make_uint4(a[0], a[1], a[2], a[3]);
-        d[1] = make_uint4(b[0], b[1], b[2], b[3]);
+        store32(dst + 32 * static_cast<size_t>(u), a, b);
       }
     }
   }
@@ -319,7 +341,6 @@ __global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constan
 }
 
 __global__ void __launch_bounds__(kApThreads) k_append_count(const __grid_constant__ AppendArgs a) {
-  tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int pair = blockIdx.x * kApThreads + threadIdx.x;
   if (pair >= a.c.pairs) return;
@@ -334,7 +355,6 @@ __global__ void __launch_bounds__(kApThreads) k_append_count(const __grid_consta
 template <typename T, int D>
 __global__ void __launch_bounds__(kApThreads) k_append_one(const __grid_constant__ AppendArgs a) {
   constexpr int N = D / 32;
-  tc::grid_dep_launch();
   tc::grid_dep_wait();
   const CacheDev& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, which = warp & 1;
@@ -461,7 +481,6 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
   constexpr int NW = NT / 32;
   __shared__ uint2 s_cnt[2][NW];
   __shared__ int s_pre[R * NW];
-  tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int mb = c.max_blocks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pair = blockIdx.x;
@@ -606,8 +625,8 @@ const char* cache_fault(const shadowkv_cache* c, skv_status* st) {
   if (c->max_blocks < 1 || c->n_pool < 1) return "cache: max_blocks and n_pool must be >= 1";
   if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->table || !c->n_tok || !c->status)
     return "cache: a required pointer is NULL";
-  if (reinterpret_cast<uintptr_t>(c->k_codes) % 16 || reinterpret_cast<uintptr_t>(c->v_codes) % 16)
-    return "cache: codes must be 16-byte aligned";
+  if (reinterpret_cast<uintptr_t>(c->k_codes) % 32 || reinterpret_cast<uintptr_t>(c->v_codes) % 32)
+    return "cache: codes must be 32-byte aligned";
   const uintptr_t words = reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale) |
                           reinterpret_cast<uintptr_t>(c->table) | reinterpret_cast<uintptr_t>(c->n_tok) |
                           reinterpret_cast<uintptr_t>(c->weight) | reinterpret_cast<uintptr_t>(c->status);
@@ -653,12 +672,12 @@ skv_status shadowkv_cache_append(const shadowkv_cache* c, int dtype, const shado
   if (st != SKV_OK) return st;
   if (dtype != SKV_DTYPE_F32 && dtype != SKV_DTYPE_BF16) return set_error(SKV_ERR_INVALID_ARG, "bad dtype");
   if (s < 0) return set_error(SKV_ERR_INVALID_ARG, "s must be >= 0");
+  if (s == 0) return SKV_OK;
   const int E = dtype == SKV_DTYPE_BF16 ? 2 : 4;
   const char* f = rows16_fault(k, E);
   if (!f) f = rows16_fault(v, E);
   if (!f && reinterpret_cast<uintptr_t>(lens) % 4) f = "lens must be 4-byte aligned";
   if (f) return set_error(SKV_ERR_INVALID_ARG, f);
-  if (s == 0) return SKV_OK;
   skv::AppendArgs a;
   a.c = skv::cache_dev(*c);
   a.k = k->ptr; a.kb = k->sb; a.kh = k->sh; a.ks = k->ss;

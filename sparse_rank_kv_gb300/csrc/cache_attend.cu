@@ -599,16 +599,16 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
 
 // ------------------------------------------------------------ merge
 constexpr int kCmThreads = 256;
+constexpr int kCmChunk = 512;    // cache blocks whose weights a CTA forms
 
 // Blocks 0 .. pairs G - 1: the output of a query head.  The others, with
-// weights: `chunk` cache blocks of a pair.
+// weights: kCmChunk cache blocks of a pair.
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kCmThreads)
-k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int chunk, int nchunk) {
+k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int nchunk) {
   constexpr int SL = kCmThreads / D, Pre = 4;   // partials per pass; rows held while the maxima are formed
   __shared__ float s_M[G], s_L[G], s_acc[SL][D];
   const int tid = threadIdx.x;
-  tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int P = a.c.pairs, bx = blockIdx.x;
   const bool head_role = bx < P * G;
@@ -676,8 +676,8 @@ k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int chunk, int nc
     return;
   }
   const int B = 1 << a.c.shift, gran = min(B, 32), nb = (ntok + B - 1) >> a.c.shift;
-  const int i0 = ((bx - P * G) % nchunk) * chunk;
-  for (int i = i0 + tid; i < min(nb, i0 + chunk); i += kCmThreads) {
+  const int i0 = ((bx - P * G) % nchunk) * kCmChunk;
+  for (int i = i0 + tid; i < min(nb, i0 + kCmChunk); i += kCmThreads) {
     float w = 0.f;
     const int tile = i * B / kCaT;
     for (int g = 0; g < G; ++g) {
@@ -697,10 +697,8 @@ static cudaError_t attend_t(const AttendArgs& a, int ncta, cudaStream_t st) {
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), Ca<T, D, G>::Smem);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ncta), dim3(kCaThreads), Ca<T, D, G>::Smem, st, a);
   if (e != cudaSuccess) return e;
-  const int chunk = 512;
-  const int nchunk = a.gather ? (a.c.max_blocks + chunk - 1) / chunk : 0;
-  return launch_pdl(k_attend_merge<T, D, G>, dim3(a.c.pairs * (G + nchunk)), dim3(kCmThreads), 0, st, a, ncta, chunk,
-                    nchunk);
+  const int nchunk = a.gather ? (a.c.max_blocks + kCmChunk - 1) / kCmChunk : 0;
+  return launch_pdl(k_attend_merge<T, D, G>, dim3(a.c.pairs * (G + nchunk)), dim3(kCmThreads), 0, st, a, ncta, nchunk);
 }
 
 template <typename T, int D>
@@ -767,6 +765,8 @@ skv_status shadowkv_cache_attend(const shadowkv_cache* c, int dtype, int h_q, co
   if (reinterpret_cast<uintptr_t>(q->ptr) % E || reinterpret_cast<uintptr_t>(out->ptr) % E ||
       reinterpret_cast<uintptr_t>(lse) % 4)
     return set_error(SKV_ERR_INVALID_ARG, "q, out and lse must be aligned to their elements");
+  if (static_cast<long long>(c->b) * c->h_kv * (8 + (c->max_blocks + skv::kCmChunk - 1) / skv::kCmChunk) >= (1LL << 31))
+    return set_error(SKV_ERR_UNSUPPORTED, "too many sequences and heads for one call");
   if (!std::isfinite(scale)) return set_error(SKV_ERR_INVALID_ARG, "scale must be finite");
   if (gather != 0 && gather != 1) return set_error(SKV_ERR_INVALID_ARG, "gather must be 0 or 1");
   if (gather && !c->weight) return set_error(SKV_ERR_INVALID_ARG, "the cache keeps no weights");

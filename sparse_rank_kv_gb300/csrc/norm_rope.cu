@@ -88,7 +88,8 @@ k_norm_rope(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Rope
   constexpr int Rows = 4 / sizeof(T);                              // rows in flight per group
   typedef typename Quad<T>::Raw Raw;
   __shared__ float2 s_cs[kNrTokens][D / 2];
-  tc::grid_dep_launch();
+  // no early launch of dependents: the decode step's selection reads the new
+  // token's key, this kernel's output, before its own grid-dependency wait
   const int half = a.rot >> 1;
   const uint32_t tok0 = blockIdx.x * kNrTokens;
   tc::grid_dep_wait();
@@ -273,6 +274,7 @@ extern "C" skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, 
     return set_error(SKV_ERR_INVALID_ARG, "eps must be > 0 and finite");
   if (p->rot && (!(p->theta > 0.f) || !std::isfinite(p->theta)))
     return set_error(SKV_ERR_INVALID_ARG, "theta must be > 0 and finite");
+  if (p->b == 0 || p->s == 0) return SKV_OK;
   const int E = p->dtype == SKV_DTYPE_BF16 ? 2 : 4;
   const shadowkv_rows* in[2] = {q, k};
   const shadowkv_rows* out[2] = {q_out, k_out};
@@ -291,7 +293,6 @@ extern "C" skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, 
     a.w[i] = w[i];
   }
   if (reinterpret_cast<uintptr_t>(pos) % 4) return set_error(SKV_ERR_INVALID_ARG, "pos must be 4-byte aligned");
-  if (p->b == 0 || p->s == 0) return SKV_OK;
   a.pos = pos;
   a.s = p->s;
   a.tokens = static_cast<uint32_t>(p->b) * static_cast<uint32_t>(p->s);

@@ -31,7 +31,7 @@ def rows(ptr=P, sb=8192, sh=1024, ss=128):
 
 @pytest.mark.parametrize("change,code", [
     (dict(b=0), 1), (dict(h_kv=0), 1), (dict(max_blocks=0), 1), (dict(n_pool=0), 1), (dict(n_pool=-4), 1),
-    (dict(k_codes=None), 1), (dict(v_codes=P + 8), 1), (dict(k_scale=None), 1), (dict(table=P + 2), 1),
+    (dict(k_codes=None), 1), (dict(v_codes=P + 8), 1), (dict(k_codes=P + 16), 1), (dict(k_scale=None), 1), (dict(table=P + 2), 1),
     (dict(n_tok=None), 1), (dict(status=None), 1), (dict(weight=P + 1), 1),
     (dict(d=96), 7), (dict(block=48), 7), (dict(block=256), 7), (dict(max_blocks=16385), 7),
     (dict(b=1 << 20, h_kv=64, max_blocks=64), 7),
@@ -121,6 +121,14 @@ def test_norm_rope_of_nothing_is_no_call(lib):
     for p in (dict(b=0), dict(s=0)):
         assert lib.shadowkv_qk_norm_rope(nr(**p), rows(), rows(), None, None, None, rows(), rows(), None) == 0
     assert lib.shadowkv_qk_norm_rope(None, rows(), rows(), None, None, None, rows(), rows(), None) == 1
+
+
+def test_packed_arguments_have_the_structures_layout():
+    r = binding.Rows.from_buffer_copy(binding._PACK_ROWS(P, 1, 2, 3))
+    assert (r.ptr, r.sb, r.sh, r.ss) == (P, 1, 2, 3) and ctypes.sizeof(binding.Rows) == 32
+    n = binding.NormRopeParams.from_buffer_copy(binding._PACK_NORM_ROPE(1, 2, 3, 4, 5, 6, 7, True, False, 0.5, 2.0))
+    got = [getattr(n, f) for f, _ in binding.NormRopeParams._fields_]
+    assert got == [1, 2, 3, 4, 5, 6, 7, 1, 0, 0.5, 2.0]
 
 
 def test_binding_refuses_wrong_tensors():

@@ -572,3 +572,126 @@ def test_attend_calls_may_overlap_without_gathering():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_new_token_made_by_norm_rope_feeds_the_sparse_decode_step():
+    """qk_norm_rope's q and k straight into shadowkv_decode_step, nothing in between:
+    the appended local-window rows and the outputs equal those of inputs made
+    beforehand (the step's kernels may start early, never before their inputs are there)."""
+    cfg = synth.CONFIGS["llama_b1_s32k"].with_(s=4096 + 64, k=32, o=16, steps=12, seed=7)
+    st = synth.make_state(cfg, device="cuda")
+    p = binding.make_params(cfg)
+    b, hq, h, d = cfg.b, cfg.h_q, cfg.h_kv, cfg.d
+    g = gen(17)
+    qkv = randn(g, cfg.steps, b, 1, hq + 2 * h, d).bfloat16()
+    pos = torch.full((b,), cfg.s, dtype=torch.int32, device="cuda")
+
+    def run(ready):
+        ctx = binding.load_state(p, st)
+        outs = []
+        made = []
+        for t in range(cfg.steps):
+            x = qkv[t]
+            if ready:
+                q, k = ready[t]
+            else:
+                q, k = torch.empty(b, hq, 1, d, dtype=x.dtype, device="cuda"), torch.zeros(b, h, 1, d, dtype=x.dtype, device="cuda")
+                v = x[:, 0, hq + h:].contiguous()
+                out = torch.empty(b, hq, d, dtype=x.dtype, device="cuda")
+                torch.cuda.synchronize()
+                binding.qk_norm_rope(x[:, :, :hq].transpose(1, 2), x[:, :, hq:hq + h].transpose(1, 2), theta=cfg.theta,
+                                     pos=pos, q_out=q, k_out=k)
+            if ready:
+                v = x[:, 0, hq + h:].contiguous()
+                out = torch.empty(b, hq, d, dtype=x.dtype, device="cuda")
+                torch.cuda.synchronize()
+            ctx.decode_step(q.view(b, hq, d), k.view(b, h, d), v, out)
+            outs.append(out)
+            made.append((q, k))
+        torch.cuda.synchronize()
+        loc = ctx.export("K_LOC")
+        ctx.check()
+        ctx.close()
+        return outs, made, loc
+
+    outs, made, loc = run(None)
+    again, _, loc2 = run(made)
+    assert torch.equal(loc, loc2)
+    for a, c in zip(outs, again):
+        assert torch.equal(a, c)
+
+
+def test_blocks_shared_by_sequences():
+    """Two sequences whose tables name the same blocks (a common prompt) attend
+    over them as over copies of their own."""
+    c, ref = filled(2, 2, 128, 16, [70, 70], torch.bfloat16, seed=3)
+    c.table[1, :, :4] = c.table[0, :, :4]
+    for h in range(2):
+        ref.blocks[1, h][:4] = ref.blocks[0, h][:4]
+    q = randn(gen(1), 2, 8, 128).bfloat16()
+    dl = attend_close(c.attend(q, decay=0.0), None, q, ref.attend(np64(q), 128 ** -0.5, 0.0), torch.bfloat16)
+    weights_close(c, ref, dl)
+
+
+def test_offsets_past_32_bits():
+    """Blocks and rows whose byte and element offsets pass 2^32: the last blocks of a
+    pool of 4.6 GB a side, and rows 2^31 + 8 elements apart."""
+    n = 560000                                                 # 8 KB each
+    big = binding.BlockCache(torch.empty(n, 8, 8, 8, 16, dtype=torch.uint8, device="cuda"),
+                             torch.empty(n, 4, 128, 16, dtype=torch.uint8, device="cuda"), torch.zeros(n, device="cuda"),
+                             torch.zeros(n, device="cuda"), torch.arange(n - 8, n, dtype=torch.int32, device="cuda").view(2, 1, 4),
+                             torch.zeros(2, 1, dtype=torch.int32, device="cuda"), torch.zeros(2, 1, 4, device="cuda"))
+    small = binding.BlockCache.empty(2, 1, 128, 4)
+    far = torch.empty(2**31 + 8 + 200 * 128, dtype=torch.bfloat16, device="cuda")
+    k = far.as_strided((2, 1, 150, 128), (2**31 + 8, 150 * 128, 128, 1))
+    k.copy_(randn(gen(2), 2, 1, 150, 128))
+    for c in (big, small):
+        c.append(k, k)
+        c.append(k[:, :, :1], k[:, :, 1:2])
+    q = randn(gen(3), 2, 4, 128).bfloat16()
+    assert torch.equal(big.attend(q, decay=0.0), small.attend(q, decay=0.0))
+    assert torch.equal(big.weight, small.weight)
+    near = k.contiguous()
+    a, _ = binding.qk_norm_rope(k, None)
+    b, _ = binding.qk_norm_rope(near, None)
+    assert torch.equal(a, b)
+    binding.qk_norm_rope(near, None, q_out=k)
+    assert torch.equal(k, b)
+    big.check()
+
+
+def test_empty_calls_and_reset():
+    c = binding.BlockCache.empty(2, 2, 64, 3, block=16)
+    e = torch.empty(2, 2, 0, 64, device="cuda")
+    c.append(e, e)
+    q, k = binding.qk_norm_rope(e, e)
+    assert q.shape == k.shape == e.shape
+    x = randn(gen(1), 2, 2, 40, 64)
+    c.append(x, x, torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert not c.n_tok.any()
+    one = x[:, :, :1]
+    c.append(one, one, torch.tensor([0, 1], dtype=torch.int32, device="cuda"))
+    assert c.n_tok.tolist() == [[0, 0], [1, 1]]
+    out = c.attend(one[:, :, 0])
+    assert not out[0].any() and torch.isfinite(out).all()
+    c.evict(1, recent=0)
+    assert c.n_tok.tolist() == [[0, 0], [1, 1]]
+    c.reset()
+    assert not c.attend(one[:, :, 0]).any()
+    c.check()
+
+
+def test_stream_handles():
+    """A raw cudaStream_t and a torch stream serve as the calls' stream."""
+    c, ref = filled(1, 2, 64, 16, [100], torch.float32, seed=6)
+    q = randn(gen(2), 1, 4, 64)
+    want = c.attend(q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = c.attend(q, stream=s.cuda_stream)
+    k = randn(gen(3), 1, 2, 5, 64)
+    s.wait_stream(torch.cuda.current_stream())
+    c.append(k, k, stream=s)
+    c.evict(4, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(got, want) and c.n_tok.tolist() == [[3 * 16 + 9, 3 * 16 + 9]]
