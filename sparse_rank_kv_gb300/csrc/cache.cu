@@ -269,7 +269,11 @@ struct Ap {
 // Group of TPJ threads = a run of `per` blocks of a pair's K or V, the next
 // block's rows loading while the current block is quantised (without that
 // every block pays its loads' latency, which bounds a CTA per block).
-// k_append_count moves the token counts after.
+// k_append_count moves the token counts after.  Measured, 8 heads of 128 in
+// bf16, blocks of 64: four prompts of up to 16,000 tokens, 39,600 in all (243 MB read and written),
+// 45 us, 5.4 TB/s; four full ones (393 MB) 65 us, 6.0 TB/s.  A CTA per block took 84 us,
+// one load per element and the next block's loads in flight 66, a path of
+// its own for whole new blocks 48.5, 32-byte accesses 45.
 template <typename T, int D, int B>
 __global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constant__ AppendArgs a, int per, int nrun) {
   typedef Ap<T, D, B> A;
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(kApThreads) k_append_count(const __grid_consta
 
 // One new token: a warp for a pair's K, one for its V, lane = D/32 adjacent
 // dimensions.  Only where the token needs a larger scale does the warp pass over
-// the block's codes.
+// the block's codes.  Three dependent loads (count, table, scale) bound it: 384 pairs about 3 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(kApThreads) k_append_one(const __grid_constant__ AppendArgs a) {
   constexpr int N = D / 32;
@@ -472,8 +476,8 @@ constexpr int kEvMax = 16384;   // blocks per pair
 // key is found two bits at a time by counting over the block (one barrier a step, ending
 // as soon as some prefix has exactly `keep` keys above it), and every block's
 // new place from ballots.  A few microseconds of latency bound it, whatever the size:
-// measured against a radix select in shared memory, 8.8 -> 2.5 us for 63 blocks, 13.3
-// -> 7.7 us for 2049.
+// measured, 8 pairs of 63 blocks 2.5 us, 64 pairs of 2049 blocks 7.1 us (8.8 and
+// 13.3 with a radix select in shared memory).
 template <int NT, int R>
 __global__ void __launch_bounds__(NT)
 k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, float* weight, int32_t* kept, int keep,
@@ -496,13 +500,22 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
   const int tok = cache_tokens(c, pair);
   const int B = 1 << c.shift, n = (tok + B - 1) >> c.shift;
   const int nk = min(n, keep);
-  // 0: no block (never chosen); 1: NaN, below every number; -0 as 0
-  auto key = [&](int r) -> uint32_t {
+  const int rows = (n + NT - 1) / NT;   // registers in use: the same for every thread
+  // 0: no block (never chosen); 1: NaN, below every number; -0 as 0.  Formed
+  // once while the registers allow it.
+  auto make_key = [&](int r) -> uint32_t {
     const int i = tid + r * NT;
     if (i >= n) return 0u;
     if (i < sink || i >= n - recent) return 0xffffffffu;
     return w[r] == w[r] ? order_key(w[r] + 0.f) : 1u;
   };
+  constexpr bool Held = R <= 4;
+  uint32_t held[Held ? R : 1];
+  if (Held) {
+#pragma unroll
+    for (int r = 0; r < (Held ? R : 0); ++r) held[r] = make_key(r);
+  }
+  auto key = [&](int r) -> uint32_t { return Held ? held[Held ? r : 0] : make_key(r); };
   // sums over the block of three counts of at most 16384 each
   int turn = 0;
   auto count3 = [&](uint32_t c1, uint32_t c2, uint32_t c3) {
@@ -551,6 +564,7 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
       uint32_t c1 = 0, c2 = 0, c3 = 0;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
         const uint32_t k = key(r);
         c1 += k >= (T | (1u << sh));
         c2 += k >= (T | (2u << sh));
