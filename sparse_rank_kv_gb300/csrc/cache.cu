@@ -441,9 +441,11 @@ static cudaError_t append_many(const AppendArgs& a, cudaStream_t st) {
   typedef Ap<T, D, B> A;
   const long long touched = (static_cast<long long>(a.s) + B - 1) / B + 1;
   const int nblk = static_cast<int>(touched < a.c.max_blocks ? touched : a.c.max_blocks);
-  // runs of up to 8 blocks as long as about 4096 groups are left
+  // runs of up to 8 blocks as long as about 1200 groups are left.  Measured,
+  // four full prompts of 16,000 tokens: 67 us, one block per run 82 us; four
+  // ragged ones of up to 4000: 14.7 us, with 4096 groups 19.0
   const long long jobs = 2LL * a.c.pairs * nblk;
-  const int per = static_cast<int>(jobs / 4096 < 1 ? 1 : jobs / 4096 > 8 ? 8 : jobs / 4096);
+  const int per = static_cast<int>(jobs / 1200 < 1 ? 1 : jobs / 1200 > 8 ? 8 : jobs / 1200);
   const int nrun = (nblk + per - 1) / per;
   const long long groups = 2LL * a.c.pairs * nrun, gpc = kApThreads / A::TPJ;
   cudaError_t e = launch_pdl(k_append_many<T, D, B>, dim3(static_cast<unsigned>((groups + gpc - 1) / gpc)),
@@ -455,6 +457,7 @@ static cudaError_t append_many(const AppendArgs& a, cudaStream_t st) {
 
 template <typename T, int D>
 static cudaError_t append_t(const AppendArgs& a, cudaStream_t st) {
+  // one token, 384 pairs: 4.1 us with the count's copy, 9.6 through the other path
   if (a.s == 1) {
     constexpr int ppc = kApThreads / 64;   // pairs per CTA
     return launch_pdl(k_append_one<T, D>, dim3((a.c.pairs + ppc - 1) / ppc), dim3(kApThreads), 0, st, a);
