@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constan
   typedef Ap<T, D, B> A;
   constexpr int NW = (A::TPJ + 31) / 32;
   __shared__ uint32_t red[2][kApThreads / 32];
+  __shared__ int2 s_range[kApThreads / A::TPJ];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int grp = threadIdx.x / A::TPJ, tid = threadIdx.x % A::TPJ, warp = threadIdx.x >> 5;
@@ -288,8 +289,12 @@ __global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constan
   const int which = static_cast<int>(pw & 1u), pair = static_cast<int>(pw >> 1);
   if (pair >= a.c.pairs) return;
   const CacheDev& c = a.c;
-  int n0, end;
-  append_range(a, pair, &n0, &end);
+  // one thread reads the counts, so that the group agrees on them whatever
+  // else happens to the cache
+  if (tid == 0) append_range(a, pair, &s_range[grp].x, &s_range[grp].y);
+  if (NW > 1) tc::named_sync(1 + grp, A::TPJ);
+  else __syncwarp();
+  const int n0 = s_range[grp].x, end = s_range[grp].y;
   constexpr int S = B == 16 ? 4 : B == 32 ? 5 : B == 64 ? 6 : 7;
   int blk = (n0 >> S) + run * per;
   const int last = min(blk + per, (end + B - 1) >> S);   // blocks [blk, last)
@@ -376,7 +381,9 @@ __global__ void __launch_bounds__(kApThreads) k_append_one(const __grid_constant
 #pragma unroll
       for (int e = 0; e < N; ++e) x[e] = Ty<T>::to_f(src[lane * N + e]);
     }
-    append_range(a, pair, &n0, &end);
+    if (lane == 0) append_range(a, pair, &n0, &end);
+    n0 = __shfl_sync(0xffffffffu, n0, 0);
+    end = __shfl_sync(0xffffffffu, end, 0);
     if (end > n0) {
       const int blk = n0 >> c.shift, e0 = n0 - (blk << c.shift);
       const int id = cache_block(c, pair, blk);
@@ -488,6 +495,7 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
   constexpr int NW = NT / 32;
   __shared__ uint2 s_cnt[2][NW];
   __shared__ int s_pre[R * NW];
+  __shared__ int s_tok;
   tc::grid_dep_wait();
   const int mb = c.max_blocks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pair = blockIdx.x;
@@ -500,7 +508,9 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
     id[r] = i < mb ? c.table[row + i] : 0;
     w[r] = i < mb ? c.weight[row + i] : 0.f;
   }
-  const int tok = cache_tokens(c, pair);
+  if (tid == 0) s_tok = cache_tokens(c, pair);
+  __syncthreads();
+  const int tok = s_tok;
   const int B = 1 << c.shift, n = (tok + B - 1) >> c.shift;
   const int nk = min(n, keep);
   const int rows = (n + NT - 1) / NT;   // registers in use: the same for every thread

@@ -91,8 +91,6 @@ __device__ __forceinline__ int share_owner(int x, int n, int T) {
 
 // Total of the tile counts, and the pair and tile at which this CTA's share
 // begins (s_where = {pair, tile in the pair, total}).  Every thread calls it.
-// The CTA that holds a pair's first tile also writes the pair's first tile
-// index for the merge (share_note).
 template <int NT>
 __device__ __forceinline__ void share_find(const AttendArgs& a, int cta, int ncta, int* s_where, int* s_scan) {
   const int tid = threadIdx.x, P = a.c.pairs;
@@ -100,6 +98,7 @@ __device__ __forceinline__ void share_find(const AttendArgs& a, int cta, int nct
   const int p0 = min(P, tid * per), p1 = min(P, p0 + per);
   int sum = 0;
   for (int p = p0; p < p1; ++p) sum += tiles_of(a.c, p);
+  if (tid < 2) s_where[tid] = 0;
   int T;
   int before = block_exclusive_scan(sum, s_scan, &T);
   if (tid == 0) s_where[2] = T;
@@ -109,7 +108,7 @@ __device__ __forceinline__ void share_find(const AttendArgs& a, int cta, int nct
     const int t0 = share_begin(cta, n, T);
     if (before <= t0 && t0 < before + sum) {
       int p = p0, b = before;
-      for (;; ++p) {
+      for (; p < p1 - 1; ++p) {
         const int k = tiles_of(a.c, p);
         if (t0 < b + k) break;
         b += k;
@@ -177,6 +176,9 @@ __device__ __forceinline__ float redux_max(float x) {
   return r;
 }
 
+// of a tile in its stage, beside its tokens (at most kCaT)
+enum : int { kFirst = 256, kLast = 512, kEnd = 1024 };
+
 // A CTA's tiles in order: `left` tiles from tile `tile` of pair `pair`.
 struct TileCursor {
   int pair, tile, left, ntok, nt;
@@ -199,7 +201,6 @@ struct TileCursor {
     } while (nt == 0);
     return true;
   }
-  __device__ __forceinline__ int run() const { return min(nt - tile, left); }   // tiles left in this pair
 };
 
 template <typename T, int D, int G>
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
   float* red = reinterpret_cast<float*>(misc + 256);    // [2][4][G] maxima, [4][G] sums
   int* s_scan = reinterpret_cast<int*>(misc + 512);     // [32], before the sums are used
   float* ssc = reinterpret_cast<float*>(misc + 672);    // [NST][20]: K scales, V factors, V reference
+  int* sinfo = reinterpret_cast<int*>(misc + 1248);     // [NST][4]: the stage's tile (below)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   tc::grid_dep_launch();
 
@@ -267,19 +269,23 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
 
   if (ntile > 0 && warp == 4) {
     // ------------------------------------------------------------ copies
+    // This warp alone walks the pairs; what the others need to know of a
+    // tile lies in its stage: pair, tile, the tile's tokens and kFirst, kLast
+    // (of the CTA's tiles of that pair), kEnd and, above them, the next tile's pair.
     // lane = block of the tile; block ids are loaded two tiles ahead, the
     // blocks' scales one ahead.  The codes are read once: evicted first from
     // L2 (without: 338 us instead of 322 at batch 8, 128K)
     TileCursor cur, nx1, nx2;
     cur.begin(a.c, s_where[0], s_where[1], ntile);
-    auto blocks = [&](const TileCursor& c) { return c.left > 0 ? (min(kCaT, c.ntok - c.tile * kCaT) + B - 1) >> shift : 0; };
+    auto tokens = [&](const TileCursor& c) { return c.left > 0 ? max(0, min(kCaT, c.ntok - c.tile * kCaT)) : 0; };
+    auto blocks = [&](const TileCursor& c) { return (tokens(c) + B - 1) >> shift; };
     auto id_of = [&](const TileCursor& c) {
       return lane < blocks(c) ? cache_block(a.c, c.pair, ((c.tile * kCaT) >> shift) + lane) : 0;
     };
     const uint64_t once = tc::l2_evict_first_policy();
     int id = id_of(cur), id1 = 0;
     float ks = 0.f, vs = 0.f;
-    int it = 0;
+    int it = 0, before = -1;   // before: the previous tile's pair
     for (;; ++it) {
       const int st = it % NST, use = it / NST;
       bool ok = true;
@@ -318,7 +324,16 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
         sc[lane] = ks;
         sc[8 + lane] = vref > 0.f ? vs / vref * 256.f : vs == vs ? 0.f : vs;
       }
-      if (lane == 0) sc[16] = vref * (1.f / 256.f);
+      if (lane == 0) {
+        sc[16] = vref * (1.f / 256.f);
+        const bool end = nx1.left <= 0;
+        reinterpret_cast<int4*>(sinfo)[st] =
+            make_int4(cur.pair, cur.tile, tokens(cur) | (cur.pair != before ? kFirst : 0) |
+                                              (end || nx1.pair != cur.pair ? kLast : 0) | (end ? kEnd : 0),
+                      nx1.pair);
+        if (cur.tile == 0) a.w.first[cur.pair] = t0 + it;
+      }
+      before = cur.pair;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&full[st]);
       if (nx1.left <= 0) { ++it; break; }
@@ -336,8 +351,6 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
   } else if (ntile > 0 && warp == 5) {
     // ------------------------------------------------------------ tensor core
     if (lane == 0) {
-      TileCursor cur;
-      cur.begin(a.c, s_where[0], s_where[1], ntile);
       const uint32_t tS = tmem, tO = tmem + 2 * N1;
       // S(i) needs its K, its pair's q, and the softmax to be done with S(i - 2)
       // (P(i - 2) is there); O(j) needs P(j).  Whichever is ready goes, O
@@ -360,8 +373,15 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
           ++j;
           did = true;
         }
-        if (more && j >= i - 1 && tc::mbar_test(&full[i % NST], (i / NST) & 1) &&
-            tc::mbar_test(&qfull[runs & 1], (runs >> 1) & 1)) {
+        int flags = 0, turn = runs;
+        bool go = more && j >= i - 1 && tc::mbar_test(&full[i % NST], (i / NST) & 1);
+        if (go) {
+          flags = sinfo[(i % NST) * 4 + 2];
+          if (i > 0 && (flags & kFirst)) ++turn;
+          go = tc::mbar_test(&qfull[turn & 1], (turn >> 1) & 1);
+        }
+        if (go) {
+          runs = turn;
           tc::fence_after();
           const uint32_t k0 = tc::smem_u32(stages + (i % NST) * C::Stage), q0 = tc::smem_u32(qbuf + (runs & 1) * C::QB);
 #pragma unroll
@@ -370,8 +390,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
                      tc::desc_k_none(q0 + k * (2 * N1 * 16), N1 * 16, 128), idesc_e4m3(N1), k > 0);
           tc::mma_commit(&sfull[i & 1]);
           ++i;
-          if (cur.next(a.c)) ++runs;
-          more = cur.left > 0;
+          more = !(flags & kEnd);
           did = true;
         }
         if (did) t_last = tc::globaltimer_ns();
@@ -384,8 +403,6 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
     __syncwarp();
   } else if (ntile > 0) {
     // ------------------------------------------------------------ softmax
-    TileCursor cur;
-    cur.begin(a.c, s_where[0], s_where[1], ntile);
     const uint32_t tS = tmem + (static_cast<uint32_t>(warp) << 21), tO = tS + 2 * N1;
     const int gran = min(B, 32);
     bool ok = true;
@@ -427,156 +444,148 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       if (lane == 0) tc::mbar_arrive(&qfull[turn & 1]);
       ok = tc::named_sync_and(1, kCaSoft, ok);
     };
-    lay_q(cur.pair, 0);
-    int it = 0, at = t0, turn = 0;
-    while (cur.left > 0 && ok) {
-      const int pair = cur.pair, ntok = cur.ntok, nrun = cur.run();
-      if (cur.tile == 0 && tid == 0) a.w.first[pair] = at;
-      // running maximum, sum and output of the run; p is relative to its own
-      // tile's maximum, whatever larger one came before (a token with most of
-      // the weight and little value must not push the others' terms out)
-      float m[G], l[G], acc[G], al[G], be[G];
+    lay_q(s_where[0], 0);
+    int turn = 0;
+    // running maximum, sum and output of the pair's run; p is relative to its own
+    // tile's maximum, whatever larger one came before (a token with most of
+    // the weight and little value must not push the others' terms out)
+    float m[G], l[G], acc[G], al[G], be[G];
+    // adds tile j's O to the run's sums
+    auto take_o = [&](int j) {
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&ofull[j & 1], (j >> 1) & 1, kWaitLimit));
+      if (!ok) return;
+      tc::fence_after();
+      float o[N2];
+#pragma unroll
+      for (int c = 0; c < N2; c += 16) tc::tmem_ld16(tO + (j & 1) * N2 + c, o + c);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        m[g] = -INFINITY;
-        l[g] = acc[g] = al[g] = be[g] = 0.f;
+        float x = o[(C::PP - 1) * G + g];
+#pragma unroll
+        for (int i = C::PP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, o[i * G + g]);
+        acc[g] = fmaf(acc[g], al[g], x * be[g]);
       }
-      // adds tile j's O to the run's sums
-      auto take_o = [&](int j) {
-        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&ofull[j & 1], (j >> 1) & 1, kWaitLimit));
-        if (!ok) return;
+    };
+    // (a wait that gave up shows at the next barrier, so that all 128 threads
+    // leave together)
+    for (int it = 0;; ++it) {
+      const int st = it % NST;
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&full[st], (it / NST) & 1, kWaitLimit) &&
+                                       tc::mbar_wait(&sfull[it & 1], (it >> 1) & 1, kWaitLimit));
+      const int4 info = reinterpret_cast<const int4*>(sinfo)[st];
+      const int pair = info.x, t = info.y, cnt = info.z & 255, flags = info.z;
+      if (flags & kFirst) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          m[g] = -INFINITY;
+          l[g] = acc[g] = al[g] = be[g] = 0.f;
+        }
+      }
+      float s[G];
+      const float* sc = ssc + st * 20;
+      const int blk = tid >> shift;
+      if (ok) {
         tc::fence_after();
-        float o[N2];
+        float v[N1];
 #pragma unroll
-        for (int c = 0; c < N2; c += 16) tc::tmem_ld16(tO + (j & 1) * N2 + c, o + c);
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float x = o[(C::PP - 1) * G + g];
-#pragma unroll
-          for (int i = C::PP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, o[i * G + g]);
-          acc[g] = fmaf(acc[g], al[g], x * be[g]);
-        }
-      };
-      TileCursor after;
-      for (int r = 0; r < nrun; ++r, ++it) {
-        const int t = cur.tile + r, st = it % NST, cnt = min(kCaT, ntok - t * kCaT);
-        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&full[st], (it / NST) & 1, kWaitLimit) &&
-                                         tc::mbar_wait(&sfull[it & 1], (it >> 1) & 1, kWaitLimit));
-        float s[G];
-        const float* sc = ssc + st * 20;
-        const int blk = tid >> shift;
-        if (ok) {
-          tc::fence_after();
-          float v[N1];
-#pragma unroll
-          for (int c = 0; c < N1; c += 16) tc::tmem_ld16(tS + (it & 1) * N1 + c, v + c);
-          const float ks = sc[blk];
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            float x = v[(C::QP - 1) * G + g];
-#pragma unroll
-            for (int i = C::QP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, v[i * G + g]);
-            s[g] = tid < cnt ? x * (sqs[(turn & 1) * 8 + g] * ks) : -INFINITY;
-          }
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const float x = redux_max(s[g]);
-            if (lane == 0) red[(it & 1) * 32 + warp * G + g] = x;
-          }
-        }
-        ok = tc::named_sync_and(1, kCaSoft, ok);
-        if (!ok) break;
-        float al_new[G], be_new[G];
-        unsigned char* pb = pbuf + (it & 1) * C::PB + (tid >> 4) * (N2 * 16) + (tid & 15);
-        const float vf = tid < cnt ? sc[8 + blk] : 0.f, vref = sc[16];
-        float p[G];
+        for (int c = 0; c < N1; c += 16) tc::tmem_ld16(tS + (it & 1) * N1 + c, v + c);
+        const float ks = sc[blk];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const float* rd = red + (it & 1) * 32 + g;
-          const float mt = fmaxf(fmaxf(rd[0], rd[G]), fmaxf(rd[2 * G], rd[3 * G]));
-          const float tref = mt == -INFINITY ? 0.f : mt, mn = fmaxf(mt, m[g]), ref = mn == -INFINITY ? 0.f : mn;
-          al_new[g] = ex2(m[g] - ref);
-          be_new[g] = ex2(mt - ref);
-          m[g] = mn;
-          p[g] = ex2(s[g] - tref);
-          l[g] = fmaf(l[g], al_new[g], p[g] * be_new[g]);
-          be_new[g] *= vref;
-          if (a.gather && tid == 0) a.w.tmax[(static_cast<size_t>(pair) * a.w.tiles + t) * G + g] = tref;
+          float x = v[(C::QP - 1) * G + g];
+#pragma unroll
+          for (int i = C::QP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, v[i * G + g]);
+          s[g] = tid < cnt ? x * (sqs[(turn & 1) * 8 + g] * ks) : -INFINITY;
         }
-        if (a.gather) {
-          float z[G];
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            z[g] = p[g];
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) z[g] += __shfl_xor_sync(0xffffffffu, z[g], o);
-            if (gran == 32) z[g] += __shfl_xor_sync(0xffffffffu, z[g], 16);
-          }
-          if ((lane & (gran - 1)) == 0) {
-            float* dst = a.w.psum + (static_cast<size_t>(pair) * a.w.granules + (t * kCaT + tid) / gran) * G;
-#pragma unroll
-            for (int g = 0; g < G; ++g) dst[g] = z[g];
-          }
-        }
-        // p's terms, times the token's V scale; rows term G + head
-#pragma unroll
-        for (int g = 0; g < G; g += 2) {
-          float u = p[g] * vf, v = G > 1 ? p[g + (G > 1)] * vf : 0.f;
-#pragma unroll
-          for (int i = 0; i < C::PP; ++i) {
-            const uint32_t c2 = e4m3_pack2(u, v);
-            pb[(i * G + g) * 16] = static_cast<unsigned char>(c2);
-            if (G > 1) pb[(i * G + g + 1) * 16] = static_cast<unsigned char>(c2 >> 8);
-            const float2 f = e4m3_unpack2(c2);
-            u = (u - f.x) * 16.f;
-            v = (v - f.y) * 16.f;
-          }
-        }
-        // V past the tokens may be any bytes, NaN too: zero under zero weights
-        if (cnt < kCaT && tid < D) {
-          unsigned char* vb = stages + st * C::Stage + C::KB + tid * 16;
-          for (int u = cnt >> 4; u < kCaT / 16; ++u) {
-            uint4* w = reinterpret_cast<uint4*>(vb + u * (D * 16));
-            const int keep = cnt - u * 16;   // bytes kept, if any
-            if (keep <= 0) {
-              *w = make_uint4(0, 0, 0, 0);
-            } else {
-              uint4 x = *w;
-              uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int kb = keep - 4 * e;
-                xw[e] = kb >= 4 ? xw[e] : kb <= 0 ? 0u : xw[e] & ((1u << (8 * kb)) - 1u);
-              }
-              *w = x;
-            }
-          }
-        }
-        tc::fence_proxy_async_smem();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&pfull[it & 1]);
-        if (r == 0) {
-          // the next pair's q, so that its S can start while this one ends
-          // (the buffer's last reader was the S of the pair before)
-          after = cur;
-          after.tile += nrun - 1;
-          after.left -= nrun - 1;
-          after.next(a.c);
-          if (after.left > 0) lay_q(after.pair, turn + 1);
-        }
-        if (r > 0) take_o(it - 1);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          al[g] = al_new[g];
-          be[g] = be_new[g];
+          const float x = redux_max(s[g]);
+          if (lane == 0) red[(it & 1) * 32 + warp * G + g] = x;
         }
       }
+      ok = tc::named_sync_and(1, kCaSoft, ok);
       if (!ok) break;
-      cur = after;
-      at += nrun;
-      ++turn;
-      take_o(it - 1);
+      float al_new[G], be_new[G];
+      unsigned char* pb = pbuf + (it & 1) * C::PB + (tid >> 4) * (N2 * 16) + (tid & 15);
+      const float vf = tid < cnt ? sc[8 + blk] : 0.f, vref = sc[16];
+      float p[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float* rd = red + (it & 1) * 32 + g;
+        const float mt = fmaxf(fmaxf(rd[0], rd[G]), fmaxf(rd[2 * G], rd[3 * G]));
+        const float tref = mt == -INFINITY ? 0.f : mt, mn = fmaxf(mt, m[g]), ref = mn == -INFINITY ? 0.f : mn;
+        al_new[g] = ex2(m[g] - ref);
+        be_new[g] = ex2(mt - ref);
+        m[g] = mn;
+        p[g] = ex2(s[g] - tref);
+        l[g] = fmaf(l[g], al_new[g], p[g] * be_new[g]);
+        be_new[g] *= vref;
+        if (a.gather && tid == 0) a.w.tmax[(static_cast<size_t>(pair) * a.w.tiles + t) * G + g] = tref;
+      }
+      if (a.gather) {
+        float z[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          z[g] = p[g];
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) z[g] += __shfl_xor_sync(0xffffffffu, z[g], o);
+          if (gran == 32) z[g] += __shfl_xor_sync(0xffffffffu, z[g], 16);
+        }
+        if ((lane & (gran - 1)) == 0) {
+          float* dst = a.w.psum + (static_cast<size_t>(pair) * a.w.granules + (t * kCaT + tid) / gran) * G;
+#pragma unroll
+          for (int g = 0; g < G; ++g) dst[g] = z[g];
+        }
+      }
+      // p's terms, times the token's V scale; rows term G + head
+#pragma unroll
+      for (int g = 0; g < G; g += 2) {
+        float u = p[g] * vf, v = G > 1 ? p[g + (G > 1)] * vf : 0.f;
+#pragma unroll
+        for (int i = 0; i < C::PP; ++i) {
+          const uint32_t c2 = e4m3_pack2(u, v);
+          pb[(i * G + g) * 16] = static_cast<unsigned char>(c2);
+          if (G > 1) pb[(i * G + g + 1) * 16] = static_cast<unsigned char>(c2 >> 8);
+          const float2 f = e4m3_unpack2(c2);
+          u = (u - f.x) * 16.f;
+          v = (v - f.y) * 16.f;
+        }
+      }
+      // V past the tokens may be any bytes, NaN too: zero under zero weights
+      if (cnt < kCaT && tid < D) {
+        unsigned char* vb = stages + st * C::Stage + C::KB + tid * 16;
+        for (int u = cnt >> 4; u < kCaT / 16; ++u) {
+          uint4* w = reinterpret_cast<uint4*>(vb + u * (D * 16));
+          const int keep = cnt - u * 16;   // bytes kept, if any
+          if (keep <= 0) {
+            *w = make_uint4(0, 0, 0, 0);
+          } else {
+            uint4 x = *w;
+            uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int kb = keep - 4 * e;
+              xw[e] = kb >= 4 ? xw[e] : kb <= 0 ? 0u : xw[e] & ((1u << (8 * kb)) - 1u);
+            }
+            *w = x;
+          }
+        }
+      }
+      tc::fence_proxy_async_smem();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&pfull[it & 1]);
+      // the next pair's q, so that its S can start while this pair ends (the
+      // buffer's last reader was the S of the pair before)
+      if ((flags & (kLast | kEnd)) == kLast) lay_q(info.w, turn + 1);
+      if (!(flags & kFirst)) take_o(it - 1);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        al[g] = al_new[g];
+        be[g] = be_new[g];
+      }
+      if (!(flags & kLast)) continue;
+      take_o(it);
       tc::fence_before();
       // the partial of (this CTA, pair)
       float* part = a.w.part + static_cast<size_t>(cta + pair) * G * (D + 2);
@@ -595,6 +604,8 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
         part[tid * (D + 2) + D] = mm;
         part[tid * (D + 2) + D + 1] = rd[0] + rd[G] + rd[2 * G] + rd[3 * G];
       }
+      ++turn;
+      if (!ok || (flags & kEnd)) break;
     }
     if (!ok && tid == 0) abort_now();
   }
@@ -642,7 +653,7 @@ k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int nchunk) {
   const int total = a.w.first[P], f = a.w.first[pair];   // (f is not written for a pair without tokens)
   const int ntok = cache_tokens(a.c, pair), nt = (ntok + kCaT - 1) / kCaT;
   const int seq = pair / a.c.h_kv, kvh = pair - seq * a.c.h_kv;
-  if (nt == 0) {
+  if (nt == 0 || total <= 0) {
     if (head_role) {
       const int h = kvh * G + bx % G;
       if (tid < D) static_cast<T*>(a.out)[seq * a.ob + h * a.oh + tid] = Ty<T>::from_f(0.f);
@@ -651,7 +662,9 @@ k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int nchunk) {
     return;
   }
   const int n = min(ncta, total);
-  const int c0 = share_owner(f, n, total), c1 = share_owner(f + nt - 1, n, total);
+  // (the bounds hold anyway unless the counts changed since the first launch)
+  const int f0 = min(max(f, 0), total - 1);
+  const int c0 = share_owner(f0, n, total), c1 = share_owner(min(f0 + nt, total) - 1, n, total);
   const int g_out = bx % G, j = tid % D, sl = tid / D;
   const float* rows = a.w.part + (static_cast<size_t>(c0 + pair) * G + g_out) * (D + 2);   // partial c0 + u: + u G (D + 2)
   float pre[Pre], pm[Pre];
