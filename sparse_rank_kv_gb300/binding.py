@@ -342,23 +342,23 @@ def _step_calls():
 
 def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> bytes:
     """A b x h x s x d (or b x h x d) tensor as strided rows (a packed Rows)."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {tuple(shape)} on "
-                         f"{device} (shape, type and device)")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        st = t.stride()
+        if st[-1] == 1 or shape[-1] <= 1:
+            return _PACK_ROWS(t.data_ptr(), st[0], st[1], st[2] if len(st) == 4 else 0)
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _PACK_ROWS(t.data_ptr(), st[0], st[1], st[2] if len(st) == 4 else 0)
+    raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {tuple(shape)} on "
+                     f"{device} (shape, type and device)")
 
 
 def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, device):
     """Data pointer of a contiguous tensor of a given shape, or None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -368,17 +368,21 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return dt
 
 
-def _call(fn, device, stream, *args) -> None:
-    """fn(*args, cudaStream_t) with the tensors' device current; stream None:
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(fn, t, stream, *args) -> None:
+    """fn(*args, cudaStream_t) with tensor t's device current; stream None:
     torch's current stream of that device."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {device}")
-    i = device.index
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    i = t.get_device()
     if stream is None:
-        st = torch._C._cuda_getCurrentRawStream(i)
+        st = _current_stream(i)
     else:
         st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if i == torch._C._cuda_getDevice():
+    if i == _current_device():
         rc = fn(*args, st)
     else:
         with torch.cuda.device(i):
@@ -405,24 +409,35 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight:
         raise ValueError("q and k must be (b, h, s, d)")
     (b, _, s, d), dev, dtype = x.shape, x.device, x.dtype
     dt = _dtype(x, "q" if q is not None else "k")
-    heads, rows, outs, ws = [0, 0], [None, None], [None, None], [None, None]
-    made = [q_out, k_out]
-    for i, (name, t, w) in enumerate((("q", q, q_weight), ("k", k, k_weight))):
-        if t is None:
-            if w is not None or made[i] is not None:
-                raise ValueError(f"{name} is None, its weight or output is not")
-            continue
-        heads[i] = t.shape[1]
-        shape = (b, heads[i], s, d)
-        if made[i] is None:
-            made[i] = torch.empty(shape, dtype=dtype, device=dev)
-        rows[i], outs[i] = _rows(t, name, shape, dtype, dev), _rows(made[i], name + "_out", shape, dtype, dev)
-        ws[i] = _dense(w, name + "_weight", (d,), dtype, dev)
-    per_token = pos is not None and pos.dim() == 2
-    pp = _dense(pos, "pos", (b, s) if per_token else (b,), torch.int32, dev)
-    p = _PACK_NORM_ROPE(b, s, heads[0], heads[1], d, d if rot is None else rot, dt, norm, per_token, eps, theta)
-    _call(_step_calls()["qk_norm_rope"], dev, stream, p, rows[0], rows[1], ws[0], ws[1], pp, outs[0], outs[1])
-    return made[0], made[1]
+    hq = hk = 0
+    rq = rk = oq = ok = wq = wk = None
+    if q is not None:
+        shape = q.shape
+        hq = shape[1]
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=dtype, device=dev)
+        rq, oq = _rows(q, "q", shape, dtype, dev), _rows(q_out, "q_out", shape, dtype, dev)
+        if q_weight is not None:
+            wq = _dense(q_weight, "q_weight", (d,), dtype, dev)
+    elif q_weight is not None or q_out is not None:
+        raise ValueError("q is None, its weight or output is not")
+    if k is not None:
+        hk = k.shape[1]
+        shape = (b, hk, s, d)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=dev)
+        rk, ok = _rows(k, "k", shape, dtype, dev), _rows(k_out, "k_out", shape, dtype, dev)
+        if k_weight is not None:
+            wk = _dense(k_weight, "k_weight", (d,), dtype, dev)
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k is None, its weight or output is not")
+    per_token, pp = False, None
+    if pos is not None:
+        per_token = pos.dim() == 2
+        pp = _dense(pos, "pos", (b, s) if per_token else (b,), torch.int32, dev)
+    p = _PACK_NORM_ROPE(b, s, hq, hk, d, d if rot is None else rot, dt, norm, per_token, eps, theta)
+    _call((_step or _step_calls())["qk_norm_rope"], x, stream, p, rq, rk, wq, wk, pp, oq, ok)
+    return q_out, k_out
 
 
 class BlockCache:
@@ -492,7 +507,7 @@ class BlockCache:
         shape = (self.b, self.h_kv, s, self.d)
         rk, rv = _rows(k, "k", shape, k.dtype, self.device), _rows(v, "v", shape, k.dtype, self.device)
         lp = _dense(lens, "lens", (self.b,), torch.int32, self.device)
-        _call(_step_calls()["cache_append"], self.device, stream, self._desc, dt, rk, rv, s, lp)
+        _call((_step or _step_calls())["cache_append"], self.n_tok, stream, self._desc, dt, rk, rv, s, lp)
 
     def attend(self, q: torch.Tensor, *, scale: Optional[float] = None, decay: Optional[float] = None,
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -504,35 +519,38 @@ class BlockCache:
         graphs share none."""
         if q.dim() != 3:
             raise ValueError("q must be (b, h_q, d)")
-        dev, hq = self.device, q.shape[1]
+        dev, hq, dtype = self.device, q.shape[1], q.dtype
         dt = _dtype(q, "q")
         shape = (self.b, hq, self.d)
-        rq = _rows(q, "q", shape, q.dtype, dev)
-        lp = _dense(lse, "lse", (self.b, hq), torch.float32, dev)
+        rq = _rows(q, "q", shape, dtype, dev)
+        lp = None if lse is None else _dense(lse, "lse", (self.b, hq), torch.float32, dev)
+        if dev.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {dev}")
         if stream is not None:
             # the output and the workspace are allocated on the stream that uses them
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), dev)
             with torch.cuda.stream(s):
                 return self.attend(q, scale=scale, decay=decay, out=out, lse=lse)
-        if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=dev)
-        ro = _rows(out, "out", shape, q.dtype, dev)
-        if dev.type == "cuda" and torch._C._cuda_getDevice() != dev.index:
+        i = dev.index
+        if _current_device() != i:
             with torch.cuda.device(dev):
                 return self.attend(q, scale=scale, decay=decay, out=out, lse=lse)
-        work, ptr, nb = self._workspace(hq)
-        _call(_step_calls()["cache_attend"], dev, None, self._desc, dt, hq, rq,
-              self.d ** -0.5 if scale is None else scale, decay is not None, 0.0 if decay is None else decay,
-              ro, lp, ptr, nb)
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        ro = _rows(out, "out", shape, dtype, dev)
+        st = _current_stream(i)
+        _, ptr, nb = self._workspace(hq, st)
+        rc = (_step or _step_calls())["cache_attend"](
+            self._desc, dt, hq, rq, self.d ** -0.5 if scale is None else scale, decay is not None,
+            0.0 if decay is None else decay, ro, lp, ptr, nb, st)
+        if rc:
+            _check(rc)
         return out
 
-    def _workspace(self, hq: int):
-        """(tensor, pointer, bytes) of attend's workspace on the current stream."""
-        if self.device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, got {self.device}")
+    def _workspace(self, hq: int, st: int):
+        """(tensor, pointer, bytes) of attend's workspace on the current stream st."""
         capturing = torch._C._cuda_isCurrentStreamCapturing()
-        key = (hq, torch._C._cuda_getCurrentRawStream(self.device.index))
-        have = None if capturing else self._work.get(key)
+        have = None if capturing else self._work.get((hq, st))
         if have is None:
             nb = lib().shadowkv_cache_attend_workspace(self._desc, hq)
             if nb == 0:
@@ -542,7 +560,7 @@ class BlockCache:
             if not capturing:
                 if len(self._work) >= 8:
                     self._work.pop(next(iter(self._work)))
-                self._work[key] = have
+                self._work[(hq, st)] = have
         return have
 
     def evict(self, keep: int, *, sink: int = 0, recent: int = 1, into: Optional["BlockCache"] = None,
@@ -555,7 +573,7 @@ class BlockCache:
         dst = None if into is None else into._desc
         if into is not None and into.device != self.device:
             raise ValueError(f"into is on {into.device}, expected {self.device}")
-        _call(_step_calls()["cache_evict"], self.device, stream, self._desc, dst, keep, sink, recent, kp)
+        _call((_step or _step_calls())["cache_evict"], self.n_tok, stream, self._desc, dst, keep, sink, recent, kp)
 
     def reset(self) -> None:
         """Drops every token (on torch's current stream)."""
