@@ -7,7 +7,7 @@
 // 128K (2.15 GB) 314 us, 6.8 TB/s; batch 1 at 128K 48 us (40 at that rate); 16
 // ragged sequences of up to 9001 tokens (163 MB) 38.5 us (24 at that rate: a
 // few CTAs' copies come at half the speed of the others', and the shares are
-// fixed beforehand); 90 tokens 7.6 us, all latency.  The CUDA-core form of the
+// fixed beforehand); 90 tokens 5.4 us, all latency.  The CUDA-core form of the
 // same split took 8.0 ms at batch 8, 128K.
 //
 // Every pair's tokens are cut into 128-token tiles; the tiles of all pairs, in
@@ -27,9 +27,20 @@ namespace skv {
 
 constexpr int kCaT = 128;         // tokens per tile
 
+// Small caches: one CTA works a pair's tiles off and finishes it, without the
+// prefix sums, the partials and the second launch.  Measured, device time of
+// the split form and of this one: 8 pairs of 2 tiles 7.8 and 5.4 us, of 4 tiles
+// 7.8 and 8.2 (3 us of host time less), of 8 tiles 8.1 and 12.0; 256 pairs of
+// 4 tiles 15.9 and 9.5, of 8 tiles 19.4 and 14.0; 384 pairs of 16 tiles 40 and 44.
+inline bool attend_solo(const shadowkv_cache& c, int nsm) {
+  const long long tiles = (static_cast<long long>(c.max_blocks) * c.block + kCaT - 1) / kCaT;
+  return tiles <= 4 || (tiles <= 8 && static_cast<long long>(c.b) * c.h_kv >= nsm);
+}
+
 // Workspace, in order: per pair the index of its first tile, the total tile
 // count, the CTAs' partials, and for the weights every tile's reference
-// maximum and the sums of p over granules of min(block, 32) tokens.
+// maximum and the sums of p over granules of min(block, 32) tokens.  (The
+// form without a second launch uses the last two alone.)
 struct AttendWork {
   int* first;      // [pairs] then the total
   float* part;     // [ctas + pairs][G][d + 2]
@@ -74,6 +85,7 @@ struct AttendArgs {
   float scale_log2;   // scale log2(e)
   float decay;
   int gather;
+  int solo;           // one CTA per pair, which finishes it: no second launch
 };
 
 __device__ __forceinline__ int tiles_of(const CacheDev& c, int pair) {
@@ -120,6 +132,53 @@ __device__ __forceinline__ void share_find(const AttendArgs& a, int cta, int nct
   __syncthreads();
 }
 
+// 2^x by the special function unit (2^-22 relative); results below 2^-126 are 0
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// G adjacent floats (16-byte aligned where G >= 4).
+template <int G>
+__device__ __forceinline__ void load_heads(const float* p, float* o) {
+  if constexpr (G >= 4) {
+#pragma unroll
+    for (int e = 0; e < G; e += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + e);
+      o[e] = v.x; o[e + 1] = v.y; o[e + 2] = v.z; o[e + 3] = v.w;
+    }
+  } else if constexpr (G == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    o[0] = v.x; o[1] = v.y;
+  } else {
+    o[0] = *p;
+  }
+}
+
+// Weight of a pair's block i from its granules' sums of p, its tile's
+// references and the heads' maxima M and sums L; stored with the decayed old one.
+template <int G>
+__device__ __forceinline__ void store_weight(const AttendArgs& a, int pair, int i, const float* M, const float* L) {
+  const int B = 1 << a.c.shift, gran = min(B, 32);
+  const int tile = i * B / kCaT, ng = B / gran;   // one granule, or 2 or 4 of 32 tokens
+  const float* ps = a.w.psum + (static_cast<size_t>(pair) * a.w.granules + static_cast<size_t>(i) * ng) * G;
+  float z[4][G], t[G], w = 0.f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u < ng) load_heads<G>(ps + u * G, z[u]);
+  load_heads<G>(a.w.tmax + (static_cast<size_t>(pair) * a.w.tiles + tile) * G, t);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    float sum = z[0][g];
+#pragma unroll
+    for (int u = 1; u < 4; ++u) sum += u < ng ? z[u][g] : 0.f;
+    w += sum * ex2(t[g] - M[g]) / L[g];
+  }
+  float* dst = a.c.weight + static_cast<size_t>(pair) * a.c.max_blocks + i;
+  *dst = a.decay == 0.f ? w : fmaf(a.decay, *dst, w);
+}
+__device__ __forceinline__ float natural_lse(float M, float L) { return (M + log2f(L)) * 0.6931471805599453f; }
+
 // ------------------------------------------------------------ tensor cores
 // The codes go to the tensor core as they are (tcgen05 kind::f8f6f4, one
 // K-major tile per 128 tokens, straight from bulk copies of whole blocks):
@@ -163,12 +222,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
 // kind::f8f6f4, e4m3 A and B (format 0), fp32 D, both K-major, M = 128
 constexpr uint32_t idesc_e4m3(int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
-}
-// 2^x by the special function unit (2^-22 relative); results below 2^-126 are 0
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
 }
 __device__ __forceinline__ float redux_max(float x) {
   float r;
@@ -228,7 +281,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
   float* ssc = reinterpret_cast<float*>(misc + 672);    // [NST][20]: K scales, V factors, V reference
   int* sinfo = reinterpret_cast<int*>(misc + 1248);     // [NST][4]: the stage's tile (below)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  tc::grid_dep_launch();
+  if (!a.solo) tc::grid_dep_launch();   // (a call's last kernel lets nothing start early)
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -258,9 +311,23 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
   const int cta = blockIdx.x;
-  share_find<kCaThreads>(a, cta, gridDim.x, s_where, s_scan);
-  const int total = s_where[2], n = min(static_cast<int>(gridDim.x), total);
-  const int t0 = cta < n ? share_begin(cta, n, total) : 0, ntile = cta < n ? share_begin(cta + 1, n, total) - t0 : 0;
+  int t0 = 0, ntile = 0;
+  if (a.solo) {
+    if (tid == 0) {
+      s_where[0] = cta;
+      s_where[1] = 0;
+      s_where[2] = tiles_of(a.c, cta);
+    }
+    __syncthreads();
+    ntile = s_where[2];
+  } else {
+    share_find<kCaThreads>(a, cta, gridDim.x, s_where, s_scan);
+    const int total = s_where[2], n = min(static_cast<int>(gridDim.x), total);
+    if (cta < n) {
+      t0 = share_begin(cta, n, total);
+      ntile = share_begin(cta + 1, n, total) - t0;
+    }
+  }
   const int shift = a.c.shift, B = 1 << shift;
   auto abort_now = [&]() {
     *s_abort = 1;
@@ -331,7 +398,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
             make_int4(cur.pair, cur.tile, tokens(cur) | (cur.pair != before ? kFirst : 0) |
                                               (end || nx1.pair != cur.pair ? kLast : 0) | (end ? kEnd : 0),
                       nx1.pair);
-        if (cur.tile == 0) a.w.first[cur.pair] = t0 + it;
+        if (cur.tile == 0 && !a.solo) a.w.first[cur.pair] = t0 + it;
       }
       before = cur.pair;
       __syncwarp();
@@ -587,14 +654,32 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       if (!(flags & kLast)) continue;
       take_o(it);
       tc::fence_before();
-      // the partial of (this CTA, pair)
-      float* part = a.w.part + static_cast<size_t>(cta + pair) * G * (D + 2);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const float z = warp_sum(l[g]);
         if (lane == 0) red[64 + warp * G + g] = z;
-        if (tid < D) part[g * (D + 2) + tid] = acc[g];
       }
+      if (a.solo) {
+        ok = tc::named_sync_and(1, kCaSoft, ok);
+        if (!ok) break;
+        const int seq = pair / a.c.h_kv, h0 = (pair - seq * a.c.h_kv) * G;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float* rd = red + 64 + g;
+          l[g] = rd[0] + rd[G] + rd[2 * G] + rd[3 * G];
+          m[g] = m[g] == -INFINITY ? 0.f : m[g];
+          if (tid < D) static_cast<T*>(a.out)[seq * a.ob + (h0 + g) * a.oh + tid] = Ty<T>::from_f(acc[g] / l[g]);
+          if (a.lse && tid == g) a.lse[static_cast<size_t>(seq) * a.c.h_kv * G + h0 + g] = natural_lse(m[g], l[g]);
+        }
+        if (a.gather)   // (the barrier stands between the sums' stores and these loads)
+          for (int i = tid; i < (t * kCaT + cnt + B - 1) >> shift; i += kCaSoft) store_weight<G>(a, pair, i, m, l);
+        break;
+      }
+      // the partial of (this CTA, pair)
+      float* part = a.w.part + static_cast<size_t>(cta + pair) * G * (D + 2);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (tid < D) part[g * (D + 2) + tid] = acc[g];
       ok = tc::named_sync_and(1, kCaSoft, ok);
       if (tid < G) {
         const float* rd = red + 64 + tid;
@@ -608,6 +693,12 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       if (!ok || (flags & kEnd)) break;
     }
     if (!ok && tid == 0) abort_now();
+  } else if (a.solo && ntile == 0) {
+    // a pair without tokens
+    const int seq = cta / a.c.h_kv, h0 = (cta - seq * a.c.h_kv) * G;
+    for (int i = tid; i < G * D; i += kCaThreads)
+      static_cast<T*>(a.out)[seq * a.ob + (h0 + i / D) * a.oh + i % D] = Ty<T>::from_f(0.f);
+    if (a.lse && tid < G) a.lse[static_cast<size_t>(seq) * a.c.h_kv * G + h0 + tid] = -INFINITY;
   }
   tc::fence_before();
   __syncthreads();
@@ -620,23 +711,6 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
 // ------------------------------------------------------------ merge
 constexpr int kCmThreads = 256;
 constexpr int kCmChunk = 512;    // cache blocks whose weights a CTA forms
-
-// G adjacent floats (16-byte aligned where G >= 4).
-template <int G>
-__device__ __forceinline__ void load_heads(const float* p, float* o) {
-  if constexpr (G >= 4) {
-#pragma unroll
-    for (int e = 0; e < G; e += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + e);
-      o[e] = v.x; o[e + 1] = v.y; o[e + 2] = v.z; o[e + 3] = v.w;
-    }
-  } else if constexpr (G == 2) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    o[0] = v.x; o[1] = v.y;
-  } else {
-    o[0] = *p;
-  }
-}
 
 // Blocks 0 .. pairs G - 1: the output of a query head.  The others, with
 // weights: kCmChunk cache blocks of a pair.
@@ -711,29 +785,14 @@ k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int nchunk) {
       const int h = kvh * G + g_out;
       static_cast<T*>(a.out)[seq * a.ob + h * a.oh + j] = Ty<T>::from_f(acc / s_L[g_out]);
       if (a.lse && j == 0)
-        a.lse[static_cast<size_t>(seq) * a.c.h_kv * G + h] = (s_M[g_out] + log2f(s_L[g_out])) * 0.6931471805599453f;
+        a.lse[static_cast<size_t>(seq) * a.c.h_kv * G + h] = natural_lse(s_M[g_out], s_L[g_out]);
     }
     return;
   }
-  const int B = 1 << a.c.shift, gran = min(B, 32), nb = (ntok + B - 1) >> a.c.shift;
+  const int nb = (ntok + (1 << a.c.shift) - 1) >> a.c.shift;
   const int i0 = ((bx - P * G) % nchunk) * kCmChunk;
   for (int i = i0 + tid; i < min(nb, i0 + kCmChunk); i += kCmThreads) {
-    const int tile = i * B / kCaT, ng = B / gran;   // one granule, or 2 or 4 of 32 tokens
-    const float* ps = a.w.psum + (static_cast<size_t>(pair) * a.w.granules + static_cast<size_t>(i) * ng) * G;
-    float z[4][G], t[G], w = 0.f;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (u < ng) load_heads<G>(ps + u * G, z[u]);
-    load_heads<G>(a.w.tmax + (static_cast<size_t>(pair) * a.w.tiles + tile) * G, t);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float sum = z[0][g];
-#pragma unroll
-      for (int u = 1; u < 4; ++u) sum += u < ng ? z[u][g] : 0.f;
-      w += sum * ex2(t[g] - s_M[g]) / s_L[g];
-    }
-    float* dst = a.c.weight + static_cast<size_t>(pair) * a.c.max_blocks + i;
-    *dst = a.decay == 0.f ? w : fmaf(a.decay, *dst, w);
+    store_weight<G>(a, pair, i, s_M, s_L);
   }
 }
 
@@ -741,8 +800,9 @@ template <typename T, int D, int G>
 static cudaError_t attend_t(const AttendArgs& a, int ncta, cudaStream_t st) {
   const auto kern = k_attend<T, D, G>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), Ca<T, D, G>::Smem);
-  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ncta), dim3(kCaThreads), Ca<T, D, G>::Smem, st, a);
-  if (e != cudaSuccess) return e;
+  if (e == cudaSuccess)
+    e = launch_pdl(kern, dim3(a.solo ? a.c.pairs : ncta), dim3(kCaThreads), Ca<T, D, G>::Smem, st, a);
+  if (e != cudaSuccess || a.solo) return e;
   const int nchunk = a.gather ? (a.c.max_blocks + kCmChunk - 1) / kCmChunk : 0;
   return launch_pdl(k_attend_merge<T, D, G>, dim3(a.c.pairs * (G + nchunk)), dim3(kCmThreads), 0, st, a, ncta, nchunk);
 }
@@ -835,6 +895,7 @@ skv_status shadowkv_cache_attend(const shadowkv_cache* c, int dtype, int h_q, co
   a.scale_log2 = scale * 1.4426950408889634f;
   a.gather = gather;
   a.decay = decay;
+  a.solo = skv::attend_solo(*c, nsm);
   const int ncta = skv::attend_ctas(*c, nsm);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == SKV_DTYPE_BF16)

@@ -336,6 +336,23 @@ def test_attend_many_splits_and_many_pairs(dtype):
     weights_close(c, ref, dl)
 
 
+@pytest.mark.parametrize("spare", [1, 60])
+@pytest.mark.parametrize("dtype,b,h,G,d,block,lens", [
+    ("bf16", 60, 3, 4, 128, 64, lambda i: (i * 173) % 961), ("f32", 2, 2, 8, 64, 16, lambda i: 500 - 313 * i),
+    ("bf16", 3, 1, 2, 64, 128, lambda i: 128 * i + (i == 2)), ("f32", 80, 2, 1, 128, 32, lambda i: (i * 29) % 300)])
+def test_attend_with_and_without_a_second_launch(spare, dtype, b, h, G, d, block, lens):
+    """The same tokens in a cache of few tiles per pair (one CTA finishes a pair)
+    and of many (shares joined by a second launch)."""
+    dt = DT[dtype]
+    c, ref = filled(b, h, d, block, [lens(i) for i in range(b)], dt, seed=b + spare, spare=spare)
+    q = randn(gen(2), b, h * G, d).to(dt)
+    lse = torch.empty(b, h * G, device="cuda")
+    want = ref.attend(np64(q), 0.1, 0.0)
+    dl = attend_close(c.attend(q, scale=0.1, decay=0.0, lse=lse), lse, q, want, dt)
+    weights_close(c, ref, dl)
+    c.check()
+
+
 def test_attend_scale_strides_out_and_peaked_rows():
     """A scale of one's own (0 and negative too), q and out as strided views,
     and logits far apart: one token takes everything."""
