@@ -77,7 +77,7 @@ class Cache:
                     self.weight[i, g].append(0.0)
                 for x, c in ((k, 0), (v, 2)):
                     new = np.asarray(x[i, g, t:t + n], np.float64)
-                    s = max(block_scale(new), bl[-1][c + 1])
+                    s = max(block_scale(new), abs(bl[-1][c + 1]))
                     if r:
                         bl[-1][c][:r] = e4m3(bl[-1][c][:r] * (bl[-1][c + 1] / s))
                     bl[-1][c][r:r + n] = e4m3(new / s)

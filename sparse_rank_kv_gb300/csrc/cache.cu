@@ -335,8 +335,9 @@ __global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constan
       m = all_max(A::top_finite(w), turn ^ 1);
       tc::named_sync(1 + grp, A::TPJ);
     }
-    const float sc = fmaxf(cache_scale_of(__uint_as_float(m)), was);
-    const bool grow = e0 > 0 && sc > was;
+    // (a caller's own scale may be negative: held codes then change sign)
+    const float sc = fmaxf(cache_scale_of(__uint_as_float(m)), fabsf(was));
+    const bool grow = e0 > 0 && sc != was;
     if (NW == 1) __syncwarp();   // every lane has read the old scale
     if (tid == 0) {
       *scale = sc;
@@ -394,8 +395,8 @@ __global__ void __launch_bounds__(kApThreads) k_append_one(const __grid_constant
 #pragma unroll
       for (int e = 0; e < N; ++e) m = max(m, __float_as_uint(finite_abs(x[e])));
       m = __reduce_max_sync(0xffffffffu, m);
-      const float sc = fmaxf(cache_scale_of(__uint_as_float(m)), was);
-      if (e0 > 0 && sc > was) {
+      const float sc = fmaxf(cache_scale_of(__uint_as_float(m)), fabsf(was));
+      if (e0 > 0 && sc != was) {
         const float ratio = was / sc;
         for (int u = lane; u < (D << c.shift) / 16; u += 32) {
           // 16 bytes: one row of K, 16 tokens of V

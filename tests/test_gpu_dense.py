@@ -218,6 +218,33 @@ def test_append_special_values():
     c.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("s", [1, 4])
+def test_append_onto_a_callers_own_scales(dtype, s):
+    """A partly filled block whose scale the caller chose (no power of two, larger
+    than the new tokens need or smaller, negative, zero) keeps its values up to one
+    rounding of its codes; new tokens are quantised by the scale that results."""
+    scales = [0.3, 1000.0, -1000.0, -0.01, 0.0, 3e-5]
+    c, ref = filled(1, len(scales), 64, 16, [21], DT[dtype], seed=44)
+    for h, x in enumerate(scales):
+        id_ = int(c.table[0, h, 1])
+        c.k_scale[id_], c.v_scale[id_] = x, -x
+        ref.blocks[0, h][1][1], ref.blocks[0, h][1][3] = np.float32(x).astype(np.float64), -np.float32(x).astype(np.float64)
+    k, v = tokens(gen(4), 1, len(scales), s, 64, DT[dtype])
+    c.append(k, v)
+    ref.append(np64(k), np64(v), [s])
+    for h in range(len(scales)):
+        kc, ks, vc, vs = codes_of(c, 0, h, 1)
+        want = ref.blocks[0, h][1]
+        assert ks == want[1] and vs == want[3]
+        for got, exp in ((kc, want[0]), (vc, want[2])):
+            # quotients here are fp32 divisions: a tie may fall to the other neighbour (a step: 2^-3 of the value, 2^-9 at least)
+            err = np.abs(got[:5 + s] - exp[:5 + s])
+            assert np.all(err <= np.maximum(2.0 ** -3 * np.abs(exp[:5 + s]), 2.0 ** -9) * 1.001)
+            assert np.mean(err > 0) < 0.02
+    c.check()
+
+
 def test_append_past_the_end_is_dropped_and_reported():
     c = binding.BlockCache.empty(1, 2, 64, 2, block=16)
     k = randn(gen(1), 1, 2, 30, 64)
