@@ -312,12 +312,13 @@ typedef struct shadowkv_norm_rope_params {
  * rows normed but not turned: the pre-RoPE keys shadowkv_prefill takes.
  *   q, k           : device rows b x h_q x s x d and b x h_kv x s x d; either may be
  *                    NULL (then its weight and output are too).
- *   q_weight, k_weight : device, d elements each, or NULL.
+ *   q_weight, k_weight : device, d elements each, or NULL; not used with norm = 0.
  *   pos            : device int32, b or b x s (pos_per_token), any value;
  *                    NULL: token t at position t.
  *   q_out, k_out   : device rows.  An output may be its own input (same pointer and
  *                    strides); otherwise no output overlaps an input or the other output.
- * Everything is computed in fp32 and rounded once; the angle is reduced in
+ * Everything is computed in fp32 and rounded once (a row whose sum of squares
+ * passes fp32's range, |x| above about 1e18, gives zeros); the angle is reduced in
  * 64-bit integers and is exact to 2^-30 of a turn at any position.  Row
  * pointers and strides must be multiples of 4 elements, and pointers aligned
  * to 4 elements (SKV_ERR_INVALID_ARG).  b = 0 or s = 0 does nothing.

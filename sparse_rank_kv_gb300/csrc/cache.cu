@@ -691,10 +691,14 @@ skv_status cache_checked(const shadowkv_cache* c) {
 
 extern "C" {
 
-skv_status shadowkv_cache_validate(const shadowkv_cache* c) { return skv::cache_checked(c); }
+skv_status shadowkv_cache_validate(const shadowkv_cache* c) try {
+  return skv::cache_checked(c);
+} catch (...) {   // host memory for an error text ran out
+  return SKV_ERR_OOM;
+}
 
 skv_status shadowkv_cache_append(const shadowkv_cache* c, int dtype, const shadowkv_rows* k, const shadowkv_rows* v,
-                                 int s, const int32_t* lens, void* stream) {
+                                 int s, const int32_t* lens, void* stream) try {
   using skv::set_error;
   skv_status st = skv::cache_checked(c);
   if (st != SKV_OK) return st;
@@ -719,10 +723,12 @@ skv_status shadowkv_cache_append(const shadowkv_cache* c, int dtype, const shado
   else
     e = c->d == 128 ? skv::append_t<float, 128>(a, q) : skv::append_t<float, 64>(a, q);
   return e == cudaSuccess ? SKV_OK : set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
+} catch (...) {   // host memory for an error text or a table ran out
+  return SKV_ERR_OOM;
 }
 
 skv_status shadowkv_cache_evict(const shadowkv_cache* src, const shadowkv_cache* dst, int keep, int sink, int recent,
-                                int32_t* kept, void* stream) {
+                                int32_t* kept, void* stream) try {
   using skv::set_error;
   skv_status st = skv::cache_checked(src);
   if (st != SKV_OK) return st;
@@ -738,9 +744,11 @@ skv_status shadowkv_cache_evict(const shadowkv_cache* src, const shadowkv_cache*
   if (reinterpret_cast<uintptr_t>(kept) % 4) return set_error(SKV_ERR_INVALID_ARG, "kept must be 4-byte aligned");
   const cudaError_t e = skv::launch_evict(*src, *dst, keep, sink, recent, kept, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SKV_OK : set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
+} catch (...) {   // host memory for an error text or a table ran out
+  return SKV_ERR_OOM;
 }
 
-skv_status shadowkv_cache_check(const shadowkv_cache* c) {
+skv_status shadowkv_cache_check(const shadowkv_cache* c) try {
   using skv::set_error;
   skv_status st = skv::cache_checked(c);
   if (st != SKV_OK) return st;
@@ -751,6 +759,8 @@ skv_status shadowkv_cache_check(const shadowkv_cache* c) {
   if (word == skv::DEV_TIMEOUT) return set_error(SKV_ERR_TIMEOUT, "a bounded device wait gave up");
   if (word) return set_error(SKV_ERR_DEVICE_CHECK, "a kernel met a block id, length or token count out of range");
   return SKV_OK;
+} catch (...) {   // host memory for an error text or a table ran out
+  return SKV_ERR_OOM;
 }
 
 }  // extern "C"

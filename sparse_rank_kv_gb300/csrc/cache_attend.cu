@@ -839,7 +839,7 @@ static bool attend_heads_ok(const shadowkv_cache& c, int h_q) {
 
 extern "C" {
 
-size_t shadowkv_cache_attend_workspace(const shadowkv_cache* c, int h_q) {
+size_t shadowkv_cache_attend_workspace(const shadowkv_cache* c, int h_q) try {
   if (skv::cache_checked(c) != SKV_OK) return 0;
   if (!skv::attend_heads_ok(*c, h_q)) {
     skv::set_error(SKV_ERR_UNSUPPORTED, "h_q / h_kv must be 1, 2, 4 or 8");
@@ -852,11 +852,13 @@ size_t shadowkv_cache_attend_workspace(const shadowkv_cache* c, int h_q) {
     return 0;
   }
   return skv::attend_layout(*c, h_q / c->h_kv, nsm, nullptr, nullptr);
+} catch (...) {   // host memory for an error text or a table ran out
+  return 0;
 }
 
 skv_status shadowkv_cache_attend(const shadowkv_cache* c, int dtype, int h_q, const shadowkv_rows* q, float scale,
                                  int gather, float decay, const shadowkv_rows* out, float* lse, void* work,
-                                 size_t work_bytes, void* stream) {
+                                 size_t work_bytes, void* stream) try {
   using skv::set_error;
   skv_status st = skv::cache_checked(c);
   if (st != SKV_OK) return st;
@@ -903,6 +905,8 @@ skv_status shadowkv_cache_attend(const shadowkv_cache* c, int dtype, int h_q, co
   else
     e = c->d == 128 ? skv::attend_g<float, 128>(a, G, ncta, s) : skv::attend_g<float, 64>(a, G, ncta, s);
   return e == cudaSuccess ? SKV_OK : set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
+} catch (...) {   // host memory for an error text or a table ran out
+  return SKV_ERR_OOM;
 }
 
 }  // extern "C"

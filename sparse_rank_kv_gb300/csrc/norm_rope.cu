@@ -254,7 +254,7 @@ static const char* rows_fault(const shadowkv_rows& r, int b, int h, int s, int E
 extern "C" skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, const shadowkv_rows* q,
                                             const shadowkv_rows* k, const void* q_weight, const void* k_weight,
                                             const int32_t* pos, const shadowkv_rows* q_out,
-                                            const shadowkv_rows* k_out, void* stream) {
+                                            const shadowkv_rows* k_out, void* stream) try {
   using skv::set_error;
   if (!p) return set_error(SKV_ERR_INVALID_ARG, "params is NULL");
   if (!q && !k) return set_error(SKV_ERR_INVALID_ARG, "q and k are both NULL");
@@ -309,4 +309,6 @@ extern "C" skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, 
   const cudaError_t e = skv::launch_norm_rope(*p, a, skv::rope_freq(p->theta, p->rot), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
   return SKV_OK;
+} catch (...) {   // host memory for an error text or a table ran out
+  return SKV_ERR_OOM;
 }
