@@ -87,8 +87,14 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* a, const uint32
 // block's largest magnitude is found.
 template <typename T, int D, int B>
 struct Ap {
-  static constexpr int TPJ = B * D / 32 < kApThreads ? B * D / 32 : kApThreads;
-  static constexpr int UV = B * D / 32 / TPJ, UK = 2 * UV;   // units per thread
+  static constexpr int TPJ = B * D / 32;                     // 32 to 512
+  static constexpr int NT = TPJ < kApThreads ? kApThreads : TPJ;   // threads per CTA
+  static constexpr int UV = 1, UK = 2;                       // units per thread
+  // CTAs per SM the registers are cut for.  Measured at 2, 3 and 4 (four ragged
+  // prompts of up to 6000 tokens, d = 128): blocks of 16 27.3, 29.1 and 26.0 us,
+  // of 32 27.4, 28.0 and 22.7, of 64 29.4, 24.4 and 23.6; d = 64, blocks of 16:
+  // 13.1, 14.5 and 16.7
+  static constexpr int MinCtas = sizeof(T) == 4 ? 1 : TPJ == 32 || TPJ == 512 ? 2 : 4;
   static constexpr int E = sizeof(T) / 2;                    // 32-bit words per two elements
   static constexpr int Words = 16 * UV * E;                  // raw words per thread
   // unit u of K: 8 consecutive threads take a group's 8 rows (128 adjacent code bytes)
@@ -275,15 +281,16 @@ struct Ap {
 // one load per element and the next block's loads in flight 66, a path of
 // its own for whole new blocks 48.5, 32-byte accesses 45.
 template <typename T, int D, int B>
-__global__ void __launch_bounds__(kApThreads) k_append_many(const __grid_constant__ AppendArgs a, int per, int nrun) {
+__global__ void __launch_bounds__((Ap<T, D, B>::NT), (Ap<T, D, B>::MinCtas))
+k_append_many(const __grid_constant__ AppendArgs a, int per, int nrun) {
   typedef Ap<T, D, B> A;
   constexpr int NW = (A::TPJ + 31) / 32;
-  __shared__ uint32_t red[2][kApThreads / 32];
-  __shared__ int2 s_range[kApThreads / A::TPJ];
+  __shared__ uint32_t red[2][A::NT / 32];
+  __shared__ int2 s_range[A::NT / A::TPJ];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int grp = threadIdx.x / A::TPJ, tid = threadIdx.x % A::TPJ, warp = threadIdx.x >> 5;
-  const uint32_t job = blockIdx.x * (kApThreads / A::TPJ) + grp;   // 2 pairs nrun < 2^32
+  const uint32_t job = blockIdx.x * (A::NT / A::TPJ) + grp;   // 2 pairs nrun < 2^32
   const uint32_t pw = job / static_cast<uint32_t>(nrun);
   const int run = static_cast<int>(job - pw * static_cast<uint32_t>(nrun));
   const int which = static_cast<int>(pw & 1u), pair = static_cast<int>(pw >> 1);
@@ -455,9 +462,9 @@ static cudaError_t append_many(const AppendArgs& a, cudaStream_t st) {
   const long long jobs = 2LL * a.c.pairs * nblk;
   const int per = static_cast<int>(jobs / 1200 < 1 ? 1 : jobs / 1200 > 8 ? 8 : jobs / 1200);
   const int nrun = (nblk + per - 1) / per;
-  const long long groups = 2LL * a.c.pairs * nrun, gpc = kApThreads / A::TPJ;
+  const long long groups = 2LL * a.c.pairs * nrun, gpc = A::NT / A::TPJ;
   cudaError_t e = launch_pdl(k_append_many<T, D, B>, dim3(static_cast<unsigned>((groups + gpc - 1) / gpc)),
-                             dim3(kApThreads), 0, st, a, per, nrun);
+                             dim3(A::NT), 0, st, a, per, nrun);
   if (e == cudaSuccess)
     e = launch_pdl(k_append_count, dim3((a.c.pairs + kApThreads - 1) / kApThreads), dim3(kApThreads), 0, st, a);
   return e;
