@@ -186,9 +186,10 @@ __device__ __forceinline__ float natural_lse(float M, float L) { return (M + log
 //   O = V^T P^T (M = d, K = 128 tokens),        P: PP rows per query head
 // q and p are not e4m3 numbers but sums of them: x = x0 + x1/16 + x2/256 + ...,
 // each term the e4m3 rounding of what the ones before leave, 4 bits each.
-// Two terms hold a bf16 query exactly (8 bits), four hold p to 16 bits, six an
+// Two terms hold a bf16 query exactly (8 bits), three hold an fp16 p (11 bits: more than
+// the bf16 output keeps, and its split costs a third of an fp32 p's), six an
 // fp32 value; e4m3's range ends them at 2^-18 16^(1-terms) of the largest entry (of
-// a tile's p V-scale, of a q row): 2^-30 for bf16's p, 2^-38 for fp32.  Decoding has
+// a tile's p V-scale, of a q row): 2^-26 for bf16's p, 2^-38 for fp32.  Decoding has
 // G <= 8 query rows for a tile of at least 16, so the terms fill rows that
 // would be padding, and no code is ever converted.  Products of e4m3 numbers accumulate in fp32 (measured: within
 // 2^-22 of the sum of magnitudes, as an fp32 matrix product).
@@ -198,7 +199,7 @@ constexpr int kCaSmemMax = 113 * 1024;        // two CTAs per SM: one computes w
 
 template <typename T, int D, int G>
 struct Ca {
-  static constexpr int QP = sizeof(T) == 2 ? 2 : 6, PP = sizeof(T) == 2 ? 4 : 6;
+  static constexpr int QP = sizeof(T) == 2 ? 2 : 6, PP = sizeof(T) == 2 ? 3 : 6;
   static constexpr int N1 = (G * QP + 15) / 16 * 16, N2 = (G * PP + 15) / 16 * 16;
   static constexpr int KB = kCaT * D, Stage = 2 * KB;       // K tile, V tile
   static constexpr int QB = N1 * D, PB = N2 * kCaT;
@@ -222,6 +223,36 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
 // kind::f8f6f4, e4m3 A and B (format 0), fp32 D, both K-major, M = 128
 constexpr uint32_t idesc_e4m3(int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+// Sum of z[g] over groups of `gran` (16 or 32) lanes: lanes exchange half of
+// their heads at each step until one is left (G = 4: 6 shuffles instead of 20).
+// Lane l of a group holds the sum of head head_of_lane<G>(l) for l < G.
+template <int G>
+__device__ __forceinline__ float granule_sum(const float* z, int lane, int gran) {
+  float v[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) v[g] = z[g];
+  int o = 1;
+#pragma unroll
+  for (int h = G / 2; h > 0; h >>= 1, o <<= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int g = 0; g < h; ++g) {
+      const float mine = up ? v[g + h] : v[g], other = up ? v[g] : v[g + h];
+      v[g] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+    }
+  }
+#pragma unroll
+  for (int w = G; w < 16; w <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+  if (gran == 32) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+  return v[0];
+}
+template <int G>
+__device__ __forceinline__ int head_of_lane(int l) {
+  int h = 0;
+#pragma unroll
+  for (int b = G / 2, o = 1; b > 0; b >>= 1, o <<= 1) h += l & o ? b : 0;
+  return h;
 }
 __device__ __forceinline__ float redux_max(float x) {
   float r;
@@ -557,12 +588,14 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
 #pragma unroll
         for (int c = 0; c < N1; c += 16) tc::tmem_ld16(tS + (it & 1) * N1 + c, v + c);
         const float ks = sc[blk];
+        float qs[G];
+        load_heads<G>(sqs + (turn & 1) * 8, qs);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           float x = v[(C::QP - 1) * G + g];
 #pragma unroll
           for (int i = C::QP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, v[i * G + g]);
-          s[g] = tid < cnt ? x * (sqs[(turn & 1) * 8 + g] * ks) : -INFINITY;
+          s[g] = tid < cnt ? x * (qs[g] * ks) : -INFINITY;
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -575,11 +608,12 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       float al_new[G], be_new[G];
       unsigned char* pb = pbuf + (it & 1) * C::PB + (tid >> 4) * (N2 * 16) + (tid & 15);
       const float vf = tid < cnt ? sc[8 + blk] : 0.f, vref = sc[16];
-      float p[G];
+      float p[G], rd[4][G];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) load_heads<G>(red + (it & 1) * 32 + w * G, rd[w]);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float* rd = red + (it & 1) * 32 + g;
-        const float mt = fmaxf(fmaxf(rd[0], rd[G]), fmaxf(rd[2 * G], rd[3 * G]));
+        const float mt = fmaxf(fmaxf(rd[0][g], rd[1][g]), fmaxf(rd[2][g], rd[3][g]));
         const float tref = mt == -INFINITY ? 0.f : mt, mn = fmaxf(mt, m[g]), ref = mn == -INFINITY ? 0.f : mn;
         al_new[g] = ex2(m[g] - ref);
         be_new[g] = ex2(mt - ref);
@@ -590,32 +624,32 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
         if (a.gather && tid == 0) a.w.tmax[(static_cast<size_t>(pair) * a.w.tiles + t) * G + g] = tref;
       }
       if (a.gather) {
-        float z[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          z[g] = p[g];
-#pragma unroll
-          for (int o = 1; o < 16; o <<= 1) z[g] += __shfl_xor_sync(0xffffffffu, z[g], o);
-          if (gran == 32) z[g] += __shfl_xor_sync(0xffffffffu, z[g], 16);
-        }
-        if ((lane & (gran - 1)) == 0) {
-          float* dst = a.w.psum + (static_cast<size_t>(pair) * a.w.granules + (t * kCaT + tid) / gran) * G;
-#pragma unroll
-          for (int g = 0; g < G; ++g) dst[g] = z[g];
-        }
+        const float z = granule_sum<G>(p, lane, gran);
+        const int l = lane & (gran - 1);
+        if (l < G)
+          a.w.psum[(static_cast<size_t>(pair) * a.w.granules + (t * kCaT + tid) / gran) * G + head_of_lane<G>(l)] = z;
       }
       // p's terms, times the token's V scale; rows term G + head
 #pragma unroll
       for (int g = 0; g < G; g += 2) {
         float u = p[g] * vf, v = G > 1 ? p[g + (G > 1)] * vf : 0.f;
+        __half2 x = __floats2half2_rn(u, v);
 #pragma unroll
         for (int i = 0; i < C::PP; ++i) {
-          const uint32_t c2 = e4m3_pack2(u, v);
+          uint32_t c2;
+          if constexpr (sizeof(T) == 2) {
+            c2 = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+            // (what is left has fewer bits than an fp16 holds: exact)
+            const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2), __NV_E4M3));
+            x = __hmul2(__hsub2(x, f), __float2half2_rn(16.f));
+          } else {
+            c2 = e4m3_pack2(u, v);
+            const float2 f = e4m3_unpack2(c2);
+            u = (u - f.x) * 16.f;
+            v = (v - f.y) * 16.f;
+          }
           pb[(i * G + g) * 16] = static_cast<unsigned char>(c2);
           if (G > 1) pb[(i * G + g + 1) * 16] = static_cast<unsigned char>(c2 >> 8);
-          const float2 f = e4m3_unpack2(c2);
-          u = (u - f.x) * 16.f;
-          v = (v - f.y) * 16.f;
         }
       }
       // V past the tokens may be any bytes, NaN too: zero under zero weights

@@ -272,16 +272,16 @@ def test_append_past_the_end_is_dropped_and_reported():
 def attend_close(out, lse, q, ref, dtype):
     """|error| <= half a step of the result + what moves p: a logit is a sum of d exact products in
     fp32 (d roundings of its largest partial sum, and 8 of its own scaling), p moves by as much twice (its own and
-    the sum's), the exponential is within 2^-21, p itself is held to 2^-16 (bf16) or 2^-23 (fp32), and
+    the sum's), the exponential is within 2^-21, p itself is held to 2^-11 (bf16: rounded to fp16, half a step of 2^-10) or 2^-23 (fp32), and
     sums over n tokens cost at most 64 roundings in tiles and partials.  Below that p has a
     floor: with its tile's largest p V-scale at 256, the last of T e4m3 terms ends at half the
-    least step, 2^-10 16^(1-T) (T = 4: 2^-22, so 2^-30 of the largest; T = 6: 2^-38), times
+    least step, 2^-10 16^(1-T) (T = 3: 2^-18, so 2^-26 of the largest; T = 6: 2^-38), times
     a code of at most 448, for each of the tile's 128 tokens."""
     o, l, mag, lm, top = ref
     bf = dtype == torch.bfloat16
     dl = (q.shape[-1] + 8) * U * lm
-    p = 2 * dl + 2.0 ** -20 + 64 * U + (2.0 ** -16 if bf else 2.0 ** -22)
-    tol = STEP[dtype] * np.abs(o) + p[..., None] * mag + (128 * 2.0 ** (-30 if bf else -38) * top)[..., None] + 1e-30
+    p = 2 * dl + 2.0 ** -20 + 64 * U + (2.0 ** -11 if bf else 2.0 ** -22)
+    tol = STEP[dtype] * np.abs(o) + p[..., None] * mag + (128 * 2.0 ** (-26 if bf else -38) * top)[..., None] + 1e-30
     err = np.abs(np64(out) - o)
     assert np.all(err <= tol), f"out: worst {np.max(err / tol):.3g} of the tolerance"
     if lse is not None:
