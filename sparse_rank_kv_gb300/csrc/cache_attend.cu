@@ -220,9 +220,10 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// kind::f8f6f4, e4m3 A and B (format 0), fp32 D, both K-major, M = 128
-constexpr uint32_t idesc_e4m3(int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+// kind::f8f6f4, e4m3 A and B (format 0), fp32 D, M = 128; A K-major, B
+// K-major or (bn: bit 16) N-major
+constexpr uint32_t idesc_e4m3(int N, bool bn = false) {
+  return (1u << 4) | (bn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
 // Sum of z[g] over groups of `gran` (16 or 32) lanes: lanes exchange half of
 // their heads at each step until one is left (G = 4: 6 shuffles instead of 20).
@@ -332,8 +333,8 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
     tc::tmem_alloc(tmem_slot, C::Cols);
     tc::tmem_relinquish();
   }
-  // operand rows past the terms stay zero
-  for (int i = tid; i < (2 * C::QB + 2 * C::PB) / 16; i += kCaThreads)
+  // q rows past the terms stay zero
+  for (int i = tid; i < 2 * C::QB / 16; i += kCaThreads)
     reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0, 0, 0, 0);
   tc::fence_proxy_async_smem();
   tc::fence_before();
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
 #pragma unroll
           for (int k = 0; k < kCaT / 32; ++k)
             mma_e4m3(tO + (j & 1) * N2, tc::desc_k_none(v0 + k * (2 * D * 16), D * 16, 128),
-                     tc::desc_k_none(p0 + k * (2 * N2 * 16), N2 * 16, 128), idesc_e4m3(N2), k > 0);
+                     tc::desc_k_none(p0 + k * 512, 128, kCaT * 16), idesc_e4m3(N2, true), k > 0);
           tc::mma_commit(&ofull[j & 1]);
           tc::mma_commit(&empty[st]);
           ++j;
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       ok = tc::named_sync_and(1, kCaSoft, ok);
       if (!ok) break;
       float al_new[G], be_new[G];
-      unsigned char* pb = pbuf + (it & 1) * C::PB + (tid >> 4) * (N2 * 16) + (tid & 15);
+      unsigned char* pb = pbuf + (it & 1) * C::PB + tid * 16;
       const float vf = tid < cnt ? sc[8 + blk] : 0.f, vref = sc[16];
       float p[G], rd[4][G];
 #pragma unroll
@@ -629,7 +630,9 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
         if (l < G)
           a.w.psum[(static_cast<size_t>(pair) * a.w.granules + (t * kCaT + tid) / gran) * G + head_of_lane<G>(l)] = z;
       }
-      // p's terms, times the token's V scale; rows term G + head
+      // p's terms, times the token's V scale; row term G + head.  The operand is
+      // N-major ([N2/16][token][16 rows]), so that a token's rows are 16-byte stores
+      uint32_t pw[N2 / 4] = {};
 #pragma unroll
       for (int g = 0; g < G; g += 2) {
         float u = p[g] * vf, v = G > 1 ? p[g + (G > 1)] * vf : 0.f;
@@ -648,10 +651,13 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
             u = (u - f.x) * 16.f;
             v = (v - f.y) * 16.f;
           }
-          pb[(i * G + g) * 16] = static_cast<unsigned char>(c2);
-          if (G > 1) pb[(i * G + g + 1) * 16] = static_cast<unsigned char>(c2 >> 8);
+          const int n = i * G + g;
+          pw[n >> 2] |= (G > 1 ? c2 : c2 & 0xffu) << (8 * (n & 3));
         }
       }
+#pragma unroll
+      for (int c = 0; c < N2 / 16; ++c)
+        *reinterpret_cast<uint4*>(pb + c * (kCaT * 16)) = make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
       // V past the tokens may be any bytes, NaN too: zero under zero weights
       if (cnt < kCaT && tid < D) {
         unsigned char* vb = stages + st * C::Stage + C::KB + tid * 16;
