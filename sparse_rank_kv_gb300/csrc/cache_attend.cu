@@ -4,10 +4,12 @@
 //
 // Memory bounds it: 2 d bytes of codes per token and KV head are read once.
 // Measured, 32 query and 8 KV heads of 128 in bf16, weights gathered: batch 8 at
-// 128K (2.15 GB) 314 us, 6.8 TB/s; batch 1 at 128K 48 us (40 at that rate); 16
-// ragged sequences of up to 9001 tokens (163 MB) 38.5 us (24 at that rate: a
+// 128K (2.15 GB) 320 us, 6.7 TB/s; batch 1 at 128K 48 us (40 at that rate); 16
+// ragged sequences of up to 9001 tokens (163 MB) 33.5 us (24 at that rate: a
 // few CTAs' copies come at half the speed of the others', and the shares are
-// fixed beforehand); 90 tokens 5.4 us, all latency.  The CUDA-core form of the
+// fixed beforehand); 90 tokens 5.1 us, all latency.  16 sequences of 9001 tokens
+// (295 MB, 43 us at that rate): 51 us, with 64 query heads 56, fp32 57, both 67, the
+// last three bound by the softmax warps' latency.  The CUDA-core form of the
 // same split took 8.0 ms at batch 8, 128K.
 //
 // Every pair's tokens are cut into 128-token tiles; the tiles of all pairs, in
@@ -26,6 +28,7 @@
 namespace skv {
 
 constexpr int kCaT = 128;         // tokens per tile
+constexpr int kCaMostPerSm = 3;   // CTAs per SM, at most
 
 // Small caches: one CTA works a pair's tiles off and finishes it, without the
 // prefix sums, the partials and the second launch.  Measured, device time of
@@ -49,9 +52,11 @@ struct AttendWork {
   int tiles, granules;   // per pair, at most
 };
 
-inline int attend_ctas(const shadowkv_cache& c, int nsm) {
+// CTAs that share the tiles, at `per_sm` on every SM.
+inline int attend_ctas(const shadowkv_cache& c, int nsm, int per_sm) {
   const long long tiles = (static_cast<long long>(c.max_blocks) * c.block + kCaT - 1) / kCaT * c.b * c.h_kv;
-  return static_cast<int>(tiles < 2LL * nsm ? tiles : 2LL * nsm);
+  const long long most = static_cast<long long>(per_sm) * nsm;
+  return static_cast<int>(tiles < most ? tiles : most);
 }
 
 inline size_t attend_layout(const shadowkv_cache& c, int G, int nsm, void* base, AttendWork* w) {
@@ -68,7 +73,7 @@ inline size_t attend_layout(const shadowkv_cache& c, int G, int nsm, void* base,
     return p;
   };
   v.first = reinterpret_cast<int*>(take((pairs + 1) * sizeof(int)));
-  v.part = reinterpret_cast<float*>(take((attend_ctas(c, nsm) + pairs) * G * (c.d + 2) * sizeof(float)));
+  v.part = reinterpret_cast<float*>(take((attend_ctas(c, nsm, kCaMostPerSm) + pairs) * G * (c.d + 2) * sizeof(float)));
   v.tmax = reinterpret_cast<float*>(take(pairs * v.tiles * G * sizeof(float)));
   v.psum = reinterpret_cast<float*>(take(pairs * v.granules * G * sizeof(float)));
   if (w) *w = v;
@@ -195,7 +200,6 @@ __device__ __forceinline__ float natural_lse(float M, float L) { return (M + log
 // 2^-22 of the sum of magnitudes, as an fp32 matrix product).
 constexpr int kCaSoft = 128;                  // softmax threads: warps 0..3, thread = token, then dimension
 constexpr int kCaThreads = kCaSoft + 64;      // warp 4: copies, warp 5: tcgen05.mma
-constexpr int kCaSmemMax = 113 * 1024;        // two CTAs per SM: one computes while the other waits for its barriers
 
 template <typename T, int D, int G>
 struct Ca {
@@ -204,7 +208,12 @@ struct Ca {
   static constexpr int KB = kCaT * D, Stage = 2 * KB;       // K tile, V tile
   static constexpr int QB = N1 * D, PB = N2 * kCaT;
   static constexpr int Misc = 2048;
-  static constexpr int NST = (kCaSmemMax - 128 - 2 * QB - 2 * PB - Misc) / Stage;
+  // CTAs per SM: while one waits for its barriers the others compute.  Heads of
+  // 64 have half the bytes per tile for the same softmax: three where the
+  // registers allow it (112): 16 sequences of 9001 tokens 42.2 -> 36.8 us.
+  static constexpr int PerSm = D == 64 && G <= (sizeof(T) == 2 ? 4 : 2) ? 3 : 2;
+  static constexpr int SmemMax = (228 / PerSm - 1) * 1024;
+  static constexpr int NST = (SmemMax - 128 - 2 * QB - 2 * PB - Misc) / Stage;
   static constexpr int Smem = 128 + NST * Stage + 2 * QB + 2 * PB + Misc;
   static constexpr int Cols0 = 2 * N1 + 2 * N2;
   static constexpr int Cols = Cols0 <= 32 ? 32 : Cols0 <= 64 ? 64 : Cols0 <= 128 ? 128 : 256;
@@ -289,7 +298,7 @@ struct TileCursor {
 };
 
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(const __grid_constant__ AttendArgs a) {
   using C = Ca<T, D, G>;
   constexpr int N1 = C::N1, N2 = C::N2, NST = C::NST;
   extern __shared__ unsigned char smem_raw[];
@@ -456,7 +465,8 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
       // first: it frees a stage for the next copy
       int i = 0, j = 0, runs = 0;      // next S, next O; runs: pair's turn of tile i
       bool more = true;
-      uint64_t t_last = tc::globaltimer_ns();
+      uint64_t t_last = 0;
+      int idle = 0;
       while (more || j < i) {
         bool did = false;
         if (j < i && tc::mbar_test(&pfull[j & 1], (j >> 1) & 1)) {
@@ -492,8 +502,13 @@ __global__ void __launch_bounds__(kCaThreads, 2) k_attend(const __grid_constant_
           more = !(flags & kEnd);
           did = true;
         }
-        if (did) t_last = tc::globaltimer_ns();
-        else if (*s_abort || tc::globaltimer_ns() - t_last > kWaitLimit) {
+        if (did) {
+          idle = 0;
+          continue;
+        }
+        // nothing ready: look at the clock now and then
+        if (idle == 0) t_last = tc::globaltimer_ns();
+        if ((++idle & 63) == 0 && (*s_abort || tc::globaltimer_ns() - t_last > kWaitLimit)) {
           abort_now();
           break;
         }
@@ -837,7 +852,8 @@ k_attend_merge(const __grid_constant__ AttendArgs a, int ncta, int nchunk) {
 }
 
 template <typename T, int D, int G>
-static cudaError_t attend_t(const AttendArgs& a, int ncta, cudaStream_t st) {
+static cudaError_t attend_t(const AttendArgs& a, const shadowkv_cache& c, int nsm, cudaStream_t st) {
+  const int ncta = attend_ctas(c, nsm, Ca<T, D, G>::PerSm);
   const auto kern = k_attend<T, D, G>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), Ca<T, D, G>::Smem);
   if (e == cudaSuccess)
@@ -848,12 +864,12 @@ static cudaError_t attend_t(const AttendArgs& a, int ncta, cudaStream_t st) {
 }
 
 template <typename T, int D>
-static cudaError_t attend_g(const AttendArgs& a, int G, int ncta, cudaStream_t st) {
+static cudaError_t attend_g(const AttendArgs& a, int G, const shadowkv_cache& c, int nsm, cudaStream_t st) {
   switch (G) {
-    case 1: return attend_t<T, D, 1>(a, ncta, st);
-    case 2: return attend_t<T, D, 2>(a, ncta, st);
-    case 4: return attend_t<T, D, 4>(a, ncta, st);
-    default: return attend_t<T, D, 8>(a, ncta, st);
+    case 1: return attend_t<T, D, 1>(a, c, nsm, st);
+    case 2: return attend_t<T, D, 2>(a, c, nsm, st);
+    case 4: return attend_t<T, D, 4>(a, c, nsm, st);
+    default: return attend_t<T, D, 8>(a, c, nsm, st);
   }
 }
 
@@ -938,12 +954,11 @@ skv_status shadowkv_cache_attend(const shadowkv_cache* c, int dtype, int h_q, co
   a.gather = gather;
   a.decay = decay;
   a.solo = skv::attend_solo(*c, nsm);
-  const int ncta = skv::attend_ctas(*c, nsm);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == SKV_DTYPE_BF16)
-    e = c->d == 128 ? skv::attend_g<skv::bf16, 128>(a, G, ncta, s) : skv::attend_g<skv::bf16, 64>(a, G, ncta, s);
+    e = c->d == 128 ? skv::attend_g<skv::bf16, 128>(a, G, *c, nsm, s) : skv::attend_g<skv::bf16, 64>(a, G, *c, nsm, s);
   else
-    e = c->d == 128 ? skv::attend_g<float, 128>(a, G, ncta, s) : skv::attend_g<float, 64>(a, G, ncta, s);
+    e = c->d == 128 ? skv::attend_g<float, 128>(a, G, *c, nsm, s) : skv::attend_g<float, 64>(a, G, *c, nsm, s);
   return e == cudaSuccess ? SKV_OK : set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
 } catch (...) {   // host memory for an error text or a table ran out
   return SKV_ERR_OOM;
