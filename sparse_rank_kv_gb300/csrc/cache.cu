@@ -488,8 +488,8 @@ static cudaError_t append_t(const AppendArgs& a, cudaStream_t st) {
 // ------------------------------------------------------------------ evict
 constexpr int kEvMax = 16384;   // blocks per pair
 
-// CTA = pair; thread t holds the table entries and weights t, t + NT, ... in
-// registers (so the tables may be rewritten in place).  Weights become
+// CTA = pair; thread t holds the entries t, t + NT, ... in registers (so the
+// tables may be rewritten in place).  Weights become
 // order-preserving keys, protected blocks the largest; the `keep`-th largest
 // key is found two bits at a time by counting over the block (one barrier a step, ending
 // as soon as some prefix has exactly `keep` keys above it), and every block's
@@ -508,13 +508,12 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
   const int mb = c.max_blocks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pair = blockIdx.x;
   const size_t row = static_cast<size_t>(pair) * mb;
-  int32_t id[R];
-  float w[R];
+  // the weights, as keys; what the tables hold is read once more below
+  uint32_t key[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int i = tid + r * NT;
-    id[r] = i < mb ? c.table[row + i] : 0;
-    w[r] = i < mb ? c.weight[row + i] : 0.f;
+    key[r] = i < mb ? __float_as_uint(c.weight[row + i]) : 0u;
   }
   if (tid == 0) s_tok = cache_tokens(c, pair);
   __syncthreads();
@@ -522,21 +521,13 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
   const int B = 1 << c.shift, n = (tok + B - 1) >> c.shift;
   const int nk = min(n, keep);
   const int rows = (n + NT - 1) / NT;   // registers in use: the same for every thread
-  // 0: no block (never chosen); 1: NaN, below every number; -0 as 0.  Formed
-  // once while the registers allow it.
-  auto make_key = [&](int r) -> uint32_t {
-    const int i = tid + r * NT;
-    if (i >= n) return 0u;
-    if (i < sink || i >= n - recent) return 0xffffffffu;
-    return w[r] == w[r] ? order_key(w[r] + 0.f) : 1u;
-  };
-  constexpr bool Held = R <= 4;
-  uint32_t held[Held ? R : 1];
-  if (Held) {
+  // 0: no block (never chosen); 1: NaN, below every number; -0 as 0
 #pragma unroll
-    for (int r = 0; r < (Held ? R : 0); ++r) held[r] = make_key(r);
+  for (int r = 0; r < R; ++r) {
+    const int i = tid + r * NT;
+    const float w = __uint_as_float(key[r]);
+    key[r] = i >= n ? 0u : i < sink || i >= n - recent ? 0xffffffffu : w == w ? order_key(w + 0.f) : 1u;
   }
-  auto key = [&](int r) -> uint32_t { return Held ? held[Held ? r : 0] : make_key(r); };
   // sums over the block of three counts of at most 16384 each
   int turn = 0;
   auto count3 = [&](uint32_t c1, uint32_t c2, uint32_t c3) {
@@ -586,7 +577,7 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r >= rows) break;
-        const uint32_t k = key(r);
+        const uint32_t k = key[r];
         c1 += k >= (T | (1u << sh));
         c2 += k >= (T | (2u << sh));
         c3 += k >= (T | (3u << sh));
@@ -597,14 +588,14 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
       else if (s.x >= keep) { T |= 1u << sh; ge = s.x; }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) stay |= (key(r) >= T && key(r) != 0u ? 1u : 0u) << r;
+    for (int r = 0; r < R; ++r) stay |= (key[r] >= T && key[r] != 0u ? 1u : 0u) << r;
     if (ge != keep) {
       // more keys equal T than fit: those of the lowest index
       uint32_t eq = 0, gt = 0;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        eq |= (key(r) == T ? 1u : 0u) << r;
-        gt += key(r) > T;
+        eq |= (key[r] == T ? 1u : 0u) << r;
+        gt += key[r] > T;
       }
       const int need = keep - count3(gt, 0, 0).x;
       int at[R];
@@ -616,6 +607,14 @@ k_evict(const __grid_constant__ CacheDev c, int32_t* table, int32_t* n_tok, floa
   } else {
 #pragma unroll
     for (int r = 0; r < R; ++r) stay |= (tid + r * NT < n ? 1u : 0u) << r;
+  }
+  int32_t id[R];
+  float w[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = tid + r * NT;
+    id[r] = i < mb ? c.table[row + i] : 0;
+    w[r] = i < mb ? c.weight[row + i] : 0.f;
   }
   int at[R];
   prefix(stay, at);   // its barriers also stand between every read and write of the tables
