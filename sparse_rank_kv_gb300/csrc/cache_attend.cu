@@ -4,10 +4,10 @@
 //
 // Memory bounds it: 2 d bytes of codes per token and KV head are read once.
 // Measured, 32 query and 8 KV heads of 128 in bf16, weights gathered: batch 8 at
-// 128K (2.15 GB) 320 us, 6.7 TB/s; batch 1 at 128K 48 us (40 at that rate); 16
-// ragged sequences of up to 9001 tokens (163 MB) 33.5 us (24 at that rate: a
+// 128K (2.15 GB) 313 us, 6.9 TB/s; batch 1 at 128K 47 us (39 at that rate); 16
+// ragged sequences of up to 9001 tokens (163 MB) 34 us (24 at that rate: a
 // few CTAs' copies come at half the speed of the others', and the shares are
-// fixed beforehand); 90 tokens 5.1 us, all latency.  16 sequences of 9001 tokens
+// fixed beforehand); 90 tokens 5.0 us, all latency.  16 sequences of 9001 tokens
 // (295 MB, 43 us at that rate): 51 us, with 64 query heads 56, fp32 57, both 67, the
 // last three bound by the softmax warps' latency.  The CUDA-core form of the
 // same split took 8.0 ms at batch 8, 128K.
@@ -208,10 +208,11 @@ struct Ca {
   static constexpr int KB = kCaT * D, Stage = 2 * KB;       // K tile, V tile
   static constexpr int QB = N1 * D, PB = N2 * kCaT;
   static constexpr int Misc = 2048;
-  // CTAs per SM: while one waits for its barriers the others compute.  Heads of
-  // 64 have half the bytes per tile for the same softmax: three where the
-  // registers allow it (112): 16 sequences of 9001 tokens 42.2 -> 36.8 us.
-  static constexpr int PerSm = D == 64 && G <= (sizeof(T) == 2 ? 4 : 2) ? 3 : 2;
+  // CTAs per SM: while one waits for its barriers the others compute; three
+  // where the registers allow it (112).  Measured against two: 16 sequences of
+  // 9001 tokens with heads of 64 42.2 -> 36.8 us, batch 8 at 128K with heads of 128
+  // 320 -> 313 us; a fourth for one or two heads of 64 gave nothing.
+  static constexpr int PerSm = G <= (sizeof(T) == 2 ? 4 : 2) ? 3 : 2;
   static constexpr int SmemMax = (228 / PerSm - 1) * 1024;
   static constexpr int NST = (SmemMax - 128 - 2 * QB - 2 * PB - Misc) / Stage;
   static constexpr int Smem = 128 + NST * Stage + 2 * QB + 2 * PB + Misc;
