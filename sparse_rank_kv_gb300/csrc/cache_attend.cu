@@ -31,10 +31,12 @@ constexpr int kCaT = 128;         // tokens per tile
 constexpr int kCaMostPerSm = 3;   // CTAs per SM, at most
 
 // Small caches: one CTA works a pair's tiles off and finishes it, without the
-// prefix sums, the partials and the second launch.  Measured, device time of
-// the split form and of this one: 8 pairs of 2 tiles 7.8 and 5.4 us, of 4 tiles
-// 7.8 and 8.2 (3 us of host time less), of 8 tiles 8.1 and 12.0; 256 pairs of
-// 4 tiles 15.9 and 9.5, of 8 tiles 19.4 and 14.0; 384 pairs of 16 tiles 40 and 44.
+// prefix sums, the partials and the second launch.  Measured with weights,
+// device time of the split form and of this one: 8 pairs of 2 tiles 8.3 and
+// 6.6 us, of 4 tiles 8.4 and 9.4 (4 us of host time less), of 8 tiles 8.6 and
+// 14.1; 152 pairs of 8 tiles 14.5 and 14.6; 256 pairs of 4 tiles 17.2 and 10.6,
+// of 8 tiles 20.6 and 16.1; 16 tiles go either way with the number of waves
+// (384 pairs 44 and 36, 512 pairs 56 and 63).
 inline bool attend_solo(const shadowkv_cache& c, int nsm) {
   const long long tiles = (static_cast<long long>(c.max_blocks) * c.block + kCaT - 1) / kCaT;
   return tiles <= 4 || (tiles <= 8 && static_cast<long long>(c.b) * c.h_kv >= nsm);
