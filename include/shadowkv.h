@@ -410,7 +410,7 @@ size_t shadowkv_cache_attend_workspace(const shadowkv_cache* c, int h_q);
  *           at the same time need workspaces of their own.
  * A pair without tokens gives zeros, an lse of -inf and no weight.
  * The products run on e4m3 operands: q and p are split into sums of e4m3 terms,
- * accumulated in fp32.  bf16: q exact, p to 2^-11 of itself and 2^-26 of the
+ * accumulated in fp32.  bf16: q exact, p to 2^-16 of itself and 2^-30 of the
  * largest p (times V scale) among its 128 tokens; f32: q to 2^-24 of itself and 2^-38 of
  * its row's largest entry, p likewise.
  * Asynchronous on `stream`; runs on the current device.

@@ -193,10 +193,10 @@ __device__ __forceinline__ float natural_lse(float M, float L) { return (M + log
 //   O = V^T P^T (M = d, K = 128 tokens),        P: PP rows per query head
 // q and p are not e4m3 numbers but sums of them: x = x0 + x1/16 + x2/256 + ...,
 // each term the e4m3 rounding of what the ones before leave, 4 bits each.
-// Two terms hold a bf16 query exactly (8 bits), three hold an fp16 p (11 bits: more than
-// the bf16 output keeps, and its split costs a third of an fp32 p's), six an
-// fp32 value; e4m3's range ends them at 2^-18 16^(1-terms) of the largest entry (of
-// a tile's p V-scale, of a q row): 2^-26 for bf16's p, 2^-38 for fp32.  Decoding has
+// Two terms hold a bf16 query exactly (8 bits), four hold p to 2^-16 of itself beside
+// a bf16 output, six an fp32 value; e4m3's range ends them at 2^-18 16^(1-terms) of
+// the largest entry (of a tile's p V-scale, of a q row): 2^-30 for bf16's p, 2^-38
+// for fp32.  Decoding has
 // G <= 8 query rows for a tile of at least 16, so the terms fill rows that
 // would be padding, and no code is ever converted.  Products of e4m3 numbers accumulate in fp32 (measured: within
 // 2^-22 of the sum of magnitudes, as an fp32 matrix product).
@@ -205,7 +205,7 @@ constexpr int kCaThreads = kCaSoft + 64;      // warp 4: copies, warp 5: tcgen05
 
 template <typename T, int D, int G>
 struct Ca {
-  static constexpr int QP = sizeof(T) == 2 ? 2 : 6, PP = sizeof(T) == 2 ? 3 : 6;
+  static constexpr int QP = sizeof(T) == 2 ? 2 : 6, PP = sizeof(T) == 2 ? 4 : 6;
   static constexpr int N1 = (G * QP + 15) / 16 * 16, N2 = (G * PP + 15) / 16 * 16;
   static constexpr int KB = kCaT * D, Stage = 2 * KB;       // K tile, V tile
   static constexpr int QB = N1 * D, PB = N2 * kCaT;
@@ -654,20 +654,22 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
 #pragma unroll
       for (int g = 0; g < G; g += 2) {
         float u = p[g] * vf, v = G > 1 ? p[g + (G > 1)] * vf : 0.f;
-        __half2 x = __floats2half2_rn(u, v);
+        __half2 x;
 #pragma unroll
         for (int i = 0; i < C::PP; ++i) {
           uint32_t c2;
-          if constexpr (sizeof(T) == 2) {
-            c2 = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
-            // (what is left has fewer bits than an fp16 holds: exact)
-            const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2), __NV_E4M3));
-            x = __hmul2(__hsub2(x, f), __float2half2_rn(16.f));
-          } else {
+          if (sizeof(T) == 4 || i == 0) {
             c2 = e4m3_pack2(u, v);
             const float2 f = e4m3_unpack2(c2);
             u = (u - f.x) * 16.f;
             v = (v - f.y) * 16.f;
+            // What the first term leaves (exact, below 2^-4 of p) as an fp16, whose 11 bits
+            // three terms hold exactly: 2^-16 of p, as four terms from fp32
+            x = __floats2half2_rn(u, v);
+          } else {
+            c2 = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+            const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2), __NV_E4M3));
+            x = __hmul2(__hsub2(x, f), __float2half2_rn(16.f));
           }
           const int n = i * G + g;
           pw[n >> 2] |= (G > 1 ? c2 : c2 & 0xffu) << (8 * (n & 3));

@@ -1,0 +1,75 @@
+"""The dense decode path where its arithmetic and its contracts are tightest.
+
+A rounding to bf16 is off by at most 2^-8 of the value, to fp32 by U = 2^-24."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import np64
+from sparse_rank_kv_gb300 import binding
+from test_gpu_dense import DT, STEP, U, _built, gen, randn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------ bits kept
+@pytest.mark.parametrize("spare", [0, 20])
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 8), (128, 1), (128, 2), (128, 4), (128, 8)])
+def test_attend_weights_keep_16_bits_in_bf16(d, G, spare):
+    """Two tokens with values 1 and -1 and logits 0 and x: out = (1 - e^x) / (1 + e^x), small
+    where x is, so that what the output loses is what the weights lose: 2^-16 of each, which
+    sum to 1 (a weight of 11 bits misses by up to 2^-13).  The exponential's 2^-21 and the
+    logit's rounding stand beside it."""
+    b, h = 16, 2
+    c = binding.BlockCache.empty(b, h, d, 1 + spare, block=64)
+    k = torch.zeros(b, h, 2, d, dtype=torch.bfloat16, device="cuda")
+    k[:, :, 1, 0] = 1
+    v = torch.ones_like(k)
+    v[:, :, 1] = -1
+    c.append(k, v)
+    g = gen(G)
+    x = torch.exp2(-6 - 3 * torch.rand(b, h * G, generator=g, device="cuda")) * torch.sign(randn(g, b, h * G))
+    q = torch.zeros(b, h * G, d, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = x
+    out = np64(c.attend(q, scale=1.0))
+    want = -np.tanh(np64(q[:, :, :1]) / 2)
+    tol = STEP[torch.bfloat16] * np.abs(want) + 2.0 ** -16 + 2.0 ** -20
+    err = np.abs(out - want)
+    assert np.all(err <= tol), f"worst {np.max(err / tol):.3g} of the tolerance"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("spare", [0, 60])
+def test_attend_token_with_the_weight_and_no_value(dtype, spare):
+    """A token of no value takes all the weight; another one of its 128, in a block of its own
+    with a V scale up to 2^8 smaller or larger, makes the output with a weight of 2^-8 to 2^-24.
+    It is off by at most 2^-16 of itself and 2^-30 of (largest weight) (largest V scale) times its
+    code of 448 (fp32: 2^-23 and 2^-38), beside logits and exponentials in fp32."""
+    b, h, G, d, dt = 32, 2, 4, 64, DT[dtype]
+    c = binding.BlockCache.empty(b, h, d, 8 + spare, block=16)
+    g = gen(7)
+    x = -8 - 16 * torch.rand(b, h, 1, generator=g, device="cuda")
+    k = torch.zeros(b, h, 128, d, device="cuda")
+    k[..., 0] = -256                                         # the others: out of the picture
+    k[:, :, 0, 0] = 0
+    k[:, :, 100, 0] = x[..., 0]
+    v = torch.zeros(b, h, 128, d, device="cuda")
+    v[:, :, 1] = 1                                           # the first block's V scale
+    v[:, :, 100] = 448 / 256 * torch.exp2(torch.randint(-8, 9, (b, h, 1), generator=g, device="cuda").float())
+    c.append(k.to(dt), v.to(dt))
+    q = torch.zeros(b, h * G, d, dtype=dt, device="cuda")
+    q[..., 0] = 1
+    scale = 0.6931471805599453
+    out = np64(c.attend(q, scale=scale))
+    # the definition on what the cache holds
+    id_ = c.table[:, :, 6].long()
+    kc = c.k_codes.view(torch.float8_e4m3fn).float()[id_][:, :, 0, 0, 4, 0].double() * c.k_scale[id_].double()
+    val = 448 * np64(c.v_scale[id_])
+    p = np.exp(np64(kc) * scale)
+    want = (p * val / (1 + p))[:, :, None]
+    big = np.maximum(2.0 ** -8, np64(c.v_scale[id_]))[:, :, None]
+    bf = dt == torch.bfloat16
+    rel = STEP[dt] + (2.0 ** -16 if bf else 2.0 ** -23) + 2.0 ** -20 + 2 * (d + 8) * U * 24 * scale
+    tol = rel * np.abs(want) + (2.0 ** -30 if bf else 2.0 ** -38) * 448 * big
+    err = np.abs(out.reshape(b, h, G * d) - want)
+    assert np.all(err <= tol), f"worst {np.max(err / tol):.3g} of the tolerance"
