@@ -350,8 +350,9 @@ skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, const shado
  * max |x| <= 448 2^e over the block's finite entries.
  *
  * A kernel that meets a table entry outside the pool or a token count outside
- * 0..max_blocks block records it in *status (see shadowkv_cache_check) and reads
- * block 0, or the nearest count, in its place.  Calls that touch the same
+ * 0..max_blocks block records it in *status (see shadowkv_cache_check).  Attention reads
+ * block 0 in such an entry's place; an append drops what belongs there (the tokens still
+ * count as held) and writes to no other block; a count is clamped.  Calls that touch the same
  * cache must be ordered (one stream, or events), except that attention calls
  * that do not gather weights may overlap each other. */
 typedef struct shadowkv_cache {

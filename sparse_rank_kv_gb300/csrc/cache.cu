@@ -321,7 +321,7 @@ k_append_many(const __grid_constant__ AppendArgs a, int per, int nrun) {
     return m;
   };
   uint32_t w[A::Words], nx[A::Words];
-  int id = cache_block(c, pair, blk);
+  int id = cache_block_or_none(c, pair, blk);
   A::load(nx, src + static_cast<long long>(blk) * B * ss, ss, which, max(n0 - blk * B, 0), min(end - blk * B, B), tid);
   for (int turn = 0; blk < last; ++blk, turn ^= 1) {
     const int e0 = max(n0 - blk * B, 0), e1 = min(end - blk * B, B);
@@ -329,11 +329,14 @@ k_append_many(const __grid_constant__ AppendArgs a, int per, int nrun) {
     for (int i = 0; i < A::Words; ++i) w[i] = nx[i];
     int id_next = 0;
     if (blk + 1 < last) {
-      id_next = cache_block(c, pair, blk + 1);
+      id_next = cache_block_or_none(c, pair, blk + 1);
       A::load(nx, src + static_cast<long long>(blk + 1) * B * ss, ss, which, 0, min(end - (blk + 1) * B, B), tid);
     }
-    float* scale = (which ? c.vs : c.ks) + id;
-    const float was = e0 > 0 ? *scale : 0.f;
+    // a block whose id is out of range is dropped: its loads and barriers are
+    // everyone's, its stores nobody's
+    const bool drop = id < 0;
+    float* scale = (which ? c.vs : c.ks) + max(id, 0);
+    const float was = e0 > 0 && !drop ? *scale : 0.f;
     // two reductions of one block use both halves of red; the next block's
     // first one, `turn` later, is behind another barrier of the group
     uint32_t m = all_max(A::top(w), turn);
@@ -347,12 +350,14 @@ k_append_many(const __grid_constant__ AppendArgs a, int per, int nrun) {
     const bool grow = e0 > 0 && sc != was;
     if (NW == 1) __syncwarp();   // every lane has read the old scale
     if (tid == 0) {
-      *scale = sc;
+      if (!drop) *scale = sc;
       if (which == 0 && e0 == 0 && c.weight) c.weight[static_cast<size_t>(pair) * c.max_blocks + blk] = 0.f;
     }
-    uint8_t* dst = (which ? c.vc : c.kc) + static_cast<size_t>(id) * (D * B);
-    if (e0 == 0 && e1 == B) A::store_full(w, dst, sc, which, tid);
-    else A::store_part(src + static_cast<long long>(blk) * B * ss, ss, dst, sc, grow, was / sc, which, e0, e1, tid);
+    uint8_t* dst = (which ? c.vc : c.kc) + static_cast<size_t>(max(id, 0)) * (D * B);
+    if (!drop) {
+      if (e0 == 0 && e1 == B) A::store_full(w, dst, sc, which, tid);
+      else A::store_part(src + static_cast<long long>(blk) * B * ss, ss, dst, sc, grow, was / sc, which, e0, e1, tid);
+    }
     id = id_next;
   }
 }
@@ -392,9 +397,9 @@ __global__ void __launch_bounds__(kApThreads) k_append_one(const __grid_constant
     if (lane == 0) append_range(a, pair, &n0, &end);
     n0 = __shfl_sync(0xffffffffu, n0, 0);
     end = __shfl_sync(0xffffffffu, end, 0);
-    if (end > n0) {
-      const int blk = n0 >> c.shift, e0 = n0 - (blk << c.shift);
-      const int id = cache_block(c, pair, blk);
+    const int blk = n0 >> c.shift, e0 = n0 - (blk << c.shift);
+    const int id = end > n0 ? cache_block_or_none(c, pair, blk) : -1;
+    if (id >= 0) {   // (a token for a block whose id is out of range is dropped)
       uint8_t* dst = (which ? c.vc : c.kc) + static_cast<size_t>(id) * (D << c.shift);
       float* scale = (which ? c.vs : c.ks) + id;
       const float was = e0 > 0 ? *scale : 0.f;
@@ -441,11 +446,10 @@ __global__ void __launch_bounds__(kApThreads) k_append_one(const __grid_constant
           w[16] = static_cast<uint8_t>(c2 >> 8);
         }
       }
-      if (lane == 0) {
-        *scale = sc;
-        if (which == 0 && e0 == 0 && c.weight) c.weight[static_cast<size_t>(pair) * c.max_blocks + blk] = 0.f;
-      }
+      if (lane == 0) *scale = sc;
     }
+    if (lane == 0 && which == 0 && end > n0 && e0 == 0 && c.weight)
+      c.weight[static_cast<size_t>(pair) * c.max_blocks + blk] = 0.f;
   }
   __syncthreads();   // both warps of a pair have read its count
   if (pair < c.pairs && which == 0 && lane == 0) c.n_tok[pair] = end;

@@ -46,12 +46,17 @@ __device__ __forceinline__ int cache_tokens(const CacheDev& c, int pair) {
   return n < 0 ? 0 : cap;
 }
 
-// Pool block of a pair's block i; an id out of range is recorded and read as 0.
-__device__ __forceinline__ int cache_block(const CacheDev& c, int pair, int i) {
+// Pool block of a pair's block i, or -1; an id out of range is recorded.
+__device__ __forceinline__ int cache_block_or_none(const CacheDev& c, int pair, int i) {
   const int id = c.table[static_cast<size_t>(pair) * c.max_blocks + i];
   if (static_cast<unsigned>(id) < static_cast<unsigned>(c.n_pool)) return id;
   flag_error(c.status, DEV_BAD_SLOT);
-  return 0;
+  return -1;
+}
+
+// The same for kernels that only read: block 0 for an id out of range.
+__device__ __forceinline__ int cache_block(const CacheDev& c, int pair, int i) {
+  return max(cache_block_or_none(c, pair, i), 0);
 }
 
 // The smallest power of two 2^e, e >= -100, with amax <= 448 2^e

@@ -73,3 +73,48 @@ def test_attend_token_with_the_weight_and_no_value(dtype, spare):
     tol = rel * np.abs(want) + (2.0 ** -30 if bf else 2.0 ** -38) * 448 * big
     err = np.abs(out.reshape(b, h, G * d) - want)
     assert np.all(err <= tol), f"worst {np.max(err / tol):.3g} of the tolerance"
+
+
+# ------------------------------------------------------------ table entries out of the pool
+def known_cache(g, b, h, d, block, max_blocks, lens):
+    """A cache of finite codes and scales, pool block 0 nobody's, lens[i] tokens held of sequence i."""
+    n = b * h * max_blocks + 1
+    codes = lambda *s: torch.randint(0, 0x70, s, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    scale = lambda: torch.exp2(torch.randint(-9, -6, (n,), generator=g, device="cuda").float())  # noqa: E731
+    table = (1 + torch.randperm(n - 1, generator=g, device="cuda")).to(torch.int32).view(b, h, max_blocks)
+    n_tok = torch.tensor(lens, dtype=torch.int32, device="cuda")[:, None].expand(b, h).contiguous()
+    return binding.BlockCache(codes(n, block // 8, d // 16, 8, 16), codes(n, block // 16, d, 16), scale(), scale(), table,
+                              n_tok, torch.full((b, h, max_blocks), 5.0, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,block", [(64, 16), (128, 64), (128, 128)])
+@pytest.mark.parametrize("s", [1, 2, 300])
+def test_append_through_a_bad_id_writes_nothing(dtype, d, block, s):
+    """The blocks whose ids are out of the pool, a held one that would be rescaled and a new one
+    among them, are dropped and recorded; every other block gets what it gets without them."""
+    b, h, mb, dt = 2, 2, 40, DT[dtype]
+    g = gen(s + d)
+    held = [block + 5, 2 * block]                             # one pair goes on in a block, one begins one
+    bad = known_cache(g, b, h, d, block, mb, held)
+    good = binding.BlockCache(*(t.clone() for t in (bad.k_codes, bad.v_codes, bad.k_scale, bad.v_scale, bad.table,
+                                                    bad.n_tok, bad.weight)))
+    lost = []
+    for i, g_, j, x in ((0, 0, 1, -1), (0, 1, 2, bad.k_scale.numel()), (1, 0, 2, 2**31 - 1), (1, 1, 3, -2**31)):
+        lost.append(int(bad.table[i, g_, j]))
+        bad.table[i, g_, j] = x
+    before = [t.clone() for t in (bad.k_codes, bad.v_codes, bad.k_scale, bad.v_scale)]
+    k, v = 100 * randn(g, b, h, s, d).to(dt), 100 * randn(g, b, h, s, d).to(dt)
+    bad.append(k, v)
+    good.append(k, v)
+    good.check()
+    keep = torch.ones(bad.k_scale.numel(), dtype=torch.bool, device="cuda")
+    keep[lost] = False
+    for name, was in zip(("k_codes", "v_codes", "k_scale", "v_scale"), before):
+        x, y = getattr(bad, name), getattr(good, name)
+        assert torch.equal(x[0], was[0]), f"{name}: block 0"
+        assert torch.equal(x[keep], y[keep]) and torch.equal(x[lost], was[lost]), name
+    assert torch.equal(bad.n_tok, good.n_tok) and torch.equal(bad.weight, good.weight)
+    with pytest.raises(binding.ShadowKVError) as e:
+        bad.check()
+    assert e.value.code == 4
