@@ -118,3 +118,25 @@ def test_append_through_a_bad_id_writes_nothing(dtype, d, block, s):
     with pytest.raises(binding.ShadowKVError) as e:
         bad.check()
     assert e.value.code == 4
+
+
+@pytest.mark.parametrize("d,block,lens", [(64, 16, [64]), (128, 64, [1500])])
+def test_attend_reads_block_0_in_a_bad_ids_place(d, block, lens):
+    """By value: what a bad id gives is what block 0 gives, and neither is what the pair's own block gives."""
+    c = known_cache(gen(3), 1, 2, d, block, 40, lens)
+    q = randn(gen(4), 1, 8, d)
+    t = c.table.clone()
+    own = c.attend(q, decay=0.0)
+    c.table[0, :, 1:3] = torch.tensor([0, 0], device="cuda")
+    want, w = c.attend(q, decay=0.0), c.weight.clone()
+    c.check()
+    c.table[0, :, 1:3] = torch.tensor([-1, 10**9], device="cuda")
+    got = c.attend(q, decay=0.0)
+    assert torch.isfinite(want).all() and not torch.equal(want, own)
+    assert torch.equal(got, want) and torch.equal(c.weight, w)
+    with pytest.raises(binding.ShadowKVError):
+        c.check()
+    c.table.copy_(t)
+    c.status.zero_()
+    assert torch.equal(c.attend(q, decay=0.0), own)
+    c.check()
