@@ -354,7 +354,9 @@ skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, const shado
  * block 0 in such an entry's place; an append drops what belongs there (the tokens still
  * count as held) and writes to no other block; a count is clamped.  Calls that touch the same
  * cache must be ordered (one stream, or events), except that attention calls
- * that do not gather weights may overlap each other. */
+ * that do not gather weights may overlap each other.  Host threads may call at
+ * the same time: a call's kernels are enqueued together, so that calls of several
+ * threads on one stream take effect one after the other. */
 typedef struct shadowkv_cache {
   int b, h_kv;        /* sequences, KV heads */
   int d;              /* head dimension: 64 or 128 */
@@ -407,8 +409,8 @@ size_t shadowkv_cache_attend_workspace(const shadowkv_cache* c, int h_q);
  *           weight[i] = decay weight[i] + sum over its tokens and the pair's query
  *           heads of p (decay = 0: the old weight is not read); needs weight.
  *   work  : device, 256-byte aligned, at least shadowkv_cache_attend_workspace bytes; its
- *           contents before and after the call mean nothing.  Calls that may run
- *           at the same time need workspaces of their own.
+ *           contents before and after the call mean nothing.  Calls on different
+ *           streams that may run at the same time need workspaces of their own.
  * A pair without tokens gives zeros, an lse of -inf and no weight.
  * The products run on e4m3 operands: q and p are split into sums of e4m3 terms,
  * accumulated in fp32.  bf16: q exact, p to 2^-16 of itself and 2^-30 of the

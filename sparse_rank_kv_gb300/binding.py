@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import threading
 from typing import Optional
 
 import numpy as np
@@ -452,7 +453,7 @@ class BlockCache:
       weight (b, h_kv, max_blocks)  float32: attention weight gathered per block, or None
 
     Copies and checkpoints are copies of these tensors.  Calls on one cache
-    must be ordered on one stream (or by events)."""
+    must be ordered on one stream (or by events), from any threads."""
 
     def __init__(self, k_codes, v_codes, k_scale, v_scale, table, n_tok, weight=None):
         if k_codes.dim() != 5 or v_codes.dim() != 4 or table.dim() != 3:
@@ -478,7 +479,7 @@ class BlockCache:
         self._desc = CacheDesc(b, h, d, block, mb, n_pool, k_codes.data_ptr(), v_codes.data_ptr(),
                                k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), n_tok.data_ptr(),
                                weight.data_ptr() if weight is not None else None, self.status.data_ptr())
-        self._work = {}
+        self._work, self._work_lock = {}, threading.Lock()
         _check(lib().shadowkv_cache_validate(self._desc))
 
     @classmethod
@@ -514,7 +515,8 @@ class BlockCache:
         """softmax(scale q K^T) V over the tokens held; q (b, h_q, d), scale 1/sqrt(d)
         by default.  decay: gather block weights, weight = decay weight + this
         call's (None: weights stay as they are).  lse (b, h_q) float32 receives the log sums.
-        The workspace comes from torch's allocator and is kept per stream; a call
+        The workspace comes from torch's allocator and is kept per stream (threads
+        that share a stream share it: their calls run one after the other there); a call
         under capture takes one of its own from the graph's memory, so that
         graphs share none."""
         if q.dim() != 3:
@@ -558,9 +560,10 @@ class BlockCache:
             t = torch.empty(nb, dtype=torch.uint8, device=self.device)
             have = (t, t.data_ptr(), nb)
             if not capturing:
-                if len(self._work) >= 8:
-                    self._work.pop(next(iter(self._work)))
-                self._work[(hq, st)] = have
+                with self._work_lock:
+                    if len(self._work) >= 8:
+                        self._work.pop(next(iter(self._work)))
+                    self._work[(hq, st)] = have
         return have
 
     def evict(self, keep: int, *, sink: int = 0, recent: int = 1, into: Optional["BlockCache"] = None,

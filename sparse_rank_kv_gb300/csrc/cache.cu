@@ -8,6 +8,7 @@
 // their inputs before their own grid-dependency wait.
 #include <cfloat>
 #include <cstdint>
+#include <mutex>
 
 #include "cache.cuh"
 #include "internal.h"
@@ -697,6 +698,10 @@ skv_status cache_checked(const shadowkv_cache* c) {
   const char* f = cache_fault(c, &st);
   return f ? set_error(st, f) : SKV_OK;
 }
+std::mutex& cache_enqueue() {
+  static std::mutex m;
+  return m;
+}
 }  // namespace skv
 
 extern "C" {
@@ -727,6 +732,7 @@ skv_status shadowkv_cache_append(const shadowkv_cache* c, int dtype, const shado
   a.lens = lens;
   a.s = s;
   cudaStream_t q = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> together(skv::cache_enqueue());
   cudaError_t e;
   if (dtype == SKV_DTYPE_BF16)
     e = c->d == 128 ? skv::append_t<skv::bf16, 128>(a, q) : skv::append_t<skv::bf16, 64>(a, q);
@@ -752,6 +758,7 @@ skv_status shadowkv_cache_evict(const shadowkv_cache* src, const shadowkv_cache*
   if (sink < 0 || recent < 0 || sink > keep || recent > keep - sink)
     return set_error(SKV_ERR_INVALID_ARG, "need sink, recent >= 0 and sink + recent <= keep");
   if (reinterpret_cast<uintptr_t>(kept) % 4) return set_error(SKV_ERR_INVALID_ARG, "kept must be 4-byte aligned");
+  std::lock_guard<std::mutex> together(skv::cache_enqueue());
   const cudaError_t e = skv::launch_evict(*src, *dst, keep, sink, recent, kept, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SKV_OK : set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
 } catch (...) {   // host memory for an error text or a table ran out

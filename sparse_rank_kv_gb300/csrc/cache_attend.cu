@@ -18,8 +18,10 @@
 // partial (max, sum, sum p v) per pair it meets, and k_attend_merge joins a
 // pair's partials in order and turns the tiles' sums of p into block weights.
 // Lengths are only known on the device: every CTA forms the prefix of the tile counts itself.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "cache.cuh"
 #include "internal.h"
@@ -880,11 +882,11 @@ static cudaError_t attend_g(const AttendArgs& a, int G, const shadowkv_cache& c,
 
 // SMs of the current device (asked once per device).
 static cudaError_t device_sms(int* n) {
-  static int have[64] = {};
+  static std::atomic<int> have[64] = {};   // (any thread may ask)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && have[dev]) { *n = have[dev]; return cudaSuccess; }
+  if (dev >= 0 && dev < 64 && (*n = have[dev])) return cudaSuccess;
   e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess && dev >= 0 && dev < 64) have[dev] = *n;
   return e;
@@ -960,6 +962,7 @@ skv_status shadowkv_cache_attend(const shadowkv_cache* c, int dtype, int h_q, co
   a.decay = decay;
   a.solo = skv::attend_solo(*c, nsm);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> together(skv::cache_enqueue());
   if (dtype == SKV_DTYPE_BF16)
     e = c->d == 128 ? skv::attend_g<skv::bf16, 128>(a, G, *c, nsm, s) : skv::attend_g<skv::bf16, 64>(a, G, *c, nsm, s);
   else

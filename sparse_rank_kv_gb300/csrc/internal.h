@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stddef.h>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -238,5 +239,10 @@ size_t svd_tc_workspace_bytes(const shadowkv_params& p, int nsm);
 cudaError_t svd_tc_basis(Ctx& c, const void* K, void* ws, cudaStream_t st);   // K: bf16 keys
 // cache.cu: the 8-bit block cache's sizes and pointers (sets the error text)
 skv_status cache_checked(const shadowkv_cache* c);
+// Held while a block cache call enqueues its kernels, so that another host
+// thread's call on the same stream does not come between them (an append's count
+// is written by its second kernel, an attention's partials are read by its own).
+// Uncontended it costs some 20 ns of a launch's 2 us.
+std::mutex& cache_enqueue();
 
 }  // namespace skv

@@ -1,13 +1,15 @@
 """The dense decode path where its arithmetic and its contracts are tightest.
 
 A rounding to bf16 is off by at most 2^-8 of the value, to fp32 by U = 2^-24."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 from helpers import np64
 from sparse_rank_kv_gb300 import binding
-from test_gpu_dense import DT, STEP, U, _built, gen, randn  # noqa: F401
+from test_gpu_dense import DT, STEP, U, _built, filled, gen, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +142,69 @@ def test_attend_reads_block_0_in_a_bad_ids_place(d, block, lens):
     c.status.zero_()
     assert torch.equal(c.attend(q, decay=0.0), own)
     c.check()
+
+
+# ------------------------------------------------------------ threads
+def in_threads(n, work):
+    """work(i) in n threads that begin together; the first exception is raised here."""
+    go, got = threading.Barrier(n), [None] * n
+
+    def one(i):
+        try:
+            go.wait()
+            got[i] = work(i)
+        except Exception as e:  # noqa: BLE001
+            got[i] = e
+
+    ts = [threading.Thread(target=one, args=(i,)) for i in range(n)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    for x in got:
+        if isinstance(x, Exception):
+            raise x
+    torch.cuda.synchronize()
+    return got
+
+
+def test_threads_attend_on_one_stream():
+    """Threads share the current stream and with it the workspace; a call of two
+    kernels gets the rows of its own query whatever the other threads enqueue."""
+    c, _ = filled(2, 2, 128, 64, [3000, 100], torch.bfloat16, seed=31)
+    n, calls = 4, 300
+    qs = [randn(gen(i), 2, 8, 128).bfloat16() for i in range(n)]
+    want = [c.attend(q) for q in qs]
+    torch.cuda.synchronize()
+    got = in_threads(n, lambda i: [c.attend(qs[i]) for _ in range(calls)])
+    for i in range(n):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_threads_attend_on_many_streams():
+    """More streams than workspaces kept: none is taken from a call in flight."""
+    c, _ = filled(2, 2, 128, 64, [3000, 100], torch.bfloat16, seed=31)
+    n = 3
+    qs = [randn(gen(i), 2, 8, 128).bfloat16() for i in range(n)]
+    want = [c.attend(q) for q in qs]
+    streams = [[torch.cuda.Stream() for _ in range(5)] for _ in range(n)]
+    torch.cuda.synchronize()
+    got = in_threads(n, lambda i: [c.attend(qs[i], stream=streams[i][t % 5]) for t in range(60)])
+    for i in range(n):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_threads_append_on_one_stream():
+    """An append of several tokens writes its counts by a second kernel: none may be
+    lost to another thread's append in between.  All tokens are alike, so that their order does not show."""
+    n, calls, s = 4, 50, 3
+    c = binding.BlockCache.empty(2, 2, 64, 40, block=16)
+    row = randn(gen(1), 1, 1, 1, 64).bfloat16()
+    k = row.expand(2, 2, s, 64)
+    in_threads(n, lambda i: [c.append(k, k) for _ in range(calls)])
+    c.check()
+    assert torch.all(c.n_tok == n * calls * s)
+    one = binding.BlockCache.empty(2, 2, 64, 40, block=16)
+    one.append(row.expand(2, 2, n * calls * s, 64), row.expand(2, 2, n * calls * s, 64))
+    for x in ("k_codes", "v_codes", "k_scale", "v_scale", "n_tok"):
+        assert torch.equal(getattr(c, x), getattr(one, x)), x
