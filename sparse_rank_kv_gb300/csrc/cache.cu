@@ -335,9 +335,8 @@ k_append_many(const __grid_constant__ AppendArgs a, int per, int nrun) {
     }
     // a block whose id is out of range is dropped: its loads and barriers are
     // everyone's, its stores nobody's
-    const bool drop = id < 0;
-    float* scale = (which ? c.vs : c.ks) + max(id, 0);
-    const float was = e0 > 0 && !drop ? *scale : 0.f;
+    float* scale = (which ? c.vs : c.ks) + id;
+    const float was = e0 > 0 && id >= 0 ? *scale : 0.f;
     // two reductions of one block use both halves of red; the next block's
     // first one, `turn` later, is behind another barrier of the group
     uint32_t m = all_max(A::top(w), turn);
@@ -351,14 +350,12 @@ k_append_many(const __grid_constant__ AppendArgs a, int per, int nrun) {
     const bool grow = e0 > 0 && sc != was;
     if (NW == 1) __syncwarp();   // every lane has read the old scale
     if (tid == 0) {
-      if (!drop) *scale = sc;
+      if (id >= 0) *scale = sc;
       if (which == 0 && e0 == 0 && c.weight) c.weight[static_cast<size_t>(pair) * c.max_blocks + blk] = 0.f;
     }
-    uint8_t* dst = (which ? c.vc : c.kc) + static_cast<size_t>(max(id, 0)) * (D * B);
-    if (!drop) {
-      if (e0 == 0 && e1 == B) A::store_full(w, dst, sc, which, tid);
-      else A::store_part(src + static_cast<long long>(blk) * B * ss, ss, dst, sc, grow, was / sc, which, e0, e1, tid);
-    }
+    uint8_t* dst = (which ? c.vc : c.kc) + static_cast<size_t>(id) * (D * B);
+    if (e0 == 0 && e1 == B && id >= 0) A::store_full(w, dst, sc, which, tid);
+    else A::store_part(src + static_cast<long long>(blk) * B * ss, ss, dst, sc, grow, was / sc, which, e0, id < 0 ? 0 : e1, tid);
     id = id_next;
   }
 }
