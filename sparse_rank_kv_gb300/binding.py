@@ -392,6 +392,12 @@ def _call(fn, t, stream, *args) -> None:
         _check(rc)
 
 
+def _on_stream(stream, device):
+    """A context in which `stream`, torch's or a raw cudaStream_t, is torch's current stream."""
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
+    return torch.cuda.stream(s)
+
+
 def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
                  k_weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6, norm: bool = True,
                  theta: float = 1e4, rot: Optional[int] = None, pos: Optional[torch.Tensor] = None,
@@ -406,6 +412,11 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight:
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
+    if stream is not None and x.is_cuda:
+        # the outputs are allocated on the stream that writes them
+        with _on_stream(stream, x.device):
+            return qk_norm_rope(q, k, q_weight, k_weight, eps=eps, norm=norm, theta=theta, rot=rot, pos=pos,
+                                q_out=q_out, k_out=k_out)
     if x.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be (b, h, s, d)")
     (b, _, s, d), dev, dtype = x.shape, x.device, x.dtype
@@ -530,8 +541,7 @@ class BlockCache:
             raise ValueError(f"tensors must be on a CUDA device, got {dev}")
         if stream is not None:
             # the output and the workspace are allocated on the stream that uses them
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), dev)
-            with torch.cuda.stream(s):
+            with _on_stream(stream, dev):
                 return self.attend(q, scale=scale, decay=decay, out=out, lse=lse)
         i = dev.index
         if _current_device() != i:

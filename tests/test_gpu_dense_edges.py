@@ -208,3 +208,25 @@ def test_threads_append_on_one_stream():
     one.append(row.expand(2, 2, n * calls * s, 64), row.expand(2, 2, n * calls * s, 64))
     for x in ("k_codes", "v_codes", "k_scale", "v_scale", "n_tok"):
         assert torch.equal(getattr(c, x), getattr(one, x)), x
+
+
+# ------------------------------------------------------------ streams
+def test_outputs_belong_to_the_stream_that_writes_them():
+    """With stream=..., what a call allocates comes from that stream's memory: the current
+    stream's pending work may still use what was freed there, and may be handed the output's
+    memory again before the other stream has written it."""
+    s = torch.cuda.Stream()
+    x = randn(gen(1), 1, 2, 700, 128).bfloat16()
+    c = binding.BlockCache.empty(1, 2, 128, 12)
+    s.wait_stream(torch.cuda.current_stream())
+    c.append(x, x, stream=s)
+    for stream in (s, s.cuda_stream):
+        q, k = binding.qk_norm_rope(x, x, stream=stream)
+        out = c.attend(x[:, :, 0], stream=stream)
+        torch.cuda.synchronize()
+        for t in (q, k, out):
+            seg = [m for m in torch.cuda.memory_snapshot()
+                   if m["address"] <= t.data_ptr() < m["address"] + m["total_size"]]
+            assert [m["stream"] for m in seg] == [s.cuda_stream]
+        a, b = binding.qk_norm_rope(x, x)
+        assert torch.equal(q, a) and torch.equal(k, b) and torch.equal(out, c.attend(x[:, :, 0]))
