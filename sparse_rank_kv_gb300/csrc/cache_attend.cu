@@ -195,10 +195,11 @@ __device__ __forceinline__ float natural_lse(float M, float L) { return (M + log
 //   O = V^T P^T (M = d, K = 128 tokens),        P: PP rows per query head
 // q and p are not e4m3 numbers but sums of them: x = x0 + x1/16 + x2/256 + ...,
 // each term the e4m3 rounding of what the ones before leave, 4 bits each.
-// Two terms hold a bf16 query exactly (8 bits), four hold p to 2^-16 of itself beside
-// a bf16 output, six an fp32 value; e4m3's range ends them at 2^-18 16^(1-terms) of
-// the largest entry (of a tile's p V-scale, of a q row): 2^-30 for bf16's p, 2^-38
-// for fp32.  Decoding has
+// Beside a bf16 output four terms hold p to 2^-16 of itself; six hold an fp32 value.
+// e4m3's range ends the terms at 2^-10 16^(1-terms) under a largest value of 256 (a
+// tile's p V-scale) or above 224 (a q row): 2^-30 and 2^-29 for bf16, 2^-38 and 2^-37
+// for fp32.  Two terms would hold a bf16 query's 8 bits, but only down to 2^-13 of
+// its row's largest; rows with an outlier have entries below that, and four hold them down to 2^-21.  Decoding has
 // G <= 8 query rows for a tile of at least 16, so the terms fill rows that
 // would be padding, and no code is ever converted.  Products of e4m3 numbers accumulate in fp32 (measured: within
 // 2^-22 of the sum of magnitudes, as an fp32 matrix product).
@@ -207,7 +208,7 @@ constexpr int kCaThreads = kCaSoft + 64;      // warp 4: copies, warp 5: tcgen05
 
 template <typename T, int D, int G>
 struct Ca {
-  static constexpr int QP = sizeof(T) == 2 ? 2 : 6, PP = sizeof(T) == 2 ? 4 : 6;
+  static constexpr int QP = sizeof(T) == 2 ? 4 : 6, PP = sizeof(T) == 2 ? 4 : 6;
   static constexpr int N1 = (G * QP + 15) / 16 * 16, N2 = (G * PP + 15) / 16 * 16;
   static constexpr int KB = kCaT * D, Stage = 2 * KB;       // K tile, V tile
   static constexpr int QB = N1 * D, PB = N2 * kCaT;
@@ -218,11 +219,11 @@ struct Ca {
   // 320 -> 313 us; a fourth for one or two heads of 64 gave nothing.
   static constexpr int PerSm = G <= (sizeof(T) == 2 ? 4 : 2) ? 3 : 2;
   static constexpr int SmemMax = (228 / PerSm - 1) * 1024;
-  static constexpr int NST = (SmemMax - 128 - 2 * QB - 2 * PB - Misc) / Stage;
-  static constexpr int Smem = 128 + NST * Stage + 2 * QB + 2 * PB + Misc;
+  static constexpr int NST = (SmemMax - 128 - QB - 2 * PB - Misc) / Stage;
+  static constexpr int Smem = 128 + NST * Stage + QB + 2 * PB + Misc;
   static constexpr int Cols0 = 2 * N1 + 2 * N2;
   static constexpr int Cols = Cols0 <= 32 ? 32 : Cols0 <= 64 ? 64 : Cols0 <= 128 ? 128 : 256;
-  static_assert(NST >= 2 && Cols0 <= 256, "attention tile");
+  static_assert(NST >= 2 && NST <= 7 && Cols0 <= 256, "attention tile");
 };
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -238,6 +239,26 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
 // K-major or (bn: bit 16) N-major
 constexpr uint32_t idesc_e4m3(int N, bool bn = false) {
   return (1u << 4) | (bn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+// x[g] = the sum of a head's products over its terms, v[i G + g] 16^-i, on pairs
+// of heads (fma.f32x2).
+template <int G, int Terms>
+__device__ __forceinline__ void join_terms(const float* v, float* x) {
+  if constexpr (G == 1) {
+    x[0] = v[Terms - 1];
+#pragma unroll
+    for (int i = Terms - 2; i >= 0; --i) x[0] = fmaf(x[0], 1.f / 16.f, v[i]);
+  } else {
+#pragma unroll
+    for (int g = 0; g < G; g += 2) {
+      const float* a = v + (Terms - 1) * G + g;
+      float2 y = make_float2(a[0], a[1]);
+#pragma unroll
+      for (int i = Terms - 2; i >= 0; --i) y = __ffma2_rn(y, make_float2(1.f / 16.f, 1.f / 16.f), make_float2(v[i * G + g], v[i * G + g + 1]));
+      x[g] = y.x;
+      x[g + 1] = y.y;
+    }
+  }
 }
 // Sum of z[g] over groups of `gran` (16 or 32) lanes: lanes exchange half of
 // their heads at each step until one is left (G = 4: 6 shuffles instead of 20).
@@ -309,8 +330,8 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   unsigned char* stages = smem;
-  unsigned char* qbuf = stages + NST * C::Stage;        // [2], by the pair's turn in this CTA
-  unsigned char* pbuf = qbuf + 2 * C::QB;               // [2], by tile
+  unsigned char* qbuf = stages + NST * C::Stage;        // the pair's q
+  unsigned char* pbuf = qbuf + C::QB;                   // [2], by tile
   unsigned char* misc = pbuf + 2 * C::PB;
   uint64_t* full = reinterpret_cast<uint64_t*>(misc);   // [NST <= 7]
   uint64_t* empty = full + 8;                           // [NST]
@@ -318,7 +339,7 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
   uint64_t* pfull = sfull + 2;
   uint64_t* ofull = pfull + 2;
   uint64_t* qfull = ofull + 2;                          // [2]
-  float* sqs = reinterpret_cast<float*>(misc + 192);    // [2][8] q scales
+  float* sqs = reinterpret_cast<float*>(misc + 192);    // [8] q scales
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 640);
   volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 644);
   int* s_where = reinterpret_cast<int*>(misc + 648);    // [3]
@@ -348,7 +369,7 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
     tc::tmem_relinquish();
   }
   // q rows past the terms stay zero
-  for (int i = tid; i < 2 * C::QB / 16; i += kCaThreads)
+  for (int i = tid; i < C::QB / 16; i += kCaThreads)
     reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0, 0, 0, 0);
   tc::fence_proxy_async_smem();
   tc::fence_before();
@@ -497,7 +518,7 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
         if (go) {
           runs = turn;
           tc::fence_after();
-          const uint32_t k0 = tc::smem_u32(stages + (i % NST) * C::Stage), q0 = tc::smem_u32(qbuf + (runs & 1) * C::QB);
+          const uint32_t k0 = tc::smem_u32(stages + (i % NST) * C::Stage), q0 = tc::smem_u32(qbuf);
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
             mma_e4m3(tS + (i & 1) * N1, tc::desc_k_none(k0 + k * 256, 128, 8 * D),
@@ -545,7 +566,7 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
         for (int e = 0; e < D / 32; e += 2) {
           float u = x[e] * inv, v = x[e + 1] * inv;
           const int j = lane + 32 * e;
-          unsigned char* dst = qbuf + (turn & 1) * C::QB + (j >> 4) * (N1 * 16) + (j & 15);
+          unsigned char* dst = qbuf + (j >> 4) * (N1 * 16) + (j & 15);
 #pragma unroll
           for (int i = 0; i < C::QP; ++i) {
             const uint32_t c2 = e4m3_pack2(u, v);
@@ -556,7 +577,7 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
             v = (v - f.y) * 16.f;
           }
         }
-        if (lane == 0) sqs[(turn & 1) * 8 + g] = s * a.scale_log2;
+        if (lane == 0) sqs[g] = s * a.scale_log2;
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
@@ -574,16 +595,12 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
       ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&ofull[j & 1], (j >> 1) & 1, kWaitLimit));
       if (!ok) return;
       tc::fence_after();
-      float o[N2];
+      float o[N2], x[G];
 #pragma unroll
       for (int c = 0; c < N2; c += 16) tc::tmem_ld16(tO + (j & 1) * N2 + c, o + c);
+      join_terms<G, C::PP>(o, x);
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        float x = o[(C::PP - 1) * G + g];
-#pragma unroll
-        for (int i = C::PP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, o[i * G + g]);
-        acc[g] = fmaf(acc[g], al[g], x * be[g]);
-      }
+      for (int g = 0; g < G; ++g) acc[g] = fmaf(acc[g], al[g], x[g] * be[g]);
     };
     // (a wait that gave up shows at the next barrier, so that all 128 threads
     // leave together)
@@ -609,15 +626,11 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
 #pragma unroll
         for (int c = 0; c < N1; c += 16) tc::tmem_ld16(tS + (it & 1) * N1 + c, v + c);
         const float ks = sc[blk];
-        float qs[G];
-        load_heads<G>(sqs + (turn & 1) * 8, qs);
+        float qs[G], x[G];
+        load_heads<G>(sqs, qs);
+        join_terms<G, C::QP>(v, x);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float x = v[(C::QP - 1) * G + g];
-#pragma unroll
-          for (int i = C::QP - 2; i >= 0; --i) x = fmaf(x, 1.f / 16.f, v[i * G + g]);
-          s[g] = tid < cnt ? x * (qs[g] * ks) : -INFINITY;
-        }
+        for (int g = 0; g < G; ++g) s[g] = tid < cnt ? x[g] * (qs[g] * ks) : -INFINITY;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const float x = redux_max(s[g]);
@@ -704,8 +717,8 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&pfull[it & 1]);
-      // the next pair's q, so that its S can start while this pair ends (the
-      // buffer's last reader was the S of the pair before)
+      // the next pair's q, so that its S can start while this pair ends (this
+      // tile's S, which is here, was the last reader of the pair's own)
       if ((flags & (kLast | kEnd)) == kLast) lay_q(info.w, turn + 1);
       if (!(flags & kFirst)) take_o(it - 1);
 #pragma unroll

@@ -40,6 +40,32 @@ def test_attend_weights_keep_16_bits_in_bf16(d, G, spare):
     assert np.all(err <= tol), f"worst {np.max(err / tol):.3g} of the tolerance"
 
 
+@pytest.mark.parametrize("dtype,exact,floor", [("bf16", 2.0 ** -21, 2.0 ** -29), ("f32", 0.0, 2.0 ** -37)])
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 4), (128, 2), (128, 4), (128, 8)])
+def test_attend_queries_with_an_outlier(dtype, exact, floor, d, G):
+    """A query entry far below its row's largest, whose keys are zero, makes the logit alone:
+    lse of the one token is q_1 k_1.  A bf16 entry is exact down to 2^-21 of the row's largest and
+    within 2^-29 of that one below (fp32: 2^-24 of itself, 2^-37 of the largest); the product
+    itself takes the roundings of the scaling and of log2 to ln."""
+    b, h, dt = 32, 2, DT[dtype]
+    c = binding.BlockCache.empty(b, h, d, 1, block=16)
+    k = torch.zeros(b, h, 1, d, dtype=dt, device="cuda")
+    k[..., 1] = 1
+    c.append(k, k)
+    g = gen(d + G)
+    q = torch.zeros(b, h * G, d, dtype=dt, device="cuda")
+    q[..., 0] = 9984                                          # 312 under the row's scale of 32
+    q[..., 1] = torch.exp2(-26 * torch.rand(b, h * G, generator=g, device="cuda")) * 5000 * torch.sign(randn(g, b, h * G))
+    lse = torch.empty(b, h * G, device="cuda")
+    c.attend(q, scale=1.0, lse=lse)
+    want = np64(q[..., 1])
+    tol = 16 * U * np.abs(want) + np.where(np.abs(want) >= exact * 9984, 0 if exact else U * np.abs(want), floor * 9984)
+    if not exact:
+        tol += floor * 9984
+    err = np.abs(np64(lse) - want)
+    assert np.all(err <= tol), f"worst {np.max(err / tol):.3g} of the tolerance"
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("spare", [0, 60])
 def test_attend_token_with_the_weight_and_no_value(dtype, spare):
