@@ -414,8 +414,9 @@ size_t shadowkv_cache_attend_workspace(const shadowkv_cache* c, int h_q);
  * A pair without tokens gives zeros, an lse of -inf and no weight.
  * The products run on e4m3 operands: q and p are split into sums of e4m3 terms,
  * accumulated in fp32.  bf16: an entry of q exact from 2^-21 of its row's largest on and
- * to 2^-29 of that below, p to 2^-16 of itself and 2^-30 of the
- * largest p (times V scale) among its 128 tokens; f32: q to 2^-24 of itself and 2^-37 of
+ * to 2^-29 of that below, p times its V scale to 2^-16 of
+ * itself and 2^-30 of the largest p times the largest V scale among its 128 tokens (each
+ * the largest by itself: they may be different tokens'); f32: q to 2^-24 of itself and 2^-37 of
  * its row's largest entry, p to 2^-23 and 2^-38.  (A row's largest counts as 2^-92 at least.)
  * Asynchronous on `stream`; runs on the current device.
  */

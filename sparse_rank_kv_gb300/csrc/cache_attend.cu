@@ -197,7 +197,7 @@ __device__ __forceinline__ float natural_lse(float M, float L) { return (M + log
 // each term the e4m3 rounding of what the ones before leave, 4 bits each.
 // Beside a bf16 output four terms hold p to 2^-16 of itself; six hold an fp32 value.
 // e4m3's range ends the terms at 2^-10 16^(1-terms) under a largest value of 256 (a
-// tile's p V-scale) or above 224 (a q row): 2^-30 and 2^-29 for bf16, 2^-38 and 2^-37
+// tile's largest p and largest V scale, whichever tokens have them) or above 224 (a q row): 2^-30 and 2^-29 for bf16, 2^-38 and 2^-37
 // for fp32.  Two terms would hold a bf16 query's 8 bits, but only down to 2^-13 of
 // its row's largest; rows with an outlier have entries below that, and four hold them down to 2^-21.  Decoding has
 // G <= 8 query rows for a tile of at least 16, so the terms fill rows that
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
     int turn = 0;
     // running maximum, sum and output of the pair's run; p is relative to its own
     // tile's maximum, whatever larger one came before (a token with most of
-    // the weight and little value must not push the others' terms out)
+    // the weight and little value must not push other tiles' terms out)
     float m[G], l[G], acc[G], al[G], be[G];
     // adds tile j's O to the run's sums
     auto take_o = [&](int j) {
