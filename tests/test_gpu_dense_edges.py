@@ -256,3 +256,136 @@ def test_outputs_belong_to_the_stream_that_writes_them():
             assert [m["stream"] for m in seg] == [s.cuda_stream]
         a, b = binding.qk_norm_rope(x, x)
         assert torch.equal(q, a) and torch.equal(k, b) and torch.equal(out, c.attend(x[:, :, 0]))
+
+
+# ------------------------------------------------------------ the attention's ring and its two forms
+def cache_of_codes(g, lens, h, d, block):
+    """A cache of random codes under scales of 2^-9 to 2^-7, blocks in any order, lens[i] tokens of each head of sequence i."""
+    b, mb = len(lens), -(-max(lens) // block)
+    n = sum(-(-x // block) for x in lens) * h + 1
+    codes = lambda *s: torch.randint(0, 0x70, s, generator=g, device="cuda", dtype=torch.uint8) | (  # noqa: E731
+        torch.randint(0, 2, s, generator=g, device="cuda", dtype=torch.uint8) << 7)
+    scale = lambda: torch.exp2(torch.randint(-9, -6, (n,), generator=g, device="cuda").float())  # noqa: E731
+    ids, at = (torch.randperm(n - 1, generator=g, device="cuda") + 1).to(torch.int32), 0
+    table = torch.zeros(b, h, mb, dtype=torch.int32, device="cuda")
+    for i, x in enumerate(lens):
+        nb = -(-x // block)
+        table[i, :, :nb] = ids[at:at + h * nb].view(h, nb)
+        at += h * nb
+    n_tok = torch.tensor(lens, dtype=torch.int32, device="cuda")[:, None].expand(b, h).contiguous()
+    return binding.BlockCache(codes(n, block // 8, d // 16, 8, 16), codes(n, block // 16, d, 16), scale(), scale(), table, n_tok,
+                              torch.full((b, h, mb), 3.0, device="cuda"))
+
+
+def attend_pair(c, q, scale, i, j):
+    """The definition in 64 bits, on the GPU, for query heads q (G, d) of pair (i, j): out, lse, block weights, sum p |v|,
+    the largest logit's sum of magnitudes, and the sum over 128-token tiles of the largest p times the largest 448 V scale."""
+    n = int(c.n_tok[i, j])
+    nb = -(-n // c.block)
+    ids = c.table[i, j, :nb].long()
+    f8 = lambda t: t.view(torch.float8_e4m3fn).float().double()  # noqa: E731
+    k = (f8(c.k_codes[ids]).permute(0, 1, 3, 2, 4).reshape(nb, c.block, c.d) * c.k_scale[ids].double()[:, None, None]).reshape(-1, c.d)[:n]
+    v = (f8(c.v_codes[ids]).permute(0, 1, 3, 2).reshape(nb, c.block, c.d) * c.v_scale[ids].double()[:, None, None]).reshape(-1, c.d)[:n]
+    q = q.double()
+    z = scale * (q @ k.T)
+    lse = torch.logsumexp(z, -1)
+    p = torch.exp(z - lse[:, None])
+    pad = lambda x, m: torch.nn.functional.pad(x, (0, -(-x.shape[-1] // m) * m - x.shape[-1]))  # noqa: E731
+    w = pad(p, c.block).view(len(q), nb, c.block).sum((0, 2))
+    tile = pad(p, 128).view(len(q), -1, 128).amax(-1)
+    vs = pad(c.v_scale[ids].double()[None], 128 // c.block).view(-1, 128 // c.block).amax(-1)
+    return p @ v, lse, w, p @ v.abs(), abs(scale) * (q.abs() @ k.abs().T).amax(-1), (tile * 448 * vs).sum(-1)
+
+
+def attend_as_defined(c, q, scale, tiles_per_share, parts):
+    """One call with its weights against the definition.  A logit takes d roundings of its sum and 8 of
+    its scaling, p as much twice and an exponential's 2^-21; a share's sum takes per tile two
+    roundings and, where the maximum moves, an exponential (2^-22), the join one per part.  p itself:
+    2^-16 (bf16) or 2^-22 and the floor of its tile."""
+    bf = q.dtype == torch.bfloat16
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = c.attend(q, scale=scale, decay=0.0, lse=lse)
+    w = c.weight.clone()
+    G = q.shape[1] // c.h_kv
+    run = 2.0 ** -20 + tiles_per_share * (2.0 ** -22 + 2 * U) + (64 + parts) * U
+    for i in range(c.b):
+        for j in range(c.h_kv):
+            n, hs = int(c.n_tok[i, j]), slice(j * G, (j + 1) * G)
+            nb = -(-n // c.block)
+            assert torch.all(w[i, j, nb:] == 3.0)
+            if n == 0:
+                assert not out[i, hs].any() and torch.all(lse[i, hs] == -float("inf"))
+                continue
+            o, l, wb, mag, lm, top = attend_pair(c, q[i, hs], scale, i, j)
+            dl = (c.d + 8) * U * lm
+            p = 2 * dl + run + (2.0 ** -16 if bf else 2.0 ** -22)
+            tol = STEP[q.dtype] * o.abs() + p[:, None] * mag + (128 * 2.0 ** (-30 if bf else -38) * top)[:, None] + 1e-30
+            err = (out[i, hs].double() - o).abs()
+            assert torch.all(err <= tol), f"out {i, j}: worst {float((err / tol).max()):.3g} of the tolerance"
+            assert torch.all((lse[i, hs].double() - l).abs() <= dl + run + 8 * U * l.abs()), f"lse {i, j}"
+            err = (w[i, j, :nb].double() - wb).abs()
+            assert torch.all(err <= (2 * dl.max() + run + 128 * U) * wb + 1e-30), f"weights {i, j}"
+    return out, w
+
+
+@pytest.mark.parametrize("dtype,d,G,block", [
+    ("bf16", 64, 1, 32), ("bf16", 64, 4, 64), ("bf16", 64, 8, 64), ("bf16", 128, 1, 128), ("bf16", 128, 2, 32),
+    ("bf16", 128, 4, 64), ("bf16", 128, 8, 32), ("f32", 64, 1, 64), ("f32", 64, 4, 32), ("f32", 64, 8, 128),
+    ("f32", 128, 1, 32), ("f32", 128, 4, 128), ("f32", 128, 8, 64)])
+def test_attend_turns_its_ring_many_times(dtype, d, G, block):
+    """A CTA's share is three times its stages or more (2 to 6 stages, two or three CTAs per SM),
+    and pairs of no, one and a few tiles end and begin inside shares; twice the same bits."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles = (36 if d == 64 else 18) * sms                    # 18 per CTA at two CTAs per SM, 12 at three; half for d = 128
+    few = [1, 0, 127, 128, 129, 300, 64, 5, 1000, 2, 640, 0, 17]
+    rest = tiles * 128 - 2 * sum(few)
+    lens = [rest // 2 + 1, *few, rest // 3, *few[::-1], rest - rest // 2 - rest // 3 + 77]
+    g = gen(d + G)
+    c = cache_of_codes(g, lens, 1, d, block)
+    q = randn(g, len(lens), G, d).to(DT[dtype])
+    out, w = attend_as_defined(c, q, 0.5, 40, 3 * sms)
+    assert torch.equal(c.attend(q, scale=0.5, decay=0.0), out) and torch.equal(c.weight, w)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,h,G,block,lens", [
+    (64, 2, 8, 16, [496, 183]), (64, 1, 1, 32, [512, 0, 1]), (128, 2, 4, 128, [512, 129, 385]), (128, 3, 2, 64, [300, 448]),
+    (64, 4, 4, 64, [64, 65, 511]), (128, 1, 8, 16, [481])])
+def test_attend_in_one_launch_and_in_two(dtype, d, h, G, block, lens):
+    """The same tokens under a table of four tiles per pair, which one CTA finishes, and under one of many, whose
+    shares a second launch joins."""
+    g = gen(d + G)
+    c = cache_of_codes(g, lens, h, d, block)
+    q = randn(g, len(lens), h * G, d).to(DT[dtype])
+    for mb in (512 // block, 4096 // block):
+        table = torch.zeros(len(lens), h, mb, dtype=torch.int32, device="cuda")
+        table[:, :, :c.max_blocks] = c.table
+        x = binding.BlockCache(c.k_codes, c.v_codes, c.k_scale, c.v_scale, table, c.n_tok, torch.full_like(table, 3, dtype=torch.float32))
+        attend_as_defined(x, q, 0.5, 4, 4)
+        x.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_wide_queries_and_scales(dtype):
+    """Query entries over 2^20 and V scales over 2^16 inside a tile, some of them zero: beside the
+    usual roundings the row's floor (2^-29 or 2^-37 of the largest entry, times sum |k|) moves the logits."""
+    d, h, G, dt = 128, 2, 4, DT[dtype]
+    g = gen(5)
+    c = cache_of_codes(g, [900, 128, 77], h, d, 16)
+    c.v_scale.copy_(torch.exp2(torch.randint(-16, 1, c.v_scale.shape, generator=g, device="cuda").float()) * (torch.rand(c.v_scale.shape, generator=g, device="cuda") > 0.1))
+    q = (randn(g, 3, h * G, d) * torch.exp2(-20 * torch.rand(3, h * G, d, generator=g, device="cuda"))).to(dt)
+    lse = torch.empty(3, h * G, device="cuda")
+    out = c.attend(q, scale=0.5, lse=lse)
+    bf = dt == torch.bfloat16
+    for i in range(3):
+        for j in range(h):
+            hs = slice(j * G, (j + 1) * G)
+            o, l, _, mag, lm, top = attend_pair(c, q[i, hs], 0.5, i, j)
+            ones = attend_pair(c, q[i, hs].abs().amax(-1, keepdim=True).expand(G, d), 0.5, i, j)[4]   # largest entry x sum |k|
+            dl = (d + 8) * U * lm + 2.0 ** (-29 if bf else -37) * ones
+            p = 2 * dl + 2.0 ** -19 + 128 * U + (2.0 ** -16 if bf else 2.0 ** -22)
+            tol = STEP[dt] * o.abs() + p[:, None] * mag + (128 * 2.0 ** (-30 if bf else -38) * top)[:, None] + 1e-30
+            err = (out[i, hs].double() - o).abs()
+            assert torch.all(err <= tol), f"out {i, j}: worst {float((err / tol).max()):.3g} of the tolerance"
+            assert torch.all((lse[i, hs].double() - l).abs() <= dl + 2.0 ** -20 + 8 * U * l.abs())
