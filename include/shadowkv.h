@@ -284,8 +284,8 @@ skv_status shadowkv_attention_noalloc(const shadowkv_params* p, const void* q, c
 /* -------------------------------------------- queries and keys for a step
  * A b x h x s x d tensor given by strides: element (i, g, t, j) lies at
  * ptr + i sb + g sh + t ss + j (strides in elements, not negative; the d
- * elements of a row are adjacent).  A projection's output b x s x (h d) read
- * in place has sh = d. */
+ * elements of a row are adjacent; the stride of an extent of 1 is not used).  A
+ * projection's output b x s x (h d) read in place has sh = d. */
 typedef struct shadowkv_rows {
   void* ptr;
   long long sb, sh, ss;

@@ -404,8 +404,8 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight:
                  q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
     """Norm of every query and key head and its rotation to the token's position.
 
-    q (b, h_q, s, d) and k (b, h_kv, s, d), float32 or bfloat16, of any strides
-    with d contiguous; either may be None.  The weights have d elements.  pos: int32, (b,)
+    q (b, h_q, s, d) and k (b, h_kv, s, d), float32 or bfloat16, d contiguous, the
+    other strides (and the outputs') multiples of 4 elements; either may be None.  The weights have d elements.  pos: int32, (b,)
     first positions or (b, s), or None for 0..s-1.  rot: rotated dimensions
     (default d; 0: none).  The outputs are made like the inputs, contiguous,
     unless given; returns (q_out, k_out)."""
@@ -510,8 +510,8 @@ class BlockCache:
                           self.n_tok.clone(), None if self.weight is None else self.weight.clone())
 
     def append(self, k: torch.Tensor, v: torch.Tensor, lens: Optional[torch.Tensor] = None, stream=None) -> None:
-        """Appends s tokens to every pair: k, v (b, h_kv, s, d), any strides with
-        d contiguous; lens (b,) int32: tokens of each sequence (default all s)."""
+        """Appends s tokens to every pair: k, v (b, h_kv, s, d), d contiguous, the
+        other strides multiples of 16 bytes; lens (b,) int32: tokens of each sequence (default all s)."""
         if k.dim() != 4:
             raise ValueError("k and v must be (b, h_kv, s, d)")
         s = k.shape[2]

@@ -678,11 +678,13 @@ const char* cache_fault(const shadowkv_cache* c, skv_status* st) {
   return nullptr;
 }
 
-// Rows read 16 bytes at a time.
-const char* rows16_fault(const shadowkv_rows* r, int E) {
+// Rows read 16 bytes at a time, of b sequences, h heads and s tokens (the stride
+// of a single one is not looked at).
+const char* rows16_fault(const shadowkv_rows* r, int b, int h, int s, int E) {
   if (!r || !r->ptr) return "k and v must be non-NULL";
-  if (r->sb < 0 || r->sh < 0 || r->ss < 0) return "row strides must not be negative";
-  if (reinterpret_cast<uintptr_t>(r->ptr) % 16 || (r->sb * E) % 16 || (r->sh * E) % 16 || (r->ss * E) % 16)
+  const long long sb = b > 1 ? r->sb : 0, sh = h > 1 ? r->sh : 0, ss = s > 1 ? r->ss : 0;
+  if (sb < 0 || sh < 0 || ss < 0) return "row strides must not be negative";
+  if (reinterpret_cast<uintptr_t>(r->ptr) % 16 || (sb * E) % 16 || (sh * E) % 16 || (ss * E) % 16)
     return "row pointers and strides must be multiples of 16 bytes";
   return nullptr;
 }
@@ -718,8 +720,8 @@ skv_status shadowkv_cache_append(const shadowkv_cache* c, int dtype, const shado
   if (s < 0) return set_error(SKV_ERR_INVALID_ARG, "s must be >= 0");
   if (s == 0) return SKV_OK;
   const int E = dtype == SKV_DTYPE_BF16 ? 2 : 4;
-  const char* f = rows16_fault(k, E);
-  if (!f) f = rows16_fault(v, E);
+  const char* f = rows16_fault(k, c->b, c->h_kv, s, E);
+  if (!f) f = rows16_fault(v, c->b, c->h_kv, s, E);
   if (!f && reinterpret_cast<uintptr_t>(lens) % 4) f = "lens must be 4-byte aligned";
   if (f) return set_error(SKV_ERR_INVALID_ARG, f);
   skv::AppendArgs a;

@@ -239,13 +239,15 @@ static const RopeFreq& rope_freq(float theta, int rot) {
 }
 
 // b x heads x s x d rows of E-byte elements: pointer and strides in whole
-// 4-element pieces; an output's tokens must not share rows.
+// 4-element pieces (a stride nothing is reached by, of one sequence, head or
+// token, is not looked at); an output's tokens must not share rows.
 static const char* rows_fault(const shadowkv_rows& r, int b, int h, int s, int E, bool out) {
   if (!r.ptr) return "a row pointer is NULL";
   if (reinterpret_cast<uintptr_t>(r.ptr) % (4 * E)) return "row pointers must be aligned to 4 elements";
-  if (r.sb < 0 || r.sh < 0 || r.ss < 0) return "row strides must not be negative";
-  if (r.sb % 4 || r.sh % 4 || r.ss % 4) return "row strides must be multiples of 4 elements";
-  if (out && ((b > 1 && !r.sb) || (h > 1 && !r.sh) || (s > 1 && !r.ss))) return "an output stride is 0";
+  const long long sb = b > 1 ? r.sb : 4, sh = h > 1 ? r.sh : 4, ss = s > 1 ? r.ss : 4;
+  if (sb < 0 || sh < 0 || ss < 0) return "row strides must not be negative";
+  if (sb % 4 || sh % 4 || ss % 4) return "row strides must be multiples of 4 elements";
+  if (out && (!sb || !sh || !ss)) return "an output stride is 0";
   return nullptr;
 }
 

@@ -389,3 +389,25 @@ def test_attend_wide_queries_and_scales(dtype):
             err = (out[i, hs].double() - o).abs()
             assert torch.all(err <= tol), f"out {i, j}: worst {float((err / tol).max()):.3g} of the tolerance"
             assert torch.all((lse[i, hs].double() - l).abs() <= dl + 2.0 ** -20 + 8 * U * l.abs())
+
+
+# ------------------------------------------------------------ calls the interface allows
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strides_of_single_sequences_heads_and_tokens_do_not_matter(dtype):
+    """One token of one sequence cut from a row of odd length: the odd strides belong to extents of 1."""
+    dt = DT[dtype]
+    n = 6 * 64 + 1
+    qkv = randn(gen(1), n).to(dt).as_strided((1, 6, 1, 64), (n, 64, n, 1))
+    same = qkv.contiguous()
+    q, k = binding.qk_norm_rope(qkv[:, :4], qkv[:, 4:5])
+    a, b = binding.qk_norm_rope(same[:, :4], same[:, 4:5])
+    assert torch.equal(q, a) and torch.equal(k, b)
+    caches = [binding.BlockCache.empty(1, 1, 64, 2, block=16) for _ in range(2)]
+    for c, y in zip(caches, (qkv, same)):
+        c.append(y[:, 4:5], y[:, 5:])
+    c, e = caches
+    assert torch.equal(c.k_codes, e.k_codes) and torch.equal(c.v_codes, e.v_codes) and torch.equal(c.n_tok, e.n_tok)
+    assert torch.equal(c.attend(qkv[:, :4, 0]), e.attend(same[:, :4, 0]))
+    odd = torch.zeros(n, dtype=dt, device="cuda").as_strided((1, 4, 1, 64), (n, 64, n, 1))
+    binding.qk_norm_rope(qkv[:, :4], None, q_out=odd)
+    assert torch.equal(odd, q)
