@@ -463,8 +463,17 @@ class BlockCache:
       n_tok (b, h_kv)               int32: tokens held
       weight (b, h_kv, max_blocks)  float32: attention weight gathered per block, or None
 
-    Copies and checkpoints are copies of these tensors.  Calls on one cache
+    Copies and checkpoints are copies of these tensors.  The calls use the memory
+    the tensors had at the start, so the attributes cannot be given other tensors:
+    copy into them, or make another cache.  Calls on one cache
     must be ordered on one stream (or by events), from any threads."""
+
+    _MEMORY = frozenset(("k_codes", "v_codes", "k_scale", "v_scale", "table", "n_tok", "weight", "status"))
+
+    def __setattr__(self, name, value):
+        if name in self._MEMORY and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} names the cache's memory: copy into it, or make another BlockCache")
+        super().__setattr__(name, value)
 
     def __init__(self, k_codes, v_codes, k_scale, v_scale, table, n_tok, weight=None):
         if k_codes.dim() != 5 or v_codes.dim() != 4 or table.dim() != 3:

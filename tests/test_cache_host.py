@@ -194,3 +194,20 @@ def test_oracle_eviction_by_hand():
     assert D.evict([0, 3, 5, 3, 1], 70, 16, 2, 0, 0) == ([1, 2], 32)
     assert D.evict([0, float("nan"), float("-inf"), 3, 1], 70, 16, 4, 0, 0) == ([0, 2, 3, 4], 3 * 16 + 6)
     assert D.evict([1, 1], 20, 16, 2, 0, 1) == ([0, 1], 20)
+
+
+def test_cache_tensors_cannot_be_exchanged():
+    """The calls hold the tensors' addresses: another tensor under the attribute would leave them
+    on memory that nobody owns. In-place changes are the cache's own."""
+    c = binding.BlockCache.empty(1, 2, 64, 3, block=16, device="cpu")
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale", "table", "n_tok", "weight", "status"):
+        t = getattr(c, name)
+        with pytest.raises(AttributeError, match=name):
+            setattr(c, name, t.clone())
+        assert getattr(c, name) is t
+    c.weight += 1
+    c.table[0, 0] = c.table[0, 0].flip(0)
+    assert c.weight.sum() == 6 and c.fork().table is not c.table
+    bare = binding.BlockCache(c.k_codes, c.v_codes, c.k_scale, c.v_scale, c.table, c.n_tok)
+    with pytest.raises(AttributeError, match="weight"):
+        bare.weight = c.weight
