@@ -369,8 +369,14 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return dt
 
 
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _torch_fn(name: str, public):
+    """torch's own short cut of that name where this build has it, else the public function."""
+    return getattr(torch._C, name, None) or public
+
+
+_current_device = _torch_fn("_cuda_getDevice", torch.cuda.current_device)
+_current_stream = _torch_fn("_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+_capturing = _torch_fn("_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _call(fn, t, stream, *args) -> None:
@@ -570,7 +576,7 @@ class BlockCache:
 
     def _workspace(self, hq: int, st: int):
         """(tensor, pointer, bytes) of attend's workspace on the current stream st."""
-        capturing = torch._C._cuda_isCurrentStreamCapturing()
+        capturing = _capturing()
         have = None if capturing else self._work.get((hq, st))
         if have is None:
             nb = lib().shadowkv_cache_attend_workspace(self._desc, hq)

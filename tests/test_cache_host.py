@@ -211,3 +211,10 @@ def test_cache_tensors_cannot_be_exchanged():
     bare = binding.BlockCache(c.k_codes, c.v_codes, c.k_scale, c.v_scale, c.table, c.n_tok)
     with pytest.raises(AttributeError, match="weight"):
         bare.weight = c.weight
+
+
+def test_torch_short_cuts_have_public_stand_ins():
+    import torch
+    assert binding._torch_fn("_no_such_function", torch.cuda.current_device) is torch.cuda.current_device
+    for f in (binding._current_device, binding._current_stream, binding._capturing):
+        assert callable(f)
