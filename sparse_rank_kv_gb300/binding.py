@@ -379,16 +379,17 @@ _current_stream = _torch_fn("_cuda_getCurrentRawStream", lambda i: torch.cuda.cu
 _capturing = _torch_fn("_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
+def _handle(stream) -> int:
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _call(fn, t, stream, *args) -> None:
     """fn(*args, cudaStream_t) with tensor t's device current; stream None:
     torch's current stream of that device."""
     if not t.is_cuda:
         raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
     i = t.get_device()
-    if stream is None:
-        st = _current_stream(i)
-    else:
-        st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    st = _current_stream(i) if stream is None else _handle(stream)
     if i == _current_device():
         rc = fn(*args, st)
     else:
@@ -400,8 +401,9 @@ def _call(fn, t, stream, *args) -> None:
 
 def _on_stream(stream, device):
     """A context in which `stream`, torch's or a raw cudaStream_t, is torch's current stream."""
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
-    return torch.cuda.stream(s)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_handle(stream), device)
+    return torch.cuda.stream(stream)
 
 
 def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
@@ -418,7 +420,8 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight:
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
-    if stream is not None and x.is_cuda:
+    if (stream is not None and x.is_cuda and (q is not None and q_out is None or k is not None and k_out is None)
+            and _handle(stream) != _current_stream(x.get_device())):
         # the outputs are allocated on the stream that writes them
         with _on_stream(stream, x.device):
             return qk_norm_rope(q, k, q_weight, k_weight, eps=eps, norm=norm, theta=theta, rot=rot, pos=pos,

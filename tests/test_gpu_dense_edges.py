@@ -411,3 +411,24 @@ def test_strides_of_single_sequences_heads_and_tokens_do_not_matter(dtype):
     odd = torch.zeros(n, dtype=dt, device="cuda").as_strided((1, 4, 1, 64), (n, 64, n, 1))
     binding.qk_norm_rope(qkv[:, :4], None, q_out=odd)
     assert torch.equal(odd, q)
+
+
+def test_norm_rope_on_a_stream_with_outputs_given():
+    """With nothing to allocate the call goes to the stream as it is: handles of any kind, one output given and one made."""
+    class Handle:
+        def __init__(self, s):
+            self.cuda_stream = s.cuda_stream
+
+    x = randn(gen(1), 2, 3, 50, 128).bfloat16()
+    want, _ = binding.qk_norm_rope(x, None)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = [torch.empty_like(x) for _ in range(4)]
+    s.wait_stream(torch.cuda.current_stream())
+    binding.qk_norm_rope(x, None, q_out=outs[0], stream=s)
+    binding.qk_norm_rope(x, x, q_out=outs[1], k_out=outs[2], stream=s.cuda_stream)
+    a, b = binding.qk_norm_rope(x, x, q_out=outs[3], stream=Handle(s))
+    s.synchronize()
+    assert a is outs[3]
+    for t in (*outs, b):
+        assert torch.equal(t, want)
