@@ -451,7 +451,7 @@ skv_status shadowkv_cache_check(const shadowkv_cache* c);
 int shadowkv_num_kernels(void);
 const char* shadowkv_kernel_name(int id);
 /* With SKV_OPT_TIMING on: total milliseconds and launch count per kernel id
- * since the last reset (arrays of n entries).  Synchronizes.  With K/V
+ * since the last reset (arrays of n entries), of the context's own kernels.  Synchronizes.  With K/V
  * records (bf16, d = 128) the value fetch runs inside the "attention" launch
  * (or, with SKV_OPT_SPLIT_TOKENS set, inside the "rebuild" launch), and
  * "fetch" counts no launches.  The events recorded between launches

@@ -5,11 +5,11 @@
 // Memory bounds it: 2 d bytes of codes per token and KV head are read once.
 // Measured, 32 query and 8 KV heads of 128 in bf16, weights gathered: batch 8 at
 // 128K (2.15 GB) 313 us, 6.9 TB/s; batch 1 at 128K 47 us (39 at that rate); 16
-// ragged sequences of up to 9001 tokens (163 MB) 34 us (24 at that rate: a
+// ragged sequences of up to 9001 tokens (163 MB) 34.4 us (24 at that rate: a
 // few CTAs' copies come at half the speed of the others', and the shares are
-// fixed beforehand); 90 tokens 5.0 us, all latency.  16 sequences of 9001 tokens
-// (295 MB, 43 us at that rate): 51 us, with 64 query heads 56, fp32 57, both 67, the
-// last three bound by the softmax warps' latency.  The CUDA-core form of the
+// fixed beforehand); 90 tokens 5.1 us, all latency.  16 sequences of 9001 tokens
+// (295 MB, 43 us at that rate): 51 us, with 64 query heads 57, fp32 51, both 66; heads
+// of 64 (22 at that rate) 37.7.  The softmax warps' latency bounds those above 51 and the last.  The CUDA-core form of the
 // same split took 8.0 ms at batch 8, 128K.
 //
 // Every pair's tokens are cut into 128-token tiles; the tiles of all pairs, in
@@ -214,7 +214,9 @@ struct Ca {
   static constexpr int QB = N1 * D, PB = N2 * kCaT;
   static constexpr int Misc = 2048;
   // CTAs per SM: while one waits for its barriers the others compute; three
-  // where the registers allow it (112).  Measured against two: 16 sequences of
+  // where the registers allow it: 18 warps on four schedulers leave 96 each, which
+  // bf16 with four heads and fp32 with two keep to (fp32 with four takes 111 to
+  // 114, bf16 with eight 146).  Measured against two: 16 sequences of
   // 9001 tokens with heads of 64 42.2 -> 36.8 us, batch 8 at 128K with heads of 128
   // 320 -> 313 us; a fourth for one or two heads of 64 gave nothing.
   static constexpr int PerSm = G <= (sizeof(T) == 2 ? 4 : 2) ? 3 : 2;
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
     // (of the CTA's tiles of that pair), kEnd and, above them, the next tile's pair.
     // lane = block of the tile; block ids are loaded two tiles ahead, the
     // blocks' scales one ahead.  The codes are read once: evicted first from
-    // L2 (without: 338 us instead of 322 at batch 8, 128K)
+    // L2 (338 us without and 322 with it, at batch 8, 128K and two CTAs per SM)
     TileCursor cur, nx1, nx2;
     cur.begin(a.c, s_where[0], s_where[1], ntile);
     auto tokens = [&](const TileCursor& c) { return c.left > 0 ? max(0, min(kCaT, c.ntok - c.tile * kCaT)) : 0; };
@@ -679,7 +681,9 @@ __global__ void __launch_bounds__(kCaThreads, (Ca<T, D, G>::PerSm)) k_attend(con
             u = (u - f.x) * 16.f;
             v = (v - f.y) * 16.f;
             // What the first term leaves (exact, below 2^-4 of p) as an fp16, whose 11 bits
-            // three terms hold exactly: 2^-16 of p, as four terms from fp32
+            // three terms hold exactly: 2^-16 of p, as four terms from fp32 in half the
+            // operations.  (p as one fp16 in three terms, 2^-11: 1% faster, and it shows in the output where
+            // values cancel)
             x = __floats2half2_rn(u, v);
           } else {
             c2 = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);

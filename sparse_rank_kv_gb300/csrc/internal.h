@@ -146,8 +146,10 @@ size_t attn_smem_bytes(int E, int G, int D, int S, int max_splits);
 skv_status set_error(skv_status st, const char* msg);
 
 // ------------------------------------------------------------ launch hooks
-// Every launcher brackets its kernel with kbegin/kend (api.cu): they count
-// the launch and, with timing on, record CUDA events on the launch stream.
+// Every launcher of a context brackets its kernel with kbegin/kend (api.cu):
+// they count the launch and, with timing on, record CUDA events on the launch
+// stream.  The calls without a context (attention_noalloc, norm and rotation,
+// the block cache) are neither counted nor timed.
 void kbegin(Ctx& c, int kid, cudaStream_t st);
 void kend(Ctx& c, int kid, cudaStream_t st);
 int num_sms(const Ctx& c);
