@@ -319,7 +319,7 @@ typedef struct shadowkv_norm_rope_params {
  *                    strides); otherwise no output overlaps an input or the other output.
  * Everything is computed in fp32 and rounded once (a row whose sum of squares
  * passes fp32's range, |x| above about 1e18, gives zeros); the angle is reduced in
- * 64-bit integers and is exact to 2^-30 of a turn at any position.  Row
+ * 64-bit integers and is exact to 2^-30 of a turn at any position (theta >= 1).  Row
  * pointers and strides must be multiples of 4 elements, and pointers aligned
  * to 4 elements (SKV_ERR_INVALID_ARG).  b = 0 or s = 0 does nothing.
  * Asynchronous on `stream`; runs on the current device.
@@ -403,7 +403,8 @@ size_t shadowkv_cache_attend_workspace(const shadowkv_cache* c, int h_q);
  *   out = sum_t p_t V_t,  p = softmax_t(scale q . K_t)  over the pair's tokens,
  * query head g reading KV head g / (h_q / h_kv); h_q / h_kv in {1, 2, 4, 8}.
  *   dtype : SKV_DTYPE_F32 or SKV_DTYPE_BF16, of q and out.
- *   q, out: device rows b x h_q x 1 x d (ss is not used), aligned to their elements.
+ *   q, out: device rows b x h_q x 1 x d (ss is not used), aligned to their elements;
+ *           out may be q itself (same pointer and strides), else it does not overlap q.
  *   lse   : device f32, b x h_q: log sum_t exp(scale q . K_t), or NULL.
  *   gather, decay : with gather = 1 every block i that holds tokens gets
  *           weight[i] = decay weight[i] + sum over its tokens and the pair's query

@@ -38,8 +38,8 @@ __device__ __forceinline__ void rope_turn(long long pos, unsigned long long f, f
   const uint32_t quarter = (u + 0x20000000u) >> 30;
   const float r = static_cast<float>(static_cast<int32_t>(u - (quarter << 30)));
   float s, c;
-  // the hardware sine and cosine are within 2^-21 here: enough for results
-  // that are rounded to bf16
+  // the hardware sine and cosine: within an eighth of a turn their errors are
+  // absolute, near 2^-22, far below a bf16 result's rounding; fp32 keeps small sines, too
   if (kFast) __sincosf(r * (6.283185307179586f / 4294967296.f), &s, &c);
   else sincospif(r * (2.f / 4294967296.f), &s, &c);
   const float a = quarter & 1 ? c : s, b = quarter & 1 ? s : c;

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from helpers import np64
+from oracle import dense_oracle as D
 from sparse_rank_kv_gb300 import binding
 from test_gpu_dense import DT, STEP, U, _built, filled, gen, randn  # noqa: F401
 
@@ -432,3 +433,29 @@ def test_norm_rope_on_a_stream_with_outputs_given():
     assert a is outs[3]
     for t in (*outs, b):
         assert torch.equal(t, want)
+
+
+def test_rotation_keeps_fp32_factors_in_bf16():
+    """Where the two products cancel, the result's own rounding is small and shows the factors: sine and
+    cosine within 2 ulp of the reduced angle (2^-23) and the angle to 2^-25, two products and a
+    sum in fp32 (2 U of the terms)."""
+    g = gen(2)
+    b, s, h, d = 4, 2048, 4, 128
+    x = randn(g, b, h, s, d).bfloat16()
+    pos = torch.randint(0, 2**31 - 1, (b, s), generator=g, device="cuda", dtype=torch.int32)
+    got, _ = binding.qk_norm_rope(x, None, norm=False, theta=5e5, pos=pos)
+    ref, mag = D.norm_rope(np64(x), None, 0, False, 5e5, d, pos.cpu().numpy().astype(np.float64))
+    tol = STEP[torch.bfloat16] * np.abs(ref) + (2.0 ** -23 + 2.0 ** -25 + 2 * U) * mag
+    err = np.abs(np64(got) - ref)
+    assert np.all(err <= tol), f"worst {np.max(err / tol):.3g} of the tolerance"
+
+
+@pytest.mark.parametrize("spare", [0, 60])
+def test_attend_output_over_its_own_query(spare):
+    c = cache_of_codes(gen(1), [500, 77], 2, 64, 64)
+    table = torch.zeros(2, 2, 8 + spare, dtype=torch.int32, device="cuda")
+    table[:, :, :8] = c.table
+    c = binding.BlockCache(c.k_codes, c.v_codes, c.k_scale, c.v_scale, table, c.n_tok)
+    q = randn(gen(2), 2, 8, 64).bfloat16()
+    want = c.attend(q)
+    assert c.attend(q, out=q) is q and torch.equal(q, want)
