@@ -443,8 +443,79 @@ skv_status shadowkv_cache_attend(const shadowkv_cache* c, int dtype, int h_q, co
 skv_status shadowkv_cache_evict(const shadowkv_cache* src, const shadowkv_cache* dst, int keep, int sink,
                                 int recent, int32_t* kept, void* stream);
 
+/* ------------------------------------------------ a pool that sequences share
+ * The calls above take a table as it is.  Those below keep one over a pool that may be
+ * smaller than all tables together, whose blocks several sequences may name:
+ *   refs : device int32, n_pool: the table entries that name each block.  A block with
+ *          refs 0 is free.
+ * A table entry of -1 names no block.  An empty cache of this kind has tables of
+ * -1, refs of 0 and n_tok of 0.  Every call leaves refs as the entries say; eviction in
+ * place does too (an evicted block stays in its pair's table, and with it its reference, until
+ * shadowkv_cache_truncate), one into another cache's tables does not.
+ * Before an append, shadowkv_cache_reserve gives every pair the blocks it writes to;
+ * without it an append through -1 is dropped and recorded, and one into a block that
+ * others name changes theirs. */
+
+/*
+ * Forks: sequence dst[k] becomes a copy of sequence src[k] (tokens, weights) that names
+ * the same blocks, k < n; no codes are moved.  What dst[k] named before is given back.
+ *   src, dst : device int32, n each; n <= b.
+ * All sources are read as they were before the call: a dst[k] that is any source, that an earlier
+ * dst names too, or a number outside 0..b-1 leaves fork k out and is recorded in *status.
+ * Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_cache_share(const shadowkv_cache* c, int32_t* refs, int n, const int32_t* src, const int32_t* dst,
+                                void* stream);
+
+/* Bytes of workspace shadowkv_cache_reserve needs for s tokens (0 if the arguments are not valid). */
+size_t shadowkv_cache_reserve_workspace(const shadowkv_cache* c, int s);
+
+/*
+ * Room for an append of s tokens per sequence (lens as there): the blocks from the one the next
+ * token goes to, as far as the tokens reach, become the pair's own, a partly filled one
+ * also where lens is 0.  An entry of -1, and one whose block others name too,
+ * gets a free block: the lowest ones, in order of sequence, head and entry; a
+ * partly filled block is copied first (codes and scales).  Blocks this call gives
+ * back are free for later calls.
+ *   granted : device int32, b: lens[i] (s without lens) where sequence i has its blocks, else 0:
+ *          the lens to append with.  A sequence gets all its blocks or none: those of the sequences
+ *          up to it, granted or not, have to be free (one that needs none is always granted).  One whose
+ *          tokens would pass max_blocks block, or whose partly filled block is missing (recorded), needs
+ *          none and is not granted.
+ *   work  : device, 256-byte aligned, at least shadowkv_cache_reserve_workspace bytes; its contents
+ *          before and after mean nothing.
+ * Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_cache_reserve(const shadowkv_cache* c, int32_t* refs, int s, const int32_t* lens, int32_t* granted,
+                                  void* work, size_t work_bytes, void* stream);
+
+/*
+ * Takes tokens off the end of every sequence: n_tok = max(n_tok - drop[i], 0) for each of
+ * its pairs.  Table entries past the tokens are given back and become -1, their weights 0.
+ *   refs  : NULL for a cache whose pool is not shared: its tables stay as they are.
+ *   drop  : device int32, b (a negative one counts as 0 and is recorded); NULL: none, which
+ *           gives back what eviction and unused reservations hold.
+ * Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_cache_truncate(const shadowkv_cache* c, int32_t* refs, const int32_t* drop, void* stream);
+
+/* Bytes of workspace shadowkv_cache_compact needs (0 if the arguments are not valid). */
+size_t shadowkv_cache_compact_workspace(const shadowkv_cache* src);
+
+/*
+ * Moves a cache to a pool of another size: the blocks in use (refs > 0), in order,
+ * become blocks 0, 1, ... of dst's pool, and dst gets the tables (with the new numbers), counts,
+ * weights (0 where src keeps none) and references.  dst's blocks behind them stay as they were; their references are 0.
+ * Where dst's pool has too few blocks, dst becomes an empty cache, recorded in its status.
+ * dst has src's b, h_kv, d, block and max_blocks, and memory of its own.
+ *   work  : as above, of shadowkv_cache_compact_workspace bytes.
+ * Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_cache_compact(const shadowkv_cache* src, const int32_t* refs, const shadowkv_cache* dst,
+                                  int32_t* dst_refs, void* work, size_t work_bytes, void* stream);
+
 /* Synchronizes the current device and reads the cache's status word;
- * SKV_ERR_DEVICE_CHECK if a kernel recorded an id, a length or a token count out of range. */
+ * SKV_ERR_DEVICE_CHECK if a kernel recorded an id, a length, a token count or a sequence out of range, or too small a pool. */
 skv_status shadowkv_cache_check(const shadowkv_cache* c);
 
 /* ------------------------------------------------------ timing / counting */

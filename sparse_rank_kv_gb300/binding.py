@@ -131,6 +131,12 @@ def lib() -> ctypes.CDLL:
             "shadowkv_cache_attend": (I, [P(CacheDesc), I, I, P(Rows), ctypes.c_float, I, ctypes.c_float,
                                           P(Rows), V, V, S, V]),
             "shadowkv_cache_evict": (I, [P(CacheDesc), P(CacheDesc), I, I, I, V, V]),
+            "shadowkv_cache_share": (I, [P(CacheDesc), V, I, V, V, V]),
+            "shadowkv_cache_reserve_workspace": (S, [P(CacheDesc), I]),
+            "shadowkv_cache_reserve": (I, [P(CacheDesc), V, I, V, V, V, S, V]),
+            "shadowkv_cache_truncate": (I, [P(CacheDesc), V, V, V]),
+            "shadowkv_cache_compact_workspace": (S, [P(CacheDesc)]),
+            "shadowkv_cache_compact": (I, [P(CacheDesc), V, P(CacheDesc), V, V, S, V]),
             "shadowkv_cache_check": (I, [P(CacheDesc)]),
         }
         for name, (res, args) in sig.items():
@@ -333,7 +339,9 @@ def _step_calls():
         fns = {}
         for name, args in (("qk_norm_rope", [V] * 9), ("cache_append", [C, I, V, V, I, V, V]),
                            ("cache_attend", [C, I, I, V, F, I, F, V, V, V, S, V]),
-                           ("cache_evict", [C, C, I, I, I, V, V])):
+                           ("cache_evict", [C, C, I, I, I, V, V]), ("cache_share", [C, V, I, V, V, V]),
+                           ("cache_reserve", [C, V, I, V, V, V, S, V]), ("cache_truncate", [C, V, V, V]),
+                           ("cache_compact", [C, V, C, V, V, S, V])):
             fn = L["shadowkv_" + name]      # a function object of its own, beside lib()'s
             fn.restype, fn.argtypes = I, args
             fns[name] = fn
@@ -471,20 +479,22 @@ class BlockCache:
       table (b, h_kv, max_blocks)   int32: the pool block of each pair's blocks
       n_tok (b, h_kv)               int32: tokens held
       weight (b, h_kv, max_blocks)  float32: attention weight gathered per block, or None
+      refs (n_pool,)                int32: the table entries that name each pool block, for a pool
+                                    that sequences share (its tables hold -1 for no block), or None
 
     Copies and checkpoints are copies of these tensors.  The calls use the memory
     the tensors had at the start, so the attributes cannot be given other tensors:
     copy into them, or make another cache.  Calls on one cache
     must be ordered on one stream (or by events), from any threads."""
 
-    _MEMORY = frozenset(("k_codes", "v_codes", "k_scale", "v_scale", "table", "n_tok", "weight", "status"))
+    _MEMORY = frozenset(("k_codes", "v_codes", "k_scale", "v_scale", "table", "n_tok", "weight", "refs", "status"))
 
     def __setattr__(self, name, value):
         if name in self._MEMORY and self.__dict__.get(name, value) is not value:
             raise AttributeError(f"{name} names the cache's memory: copy into it, or make another BlockCache")
         super().__setattr__(name, value)
 
-    def __init__(self, k_codes, v_codes, k_scale, v_scale, table, n_tok, weight=None):
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, table, n_tok, weight=None, refs=None):
         if k_codes.dim() != 5 or v_codes.dim() != 4 or table.dim() != 3:
             raise ValueError("k_codes must have 5 dimensions, v_codes 4 and table 3")
         n_pool, b8, d16, _, _ = k_codes.shape
@@ -499,10 +509,11 @@ class BlockCache:
         for name, t, shape, dt in (("k_scale", k_scale, (n_pool,), torch.float32),
                                    ("v_scale", v_scale, (n_pool,), torch.float32),
                                    ("table", table, (b, h, mb), torch.int32), ("n_tok", n_tok, (b, h), torch.int32),
-                                   ("weight", weight, (b, h, mb), torch.float32)):
+                                   ("weight", weight, (b, h, mb), torch.float32),
+                                   ("refs", refs, (n_pool,), torch.int32)):
             _dense(t, name, shape, dt, dev)
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
-        self.table, self.n_tok, self.weight = table, n_tok, weight
+        self.table, self.n_tok, self.weight, self.refs = table, n_tok, weight, refs
         self.b, self.h_kv, self.d, self.block, self.max_blocks, self.device = b, h, d, block, mb, dev
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._desc = CacheDesc(b, h, d, block, mb, n_pool, k_codes.data_ptr(), v_codes.data_ptr(),
@@ -521,9 +532,22 @@ class BlockCache:
                    z(n), z(n), torch.arange(n, dtype=torch.int32, device=dev).view(b, h_kv, max_blocks),
                    z(b, h_kv, dtype=torch.int32), z(b, h_kv, max_blocks))
 
+    @classmethod
+    def pooled(cls, b: int, h_kv: int, d: int, max_blocks: int, n_pool: int, block: int = 64, device="cuda"):
+        """A cache without tokens over a pool of n_pool free blocks that its sequences share."""
+        dev = torch.device(device)
+        z = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype, device=dev)  # noqa: E731
+        return cls(z(n_pool, block // 8, d // 16, 8, 16, dtype=torch.uint8),
+                   z(n_pool, block // 16, d, 16, dtype=torch.uint8), z(n_pool), z(n_pool),
+                   torch.full((b, h_kv, max_blocks), -1, dtype=torch.int32, device=dev), z(b, h_kv, dtype=torch.int32),
+                   z(b, h_kv, max_blocks), z(n_pool, dtype=torch.int32))
+
     def fork(self) -> "BlockCache":
         """A cache with tables, counts and weights of its own over the same pool.
-        Blocks the two share must not be appended to."""
+        Blocks the two share must not be appended to.  (Not for a pool with reference
+        counts: share() forks its sequences.)"""
+        if self.refs is not None:
+            raise ValueError("the pool's references count one cache's tables: fork sequences with share()")
         return BlockCache(self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.table.clone(),
                           self.n_tok.clone(), None if self.weight is None else self.weight.clone())
 
@@ -601,13 +625,80 @@ class BlockCache:
         that takes the table, counts and weights (default: in place).  kept (b, h_kv, keep) int32
         receives the old index of each block still held, then -1."""
         kp = _dense(kept, "kept", (self.b, self.h_kv, keep), torch.int32, self.device)
+        if into is not None and into is not self and (self.refs is not None or into.refs is not None):
+            raise ValueError("the pool's references count one cache's tables: evict in place")
         dst = None if into is None else into._desc
         if into is not None and into.device != self.device:
             raise ValueError(f"into is on {into.device}, expected {self.device}")
         _call((_step or _step_calls())["cache_evict"], self.n_tok, stream, self._desc, dst, keep, sink, recent, kp)
 
+    def _counts(self) -> torch.Tensor:
+        if self.refs is None:
+            raise ValueError("the cache's pool keeps no reference counts (refs)")
+        return self.refs
+
+    def share(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+        """Forks: sequence dst[k] becomes a copy of sequence src[k] that names the same
+        blocks; src, dst (n,) int32.  A dst that is any source, or named twice,
+        is left out and recorded (check())."""
+        refs, n = self._counts(), src.numel()
+        sp, dp = _dense(src, "src", (n,), torch.int32, self.device), _dense(dst, "dst", (n,), torch.int32, self.device)
+        _call((_step or _step_calls())["cache_share"], self.n_tok, stream, self._desc, refs.data_ptr(), n, sp, dp)
+
+    def reserve(self, s: int, lens: Optional[torch.Tensor] = None, granted: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """Room for an append of s tokens to every sequence (lens (b,) int32: of each): the blocks it
+        writes to, and partly filled ones in any case, become the pairs' own, free ones or copies.  Returns granted (b,) int32: lens
+        where the pool had the blocks, else 0, to append with."""
+        refs = self._counts()
+        lp = _dense(lens, "lens", (self.b,), torch.int32, self.device)
+        if self.device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {self.device}")
+        if stream is not None and _handle(stream) != _current_stream(self.device.index):
+            # the output and the workspace are allocated on the stream that uses them
+            with _on_stream(stream, self.device):
+                return self.reserve(s, lens, granted)
+        if granted is None:
+            granted = torch.empty(self.b, dtype=torch.int32, device=self.device)
+        gp = _dense(granted, "granted", (self.b,), torch.int32, self.device)
+        work = self._scratch(lib().shadowkv_cache_reserve_workspace(self._desc, s))
+        _call((_step or _step_calls())["cache_reserve"], self.n_tok, None, self._desc, refs.data_ptr(), s, lp, gp,
+              work.data_ptr(), work.numel())
+        return granted
+
+    def truncate(self, drop: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Takes drop[i] tokens (drop (b,) int32, default none) off the end of every sequence i; blocks past the
+        tokens go back to a shared pool."""
+        dp = _dense(drop, "drop", (self.b,), torch.int32, self.device)
+        _call((_step or _step_calls())["cache_truncate"], self.n_tok, stream, self._desc,
+              None if self.refs is None else self.refs.data_ptr(), dp)
+
+    def compact(self, into: "BlockCache", stream=None) -> None:
+        """Moves the cache to `into`, a cache of the same sizes over a pool of another size:
+        the blocks in use become its blocks 0, 1, ...; self stays as it is."""
+        refs, to = self._counts(), into._counts()
+        if into.device != self.device:
+            raise ValueError(f"into is on {into.device}, expected {self.device}")
+        if self.device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {self.device}")
+        if stream is not None and _handle(stream) != _current_stream(self.device.index):
+            with _on_stream(stream, self.device):   # for the workspace
+                return self.compact(into)
+        work = self._scratch(lib().shadowkv_cache_compact_workspace(self._desc))
+        _call((_step or _step_calls())["cache_compact"], self.n_tok, None, self._desc, refs.data_ptr(), into._desc,
+              to.data_ptr(), work.data_ptr(), work.numel())
+
+    def _scratch(self, nb: int) -> torch.Tensor:
+        """A workspace from torch's allocator, for one call on the current stream."""
+        if nb == 0:
+            _check(1)
+        return torch.empty(nb, dtype=torch.uint8, device=self.device)
+
     def reset(self) -> None:
         """Drops every token (on torch's current stream)."""
+        if self.refs is not None:
+            self.truncate(torch.full((self.b,), 2**31 - 1, dtype=torch.int32, device=self.device))
+            return
         self.n_tok.zero_()
 
     def check(self) -> None:

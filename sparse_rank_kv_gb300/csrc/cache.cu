@@ -773,6 +773,9 @@ skv_status shadowkv_cache_check(const shadowkv_cache* c) try {
   if (e == cudaSuccess) e = cudaMemcpy(&word, c->status, sizeof(int), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
   if (word == skv::DEV_TIMEOUT) return set_error(SKV_ERR_TIMEOUT, "a bounded device wait gave up");
+  if (word == skv::DEV_BAD_SEQUENCE)
+    return set_error(SKV_ERR_DEVICE_CHECK, "a call met a sequence number out of range or named twice");
+  if (word == skv::DEV_POOL_FULL) return set_error(SKV_ERR_DEVICE_CHECK, "the pool has fewer blocks than are in use");
   if (word) return set_error(SKV_ERR_DEVICE_CHECK, "a kernel met a block id, length or token count out of range");
   return SKV_OK;
 } catch (...) {   // host memory for an error text or a table ran out

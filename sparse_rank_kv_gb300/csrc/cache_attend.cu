@@ -898,7 +898,7 @@ static cudaError_t attend_g(const AttendArgs& a, int G, const shadowkv_cache& c,
 }
 
 // SMs of the current device (asked once per device).
-static cudaError_t device_sms(int* n) {
+cudaError_t device_sms(int* n) {
   static std::atomic<int> have[64] = {};   // (any thread may ask)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -18,6 +18,8 @@ enum : int {
   DEV_BAD_COUNT = 4,
   DEV_TIMEOUT = 5,      // a bounded mbarrier wait gave up
   DEV_NUMERIC = 6,      // the SVD's orthonormalisation met a non-positive pivot
+  DEV_BAD_SEQUENCE = 7, // a sequence's number out of range, or named twice
+  DEV_POOL_FULL = 8,    // a pool has fewer blocks than are in use
 };
 
 // Nanoseconds a bounded mbarrier wait lasts before a kernel gives up and

@@ -246,5 +246,7 @@ skv_status cache_checked(const shadowkv_cache* c);
 // is written by its second kernel, an attention's partials are read by its own).
 // Uncontended it costs some 20 ns of a launch's 2 us.
 std::mutex& cache_enqueue();
+// SMs of the current device (cache_attend.cu)
+cudaError_t device_sms(int* n);
 
 }  // namespace skv

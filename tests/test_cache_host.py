@@ -218,3 +218,39 @@ def test_torch_short_cuts_have_public_stand_ins():
     assert binding._torch_fn("_no_such_function", torch.cuda.current_device) is torch.cuda.current_device
     for f in (binding._current_device, binding._current_stream, binding._capturing):
         assert callable(f)
+
+
+@pytest.mark.parametrize("call,args,code", [
+    ("share", dict(n=-1), 1), ("share", dict(n=3), 1), ("share", dict(refs=None), 1), ("share", dict(src=None), 1),
+    ("share", dict(dst=P + 2), 1), ("share", dict(c=dict(d=96)), 7),
+    ("truncate", dict(refs=P + 1), 1), ("truncate", dict(drop=P + 2), 1), ("truncate", dict(c=dict(b=0)), 1),
+    ("reserve", dict(s=-1), 1), ("reserve", dict(refs=None), 1), ("reserve", dict(granted=None), 1),
+    ("reserve", dict(lens=P + 3), 1), ("reserve", dict(work=None), 1), ("reserve", dict(work=P + 8), 1),
+    ("reserve", dict(nb=255), 1), ("reserve", dict(c=dict(block=48)), 7), ("reserve", dict(c=dict(n_pool=(1 << 30) + 1)), 7),
+    ("reserve", dict(s=1 << 30, c=dict(b=1 << 12, max_blocks=16384 * 2)), 7),
+    ("compact", dict(to=dict(b=1)), 1), ("compact", dict(to=dict(d=64)), 1), ("compact", dict(to=dict(block=32)), 1),
+    ("compact", dict(to=dict(max_blocks=9)), 1), ("compact", dict(to={}), 1), ("compact", dict(refs=None), 1),
+    ("compact", dict(to_refs=None), 1), ("compact", dict(work=P + 128), 1), ("compact", dict(nb=100), 1),
+    ("compact", dict(to=dict(n_pool=0)), 1), ("compact", dict(c=dict(n_pool=(1 << 30) + 1)), 7),
+])
+def test_pool_calls_refuse(lib, call, args, code):
+    other = {f: 2 * P for f in ("k_codes", "v_codes", "k_scale", "v_scale", "table", "n_tok", "weight", "status")}
+    a = dict(c={}, n=1, src=P, dst=P, refs=P, drop=P, s=4, lens=P, granted=P, work=P, nb=1 << 40, to=other, to_refs=2 * P)
+    a.update(args)
+    if call == "compact" and a["to"] and a["to"] is not other:
+        a["to"] = dict(other, **a["to"])
+    c = desc(**a["c"])
+    got = {"share": lambda: lib.shadowkv_cache_share(c, a["refs"], a["n"], a["src"], a["dst"], None),
+           "truncate": lambda: lib.shadowkv_cache_truncate(c, a["refs"], a["drop"], None),
+           "reserve": lambda: lib.shadowkv_cache_reserve(c, a["refs"], a["s"], a["lens"], a["granted"], a["work"], a["nb"], None),
+           "compact": lambda: lib.shadowkv_cache_compact(c, a["refs"], desc(**a["to"]), a["to_refs"], a["work"], a["nb"], None)}
+    assert got[call]() == code
+    assert lib.shadowkv_last_error().decode()
+
+
+def test_pool_workspaces(lib):
+    assert lib.shadowkv_cache_reserve_workspace(desc(), -1) == 0 == lib.shadowkv_cache_reserve_workspace(desc(b=0), 1)
+    assert lib.shadowkv_cache_compact_workspace(desc(d=96)) == 0
+    assert lib.shadowkv_cache_reserve_workspace(desc(), 0) == lib.shadowkv_cache_reserve_workspace(desc(), 1) > 0
+    assert lib.shadowkv_cache_compact_workspace(desc()) >= 2 * 4 * 160
+    assert lib.shadowkv_cache_share(desc(), P, 0, None, None, None) == 0        # no forks: no call
