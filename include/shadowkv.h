@@ -518,6 +518,51 @@ skv_status shadowkv_cache_compact(const shadowkv_cache* src, const int32_t* refs
  * SKV_ERR_DEVICE_CHECK if a kernel recorded an id, a length, a token count or a sequence out of range, or too small a pool. */
 skv_status shadowkv_cache_check(const shadowkv_cache* c);
 
+/* ------------------------------------------------ verification of drafted tokens */
+typedef struct shadowkv_verify_params {
+  int b, s;            /* sequences, drafted tokens of each at most */
+  int vocab;           /* tokens of the vocabulary: 1..2^19 */
+  int dtype;           /* SKV_DTYPE_F32 or SKV_DTYPE_BF16, of the logits */
+  double temperature;  /* of every sequence, where no temperatures are given; 0: greedy */
+  long long logits_sb, logits_ss;   /* strides of sequences and positions, in elements */
+  long long probs_sb, probs_ss;
+} shadowkv_verify_params;
+
+/* Bytes of workspace shadowkv_verify_drafts needs (0 if the arguments are not valid). */
+size_t shadowkv_verify_workspace(const shadowkv_verify_params* p);
+
+/*
+ * How many of a sequence's drafted tokens stand, and the token that follows them, such
+ * that the tokens are distributed as if sampled one by one from the target (speculative sampling):
+ *   p_j = softmax(logits_j / T); T = 0: 1 at the first largest logit, else 0;
+ *   draft x_j stands if those before it do and accept_j q_j(x_j) < p_j(x_j);
+ *   the next token is drawn from p_n if all n stand, else from max(p_a - q_a, 0), a being the
+ *   first that does not (p_a, if that is 0 everywhere): the lowest v with sum_{w <= v} > sample times the total.
+ *   logits : device, b x (s + 1) x vocab, the vocab elements of a row adjacent; row j follows j drafts.
+ *            NaN counts as -inf, +inf as the largest float.
+ *   drafts : device int32, b x s; one outside the vocabulary does not stand.
+ *   probs  : device f32, b x s x vocab: q_j, the distributions the drafts were sampled from; or
+ *            NULL: drafts that were not sampled (looked up): q_j is 1 at x_j.  A negative or NaN entry
+ *            counts as 0 in what is left of p_a.
+ *   accept, sample : device f32, b x s and b: random numbers in [0, 1).  An accept that is NaN
+ *            does not stand; a sample below 0 or NaN counts as 0, one of 1 or more as the largest below 1.
+ *   lens   : device int32, b: drafts of each sequence (clamped to 0..s; nothing is read past them); NULL: s each.
+ *   temperatures : device f32, b, or NULL.  One below 1e-30 or NaN counts as 0.
+ *   tokens : device int32, b x (s + 1): the drafts that stand, the next token, then -1.  A row without a
+ *            logit above -inf accepts nothing and gives -1.
+ *   accepted : device int32, b: drafts that stand.
+ *   work   : device, 256-byte aligned, at least shadowkv_verify_workspace bytes; its contents before
+ *            and after mean nothing.
+ * The sampled row's weights exp((l - max) / T) are whole numbers of 2^-43, each within 2^-37 of
+ * itself, and their sums exact; acceptance is decided to 2^-36 of its border.  Results do not depend on
+ * timing.  b (s + 1) <= 65535 (SKV_ERR_UNSUPPORTED).
+ * b = 0 does nothing.  Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_verify_drafts(const shadowkv_verify_params* p, const void* logits, const int32_t* drafts,
+                                  const float* probs, const float* accept, const float* sample, const int32_t* lens,
+                                  const float* temperatures, int32_t* tokens, int32_t* accepted, void* work,
+                                  size_t work_bytes, void* stream);
+
 /* ------------------------------------------------------ timing / counting */
 /* Kernels are numbered 0..shadowkv_num_kernels()-1 with stable names. */
 int shadowkv_num_kernels(void);

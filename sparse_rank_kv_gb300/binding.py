@@ -77,6 +77,12 @@ class CacheDesc(ctypes.Structure):
                 ("status", ctypes.c_void_p)]
 
 
+class VerifyParams(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int), ("s", ctypes.c_int), ("vocab", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("temperature", ctypes.c_double), ("logits_sb", ctypes.c_longlong), ("logits_ss", ctypes.c_longlong),
+                ("probs_sb", ctypes.c_longlong), ("probs_ss", ctypes.c_longlong)]
+
+
 class Layout(ctypes.Structure):
     _fields_ = [("kv_records", ctypes.c_int), ("a_tiled", ctypes.c_int), ("tc_score", ctypes.c_int),
                 ("tc_rebuild", ctypes.c_int), ("tc_attention", ctypes.c_int),
@@ -138,6 +144,8 @@ def lib() -> ctypes.CDLL:
             "shadowkv_cache_compact_workspace": (S, [P(CacheDesc)]),
             "shadowkv_cache_compact": (I, [P(CacheDesc), V, P(CacheDesc), V, V, S, V]),
             "shadowkv_cache_check": (I, [P(CacheDesc)]),
+            "shadowkv_verify_workspace": (S, [P(VerifyParams)]),
+            "shadowkv_verify_drafts": (I, [P(VerifyParams)] + [V] * 10 + [S, V]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -467,6 +475,64 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight:
     p = _PACK_NORM_ROPE(b, s, hq, hk, d, d if rot is None else rot, dt, norm, per_token, eps, theta)
     _call((_step or _step_calls())["qk_norm_rope"], x, stream, p, rq, rk, wq, wk, pp, oq, ok)
     return q_out, k_out
+
+
+def _stacked(t: torch.Tensor, name: str, shape, dtype, device):
+    """(pointer, stride of sequences, stride of positions) of a b x s x n tensor, its n elements adjacent."""
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        st = t.stride()
+        if st[2] == 1 or shape[2] <= 1:
+            return t.data_ptr(), st[0], st[1]
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {tuple(shape)} on "
+                     f"{device} (shape, type and device)")
+
+
+def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, probs: Optional[torch.Tensor], accept: torch.Tensor,
+                  sample: torch.Tensor, *, lens: Optional[torch.Tensor] = None, temperature=1.0,
+                  tokens: Optional[torch.Tensor] = None, accepted: Optional[torch.Tensor] = None, stream=None):
+    """How many drafted tokens stand, and the token that follows them, from given random
+    numbers (speculative sampling; shadowkv_verify_drafts).
+
+    logits (b, s + 1, vocab) float32 or bfloat16, the target's after 0..s drafts; drafts (b, s) int32;
+    probs (b, s, vocab) float32, what the drafts were sampled from, or None for
+    drafts that were looked up (the last dimension of both contiguous, the others of any stride); accept (b, s)
+    and sample (b,) float32 in [0, 1); lens (b,) int32: drafts of each sequence; temperature: a number or (b,)
+    float32, 0: greedy.  Returns tokens (b, s + 1) int32 (the drafts that stand, the
+    next token, then -1) and accepted (b,) int32."""
+    if not logits.is_cuda:
+        raise ValueError(f"tensors must be on a CUDA device, got {logits.device}")
+    dev = logits.device
+    if stream is not None and _handle(stream) != _current_stream(dev.index):
+        # the outputs and the workspace are allocated on the stream that uses them
+        with _on_stream(stream, dev):
+            return verify_drafts(logits, drafts, probs, accept, sample, lens=lens, temperature=temperature, tokens=tokens,
+                                 accepted=accepted)
+    if logits.dim() != 3 or drafts.dim() != 2 or logits.shape[1] < 1:
+        raise ValueError("logits must be (b, s + 1, vocab) and drafts (b, s)")
+    b, s, v = logits.shape[0], logits.shape[1] - 1, logits.shape[2]
+    dt = _dtype(logits, "logits")
+    lp, lb, ls = _stacked(logits, "logits", (b, s + 1, v), logits.dtype, dev)
+    pp, pb, ps = (None, 0, 0) if probs is None else _stacked(probs, "probs", (b, s, v), torch.float32, dev)
+    dp, ap = _dense(drafts, "drafts", (b, s), torch.int32, dev), _dense(accept, "accept", (b, s), torch.float32, dev)
+    sp, np_ = _dense(sample, "sample", (b,), torch.float32, dev), _dense(lens, "lens", (b,), torch.int32, dev)
+    tp, t = None, 0.0
+    if isinstance(temperature, torch.Tensor):
+        tp = _dense(temperature, "temperature", (b,), torch.float32, dev)
+    else:
+        t = float(temperature)
+    if tokens is None:
+        tokens = torch.empty((b, s + 1), dtype=torch.int32, device=dev)
+    if accepted is None:
+        accepted = torch.empty(b, dtype=torch.int32, device=dev)
+    to, ao = _dense(tokens, "tokens", (b, s + 1), torch.int32, dev), _dense(accepted, "accepted", (b,), torch.int32, dev)
+    p = VerifyParams(b, s, v, dt, t, lb, ls, pb, ps)
+    nb = lib().shadowkv_verify_workspace(p)
+    if nb == 0:
+        _check(1)
+    work = torch.empty(nb, dtype=torch.uint8, device=dev)
+    _call(lib().shadowkv_verify_drafts, logits, None, p, lp, dp, pp, ap, sp, np_, tp, to, ao, work.data_ptr(), nb)
+    return tokens, accepted
 
 
 class BlockCache:

@@ -1,0 +1,490 @@
+// Verification of drafted tokens against the target's logits
+// (shadowkv_verify_drafts): how many of a sequence's drafts stand, and the token
+// that follows them, from given random numbers.
+//
+// Which token a number falls on is decided next to borders (a vocabulary of 2^17 has as
+// many), so the weights w_v = exp((l_v - max) / T) of the row that is sampled from are
+// whole numbers: 2^43 w_v, each within 2^-37 of itself, by a table of 2^(j/64) and a
+// short polynomial (Tang, "Table-driven implementation of the exponential function",
+// 1989) on pairs of floats.  Their sums are exact and do not depend on the order.  The rows'
+// sums for the acceptance tests are fp32 and good to 2^-14; a test that close to its
+// border (one in 10,000) is decided again with the row's whole-number sum.
+//
+// Memory bounds it: the logits are read once by k_verify_rows, one row per sequence (from L2) and
+// the draft's distribution again by k_verify_pick.
+#include <cooperative_groups.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace skv {
+namespace cg = cooperative_groups;
+
+struct VerifyArgs {
+  const void* logits;
+  const int32_t* drafts;
+  const float* probs;
+  const float *accept, *sample;
+  const int32_t* lens;
+  const float* temperatures;
+  int32_t *tokens, *accepted;
+  float4* part;        // [b (s + 1)][splits]: maximum, its index, sum
+  long long lb, ls, pb, ps;
+  double temperature;
+  int b, s, vocab, splits, per;   // per: elements of a split
+};
+
+// Logits are taken as finite: NaN counts as -inf, +inf as the largest float.
+__device__ __forceinline__ float logit(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f); }
+
+// The temperature's factor of the logits, log2(e) / T; 0: greedy.
+__device__ __forceinline__ double log2_factor(const VerifyArgs& a, int seq) {
+  const double t = a.temperatures ? static_cast<double>(a.temperatures[seq]) : a.temperature;
+  return t >= 1e-30 ? 1.4426950408889634 / t : 0.0;
+}
+__device__ __forceinline__ int drafts_of(const VerifyArgs& a, int seq) {
+  return a.lens ? min(max(a.lens[seq], 0), a.s) : a.s;
+}
+
+// ------------------------------------------------------------------ rows
+constexpr int kVrThreads = 256;
+
+struct Best {
+  float m;
+  int at;
+};
+__device__ __forceinline__ Best better(Best x, Best y) {
+  return y.m > x.m || (y.m == x.m && y.at < x.at) ? y : x;
+}
+__device__ __forceinline__ Best warp_best(Best x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Best y;
+    y.m = __shfl_xor_sync(0xffffffffu, x.m, o);
+    y.at = __shfl_xor_sync(0xffffffffu, x.at, o);
+    x = better(x, y);
+  }
+  return x;
+}
+
+// CTA = (split of the vocabulary, row): its largest logit, the first index of it, and
+// the sum of 2^(c (l - max)).
+template <typename T>
+__global__ void __launch_bounds__(kVrThreads)
+k_verify_rows(const __grid_constant__ VerifyArgs a) {
+  __shared__ Best s_best[kVrThreads / 32];
+  __shared__ float s_sum[kVrThreads / 32];
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
+  const int row = blockIdx.y, seq = row / (a.s + 1), j = row - seq * (a.s + 1), tid = threadIdx.x;
+  if (j > drafts_of(a, seq)) return;
+  const T* l = static_cast<const T*>(a.logits) + seq * a.lb + j * a.ls;
+  const int v0 = blockIdx.x * a.per, v1 = min(a.vocab, v0 + a.per);
+  Best mine{-INFINITY, a.vocab};
+  for (int v = v0 + tid; v < v1; v += kVrThreads) mine = better(mine, Best{logit(Ty<T>::to_f(l[v])), v});
+  mine = warp_best(mine);
+  if ((tid & 31) == 0) s_best[tid >> 5] = mine;
+  __syncthreads();
+  Best best = s_best[0];
+#pragma unroll
+  for (int w = 1; w < kVrThreads / 32; ++w) best = better(best, s_best[w]);
+  const float c = static_cast<float>(log2_factor(a, seq));
+  float z = 0.f;
+  if (best.m > -INFINITY)
+    for (int v = v0 + tid; v < v1; v += kVrThreads) z += exp2f((logit(Ty<T>::to_f(l[v])) - best.m) * c);
+  z = warp_sum(z);
+  if ((tid & 31) == 0) s_sum[tid >> 5] = z;
+  __syncthreads();
+  if (tid == 0) {
+    z = 0.f;
+#pragma unroll
+    for (int w = 0; w < kVrThreads / 32; ++w) z += s_sum[w];
+    a.part[static_cast<size_t>(row) * a.splits + blockIdx.x] = make_float4(best.m, __int_as_float(best.at), z, 0.f);
+  }
+}
+
+// ------------------------------------------------------------------ whole-number weights
+struct Exp {
+  float m;          // the row's largest logit
+  float ch, cl;     // log2(e) / T
+  const ulonglong2* table;   // 2^(43 + j/64), rounded; its leading 24 bits and the rest as floats
+};
+
+// round(2^43 2^((l - m) log2(e) / T))
+__device__ __forceinline__ unsigned long long weight_of(const Exp& e, float l) {
+  // l - m and its error, times the factor, as a sum of two floats
+  const float s = l - e.m, bb = s - l, err = (l - (s - bb)) + (-e.m - bb);
+  const float th = s * e.ch;
+  if (!(th >= -50.f)) return 0;   // below half a unit (-inf, too)
+  const float tl = fmaf(s, e.ch, -th) + fmaf(s, e.cl, err * e.ch);
+  const float kf = rintf(th * 64.f);
+  const int k = static_cast<int>(kf);
+  const float g = fmaf(kf, -1.f / 64.f, th);   // exact; |g| <= 1/128
+  // 2^(g + tl) - 1 = yh + e2, y = (g + tl) ln 2
+  const float yh = g * 0.693147182f;
+  const float yl = fmaf(g, 0.693147182f, -yh) + fmaf(g, -1.90465421e-9f, tl * 0.693147182f);
+  const float e2 = yl + yh * yh * fmaf(yh, fmaf(yh, 1.f / 24.f, 1.f / 6.f), 0.5f);
+  const ulonglong2 t = e.table[k & 63];
+  const float tf = __uint_as_float(static_cast<uint32_t>(t.y)), tr = __uint_as_float(static_cast<uint32_t>(t.y >> 32));
+  const float ph = tf * yh, pl = fmaf(tf, yh, -ph) + fmaf(tr, yh, tf * e2);
+  // the table's value is in [1, 2): ph below 2^-6, pl below 2^-14
+  const float a0 = rintf(ph * 0x1p36f);
+  const float b0 = rintf((pl + fmaf(a0, -0x1p-36f, ph)) * 0x1p43f);
+  const unsigned long long w = t.x + (static_cast<long long>(static_cast<int>(a0)) << 7) + static_cast<long long>(static_cast<int>(b0));
+  const int sh = -(k >> 6);   // 0 .. 50
+  return sh ? ((w >> (sh - 1)) + 1) >> 1 : w;
+}
+
+// floor(f x) of a float f >= 0 (infinite or above: the largest) and a whole number.
+__device__ __forceinline__ unsigned long long times(float f, unsigned long long x) {
+  const uint32_t u = __float_as_uint(f);
+  const int e = static_cast<int>(u >> 23) - 127 - 23;       // f = m 2^e, m < 2^24
+  if (!(f > 0.f)) return 0;
+  const unsigned long long m = u >> 23 ? (u & 0x7fffffu) | 0x800000u : (u & 0x7fffffu) << 1;
+  const unsigned long long lo = m * x, hi = __umul64hi(m, x);   // below 2^88
+  if (e >= 0) return hi || e > 40 || (lo >> (63 - e)) ? 0x7fffffffffffffffull : lo << e;
+  const int r = -e;
+  if (r >= 128) return 0;
+  if (r >= 64) return hi >> (r - 64);
+  return hi >> r ? 0x7fffffffffffffffull : (hi << (64 - r)) | (lo >> r);
+}
+
+// ------------------------------------------------------------------ pick
+constexpr int kVpCtas = 8, kVpThreads = 512, kVpWarps = kVpThreads / 32;
+constexpr int kVpChunk = 512;   // elements whose sum is kept, one warp's work
+
+struct PickShared {
+  ulonglong2 table[64];
+  unsigned long long cta[2][kVpCtas];   // the CTAs' sums
+  unsigned long long warp[kVpWarps];
+};
+
+__device__ __forceinline__ unsigned long long warp_add(unsigned long long x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Sum over the cluster; ahead: of the CTAs before this one.  `turn` alternates between calls.
+__device__ __forceinline__ unsigned long long cluster_add(cg::cluster_group& cl, PickShared* sh, unsigned long long warp_sum,
+                                                          int turn, unsigned long long* ahead) {
+  const int tid = threadIdx.x;
+  if ((tid & 31) == 0) sh->warp[tid >> 5] = warp_sum;
+  __syncthreads();
+  if (tid < kVpCtas) {
+    unsigned long long x = 0;
+    for (int w = 0; w < kVpWarps; ++w) x += sh->warp[w];
+    *cl.map_shared_rank(&sh->cta[turn][cl.block_rank()], tid) = x;
+  }
+  cl.sync();
+  unsigned long long all = 0, before = 0;
+#pragma unroll
+  for (unsigned u = 0; u < kVpCtas; ++u) {
+    if (u < cl.block_rank()) before += sh->cta[turn][u];
+    all += sh->cta[turn][u];
+  }
+  if (ahead) *ahead = before;
+  return all;
+}
+
+// Cluster = sequence.  Every CTA decides the acceptance tests by itself (on the same
+// numbers); the sampled row is dealt in chunks, a run of them to each CTA.
+template <typename T>
+__global__ void __cluster_dims__(kVpCtas, 1, 1) __launch_bounds__(kVpThreads)
+k_verify_pick(const __grid_constant__ VerifyArgs a) {
+  extern __shared__ unsigned long long s_chunk[];   // sums of this CTA's chunks
+  __shared__ PickShared sh;
+  __shared__ float s_max;
+  __shared__ int s_arg, s_yes;
+  __shared__ double s_z;
+  cg::cluster_group cl = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 64) {
+    const double x = exp2(tid / 64.0);
+    const unsigned long long t = static_cast<unsigned long long>(__double2ll_rn(x * 0x1p43));
+    const float tf = static_cast<float>(x);
+    sh.table[tid].x = t;
+    sh.table[tid].y = __float_as_uint(tf) |
+                      static_cast<unsigned long long>(__float_as_uint(static_cast<float>(x - tf))) << 32;
+  }
+  tc::grid_dep_wait();
+  cl.sync();   // every CTA's shared memory is there
+  const int seq = blockIdx.x / kVpCtas, n = drafts_of(a, seq), rank = cl.block_rank();
+  const double factor = log2_factor(a, seq);
+  const float ch = static_cast<float>(factor), cl_ = static_cast<float>(factor - ch);
+  const int chunks = (a.vocab + kVpChunk - 1) / kVpChunk, c0 = static_cast<int>(static_cast<long long>(chunks) * rank / kVpCtas),
+            c1 = static_cast<int>(static_cast<long long>(chunks) * (rank + 1) / kVpCtas);
+  const T* rows = static_cast<const T*>(a.logits) + seq * a.lb;
+  int turn = 0;
+
+  // The row's maximum and fp32 sum from its splits (warp 0, to shared memory).
+  auto row_stats = [&](int j) {
+    if (warp == 0) {
+      const float4* p = a.part + (static_cast<size_t>(seq) * (a.s + 1) + j) * a.splits;
+      Best best{-INFINITY, a.vocab};
+      for (int u = lane; u < a.splits; u += 32) best = better(best, Best{p[u].x, __float_as_int(p[u].y)});
+      best = warp_best(best);
+      double z = 0.0;
+      for (int u = lane; u < a.splits; u += 32)
+        if (p[u].x > -INFINITY) z += static_cast<double>(p[u].z * exp2f((p[u].x - best.m) * ch));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      if (lane == 0) {
+        s_max = best.m;
+        s_arg = best.at;
+        s_z = z;
+      }
+    }
+    __syncthreads();
+  };
+  // Whole-number sum of row j's weights, and of each of this CTA's chunks.
+  auto row_sum = [&](int j, unsigned long long* ahead) {
+    const Exp e{s_max, ch, cl_, sh.table};
+    const T* l = rows + j * a.ls;
+    unsigned long long sum = 0;
+    for (int c = c0 + warp; c < c1; c += kVpWarps) {
+      unsigned long long x = 0;
+#pragma unroll 4
+      for (int u = 0; u < kVpChunk / 32; ++u) {
+        const int v = c * kVpChunk + u * 32 + lane;
+        if (v < a.vocab) x += weight_of(e, logit(Ty<T>::to_f(l[v])));
+      }
+      x = warp_add(x);
+      if (lane == 0) s_chunk[c - c0] = x;
+      sum += x;
+    }
+    const unsigned long long all = cluster_add(cl, &sh, sum, turn, ahead);
+    turn ^= 1;
+    return all;
+  };
+
+  int j = 0;
+  for (; j < n; ++j) {
+    row_stats(j);
+    const int y = a.drafts[static_cast<size_t>(seq) * a.s + j];
+    const bool real = static_cast<unsigned>(y) < static_cast<unsigned>(a.vocab) && s_max > -INFINITY;
+    bool yes = false;
+    if (real && factor == 0.0) {
+      yes = y == s_arg && static_cast<double>(a.accept[static_cast<size_t>(seq) * a.s + j]) *
+                                  (a.probs ? a.probs[seq * a.pb + j * a.ps + y] : 1.f) < 1.0;
+    } else if (real) {
+      int v = 0;   // 0, 1: decided; 2: too near
+      double u = 0.0, w = 0.0;
+      if (tid == 0) {
+        const float q = a.probs ? a.probs[seq * a.pb + j * a.ps + y] : 1.f;
+        u = static_cast<double>(a.accept[static_cast<size_t>(seq) * a.s + j]) * q;   // exact
+        w = exp2((static_cast<double>(logit(Ty<T>::to_f(rows[j * a.ls + y]))) - s_max) * factor);
+        const double uz = u * s_z;
+        s_yes = fabs(uz - w) <= 0x1p-14 * w && w > 0.0 ? 2 : uz < w;
+      }
+      __syncthreads();
+      v = s_yes;
+      if (v == 2) {
+        const unsigned long long z = row_sum(j, nullptr);
+        if (tid == 0) s_yes = u * (static_cast<double>(z) * 0x1p-43) < w;
+        __syncthreads();
+        v = s_yes;
+      }
+      yes = v == 1;
+    }
+    __syncthreads();   // the row's numbers are written again
+    if (!yes) break;
+  }
+  // the drafts that stand, and what follows them
+  if (rank == 0) {
+    for (int i = tid; i <= a.s; i += kVpThreads)
+      if (i != j) a.tokens[static_cast<size_t>(seq) * (a.s + 1) + i] = i < j ? a.drafts[static_cast<size_t>(seq) * a.s + i] : -1;
+    if (tid == 0) a.accepted[seq] = j;
+  }
+  int32_t* next = a.tokens + static_cast<size_t>(seq) * (a.s + 1) + j;
+  row_stats(j);
+  if (factor == 0.0 || s_max == -INFINITY) {
+    if (rank == 0 && tid == 0) *next = s_max == -INFINITY ? -1 : s_arg;
+    return;
+  }
+  unsigned long long ahead, total = row_sum(j, &ahead);
+  const Exp e{s_max, ch, cl_, sh.table};
+  const T* l = rows + j * a.ls;
+  const float* q = j < n && a.probs ? a.probs + seq * a.pb + j * a.ps : nullptr;
+  const int out = j < n && !a.probs ? a.drafts[static_cast<size_t>(seq) * a.s + j] : -1;   // the token left out
+  const unsigned long long z = total;
+  // what is left of token v's weight
+  bool plain = j == n;
+  auto left = [&](int v) {
+    const unsigned long long w = weight_of(e, logit(Ty<T>::to_f(l[v])));
+    if (plain) return w;
+    if (!q) return v == out ? 0ull : w;
+    const unsigned long long t = times(q[v], z);
+    return w > t ? w - t : 0ull;
+  };
+  auto left_sum = [&](unsigned long long* before) {
+    unsigned long long sum = 0;
+    for (int c = c0 + warp; c < c1; c += kVpWarps) {
+      unsigned long long x = 0;
+#pragma unroll 4
+      for (int u = 0; u < kVpChunk / 32; ++u) {
+        const int v = c * kVpChunk + u * 32 + lane;
+        if (v < a.vocab) x += left(v);
+      }
+      x = warp_add(x);
+      if (lane == 0) s_chunk[c - c0] = x;
+      sum += x;
+    }
+    const unsigned long long all = cluster_add(cl, &sh, sum, turn, before);
+    turn ^= 1;
+    return all;
+  };
+  if (!plain) {
+    total = left_sum(&ahead);
+    if (total == 0) {   // nothing left: from the row itself
+      plain = true;
+      total = left_sum(&ahead);
+    }
+  }
+  // the first token whose running sum passes sample times the total
+  const float r = a.sample[seq];
+  const unsigned long long at = min(times(r, total), total - 1);
+  __syncthreads();
+  // the chunk (warp 0 of the CTA that has it), then the token in it
+  if (warp == 0) {
+    unsigned long long run = ahead;
+    int found = -1;
+    for (int c = c0; c < c1 && found < 0; c += 32) {
+      const unsigned long long mine = c + lane < c1 ? s_chunk[c + lane - c0] : 0;
+      unsigned long long x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, c + lane < c1 && run + x > at);
+      if (past) {
+        found = __ffs(past) - 1;
+        run += __shfl_sync(0xffffffffu, x - mine, found);
+        found += c;
+      } else {
+        run += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+    if (found >= 0 && ahead <= at) {
+      for (int u = 0; u < kVpChunk / 32; ++u) {
+        const int v = found * kVpChunk + u * 32 + lane;
+        unsigned long long x = v < a.vocab ? left(v) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, run + x > at);
+        if (past) {
+          if (lane == 0) *next = found * kVpChunk + u * 32 + __ffs(past) - 1;
+          break;
+        }
+        run += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+  }
+}
+
+static int verify_splits(const shadowkv_verify_params& p, int* per) {
+  // 8 KB of logits or more to a CTA, four CTAs per SM or more
+  const int least = 4096;
+  const long long rows = static_cast<long long>(p.b) * (p.s + 1);
+  long long n = (4 * 152 + rows - 1) / rows;
+  const long long most = (p.vocab + least - 1) / least;
+  n = n < most ? n : most;
+  *per = static_cast<int>(((p.vocab + n - 1) / n + 7) / 8 * 8);
+  return (p.vocab + *per - 1) / *per;
+}
+
+template <typename T>
+static cudaError_t verify_t(const VerifyArgs& a, cudaStream_t st) {
+  cudaError_t e = launch_pdl(k_verify_rows<T>, dim3(a.splits, a.b * (a.s + 1)), dim3(kVrThreads), 0, st, a);
+  const int chunks = (a.vocab + kVpChunk - 1) / kVpChunk, mine = (chunks + kVpCtas - 1) / kVpCtas + 1;
+  if (e == cudaSuccess)
+    e = launch_pdl(k_verify_pick<T>, dim3(a.b * kVpCtas), dim3(kVpThreads), mine * sizeof(unsigned long long), st, a);
+  return e;
+}
+
+static const char* verify_fault(const shadowkv_verify_params* p, skv_status* st) {
+  *st = SKV_ERR_INVALID_ARG;
+  if (!p) return "params is NULL";
+  if (p->b < 0 || p->s < 0) return "b and s must be >= 0";
+  if (p->vocab < 1) return "vocab must be >= 1";
+  if (p->dtype != SKV_DTYPE_F32 && p->dtype != SKV_DTYPE_BF16) return "bad dtype";
+  if (!(p->temperature >= 0.0) || !std::isfinite(p->temperature)) return "temperature must be finite and >= 0";
+  if (p->logits_sb < 0 || p->logits_ss < 0 || p->probs_sb < 0 || p->probs_ss < 0) return "strides must not be negative";
+  *st = SKV_ERR_UNSUPPORTED;
+  if (p->vocab > 1 << 19) return "vocab must be at most 2^19";
+  if (p->s > 65534 || static_cast<long long>(p->b) * (p->s + 1) > 65535) return "b * (s + 1) must be at most 65535";
+  *st = SKV_OK;
+  return nullptr;
+}
+
+}  // namespace skv
+
+extern "C" {
+
+size_t shadowkv_verify_workspace(const shadowkv_verify_params* p) try {
+  skv_status st;
+  if (const char* f = skv::verify_fault(p, &st)) {
+    skv::set_error(st, f);
+    return 0;
+  }
+  if (p->b == 0) return 256;
+  int per;
+  return static_cast<size_t>(p->b) * (p->s + 1) * skv::verify_splits(*p, &per) * sizeof(float4);
+} catch (...) {   // host memory for an error text ran out
+  return 0;
+}
+
+skv_status shadowkv_verify_drafts(const shadowkv_verify_params* p, const void* logits, const int32_t* drafts,
+                                  const float* probs, const float* accept, const float* sample, const int32_t* lens,
+                                  const float* temperatures, int32_t* tokens, int32_t* accepted, void* work,
+                                  size_t work_bytes, void* stream) try {
+  using skv::set_error;
+  skv_status st;
+  if (const char* f = skv::verify_fault(p, &st)) return set_error(st, f);
+  if (p->b == 0) return SKV_OK;
+  if (!logits || !sample || !tokens || !accepted || (p->s > 0 && (!drafts || !accept)))
+    return set_error(SKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  const uintptr_t words = reinterpret_cast<uintptr_t>(drafts) | reinterpret_cast<uintptr_t>(probs) |
+                          reinterpret_cast<uintptr_t>(accept) | reinterpret_cast<uintptr_t>(sample) |
+                          reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(temperatures) |
+                          reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(accepted);
+  if (words % 4 || reinterpret_cast<uintptr_t>(logits) % (p->dtype == SKV_DTYPE_BF16 ? 2 : 4))
+    return set_error(SKV_ERR_INVALID_ARG, "pointers must be aligned to their elements");
+  if (!work || reinterpret_cast<uintptr_t>(work) % 256)
+    return set_error(SKV_ERR_INVALID_ARG, "the workspace must be non-NULL and 256-byte aligned");
+  skv::VerifyArgs a;
+  a.splits = skv::verify_splits(*p, &a.per);
+  if (work_bytes < static_cast<size_t>(p->b) * (p->s + 1) * a.splits * sizeof(float4))
+    return set_error(SKV_ERR_INVALID_ARG, "the workspace is smaller than shadowkv_verify_workspace");
+  a.logits = logits;
+  a.drafts = drafts;
+  a.probs = probs;
+  a.accept = accept;
+  a.sample = sample;
+  a.lens = lens;
+  a.temperatures = temperatures;
+  a.tokens = tokens;
+  a.accepted = accepted;
+  a.part = static_cast<float4*>(work);
+  a.lb = p->logits_sb; a.ls = p->logits_ss;
+  a.pb = p->probs_sb; a.ps = p->probs_ss;
+  a.temperature = p->temperature;
+  a.b = p->b; a.s = p->s; a.vocab = p->vocab;
+  cudaStream_t q = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> together(skv::cache_enqueue());
+  const cudaError_t e = p->dtype == SKV_DTYPE_BF16 ? skv::verify_t<skv::bf16>(a, q) : skv::verify_t<float>(a, q);
+  return e == cudaSuccess ? SKV_OK : set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
+} catch (...) {   // host memory for an error text ran out
+  return SKV_ERR_OOM;
+}
+
+}  // extern "C"

@@ -254,3 +254,33 @@ def test_pool_workspaces(lib):
     assert lib.shadowkv_cache_reserve_workspace(desc(), 0) == lib.shadowkv_cache_reserve_workspace(desc(), 1) > 0
     assert lib.shadowkv_cache_compact_workspace(desc()) >= 2 * 4 * 160
     assert lib.shadowkv_cache_share(desc(), P, 0, None, None, None) == 0        # no forks: no call
+
+
+def vp(**kw):
+    f = dict(b=2, s=3, vocab=1000, dtype=1, temperature=1.0, logits_sb=4000, logits_ss=1000, probs_sb=3000, probs_ss=1000)
+    f.update(kw)
+    return binding.VerifyParams(**f)
+
+
+@pytest.mark.parametrize("p,args,code", [
+    (dict(b=-1), {}, 1), (dict(s=-1), {}, 1), (dict(vocab=0), {}, 1), (dict(dtype=4), {}, 1), (dict(temperature=-1.0), {}, 1),
+    (dict(temperature=float("nan")), {}, 1), (dict(temperature=float("inf")), {}, 1), (dict(logits_ss=-1), {}, 1),
+    (dict(probs_sb=-1), {}, 1), (dict(vocab=(1 << 19) + 1), {}, 7), (dict(b=20000), {}, 7), (dict(s=70000), {}, 7),
+    (dict(s=2**31 - 1), {}, 7),
+    ({}, dict(logits=None), 1), ({}, dict(drafts=None), 1), ({}, dict(accept=None), 1), ({}, dict(sample=None), 1),
+    ({}, dict(tokens=None), 1), ({}, dict(accepted=None), 1), ({}, dict(logits=P + 1), 1), ({}, dict(probs=P + 2), 1),
+    ({}, dict(lens=P + 1), 1), ({}, dict(temps=P + 2), 1), ({}, dict(work=None), 1), ({}, dict(work=P + 16), 1), ({}, dict(nb=15), 1),
+])
+def test_verify_refuses(lib, p, args, code):
+    a = dict(logits=P, drafts=P, probs=P, accept=P, sample=P, lens=None, temps=None, tokens=P, accepted=P, work=P, nb=1 << 30)
+    a.update(args)
+    assert lib.shadowkv_verify_drafts(vp(**p), *(a[k] for k in ("logits", "drafts", "probs", "accept", "sample", "lens", "temps",
+                                                               "tokens", "accepted", "work", "nb")), None) == code
+    assert lib.shadowkv_last_error().decode()
+    if p:
+        assert lib.shadowkv_verify_workspace(vp(**p)) == 0
+
+
+def test_verify_of_nothing_is_no_call(lib):
+    assert lib.shadowkv_verify_drafts(vp(b=0), *[None] * 10, 0, None) == 0
+    assert lib.shadowkv_verify_workspace(vp()) >= 2 * 4 * 16
