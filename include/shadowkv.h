@@ -425,6 +425,37 @@ skv_status shadowkv_cache_attend(const shadowkv_cache* c, int dtype, int h_q, co
                                  float scale, int gather, float decay, const shadowkv_rows* out,
                                  float* lse, void* work, size_t work_bytes, void* stream);
 
+/* Bytes of workspace shadowkv_cache_attend_tokens needs for h_q query heads and s tokens on
+ * the current device (0 if the arguments are not valid). */
+size_t shadowkv_cache_attend_tokens_workspace(const shadowkv_cache* c, int h_q, int s);
+
+/*
+ * Attention of several tokens per sequence over the cache: a piece of a prompt or
+ * drafted tokens, whose own keys and values have been appended (causal = 1), or
+ * queries over the states of an encoder (causal = 0):
+ *   out_j = sum_t p_t V_t,  p = softmax_t(scale q_j . K_t)  over the tokens t that query j sees:
+ *   causal = 1: t <= n_tok - lens[i] + j (the sequence's last token is query lens[i] - 1);
+ *   causal = 0: all n_tok of the pair.
+ * Query head g reads KV head g / (h_q / h_kv); h_q / h_kv <= 128.
+ *   dtype : SKV_DTYPE_F32 or SKV_DTYPE_BF16, of q and out.
+ *   q, out: device rows b x h_q x s x d, aligned to their elements (the loads are widest where
+ *           pointers and strides are multiples of 16 bytes); out may be q itself (same pointer and
+ *           strides), else it does not overlap q.
+ *   lens  : device int32, b: queries of each sequence, 0..s (others are clamped and recorded); NULL: s
+ *           each.  q is not read past them, and out and lse stay as they were there.
+ *   lse   : device f32, b x h_q x s: log sum_t exp(scale q_j . K_t), or NULL.
+ *   work  : device, 256-byte aligned, at least shadowkv_cache_attend_tokens_workspace bytes; its
+ *           contents before and after mean nothing.  Calls that may run at the same time need
+ *           workspaces of their own.
+ * A query that sees no token gives zeros and an lse of -inf.  A key or value that is NaN reaches the
+ * queries that see it and no others; a query with an entry that is not finite gives NaN.
+ * s h_q / h_kv <= 2^24 (SKV_ERR_UNSUPPORTED).  s = 0 does nothing.
+ * Asynchronous on `stream`; runs on the current device.
+ */
+skv_status shadowkv_cache_attend_tokens(const shadowkv_cache* c, int dtype, int h_q, int s, const shadowkv_rows* q,
+                                        const int32_t* lens, int causal, float scale, const shadowkv_rows* out, float* lse,
+                                        void* work, size_t work_bytes, void* stream);
+
 /*
  * Evicts whole blocks by gathered weight.  A pair with more than `keep`
  * blocks (its last, partly filled one counts) keeps its first `sink`, its

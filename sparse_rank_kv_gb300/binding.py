@@ -136,6 +136,8 @@ def lib() -> ctypes.CDLL:
             "shadowkv_cache_attend_workspace": (S, [P(CacheDesc), I]),
             "shadowkv_cache_attend": (I, [P(CacheDesc), I, I, P(Rows), ctypes.c_float, I, ctypes.c_float,
                                           P(Rows), V, V, S, V]),
+            "shadowkv_cache_attend_tokens_workspace": (S, [P(CacheDesc), I, I]),
+            "shadowkv_cache_attend_tokens": (I, [P(CacheDesc), I, I, I, P(Rows), V, I, ctypes.c_float, P(Rows), V, V, S, V]),
             "shadowkv_cache_evict": (I, [P(CacheDesc), P(CacheDesc), I, I, I, V, V]),
             "shadowkv_cache_share": (I, [P(CacheDesc), V, I, V, V, V]),
             "shadowkv_cache_reserve_workspace": (S, [P(CacheDesc), I]),
@@ -347,6 +349,7 @@ def _step_calls():
         fns = {}
         for name, args in (("qk_norm_rope", [V] * 9), ("cache_append", [C, I, V, V, I, V, V]),
                            ("cache_attend", [C, I, I, V, F, I, F, V, V, V, S, V]),
+                           ("cache_attend_tokens", [C, I, I, I, V, V, I, F, V, V, V, S, V]),
                            ("cache_evict", [C, C, I, I, I, V, V]), ("cache_share", [C, V, I, V, V, V]),
                            ("cache_reserve", [C, V, I, V, V, V, S, V]), ("cache_truncate", [C, V, V, V]),
                            ("cache_compact", [C, V, C, V, V, S, V])):
@@ -684,6 +687,41 @@ class BlockCache:
                     self._work[(hq, st)] = have
         return have
 
+    def attend_tokens(self, q: torch.Tensor, *, lens: Optional[torch.Tensor] = None, causal: bool = True,
+                      scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """softmax(scale q K^T) V of several tokens per sequence; q (b, h_q, s, d), the last dimension
+        contiguous, scale 1/sqrt(d) by default.  causal: the queries are the last tokens held (append
+        them first), and each sees the tokens up to its own; else every query sees every token (an encoder's
+        states).  lens (b,) int32: queries of each sequence (default s); rows past them are left as they
+        were (zeros in an output made here).  lse (b, h_q, s) float32 receives the log sums.  The workspace
+        comes from torch's allocator, for each call."""
+        if q.dim() != 4:
+            raise ValueError("q must be (b, h_q, s, d)")
+        dev, dtype = self.device, q.dtype
+        dt = _dtype(q, "q")
+        hq, s = q.shape[1], q.shape[2]
+        shape = (self.b, hq, s, self.d)
+        rq = _rows(q, "q", shape, dtype, dev)
+        lp = _dense(lens, "lens", (self.b,), torch.int32, dev)
+        sp = _dense(lse, "lse", (self.b, hq, s), torch.float32, dev)
+        if dev.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {dev}")
+        if stream is not None and _handle(stream) != _current_stream(dev.index):
+            # the output and the workspace are allocated on the stream that uses them
+            with _on_stream(stream, dev):
+                return self.attend_tokens(q, lens=lens, causal=causal, scale=scale, out=out, lse=lse)
+        if _current_device() != dev.index:      # the workspace's size goes by the device
+            with torch.cuda.device(dev):
+                return self.attend_tokens(q, lens=lens, causal=causal, scale=scale, out=out, lse=lse)
+        if out is None:
+            out = (torch.empty if lens is None else torch.zeros)(shape, dtype=dtype, device=dev)
+        ro = _rows(out, "out", shape, dtype, dev)
+        work = self._scratch(lib().shadowkv_cache_attend_tokens_workspace(self._desc, hq, s))
+        _call((_step or _step_calls())["cache_attend_tokens"], q, None, self._desc, dt, hq, s, rq, lp, bool(causal),
+              self.d ** -0.5 if scale is None else scale, ro, sp, work.data_ptr(), work.numel())
+        return out
+
     def evict(self, keep: int, *, sink: int = 0, recent: int = 1, into: Optional["BlockCache"] = None,
               kept: Optional[torch.Tensor] = None, stream=None) -> None:
         """Keeps at most `keep` blocks of every pair: the first `sink`, the last
@@ -757,7 +795,7 @@ class BlockCache:
     def _scratch(self, nb: int) -> torch.Tensor:
         """A workspace from torch's allocator, for one call on the current stream."""
         if nb == 0:
-            _check(1)
+            _check(7)
         return torch.empty(nb, dtype=torch.uint8, device=self.device)
 
     def reset(self) -> None:

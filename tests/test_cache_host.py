@@ -284,3 +284,24 @@ def test_verify_refuses(lib, p, args, code):
 def test_verify_of_nothing_is_no_call(lib):
     assert lib.shadowkv_verify_drafts(vp(b=0), *[None] * 10, 0, None) == 0
     assert lib.shadowkv_verify_workspace(vp()) >= 2 * 4 * 16
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(dtype=7), 1), (dict(hq=12), 7), (dict(hq=8 * 129), 7), (dict(hq=0), 7), (dict(s=-1), 1), (dict(s=1 << 23), 7),
+    (dict(q=None), 1), (dict(out=rows(None)), 1), (dict(q=rows(P + 1)), 1), (dict(out=rows(sh=-128)), 1),
+    (dict(out=rows(sh=0)), 1), (dict(out=rows(ss=0)), 1), (dict(q=rows(ss=-1)), 1), (dict(lse=P + 2), 1), (dict(lens=P + 1), 1),
+    (dict(scale=float("nan")), 1), (dict(causal=2), 1), (dict(work=None), 1), (dict(work=P + 64), 1), (dict(c=dict(d=96)), 7),
+])
+def test_attend_tokens_refuses(lib, args, code):
+    a = dict(dtype=1, hq=32, s=5, q=rows(), lens=None, causal=1, scale=0.1, out=rows(), lse=None, work=P, c={})
+    a.update(args)
+    assert lib.shadowkv_cache_attend_tokens(desc(**a["c"]), a["dtype"], a["hq"], a["s"], a["q"], a["lens"], a["causal"],
+                                            a["scale"], a["out"], a["lse"], a["work"], 1 << 40, None) == code
+    assert lib.shadowkv_last_error().decode()
+
+
+def test_attend_tokens_of_nothing_is_no_call(lib):
+    assert lib.shadowkv_cache_attend_tokens(desc(), 1, 32, 0, None, None, 1, 0.1, None, None, None, 0, None) == 0
+    assert lib.shadowkv_cache_attend_tokens_workspace(desc(d=96), 32, 4) == 0
+    assert lib.shadowkv_cache_attend_tokens_workspace(desc(), 12, 4) == 0
+    assert lib.shadowkv_cache_attend_tokens_workspace(desc(), 32, -1) == 0
