@@ -1,9 +1,28 @@
 // Attention of several tokens per sequence over the 8-bit block cache
 // (shadowkv_cache_attend_tokens): a piece of a prompt, drafted tokens, or queries
 // over an encoder's states.
+//
+// Rows: the queries of a sequence and the G query heads of a KV head together, row
+// r = query r / G, head r % G; a tile of 128 rows is the M of the tensor core's
+// products, 128 tokens are their N (S = Q K^T) and K (O += P V).  The codes become fp16 on
+// their way (exact: e4m3 has 4 bits and fp16 more range), their scales go to the
+// logits and to p in fp32.  A bf16 query row is exact in fp16 after division by the power
+// of two of its largest entry (entries down to 2^-31 of it, the others to 2^-39 of it); an fp32
+// row, and p beside it, are sums of two fp16 terms (2^-22 of themselves).  p times its V scale, relative to
+// the largest scale so far, has fp16's 11 bits (2^-11 of itself) down to 2^-25 of the largest and is good to 2^-36 of
+// that below: p is at most 2^4 (the running maximum is only raised where a tile
+// passes it by more than 4 in base 2, so that O is rarely rescaled).
+//
+// All tiles (of 128 tokens) that all row tiles see are numbered through, and every
+// CTA takes an equal run of them: one prompt, ragged batches and few rows over a long cache fill the
+// GPU alike.  A row tile that several CTAs work on is joined by k_tokens_merge.
+#include <cuda_fp16.h>
+
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "cache.cuh"
 #include "internal.h"
@@ -11,83 +30,930 @@
 
 namespace skv {
 
+constexpr int kCtT = 128;       // tokens of a tile, rows of an MMA
+constexpr int kCtThreads = 448; // warps 0-3 and 4-7: softmax of stream 0 and 1; 8-11: conversion; 12: copies; 13: tcgen05.mma
+constexpr int kCtInfo = 8;      // tiles described ahead
+
 struct TokensArgs {
   CacheDev c;
   const void* q;
   void* out;
   float* lse;
   const int32_t* lens;
+  int4* rec;          // [ctas]: row tile in which the CTA's run begins (pair, tile, its first number, its tiles), pair -1: none
+  float* part_o;      // [2 ctas][Rows][d]
+  float2* part_ml;    // [2 ctas][Rows]
+  uint32_t* nan;      // [ctas][3][128][4]
   long long qb, qh, qs, ob, oh, os;
   float scale_log2;   // scale log2(e)
-  int s, h_q, G, causal;
+  int s, h_q, G, causal, wide_q, wide_o;   // wide: rows in 16-byte pieces
 };
 
 __device__ __forceinline__ int tokens_len(const TokensArgs& a, int seq) {
   const int n = a.lens ? a.lens[seq] : a.s;
-  if (a.lens && static_cast<unsigned>(n) > static_cast<unsigned>(a.s)) flag_error(a.c.status, DEV_BAD_COUNT);
-  return min(max(n, 0), a.s);
+  if (static_cast<unsigned>(n) <= static_cast<unsigned>(a.s)) return n;
+  flag_error(a.c.status, DEV_BAD_COUNT);
+  return n < 0 ? 0 : a.s;
 }
 // Tokens query j of `len` sees of the n held.
 __device__ __forceinline__ int tokens_seen(const TokensArgs& a, int n, int len, int j) {
   return a.causal ? max(n - len + j + 1, 0) : n;
 }
 
-// CTA = (query, head).
-template <typename T, int D>
-__global__ void __launch_bounds__(128)
-k_attend_tokens(const __grid_constant__ TokensArgs a) {
-  __shared__ float sq[D], sp[128], red[8];
-  const int tid = threadIdx.x, j = blockIdx.x, h = blockIdx.y, seq = blockIdx.z, pair = seq * a.c.h_kv + h / a.G;
-  tc::grid_dep_wait();
-  const int len = tokens_len(a, seq), n = cache_tokens(a.c, pair);
-  if (j >= len) return;
-  const int seen = tokens_seen(a, n, len, j), B = 1 << a.c.shift;
-  const T* q = static_cast<const T*>(a.q) + seq * a.qb + h * a.qh + j * a.qs;
-  if (tid < D) sq[tid] = Ty<T>::to_f(q[tid]);
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int t0 = 0; t0 < seen; t0 += 128) {
-    __syncthreads();
-    const int t = t0 + tid;
-    float x = -INFINITY, vs = 0.f;
-    if (t < seen) {
-      const int id = cache_block(a.c, pair, t >> a.c.shift), r = t & (B - 1);
-      const uint8_t* k = a.c.kc + static_cast<size_t>(id) * B * D + (r / 8) * 8 * D + (r % 8) * 16;
-      float z = 0.f;
-      for (int e = 0; e < D; e += 2) {
-        const float2 f = e4m3_unpack2(*reinterpret_cast<const uint16_t*>(k + (e / 16) * 128 + e % 16));
-        z = fmaf(sq[e], f.x, fmaf(sq[e + 1], f.y, z));
-      }
-      x = z * a.c.ks[id] * a.scale_log2;
-      vs = a.c.vs[id];
-    }
-    float w = warp_max(x);
-    if ((tid & 31) == 0) red[tid >> 5] = w;
-    __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float ref = mn == -INFINITY ? 0.f : mn, p = exp2f(x - ref), scale = exp2f(m - ref);
-    m = mn;
-    sp[tid] = t < seen ? p * vs : 0.f;
-    w = warp_sum(p);
-    if ((tid & 31) == 0) red[4 + (tid >> 5)] = w;
-    __syncthreads();
-    l = l * scale + (red[4] + red[5] + red[6] + red[7]);
-    acc *= scale;
-    if (tid < D)
-      for (int u = 0; u < min(128, seen - t0); ++u) {
-        const int id = cache_block(a.c, pair, (t0 + u) >> a.c.shift), r = (t0 + u) & (B - 1);
-        const uint8_t c = a.c.vc[static_cast<size_t>(id) * B * D + (r / 16) * 16 * D + tid * 16 + r % 16];
-        acc = fmaf(sp[u], e4m3_unpack2(c).x, acc);
-      }
+// One of bf16's or fp32's forms.  Two: a CTA works on two row tiles with the same tokens at a
+// time (stream 0 and 1); else on one, whose tokens' tiles the streams take in turn.
+template <typename T, int D, bool Two>
+struct Ct {
+  static constexpr int NT = sizeof(T) == 2 ? 1 : 2;        // fp16 terms of q and p
+  static constexpr int Rows = Two ? 256 : 128;
+  static constexpr int QT = kCtT * D * 2;                   // an operand tile in fp16
+  static constexpr int QB = (Two ? 2 : NT) * QT;
+  static constexpr int KB = kCtT * D, Stage = 2 * KB;       // codes of K, of V
+  static constexpr int Misc = 2816;
+  static constexpr int Most = 227 * 1024 - 128 - Misc;
+  static constexpr int NST0 = (Most - QB - 4 * QT) / Stage, NST = NST0 > 4 ? 4 : NST0;
+  static constexpr int Smem = 128 + QB + 4 * QT + NST * Stage + Misc;
+  static_assert(NST >= 1 && !(Two && NT > 1), "tile");
+};
+
+// ------------------------------------------------------------ tensor core
+// D (+)= A B^T, fp16, A in TMEM (lane = row, two elements of K to a column)
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// kind::f16, fp16 A and B (format 0), fp32 D, both K-major, M = 128
+constexpr uint32_t idesc_f16(int N) { return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24); }
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {   // 2^-22 relative; results below 2^-126 are 0
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+// ------------------------------------------------------------ the tiles in order
+// A run of tiles: row tile q of a pair, its tiles from `tile` on.
+struct Walk {
+  int pair, q, tile, left;
+  int n, len, nq, nt, seen0;   // of the pair: tokens, queries, row tiles; of the row tile: tiles, tokens its first row sees
+  int lim;                     // tokens its last row sees
+};
+template <int Rows>
+__device__ __forceinline__ int row_tiles(const TokensArgs& a, int len) { return (len * a.G + Rows - 1) / Rows; }
+// Tokens that row tile q sees (its last row), and its tiles: one at least, so that rows that see nothing are written.
+template <int Rows>
+__device__ __forceinline__ int tile_lim(const TokensArgs& a, int n, int len, int q) {
+  return tokens_seen(a, n, len, min(len - 1, (q * Rows + Rows - 1) / a.G));
+}
+__device__ __forceinline__ int lim_tiles(int lim) { return max(1, (lim + kCtT - 1) / kCtT); }
+
+template <int Rows>
+__device__ __forceinline__ void walk_item(const TokensArgs& a, Walk& w) {
+  w.lim = tile_lim<Rows>(a, w.n, w.len, w.q);
+  w.seen0 = tokens_seen(a, w.n, w.len, w.q * Rows / a.G);
+  w.nt = lim_tiles(w.lim);
+}
+template <int Rows>
+__device__ __forceinline__ void walk_pair(const TokensArgs& a, Walk& w) {
+  w.n = cache_tokens(a.c, w.pair);
+  w.len = tokens_len(a, w.pair / a.c.h_kv);
+  w.nq = row_tiles<Rows>(a, w.len);
+}
+// To the next tile; true when it is another row tile's.
+template <int Rows>
+__device__ __forceinline__ bool walk_next(const TokensArgs& a, Walk& w) {
+  if (--w.left <= 0) return false;
+  if (++w.tile < w.nt) return false;
+  w.tile = 0;
+  if (++w.q >= w.nq) {
+    w.q = 0;
+    do {
+      if (++w.pair >= a.c.pairs) { w.left = 0; return false; }
+      walk_pair<Rows>(a, w);
+    } while (w.nq == 0);
   }
-  T* out = static_cast<T*>(a.out) + seq * a.ob + h * a.oh + j * a.os;
-  if (tid < D) out[tid] = Ty<T>::from_f(seen > 0 ? acc / l : 0.f);
-  if (a.lse && tid == 0)
-    a.lse[(static_cast<size_t>(seq) * a.h_q + h) * a.s + j] = seen > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  walk_item<Rows>(a, w);
+  return true;
 }
 
-template <typename T, int D>
-static cudaError_t attend_tokens_t(const TokensArgs& a, const shadowkv_cache& c, cudaStream_t st) {
-  return launch_pdl(k_attend_tokens<T, D>, dim3(a.s, a.h_q, c.b), dim3(128), 0, st, a);
+__device__ __forceinline__ int run_begin(int cta, int n, int total) {
+  return static_cast<int>(static_cast<long long>(cta) * total / n);
+}
+__device__ __forceinline__ int run_owner(int x, int n, int total) {
+  return static_cast<int>(((static_cast<long long>(x) + 1) * n - 1) / total);
+}
+
+// Where this CTA's run begins: s_where = {pair, row tile, tile, total of all tiles}; s_first: its row tile's first
+// number.  Groups of 2^lg lanes take runs of pairs, a lane every 2^lg-th row tile.
+template <int Rows>
+__device__ __forceinline__ void run_find(const TokensArgs& a, int cta, int ncta, int* s_where, int* s_scan) {
+  const int tid = threadIdx.x, P = a.c.pairs, most = row_tiles<Rows>(a, a.s);
+  const int lg = most <= 2 ? 0 : most <= 8 ? 2 : 5, gs = 1 << lg, sub = tid & (gs - 1);
+  const int ng = kCtThreads >> lg, per = (P + ng - 1) / ng, p0 = min(P, (tid >> lg) * per), p1 = min(P, p0 + per);
+  auto pair_sum = [&](int p) {   // this lane's part
+    const int n = cache_tokens(a.c, p), len = tokens_len(a, p / a.c.h_kv), nq = row_tiles<Rows>(a, len);
+    int x = 0;
+    for (int q = sub; q < nq; q += gs) x += lim_tiles(tile_lim<Rows>(a, n, len, q));
+    return x;
+  };
+  auto group_sum = [&](int x) {
+    for (int o = gs >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+  int sum = 0;
+  for (int i = 0; i < per; ++i) sum += p0 + i < p1 ? pair_sum(p0 + i) : 0;
+  sum = group_sum(sum);
+  if (tid < 4) s_where[tid] = tid == 0 ? -1 : 0;
+  int total;
+  const int scan = block_exclusive_scan(sub == 0 ? sum : 0, s_scan, &total);
+  int before = __shfl_sync(0xffffffffu, scan, tid & 31 & ~(gs - 1));
+  const int n = min(ncta, total);
+  const int t0 = cta < n ? run_begin(cta, n, total) : -1;
+  // the groups walk their pairs once more, in step within the warp
+  for (int i = 0; i < per; ++i) {
+    const int p = p0 + i, mine = p < p1 ? pair_sum(p) : 0, all = group_sum(mine);
+    const bool here = before <= t0 && t0 < before + all;
+    if (__any_sync(0xffffffffu, here)) {
+      const int cn = p < p1 ? cache_tokens(a.c, p) : 0, len = p < p1 ? tokens_len(a, p / a.c.h_kv) : 0;
+      const int nq = here ? row_tiles<Rows>(a, len) : 0;
+      int run = before;
+      for (int q0 = 0; __any_sync(0xffffffffu, q0 < nq); q0 += gs) {
+        const int q = q0 + sub, x = q < nq ? lim_tiles(tile_lim<Rows>(a, cn, len, q)) : 0;
+        int inc = x;
+        for (int o = 1; o < gs; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (sub >= o) inc += y;
+        }
+        const int at = run + inc - x;
+        if (x > 0 && at <= t0 && t0 < at + x) {
+          s_where[0] = p;
+          s_where[1] = q;
+          s_where[2] = t0 - at;
+        }
+        run += __shfl_sync(0xffffffffu, inc, tid & 31 | (gs - 1));
+      }
+    }
+    before += all;
+  }
+  if (tid == 0) s_where[3] = total;
+  __syncthreads();
+}
+
+// of a tile, beside its tokens (at most 128)
+enum : int {
+  kTFirst = 256,    // first of its row tile in this CTA
+  kTLast = 512,     // last
+  kSFirst = 1024,   // first that its stream has of the row tile
+  kSLast = 2048,
+  kMixed = 4096,    // some rows do not see some of its tokens
+  kOdd = 8192,      // a scale that is negative or no number
+  kWhole = 16384    // this CTA has all of the row tile
+};
+struct TileInfo {
+  int pair, q, tile, flags, n, len, turn, vexp;   // turn: number of the row tile in this CTA; V scales are below 2^vexp
+  float ks[8], vs[8];                             // of every 16 tokens
+};
+
+template <typename T, int D, bool Two>
+__global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_constant__ TokensArgs a) {
+  using C = Ct<T, D, Two>;
+  constexpr int NST = C::NST, Rows = C::Rows;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  unsigned char* qbuf = smem;
+  unsigned char* kbuf = qbuf + C::QB;                    // [2] K in fp16
+  unsigned char* vbuf = kbuf + 2 * C::QT;                // [2] V
+  unsigned char* stages = vbuf + 2 * C::QT;              // [NST] codes
+  unsigned char* misc = stages + NST * C::Stage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc);    // [4] codes are there
+  uint64_t* sempty = full + 4;                           // [4] codes are converted
+  uint64_t* kfull = full + 8;                            // [2]
+  uint64_t* kempty = full + 10;
+  uint64_t* vfull = full + 12;
+  uint64_t* vempty = full + 14;
+  uint64_t* sfull = full + 16;                           // [2], by stream
+  uint64_t* pfull = full + 18;
+  uint64_t* ofin = full + 20;                            // a row tile's last product is done
+  uint64_t* qfull = full + 22;
+  uint64_t* jfull = full + 24;                           // stream 1's sums are there
+  uint64_t* jdone = full + 25;                           // stream 0 has joined the two
+  uint64_t* ifull = full + 26;                           // [8]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 272);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 276);
+  int* s_where = reinterpret_cast<int*>(misc + 280);     // [4]
+  volatile int* s_nan = reinterpret_cast<volatile int*>(misc + 296);   // [2]: V's tile has NaN
+  int* s_scan = reinterpret_cast<int*>(misc + 304);      // [32]
+  TileInfo* infos = reinterpret_cast<TileInfo*>(misc + 448);
+  float* sqs = reinterpret_cast<float*>(misc + 1216);    // [128] rows' factors (one row tile)
+  float2* s_ml = reinterpret_cast<float2*>(misc + 1728); // [128] stream 1's maxima and sums
+  int2* s_join = reinterpret_cast<int2*>(misc + 2752);   // [4 warps] its vexp, and whether NaN is recorded
+  static_assert(sizeof(TileInfo) == 96, "misc");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+  if (gridDim.x > 1) tc::grid_dep_launch();   // (a call's last kernel lets nothing start early)
+
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      tc::mbar_init(&full[i], 2);   // the copies, and the tile's description
+      tc::mbar_init(&sempty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&kfull[i], 4);
+      tc::mbar_init(&kempty[i], 1);
+      tc::mbar_init(&vfull[i], 4);
+      tc::mbar_init(&vempty[i], 1);
+      tc::mbar_init(&sfull[i], 1);
+      tc::mbar_init(&pfull[i], 4);
+      tc::mbar_init(&ofin[i], 1);
+      tc::mbar_init(&qfull[i], 4);
+    }
+    tc::mbar_init(jfull, 4);
+    tc::mbar_init(jdone, 4);
+    for (int i = 0; i < kCtInfo; ++i) tc::mbar_init(&ifull[i], 1);
+    tc::fence_mbar_init();
+    *s_abort = 0;
+  }
+  if (warp == 13) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before();
+  tc::grid_dep_wait();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  run_find<Rows>(a, cta, gridDim.x, s_where, s_scan);
+  int ntile = 0;
+  {
+    const int total = s_where[3], n = min(static_cast<int>(gridDim.x), total);
+    if (cta < n && s_where[0] >= 0) ntile = run_begin(cta + 1, n, total) - run_begin(cta, n, total);
+    if (tid == 0)
+      a.rec[cta] = ntile > 0 && s_where[2] > 0 ? make_int4(s_where[0], s_where[1], run_begin(cta, n, total) - s_where[2], total)
+                                               : make_int4(-1, 0, 0, total);
+  }
+  const int shift = a.c.shift, B = 1 << shift;
+  uint32_t* nan_masks = a.nan + static_cast<size_t>(cta) * 3 * 128 * 4;
+  auto abort_now = [&]() {
+    *s_abort = 1;
+    flag_error(a.c.status, DEV_TIMEOUT);
+  };
+  auto warp_wait = [&](uint64_t* bar, uint32_t phase) {
+    const bool ok = __all_sync(0xffffffffu, !*s_abort && tc::mbar_wait(bar, phase & 1, kWaitLimit));
+    if (!ok && lane == 0) abort_now();
+    return ok;
+  };
+
+  if (ntile > 0 && warp == 12) {
+    // ------------------------------------------------------------ copies
+    // Block ids are loaded two tiles ahead, scales one.
+    Walk cur;
+    cur.pair = s_where[0];
+    cur.q = s_where[1];
+    cur.tile = s_where[2];
+    cur.left = ntile;
+    walk_pair<Rows>(a, cur);
+    walk_item<Rows>(a, cur);
+    auto tokens = [&](const Walk& w) { return w.left > 0 ? max(0, min(kCtT, w.lim - w.tile * kCtT)) : 0; };
+    auto blocks = [&](const Walk& w) { return (tokens(w) + B - 1) >> shift; };
+    auto id_of = [&](const Walk& w) {
+      return lane < blocks(w) ? cache_block(a.c, w.pair, ((w.tile * kCtT) >> shift) + lane) : 0;
+    };
+    Walk nx = cur;
+    int id = id_of(cur);
+    walk_next<Rows>(a, nx);
+    int id1 = id_of(nx), turn = 0, seg0 = 0;   // seg0: number of the row tile's first tile here
+    int whole = cur.tile == 0 && cur.left >= cur.nt ? kWhole : 0;
+    int seg_end = min(ntile, cur.nt - cur.tile);
+    float ks = a.c.ks[id], vs = a.c.vs[id];
+    int it = 0;
+    for (;; ++it) {
+      const int st = it % NST;
+      if (!warp_wait(&sempty[st], (it / NST) ^ 1)) break;
+      const int nb = blocks(cur), cnt = tokens(cur);
+      if (lane == 0) tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb) * 2u * (B * D));
+      __syncwarp();
+      if (lane < nb) {
+        unsigned char* dst = stages + st * C::Stage + lane * (B * D);
+        const size_t src = static_cast<size_t>(id) * (B * D);
+        tc::bulk_load(dst, a.c.kc + src, B * D, &full[st]);
+        tc::bulk_load(dst + C::KB, a.c.vc + src, B * D, &full[st]);
+      }
+      Walk nx2 = nx;
+      if (nx2.left > 0) walk_next<Rows>(a, nx2);
+      const int id2 = id_of(nx2);
+      const float ks1 = a.c.ks[id1], vs1 = a.c.vs[id1];
+      TileInfo* in = infos + it % kCtInfo;
+      if (lane >= nb) ks = vs = 0.f;
+      // largest finite V scale, as an exponent above it
+      float top = fabsf(vs) < INFINITY ? fabsf(vs) : 0.f;
+      const bool odd = __any_sync(0xffffffffu, !(ks * a.scale_log2 >= 0.f));
+      top = warp_max(top);
+      if (lane < 8) {
+        in->ks[lane] = 0.f;
+        in->vs[lane] = 0.f;
+      }
+      const int g16 = lane << 4 >> shift;   // block of 16-token group `lane`
+      const float ksg = __shfl_sync(0xffffffffu, ks, g16 & 7), vsg = __shfl_sync(0xffffffffu, vs, g16 & 7);
+      if (lane < 8) {
+        in->ks[lane] = ksg;
+        in->vs[lane] = vsg;
+      }
+      if (lane == 0) {
+        const int k = it - seg0, stride = Two ? 1 : 2;
+        in->pair = cur.pair;
+        in->q = cur.q;
+        in->tile = cur.tile;
+        in->flags = cnt | (k == 0 ? kTFirst : 0) | (it == seg_end - 1 ? kTLast : 0) | (k < stride ? kSFirst : 0) |
+                    (it >= seg_end - stride ? kSLast : 0) | (cur.tile * kCtT + cnt > cur.seen0 ? kMixed : 0) | (odd ? kOdd : 0) | whole;
+        in->n = cur.n;
+        in->len = cur.len;
+        in->turn = turn;
+        in->vexp = max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -110);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&ifull[it % kCtInfo]);
+        tc::mbar_arrive(&full[st]);
+      }
+      if (nx.left <= 0) { ++it; break; }
+      if (it + 1 == seg_end) {   // another row tile
+        ++turn;
+        seg0 = seg_end;
+        whole = nx.left >= nx.nt ? kWhole : 0;
+        seg_end = min(ntile, seg0 + nx.nt);
+      }
+      cur = nx;
+      nx = nx2;
+      id = id1;
+      id1 = id2;
+      ks = ks1;
+      vs = vs1;
+    }
+    // after an abort, no copy may still be on its way when the CTA ends
+    if (lane == 0 && *s_abort)
+      for (int u = max(0, it - NST); u < it; ++u) tc::mbar_wait(&full[u % NST], (u / NST) & 1, kWaitLimit);
+    __syncwarp();
+  } else if (ntile > 0 && warp == 13) {
+    // ------------------------------------------------------------ tensor core
+    if (lane == 0) {
+      // Per stream: S(i), then (once P(i) is there, over S's columns) O += P(i) V(i), then the next S.  While one stream's softmax
+      // runs the other's products do.
+      constexpr int stride = Two ? 1 : 2;
+      int nS[2] = {0, Two ? 0 : 1}, nP[2] = {0, Two ? 0 : 1};
+      uint32_t useP[2] = {0, 0}, kdone = 0, vdone = 0;
+      uint64_t t_last = 0;
+      int idle = 0;
+      const uint32_t q0 = tc::smem_u32(qbuf), k0 = tc::smem_u32(kbuf), v0 = tc::smem_u32(vbuf);
+      while (nP[0] < ntile || nP[1] < ntile) {
+        bool did = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t tS = tmem + x * kCtT, tO = tmem + 2 * kCtT + x * D;
+          if (nP[x] < nS[x]) {
+            const int i = nP[x];
+            if (tc::mbar_test(&pfull[x], useP[x] & 1) && tc::mbar_test(&vfull[i & 1], (i >> 1) & 1)) {
+              tc::fence_after();
+              const int flags = infos[i % kCtInfo].flags;
+#pragma unroll
+              for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+                for (int k = 0; k < kCtT / 16; ++k)
+                  mma_f16_ts(tO, tS + t * 64 + k * 8, tc::desc_k_none(v0 + (i & 1) * C::QT + k * (2 * D * 16), D * 16, 128),
+                             idesc_f16(D), !(flags & kSFirst) || t + k > 0);
+              if (!Two || (vdone ^= 1u << (i & 1), !(vdone >> (i & 1) & 1))) tc::mma_commit(&vempty[i & 1]);
+              if (flags & kSLast) tc::mma_commit(&ofin[x]);
+              nP[x] += stride;
+              ++useP[x];
+              did = true;
+            }
+          }
+          if (nS[x] == nP[x] && nS[x] < ntile) {
+            const int i = nS[x];
+            if (tc::mbar_test(&kfull[i & 1], (i >> 1) & 1) && tc::mbar_test(&qfull[Two ? x : 0], infos[i % kCtInfo].turn & 1)) {
+              tc::fence_after();
+#pragma unroll
+              for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                  tc::mma_bf16(tS, tc::desc_k_none(q0 + (Two ? x : t) * C::QT + k * 4096, 2048, 128),
+                               tc::desc_k_none(k0 + (i & 1) * C::QT + k * 4096, 2048, 128), idesc_f16(kCtT), t + k > 0);
+              tc::mma_commit(&sfull[x]);
+              if (!Two || (kdone ^= 1u << (i & 1), !(kdone >> (i & 1) & 1))) tc::mma_commit(&kempty[i & 1]);
+              nS[x] += stride;
+              did = true;
+            }
+          }
+        }
+        if (did) {
+          idle = 0;
+          continue;
+        }
+        // nothing ready: look at the clock now and then
+        if (idle == 0) t_last = tc::globaltimer_ns();
+        if ((++idle & 63) == 0 && (*s_abort || tc::globaltimer_ns() - t_last > kWaitLimit)) {
+          abort_now();
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (ntile > 0 && warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------ conversion
+    const int t = tid - 256;
+    auto to_half = [](const uint4& w, uint4* lo, uint4* hi) {
+      const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+      uint32_t h[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c[e] >> (16 * u)), __NV_E4M3);
+          h[2 * e + u] = r.x | static_cast<uint32_t>(r.y) << 16;
+        }
+      *lo = make_uint4(h[0], h[1], h[2], h[3]);
+      *hi = make_uint4(h[4], h[5], h[6], h[7]);
+    };
+    for (int i = 0; i < ntile; ++i) {
+      const int st = i % NST, b = i & 1;
+      if (!warp_wait(&full[st], i / NST)) break;
+      const int flags = infos[i % kCtInfo].flags, cnt = flags & 255;
+      const unsigned char* kc = stages + st * C::Stage;
+      const unsigned char* vc = kc + C::KB;
+      if (!warp_wait(&kempty[b], (i >> 1) ^ 1)) break;
+      // (codes past the tokens are whatever was there: their logits are not used)
+#pragma unroll 4
+      for (int j = 0; j < D / 16; ++j) {
+        uint4 lo, hi;
+        to_half(*reinterpret_cast<const uint4*>(kc + (t >> 3) * (8 * D) + j * 128 + (t & 7) * 16), &lo, &hi);
+        uint4* dst = reinterpret_cast<uint4*>(kbuf + b * C::QT + j * 4096 + t * 16);
+        dst[0] = lo;
+        dst[2048 / 16] = hi;
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&kfull[b]);
+      if (!warp_wait(&vempty[b], (i >> 1) ^ 1)) break;
+      bool nan = false;
+#pragma unroll 4
+      for (int u = 0; u < D / 16; ++u) {
+        const int x = u * 128 + t, g = x / D, j = x % D;   // 16 tokens, dimension
+        uint4 w = *reinterpret_cast<const uint4*>(vc + x * 16);
+        if (flags & kMixed || cnt < kCtT) {
+          // V past the tokens counts as zero.  NaN that not all rows see is taken out and noted: bit e
+          // of a half word: token e of the 16
+          uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+          uint32_t bits = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t c = ww[e >> 2] >> (8 * (e & 3)) & 0x7f;
+            const bool held = g * 16 + e < cnt, bad = held && c == 0x7f && (flags & kMixed);
+            if (!held || bad) ww[e >> 2] &= ~(0xffu << (8 * (e & 3)));
+            bits |= (bad ? 1u : 0u) << e;
+          }
+          if (flags & kMixed) reinterpret_cast<uint16_t*>(nan_masks)[(b * 128 + j) * 8 + g] = static_cast<uint16_t>(bits);
+          nan |= bits != 0;
+        }
+        uint4 lo, hi;
+        to_half(w, &lo, &hi);
+        uint4* dst = reinterpret_cast<uint4*>(vbuf + b * C::QT + g * (2 * D * 16) + j * 16);
+        dst[0] = lo;
+        dst[D] = hi;
+      }
+      if (flags & kMixed) {
+        const bool any = !tc::named_sync_and(1, 128, !nan);
+        if (t == 0) s_nan[b] = any;
+        __syncwarp();
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&vfull[b]);
+        tc::mbar_arrive(&sempty[st]);
+      }
+    }
+  } else if (ntile > 0 && warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(wq) << 21;
+    const uint32_t tS = tmem + x * kCtT + lanes, tO0 = tmem + 2 * kCtT + lanes, tO = tO0 + x * D;
+    float m = -INFINITY, l = 0.f, rowf = 0.f;
+    int lim = 0, vexp = 0, seq = 0, j = 0, h = 0;
+    bool valid = false, active = false, used = false;
+    uint32_t nanrow[D / 32];
+    uint32_t use = 0, fin0 = 0, fin1 = 0;
+    int joined = 0;   // stream 1: row tiles that stream 0 is known to have joined
+    auto wait_joined = [&](int turn) {
+      if (joined >= turn) return true;
+      joined = turn;
+      return warp_wait(jdone, turn - 1);
+    };
+
+    // The row's query, in fp16 terms, and the factor of its logits.
+    auto lay_q = [&]() {
+      const T* src = static_cast<const T*>(a.q) + seq * a.qb + h * a.qh + j * a.qs;
+      constexpr int V = Ty<T>::kVec;   // elements of 16 bytes
+      float top = 0.f;
+      bool bad = false;
+      float v[8];
+      auto load8 = [&](int e) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = 0.f;
+        if (!valid) return;
+        if (a.wide_q) {
+#pragma unroll
+          for (int u = 0; u < 8; u += V) Ty<T>::load16(src + e + u, v + u);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) v[u] = Ty<T>::to_f(src[e + u]);
+        }
+      };
+#pragma unroll 4
+      for (int e = 0; e < D; e += 8) {
+        load8(e);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float z = fabsf(v[u]);
+          bad |= !(z < INFINITY);
+          top = fmaxf(top, z);
+        }
+      }
+      const int ex = bad ? 0 : max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+      const float down = exp2i(14 - ex);   // the largest to [2^14, 2^15)
+      rowf = exp2i(ex - 14) * a.scale_log2;
+#pragma unroll 4
+      for (int e = 0; e < D; e += 8) {
+        load8(e);
+        uint32_t w[C::NT][4];
+#pragma unroll
+        for (int u = 0; u < 8; u += 2) {
+          float y0 = bad ? __int_as_float(0x7fffffff) : v[u] * down, y1 = bad ? y0 : v[u + 1] * down;
+#pragma unroll
+          for (int n = 0; n < C::NT; ++n) {
+            const __half2 z = __floats2half2_rn(y0, y1);
+            w[n][u / 2] = *reinterpret_cast<const uint32_t*>(&z);
+            y0 -= __low2float(z);
+            y1 -= __high2float(z);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+          *reinterpret_cast<uint4*>(qbuf + (Two ? x : n) * C::QT + e * 256 + row * 16) = make_uint4(w[n][0], w[n][1], w[n][2], w[n][3]);
+      }
+      if (!Two) sqs[row] = rowf;
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&qfull[Two ? x : 0]);
+    };
+
+    // S of one tile to P over its columns.  General: tokens the row does not see, scales of any kind.
+    auto softmax = [&](const TileInfo& in, bool first, auto general) {
+      constexpr bool General = decltype(general)::value;
+      const int rem = lim - in.tile * kCtT;
+      float f[8], mt = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) f[g] = rowf * in.ks[g];
+#pragma unroll
+      for (int c = 0; c < kCtT; c += 32) {
+        float s[32];
+        tc::tmem_ld32(tS + c, s);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float top = General ? -INFINITY : s[16 * g];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float z = s[16 * g + e];
+            if (General) top = fmaxf(top, c + 16 * g + e < rem ? z * f[c / 16 + g] : -INFINITY);
+            else top = fmaxf(top, z);
+          }
+          mt = fmaxf(mt, General ? top : top * f[c / 16 + g]);
+        }
+      }
+      const int v2 = first ? in.vexp : max(vexp, in.vexp);
+      if (first) {
+        m = mt;
+      } else if (__any_sync(0xffffffffu, mt > m + 4.f) || v2 > vexp) {
+        const float m2 = fmaxf(m, mt), al = m2 == -INFINITY ? 1.f : ex2(m - m2);
+        m = m2;
+        l *= al;
+        const float r = al * exp2i(max(vexp - v2, -126));
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          tc::tmem_ld16(tO + c, o);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * r);
+          tmem_st16(tO + c, w);
+        }
+      }
+      vexp = v2;
+      const float ref = m == -INFINITY ? 0.f : m, up = exp2i(11 - vexp);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      [[maybe_unused]] uint32_t low[C::NT > 1 ? 64 : 1];
+#pragma unroll
+      for (int c = 0; c < kCtT; c += 32) {
+        float s[32];
+        tc::tmem_ld32(tS + c, s);
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float fg = f[(c + e) / 16], fv = in.vs[(c + e) / 16] * up;
+          float p0 = ex2(fmaf(s[e], fg, -ref)), p1 = ex2(fmaf(s[e + 1], fg, -ref));
+          if (General) {
+            p0 = c + e < rem ? p0 : 0.f;
+            p1 = c + e + 1 < rem ? p1 : 0.f;
+          }
+          sum[e / 2 & 3] += p0 + p1;
+          p0 = !General || c + e < rem ? p0 * fv : 0.f;
+          p1 = !General || c + e + 1 < rem ? p1 * fv : 0.f;
+          const __half2 z = __floats2half2_rn(p0, p1);
+          w[e / 2] = *reinterpret_cast<const uint32_t*>(&z);
+          if constexpr (C::NT > 1) {
+            const __half2 y = __floats2half2_rn(p0 - __low2float(z), p1 - __high2float(z));
+            low[(c + e) / 2] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+        }
+        // (columns c / 2 .. c / 2 + 16 of S have been read)
+        tmem_st16(tS + c / 2, w);
+      }
+      if constexpr (C::NT > 1) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) tmem_st16(tS + 64 + c, low + c);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+    };
+
+    // The finished row (o times 2^(vexp - 11) / l), or this CTA's part of it.
+    auto store = [&](const float* o, int c, float r, bool whole, size_t part) {   // 16 columns from c
+      if (!whole) {
+        float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e] * r, o[4 * e + 1] * r, o[4 * e + 2] * r, o[4 * e + 3] * r);
+        return;
+      }
+      T* dst = static_cast<T*>(a.out) + seq * a.ob + h * a.oh + j * a.os + c;
+      T v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = Ty<T>::from_f(lim > 0 ? o[e] * r : 0.f);
+      if (a.wide_o) {
+#pragma unroll
+        for (int e = 0; e < static_cast<int>(sizeof(v) / 16); ++e) reinterpret_cast<uint4*>(dst)[e] = reinterpret_cast<const uint4*>(v)[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dst[e] = v[e];
+      }
+    };
+
+    for (int i = 0; i < ntile; ++i) {
+      if (!warp_wait(&ifull[i % kCtInfo], i / kCtInfo)) break;
+      const TileInfo& in = infos[i % kCtInfo];
+      const int flags = in.flags, turn = in.turn;
+      if (flags & kTFirst) {
+        const int r = in.q * Rows + (Two ? x * kCtT : 0) + row, kvh = in.pair % a.c.h_kv;
+        seq = in.pair / a.c.h_kv;
+        valid = r < in.len * a.G;
+        j = valid ? r / a.G : 0;
+        h = kvh * a.G + (valid ? r - j * a.G : 0);
+        lim = valid ? tokens_seen(a, in.n, in.len, j) : 0;
+        active = __any_sync(0xffffffffu, valid);
+        m = -INFINITY;
+        l = 0.f;
+        used = false;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) nanrow[e] = 0;
+        if (Two || x == 0) {
+          lay_q();
+        } else {
+          if (!warp_wait(&qfull[0], turn)) break;
+          rowf = sqs[row];
+        }
+      }
+      if (Two || (i & 1) == x) {
+        if (!warp_wait(&sfull[x], use)) break;
+        ++use;
+        tc::fence_after();
+        if (!Two && x == 1 && !wait_joined(turn)) break;   // O is free
+        if (active) {
+          const int rem = lim - in.tile * kCtT;
+          if (__any_sync(0xffffffffu, rem < kCtT && valid) || (flags & kOdd))
+            softmax(in, !used, std::true_type{});
+          else
+            softmax(in, !used, std::false_type{});
+          if (flags & kMixed) {
+            if (!warp_wait(&vfull[i & 1], i >> 1)) break;
+            if (s_nan[i & 1])
+              for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int k = rem - 32 * e;   // tokens of this word that the row sees
+                  const uint32_t see = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+                  const uint32_t hit = nan_masks[((i & 1) * 128 + d) * 4 + e] & see ? 1u << (d & 31) : 0u;
+#pragma unroll
+                  for (int u = 0; u < D / 32; ++u) nanrow[u] |= d / 32 == u ? hit : 0u;
+                }
+          }
+        }
+        used = true;
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&pfull[x]);
+      }
+      if (!(flags & kTLast)) continue;
+      // ---- the row tile's end
+      bool nan_any = false;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) nan_any |= nanrow[e] != 0;
+      nan_any = __any_sync(0xffffffffu, nan_any);
+      if (!Two && x == 1) {
+        if (!wait_joined(turn)) break;
+        s_ml[row] = make_float2(m, l);
+        if (nan_any)
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) nan_masks[(2 * 128 + row) * 4 + e] = nanrow[e];
+        if (lane == 0) s_join[wq] = make_int2(used ? vexp : INT_MIN, nan_any);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(jfull);
+        continue;
+      }
+      float m1 = -INFINITY, l1 = 0.f;
+      int vexp1 = INT_MIN;
+      if (!Two) {
+        if (!warp_wait(jfull, turn)) break;
+        const float2 ml = s_ml[row];
+        const int2 sj = s_join[wq];
+        vexp1 = sj.x;
+        if (vexp1 != INT_MIN) {
+          m1 = ml.x;
+          l1 = ml.y;
+          if (!warp_wait(&ofin[1], fin1++)) break;
+        }
+        if (sj.y) {
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) nanrow[e] |= nan_masks[(2 * 128 + row) * 4 + e];
+          nan_any = true;
+        }
+      }
+      if (used && !warp_wait(&ofin[Two ? x : 0], fin0++)) break;
+      tc::fence_after();
+      if (active) {
+        const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
+        float r0 = used ? ex2(m - ref) : 0.f, r1 = vexp1 != INT_MIN ? ex2(m1 - ref) : 0.f;
+        const float sum = (used ? l * r0 : 0.f) + (vexp1 != INT_MIN ? l1 * r1 : 0.f);
+        r0 *= exp2i(used ? vexp - 11 : 0);
+        r1 *= exp2i(vexp1 != INT_MIN ? vexp1 - 11 : 0);
+        const bool whole = flags & kWhole;
+        const float inv = whole ? 1.f / sum : 1.f;
+        const size_t part = static_cast<size_t>(2 * cta + (turn > 0)) * Rows + (Two ? x * kCtT : 0) + row;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16], z[16];
+          if (used) {
+            tc::tmem_ld16(tO + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= r0;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          }
+          if (!Two && vexp1 != INT_MIN) {
+            tc::tmem_ld16(tO0 + D + c, z);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(z[e], r1, o[e]);
+          }
+          if (nan_any) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) bits = c / 32 == u ? nanrow[u] : bits;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (bits >> ((c & 31) + e) & 1) o[e] = __int_as_float(0x7fffffff);
+          }
+          if (valid) store(o, c, inv, whole, part);
+        }
+        if (valid && !whole) a.part_ml[part] = make_float2(mm, sum);
+        if (valid && whole && a.lse)
+          a.lse[(static_cast<size_t>(seq) * a.h_q + h) * a.s + j] = lim > 0 ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      }
+      tc::fence_before();
+      if (!Two) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(jdone);
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ merge
+constexpr int kCgThreads = 256, kCgRows = 8;
+
+// Row (x) = boundary between two CTAs' runs: the first one inside a row tile joins its
+// parts, in order; kCgRows rows to a CTA, a warp to a row.
+template <typename T, int D, int Rows>
+__global__ void __launch_bounds__(kCgThreads) k_tokens_merge(const __grid_constant__ TokensArgs a, int ncta) {
+  constexpr int E = D / 32;
+  tc::grid_dep_wait();
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  const int4 rec = a.rec[c];
+  if (rec.x < 0) return;
+  const int total = rec.w, n = min(ncta, total), first = rec.z;
+  if (run_begin(c - 1, n, total) > first) return;
+  const int seq = rec.x / a.c.h_kv, kvh = rec.x - seq * a.c.h_kv, len = tokens_len(a, seq), tok = cache_tokens(a.c, rec.x);
+  const int nt = lim_tiles(tile_lim<Rows>(a, tok, len, rec.y));
+  const int c1 = run_owner(min(first + nt, total) - 1, n, total);
+  const int slot0 = 2 * (c - 1) + (run_begin(c - 1, n, total) < first);   // CTA c - 1's last part; the others' first
+  for (int u = threadIdx.x >> 5; u < kCgRows; u += kCgThreads / 32) {
+    const int row = blockIdx.y * kCgRows + u, r = rec.y * Rows + row;
+    if (r >= len * a.G) return;
+    const int j = r / a.G, h = kvh * a.G + r - j * a.G;
+    auto at = [&](int v) { return static_cast<size_t>(v == c - 1 ? slot0 : 2 * v) * Rows + row; };
+    float M = -INFINITY;
+    for (int v = c - 1 + lane; v <= c1; v += 32) M = fmaxf(M, a.part_ml[at(v)].x);
+    M = warp_max(M);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f, o[E] = {};
+    for (int v = c - 1; v <= c1; ++v) {
+      const float2 ml = a.part_ml[at(v)];
+      const float w = ex2(ml.x - ref);
+      L = fmaf(ml.y, w, L);
+      const float* src = a.part_o + at(v) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], w, o[e]);
+    }
+    const bool sees = tokens_seen(a, tok, len, j) > 0;
+    T* dst = static_cast<T*>(a.out) + seq * a.ob + h * a.oh + j * a.os + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) dst[e] = Ty<T>::from_f(sees ? o[e] / L : 0.f);
+    if (a.lse && lane == 0)
+      a.lse[(static_cast<size_t>(seq) * a.h_q + h) * a.s + j] = sees ? (ref + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+// Two row tiles at a time where a sequence's rows fill more than one (bf16; an fp32 row's terms take the
+// room of the second).
+static bool tokens_two(int dtype, int rows) { return dtype == SKV_DTYPE_BF16 && rows > kCtT; }
+
+static int tokens_ctas(const shadowkv_cache& c, int rows, int per, int nsm) {
+  const long long tiles = (static_cast<long long>(c.max_blocks) * c.block + kCtT - 1) / kCtT;
+  const long long all = tiles * ((rows + per - 1) / per) * c.b * c.h_kv;
+  return static_cast<int>(all < nsm ? all : nsm);
+}
+
+static size_t tokens_layout(const shadowkv_cache& c, int nsm, char* base, TokensArgs* a) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base + off;
+    off += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  char* rec = take(nsm * sizeof(int4));
+  char* ml = take(static_cast<size_t>(2 * nsm) * 256 * sizeof(float2));
+  char* nan = take(static_cast<size_t>(nsm) * 3 * 128 * 4 * sizeof(uint32_t));
+  char* o = take(static_cast<size_t>(2 * nsm) * 256 * c.d * sizeof(float));
+  if (a) {
+    a->rec = reinterpret_cast<int4*>(rec);
+    a->part_ml = reinterpret_cast<float2*>(ml);
+    a->nan = reinterpret_cast<uint32_t*>(nan);
+    a->part_o = reinterpret_cast<float*>(o);
+  }
+  return off;
+}
+
+template <typename T, int D, bool Two>
+static cudaError_t attend_tokens_t(const TokensArgs& a, const shadowkv_cache& c, int nsm, cudaStream_t st) {
+  using C = Ct<T, D, Two>;
+  const int ncta = tokens_ctas(c, a.s * a.G, C::Rows, nsm);
+  const auto kern = k_attend_tokens<T, D, Two>;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), C::Smem);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ncta), dim3(kCtThreads), C::Smem, st, a);
+  if (e != cudaSuccess || ncta == 1) return e;
+  const int rows = a.s * a.G < C::Rows ? a.s * a.G : C::Rows;
+  return launch_pdl(k_tokens_merge<T, D, C::Rows>, dim3(ncta - 1, (rows + kCgRows - 1) / kCgRows), dim3(kCgThreads), 0, st, a, ncta);
+}
+
+template <int D>
+static cudaError_t attend_tokens_d(const TokensArgs& a, const shadowkv_cache& c, int dtype, int nsm, cudaStream_t st) {
+  if (dtype != SKV_DTYPE_BF16) return attend_tokens_t<float, D, false>(a, c, nsm, st);
+  return tokens_two(dtype, a.s * a.G) ? attend_tokens_t<bf16, D, true>(a, c, nsm, st) : attend_tokens_t<bf16, D, false>(a, c, nsm, st);
 }
 
 static const char* tokens_fault(const shadowkv_cache& c, int h_q, int s, skv_status* st) {
@@ -95,7 +961,10 @@ static const char* tokens_fault(const shadowkv_cache& c, int h_q, int s, skv_sta
   if (s < 0) return "s must be >= 0";
   *st = SKV_ERR_UNSUPPORTED;
   if (h_q < 1 || h_q % c.h_kv || h_q / c.h_kv > 128) return "h_q must be a multiple of h_kv, of at most 128";
-  if (static_cast<long long>(s) * (h_q / c.h_kv) > 1 << 24) return "s h_q / h_kv must be at most 2^24";
+  const long long rows = static_cast<long long>(s) * (h_q / c.h_kv);
+  if (rows > 1 << 24) return "s h_q / h_kv must be at most 2^24";
+  if (((rows + 127) / 128) * ((static_cast<long long>(c.max_blocks) * c.block + 127) / 128) >= (1LL << 31) / (static_cast<long long>(c.b) * c.h_kv))
+    return "too many queries and tokens for one call";
   *st = SKV_OK;
   return nullptr;
 }
@@ -120,7 +989,13 @@ size_t shadowkv_cache_attend_tokens_workspace(const shadowkv_cache* c, int h_q, 
     skv::set_error(st, f);
     return 0;
   }
-  return 256;
+  int nsm = 0;
+  const cudaError_t e = skv::device_sms(&nsm);
+  if (e != cudaSuccess) {
+    skv::set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
+    return 0;
+  }
+  return skv::tokens_layout(*c, nsm, nullptr, nullptr);
 } catch (...) {   // host memory for an error text or a table ran out
   return 0;
 }
@@ -142,9 +1017,13 @@ skv_status shadowkv_cache_attend_tokens(const shadowkv_cache* c, int dtype, int 
   if (!f && !std::isfinite(scale)) f = "scale must be finite";
   if (!f && causal != 0 && causal != 1) f = "causal must be 0 or 1";
   if (!f && (!work || reinterpret_cast<uintptr_t>(work) % 256)) f = "the workspace must be non-NULL and 256-byte aligned";
-  if (!f && work_bytes < 256) f = "the workspace is smaller than shadowkv_cache_attend_tokens_workspace";
   if (f) return set_error(SKV_ERR_INVALID_ARG, f);
+  int nsm = 0;
+  cudaError_t e = skv::device_sms(&nsm);
+  if (e != cudaSuccess) return set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
   skv::TokensArgs a;
+  if (work_bytes < skv::tokens_layout(*c, nsm, static_cast<char*>(work), &a))
+    return set_error(SKV_ERR_INVALID_ARG, "the workspace is smaller than shadowkv_cache_attend_tokens_workspace");
   a.c = skv::cache_dev(*c);
   a.q = q->ptr;
   a.out = out->ptr;
@@ -158,13 +1037,14 @@ skv_status shadowkv_cache_attend_tokens(const shadowkv_cache* c, int dtype, int 
   a.h_q = h_q;
   a.G = h_q / c->h_kv;
   a.causal = causal;
+  auto wide = [&](const void* ptr, long long sb, long long sh, long long ss) {
+    return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && (sb * E) % 16 == 0 && (sh * E) % 16 == 0 && (ss * E) % 16 == 0;
+  };
+  a.wide_q = wide(q->ptr, a.qb, a.qh, a.qs);
+  a.wide_o = wide(out->ptr, a.ob, a.oh, a.os);
   cudaStream_t p = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> together(skv::cache_enqueue());
-  cudaError_t e;
-  if (dtype == SKV_DTYPE_BF16)
-    e = c->d == 128 ? skv::attend_tokens_t<skv::bf16, 128>(a, *c, p) : skv::attend_tokens_t<skv::bf16, 64>(a, *c, p);
-  else
-    e = c->d == 128 ? skv::attend_tokens_t<float, 128>(a, *c, p) : skv::attend_tokens_t<float, 64>(a, *c, p);
+  e = c->d == 128 ? skv::attend_tokens_d<128>(a, *c, dtype, nsm, p) : skv::attend_tokens_d<64>(a, *c, dtype, nsm, p);
   return e == cudaSuccess ? SKV_OK : set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
 } catch (...) {   // host memory for an error text or a table ran out
   return SKV_ERR_OOM;

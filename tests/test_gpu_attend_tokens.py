@@ -3,9 +3,11 @@ definition in 64 bits on the same codes.
 
 Tolerance, for a result out = sum p v with M = sum p |v| (the magnitudes it is made of):
   its own rounding: half a step, bf16 2^-8, fp32 2^-24 of the value;
-  p times its V scale as an MMA operand: bf16 11 bits (2^-12 of itself), fp32 22 (2^-23), and
-    2^-36 of the largest p times the largest V scale below that (fp16's subnormals; FLOOR);
-  the logit: exact products of fp16 operands (fp32 queries: to 2^-23), summed in fp32 with
+  p times its V scale as an fp16 operand: half a step is 2^-11 of itself (11 bits: steps of 2^-10 of
+    the power of two below a value); beside fp32 two terms, the second half a step of what the first
+    leaves: 2^-11 of 2^-11 = 2^-22; and 2^-36 of the largest p times the largest V scale at
+    least (fp16's subnormals: half a step is 2^-25, and the largest product is 2^11 or more);
+  the logit: exact products of fp16 operands (fp32 queries, two terms: to 2^-22), summed in fp32 with
     errors of at most 2^-21 of the sum of magnitudes L, three roundings more;
   2^x by the hardware: 2^-22, its argument's rounding 2^-23 of the logit in base 2;
   the sum of p: fp32, in partial sums: (64 + tiles) roundings of 2^-24;
@@ -107,9 +109,9 @@ def close(got, lse, c, q, lens=None, causal=True, scale=None, before=None):
             L = abs(scale) * (x.abs() @ k.abs().T).masked_fill(hide, 0).amax(-1, keepdim=True)
             tiles = -(-n // 128)
             dp = (2.0 ** -21 + 3 * U + 2 * U * 1.45) * L + 2.0 ** -22 + 2 * U * top.abs().masked_fill(empty, 0) * 1.45 + (64 + tiles) * U
-            dp = dp + (0 if bf else 2.0 ** -23 * L)
+            dp = dp + (0 if bf else 2.0 ** -22 * L)
             floor = n * 2.0 ** -36 * 448 * (p.amax(-1, keepdim=True)) * vs.max()
-            tol = (2.0 ** -8 if bf else U) * ref.abs() + (2 * dp + (2.0 ** -12 if bf else 2.0 ** -23) + 2.0 ** -21 + tiles * U) * mag + floor
+            tol = (2.0 ** -8 if bf else U) * ref.abs() + (2 * dp + (2.0 ** -11 if bf else 2.0 ** -22) + 2.0 ** -21 + tiles * U) * mag + floor
             err = (o - ref).abs()
             assert bool((err <= tol + 1e-38).all()), (i, g, float((err / (tol + 1e-38)).max()))
             worst = max(worst, float((err / (tol + 1e-38)).max()))
