@@ -61,19 +61,22 @@ __device__ __forceinline__ int tokens_seen(const TokensArgs& a, int n, int len, 
 }
 
 // One of bf16's or fp32's forms.  Two: a CTA works on two row tiles with the same tokens at a
-// time (stream 0 and 1); else on one, whose tokens' tiles the streams take in turn.
-template <typename T, int D, bool Two>
+// time (stream 0 and 1); else on one, whose tokens' tiles the streams take in turn.  Copies = 4: at most
+// 32 rows, which stand in the MMA's rows four times, so that each of the softmax's warps takes 32 of a tile's 128 columns (its
+// P is zero elsewhere) and has sums of its own.
+template <typename T, int D, bool Two, int Copies>
 struct Ct {
   static constexpr int NT = sizeof(T) == 2 ? 1 : 2;        // fp16 terms of q and p
-  static constexpr int Rows = Two ? 256 : 128;
+  static constexpr int Rows = (Two ? 256 : 128) / Copies;
+  static constexpr int PartRows = Two ? 256 : 128;          // rows of a part, copies and all
   static constexpr int QT = kCtT * D * 2;                   // an operand tile in fp16
   static constexpr int QB = (Two ? 2 : NT) * QT;
-  static constexpr int KB = kCtT * D, Stage = 2 * KB;       // codes of K, of V
+  static constexpr int KB = kCtT * D;                       // codes of K or of V: a stage
   static constexpr int Misc = 2816;
   static constexpr int Most = 227 * 1024 - 128 - Misc;
-  static constexpr int NST0 = (Most - QB - 4 * QT) / Stage, NST = NST0 > 4 ? 4 : NST0;
-  static constexpr int Smem = 128 + QB + 4 * QT + NST * Stage + Misc;
-  static_assert(NST >= 1 && !(Two && NT > 1), "tile");
+  static constexpr int NST0 = (Most - QB - 4 * QT) / KB, NST = NST0 > 8 ? 8 : NST0;
+  static constexpr int Smem = 128 + QB + 4 * QT + NST * KB + Misc;
+  static_assert(NST >= 2 && !(Two && (NT > 1 || Copies > 1)), "tile");
 };
 
 // ------------------------------------------------------------ tensor core
@@ -228,9 +231,41 @@ struct TileInfo {
   float ks[8], vs[8];                             // of every 16 tokens
 };
 
-template <typename T, int D, bool Two>
+// One row of a row tile from its parts (numbers u of n; a part's Copies sub-rows lie `step` apart): a warp's work.
+template <typename T, int D, int Copies, typename At>
+__device__ __forceinline__ void join_row(const TokensArgs& a, int seq, int h, int j, bool sees, int n, int step, At&& at) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY;
+  for (int u = lane; u < n * Copies; u += 32) M = fmaxf(M, __ldcg(&a.part_ml[at(u / Copies) + u % Copies * step].x));
+  M = warp_max(M);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f, o[E] = {};
+#pragma unroll 4
+  for (int u = 0; u < n * Copies; ++u) {
+    const size_t row = at(u / Copies) + u % Copies * step;
+    const float2 ml = __ldcg(&a.part_ml[row]);
+    const float w = ex2(ml.x - ref);
+    L = fmaf(ml.y, w, L);
+    const float* src = a.part_o + row * D + lane * E;
+    if constexpr (E == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      o[0] = fmaf(v.x, w, o[0]); o[1] = fmaf(v.y, w, o[1]); o[2] = fmaf(v.z, w, o[2]); o[3] = fmaf(v.w, w, o[3]);
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+      o[0] = fmaf(v.x, w, o[0]); o[1] = fmaf(v.y, w, o[1]);
+    }
+  }
+  T* dst = static_cast<T*>(a.out) + seq * a.ob + h * a.oh + j * a.os + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) dst[e] = Ty<T>::from_f(sees ? o[e] / L : 0.f);
+  if (a.lse && lane == 0)
+    a.lse[(static_cast<size_t>(seq) * a.h_q + h) * a.s + j] = sees ? (ref + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <typename T, int D, bool Two, int Copies>
 __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_constant__ TokensArgs a) {
-  using C = Ct<T, D, Two>;
+  using C = Ct<T, D, Two, Copies>;
   constexpr int NST = C::NST, Rows = C::Rows;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -238,25 +273,25 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
   unsigned char* kbuf = qbuf + C::QB;                    // [2] K in fp16
   unsigned char* vbuf = kbuf + 2 * C::QT;                // [2] V
   unsigned char* stages = vbuf + 2 * C::QT;              // [NST] codes
-  unsigned char* misc = stages + NST * C::Stage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(misc);    // [4] codes are there
-  uint64_t* sempty = full + 4;                           // [4] codes are converted
-  uint64_t* kfull = full + 8;                            // [2]
-  uint64_t* kempty = full + 10;
-  uint64_t* vfull = full + 12;
-  uint64_t* vempty = full + 14;
-  uint64_t* sfull = full + 16;                           // [2], by stream
-  uint64_t* pfull = full + 18;
-  uint64_t* ofin = full + 20;                            // a row tile's last product is done
-  uint64_t* qfull = full + 22;
-  uint64_t* jfull = full + 24;                           // stream 1's sums are there
-  uint64_t* jdone = full + 25;                           // stream 0 has joined the two
-  uint64_t* ifull = full + 26;                           // [8]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 272);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 276);
-  int* s_where = reinterpret_cast<int*>(misc + 280);     // [4]
-  volatile int* s_nan = reinterpret_cast<volatile int*>(misc + 296);   // [2]: V's tile has NaN
-  int* s_scan = reinterpret_cast<int*>(misc + 304);      // [32]
+  unsigned char* misc = stages + NST * C::KB;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc);    // [8] codes are there: K and V of the tiles in turn
+  uint64_t* sempty = full + 8;                           // [8] codes are converted
+  uint64_t* kfull = full + 16;                           // [2]
+  uint64_t* kempty = full + 18;
+  uint64_t* vfull = full + 20;
+  uint64_t* vempty = full + 22;
+  uint64_t* sfull = full + 24;                           // [2], by stream
+  uint64_t* pfull = full + 26;
+  uint64_t* ofin = full + 28;                            // a row tile's last product is done
+  uint64_t* qfull = full + 30;
+  uint64_t* jfull = full + 32;                           // stream 1's sums are there
+  uint64_t* jdone = full + 33;                           // stream 0 has joined the two
+  uint64_t* ifull = full + 34;                           // [8]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 336);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 340);
+  int* s_where = reinterpret_cast<int*>(misc + 344);     // [4]
+  volatile int* s_nan = reinterpret_cast<volatile int*>(misc + 360);   // [2]: V's tile has NaN
+  int* s_scan = reinterpret_cast<int*>(misc + 448);      // [32], before the tiles are described
   TileInfo* infos = reinterpret_cast<TileInfo*>(misc + 448);
   float* sqs = reinterpret_cast<float*>(misc + 1216);    // [128] rows' factors (one row tile)
   float2* s_ml = reinterpret_cast<float2*>(misc + 1728); // [128] stream 1's maxima and sums
@@ -267,7 +302,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      tc::mbar_init(&full[i], 2);   // the copies, and the tile's description
+      tc::mbar_init(&full[i], 1);
       tc::mbar_init(&sempty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -311,6 +346,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     flag_error(a.c.status, DEV_TIMEOUT);
   };
   auto warp_wait = [&](uint64_t* bar, uint32_t phase) {
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, phase & 1))) return true;
     const bool ok = __all_sync(0xffffffffu, !*s_abort && tc::mbar_wait(bar, phase & 1, kWaitLimit));
     if (!ok && lane == 0) abort_now();
     return ok;
@@ -338,33 +374,24 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     int whole = cur.tile == 0 && cur.left >= cur.nt ? kWhole : 0;
     int seg_end = min(ntile, cur.nt - cur.tile);
     float ks = a.c.ks[id], vs = a.c.vs[id];
-    int it = 0;
-    for (;; ++it) {
-      const int st = it % NST;
-      if (!warp_wait(&sempty[st], (it / NST) ^ 1)) break;
-      const int nb = blocks(cur), cnt = tokens(cur);
-      if (lane == 0) tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb) * 2u * (B * D));
-      __syncwarp();
-      if (lane < nb) {
-        unsigned char* dst = stages + st * C::Stage + lane * (B * D);
-        const size_t src = static_cast<size_t>(id) * (B * D);
-        tc::bulk_load(dst, a.c.kc + src, B * D, &full[st]);
-        tc::bulk_load(dst + C::KB, a.c.vc + src, B * D, &full[st]);
+    int it = 0, copied = 0;
+    int st = 0;           // stage and its turn
+    uint32_t ph = 1;
+    auto next_stage = [&]() {
+      if (++st == NST) {
+        st = 0;
+        ph ^= 1;
       }
-      Walk nx2 = nx;
-      if (nx2.left > 0) walk_next<Rows>(a, nx2);
-      const int id2 = id_of(nx2);
-      const float ks1 = a.c.ks[id1], vs1 = a.c.vs[id1];
+    };
+    for (;; ++it) {
+      const int nb = blocks(cur), cnt = tokens(cur);
+      if (!warp_wait(&sempty[st], ph)) break;
+      // (the stage is free: the tile kCtInfo before this one has been described to all and used)
       TileInfo* in = infos + it % kCtInfo;
       if (lane >= nb) ks = vs = 0.f;
       // largest finite V scale, as an exponent above it
-      float top = fabsf(vs) < INFINITY ? fabsf(vs) : 0.f;
       const bool odd = __any_sync(0xffffffffu, !(ks * a.scale_log2 >= 0.f));
-      top = warp_max(top);
-      if (lane < 8) {
-        in->ks[lane] = 0.f;
-        in->vs[lane] = 0.f;
-      }
+      const float top = warp_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.f);
       const int g16 = lane << 4 >> shift;   // block of 16-token group `lane`
       const float ksg = __shfl_sync(0xffffffffu, ks, g16 & 7), vsg = __shfl_sync(0xffffffffu, vs, g16 & 7);
       if (lane < 8) {
@@ -386,9 +413,24 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       __syncwarp();
       if (lane == 0) {
         tc::mbar_arrive(&ifull[it % kCtInfo]);
-        tc::mbar_arrive(&full[st]);
+        tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb * B * D));
       }
-      if (nx.left <= 0) { ++it; break; }
+      __syncwarp();
+      const size_t src = static_cast<size_t>(id) * (B * D);
+      if (lane < nb) tc::bulk_load(stages + st * C::KB + lane * (B * D), a.c.kc + src, B * D, &full[st]);
+      ++copied;
+      next_stage();
+      if (!warp_wait(&sempty[st], ph)) break;
+      if (lane == 0) tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb * B * D));
+      __syncwarp();
+      if (lane < nb) tc::bulk_load(stages + st * C::KB + lane * (B * D), a.c.vc + src, B * D, &full[st]);
+      ++copied;
+      next_stage();
+      Walk nx2 = nx;
+      if (nx2.left > 0) walk_next<Rows>(a, nx2);
+      const int id2 = id_of(nx2);
+      const float ks1 = a.c.ks[id1], vs1 = a.c.vs[id1];
+      if (nx.left <= 0) break;
       if (it + 1 == seg_end) {   // another row tile
         ++turn;
         seg0 = seg_end;
@@ -404,7 +446,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     }
     // after an abort, no copy may still be on its way when the CTA ends
     if (lane == 0 && *s_abort)
-      for (int u = max(0, it - NST); u < it; ++u) tc::mbar_wait(&full[u % NST], (u / NST) & 1, kWaitLimit);
+      for (int u = max(0, copied - NST); u < copied; ++u) tc::mbar_wait(&full[u % NST], (u / NST) & 1, kWaitLimit);
     __syncwarp();
   } else if (ntile > 0 && warp == 13) {
     // ------------------------------------------------------------ tensor core
@@ -416,7 +458,9 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       uint32_t useP[2] = {0, 0}, kdone = 0, vdone = 0;
       uint64_t t_last = 0;
       int idle = 0;
-      const uint32_t q0 = tc::smem_u32(qbuf), k0 = tc::smem_u32(kbuf), v0 = tc::smem_u32(vbuf);
+      // (a descriptor's low bits are its address / 16)
+      const uint64_t dq = tc::desc_k_none(tc::smem_u32(qbuf), 2048, 128), dk = tc::desc_k_none(tc::smem_u32(kbuf), 2048, 128),
+                     dv = tc::desc_k_none(tc::smem_u32(vbuf), D * 16, 128);
       while (nP[0] < ntile || nP[1] < ntile) {
         bool did = false;
 #pragma unroll
@@ -431,7 +475,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
               for (int t = 0; t < C::NT; ++t)
 #pragma unroll
                 for (int k = 0; k < kCtT / 16; ++k)
-                  mma_f16_ts(tO, tS + t * 64 + k * 8, tc::desc_k_none(v0 + (i & 1) * C::QT + k * (2 * D * 16), D * 16, 128),
+                  mma_f16_ts(tO, tS + t * 64 + k * 8, dv + ((i & 1) * C::QT + k * (2 * D * 16)) / 16,
                              idesc_f16(D), !(flags & kSFirst) || t + k > 0);
               if (!Two || (vdone ^= 1u << (i & 1), !(vdone >> (i & 1) & 1))) tc::mma_commit(&vempty[i & 1]);
               if (flags & kSLast) tc::mma_commit(&ofin[x]);
@@ -448,8 +492,8 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
               for (int t = 0; t < C::NT; ++t)
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                  tc::mma_bf16(tS, tc::desc_k_none(q0 + (Two ? x : t) * C::QT + k * 4096, 2048, 128),
-                               tc::desc_k_none(k0 + (i & 1) * C::QT + k * 4096, 2048, 128), idesc_f16(kCtT), t + k > 0);
+                  tc::mma_bf16(tS, dq + ((Two ? x : t) * C::QT + k * 4096) / 16, dk + ((i & 1) * C::QT + k * 4096) / 16,
+                               idesc_f16(kCtT), t + k > 0);
               tc::mma_commit(&sfull[x]);
               if (!Two || (kdone ^= 1u << (i & 1), !(kdone >> (i & 1) & 1))) tc::mma_commit(&kempty[i & 1]);
               nS[x] += stride;
@@ -486,61 +530,60 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       *lo = make_uint4(h[0], h[1], h[2], h[3]);
       *hi = make_uint4(h[4], h[5], h[6], h[7]);
     };
-    for (int i = 0; i < ntile; ++i) {
-      const int st = i % NST, b = i & 1;
+    constexpr int U = D / 16;   // 16-byte pieces of a thread
+    // (one code for K and V: the kernel's instructions should stay in the instruction cache)
+    const int src_k = (t >> 3) * (8 * D) + (t & 7) * 16, dst_v = t / D * (2 * D * 16) + t % D * 16;
+    for (int i = 0; i < 2 * ntile; ++i) {
+      const bool v = i & 1;
+      const int b = (i >> 1) & 1, st = i % NST;
       if (!warp_wait(&full[st], i / NST)) break;
-      const int flags = infos[i % kCtInfo].flags, cnt = flags & 255;
-      const unsigned char* kc = stages + st * C::Stage;
-      const unsigned char* vc = kc + C::KB;
-      if (!warp_wait(&kempty[b], (i >> 1) ^ 1)) break;
-      // (codes past the tokens are whatever was there: their logits are not used)
-#pragma unroll 4
-      for (int j = 0; j < D / 16; ++j) {
-        uint4 lo, hi;
-        to_half(*reinterpret_cast<const uint4*>(kc + (t >> 3) * (8 * D) + j * 128 + (t & 7) * 16), &lo, &hi);
-        uint4* dst = reinterpret_cast<uint4*>(kbuf + b * C::QT + j * 4096 + t * 16);
-        dst[0] = lo;
-        dst[2048 / 16] = hi;
-      }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&kfull[b]);
-      if (!warp_wait(&vempty[b], (i >> 1) ^ 1)) break;
-      bool nan = false;
-#pragma unroll 4
-      for (int u = 0; u < D / 16; ++u) {
-        const int x = u * 128 + t, g = x / D, j = x % D;   // 16 tokens, dimension
-        uint4 w = *reinterpret_cast<const uint4*>(vc + x * 16);
-        if (flags & kMixed || cnt < kCtT) {
-          // V past the tokens counts as zero.  NaN that not all rows see is taken out and noted: bit e
-          // of a half word: token e of the 16
-          uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+      if (!warp_wait(v ? &vempty[b] : &kempty[b], (i >> 2) ^ 1)) break;
+      const int flags = infos[(i >> 1) % kCtInfo].flags, cnt = flags & 255;
+      unsigned char* src = stages + st * C::KB + (v ? t * 16 : src_k);
+      // (keys past the tokens are whatever was there: their logits are not used)
+      if (v && (flags & kMixed || cnt < kCtT)) {
+        // V past the tokens counts as zero.  NaN that not all rows see is taken out and noted: bit e
+        // of a half word: token e of the 16
+        bool nan = false;
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+          const int x = u * 128 + t, g = x / D, j = x % D;   // 16 tokens, dimension
+          uint32_t* ww = reinterpret_cast<uint32_t*>(src + u * 2048);
           uint32_t bits = 0;
+#pragma unroll 1
+          for (int e = 0; e < 16; e += 4) {
+            uint32_t w = ww[e / 4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint32_t c = ww[e >> 2] >> (8 * (e & 3)) & 0x7f;
-            const bool held = g * 16 + e < cnt, bad = held && c == 0x7f && (flags & kMixed);
-            if (!held || bad) ww[e >> 2] &= ~(0xffu << (8 * (e & 3)));
-            bits |= (bad ? 1u : 0u) << e;
+            for (int k = 0; k < 4; ++k) {
+              const bool held = g * 16 + e + k < cnt, bad = held && (w >> (8 * k) & 0x7f) == 0x7f && (flags & kMixed);
+              if (!held || bad) w &= ~(0xffu << (8 * k));
+              bits |= (bad ? 1u : 0u) << (e + k);
+            }
+            ww[e / 4] = w;
           }
           if (flags & kMixed) reinterpret_cast<uint16_t*>(nan_masks)[(b * 128 + j) * 8 + g] = static_cast<uint16_t>(bits);
           nan |= bits != 0;
         }
-        uint4 lo, hi;
-        to_half(w, &lo, &hi);
-        uint4* dst = reinterpret_cast<uint4*>(vbuf + b * C::QT + g * (2 * D * 16) + j * 16);
-        dst[0] = lo;
-        dst[D] = hi;
+        if (flags & kMixed) {
+          const bool any = !tc::named_sync_and(1, 128, !nan);
+          if (t == 0) s_nan[b] = any;
+        }
       }
-      if (flags & kMixed) {
-        const bool any = !tc::named_sync_and(1, 128, !nan);
-        if (t == 0) s_nan[b] = any;
-        __syncwarp();
+      const int sstep = v ? 2048 : 128, dhalf = v ? D * 16 : 2048;
+      unsigned char* dst = (v ? vbuf + dst_v : kbuf + t * 16) + b * C::QT;
+      uint4 w[U], lo, hi;
+#pragma unroll
+      for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const uint4*>(src + u * sstep);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        to_half(w[u], &lo, &hi);
+        *reinterpret_cast<uint4*>(dst + u * 4096) = lo;
+        *reinterpret_cast<uint4*>(dst + u * 4096 + dhalf) = hi;
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tc::mbar_arrive(&vfull[b]);
+        tc::mbar_arrive(v ? &vfull[b] : &kfull[b]);
         tc::mbar_arrive(&sempty[st]);
       }
     }
@@ -561,56 +604,69 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       return warp_wait(jdone, turn - 1);
     };
 
-    // The row's query, in fp16 terms, and the factor of its logits.
+    // The warp's 32 queries, in fp16 terms, and the factors of their logits.  A lane loads 16-byte pieces
+    // of rows lane % 8 + 8 g: four lanes take 64 adjacent bytes, and eight rows' pieces are 128 adjacent bytes of
+    // the operand.
+    constexpr int V = Ty<T>::kVec, N = D / V;   // elements of a piece, pieces of a row
+    auto row_of = [&](int g) { return g * 8 + (lane & 7); };   // of the warp's
     auto lay_q = [&]() {
-      const T* src = static_cast<const T*>(a.q) + seq * a.qb + h * a.qh + j * a.qs;
-      constexpr int V = Ty<T>::kVec;   // elements of 16 bytes
-      float top = 0.f;
-      bool bad = false;
-      float v[8];
-      auto load8 = [&](int e) {
+      const long long mine = valid ? seq * a.qb + h * a.qh + j * a.qs : -1;
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+        const long long off = __shfl_sync(0xffffffffu, mine, row_of(g));
+        const T* src = static_cast<const T*>(a.q) + off + (lane >> 3) * V;
+        uint4 raw[N / 4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = 0.f;
-        if (!valid) return;
-        if (a.wide_q) {
-#pragma unroll
-          for (int u = 0; u < 8; u += V) Ty<T>::load16(src + e + u, v + u);
-        } else {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = Ty<T>::to_f(src[e + u]);
+        for (int u = 0; u < N / 4; ++u) {
+          raw[u] = make_uint4(0, 0, 0, 0);
+          if (off >= 0 && a.wide_q) raw[u] = *reinterpret_cast<const uint4*>(src + u * 4 * V);
         }
-      };
-#pragma unroll 4
-      for (int e = 0; e < D; e += 8) {
-        load8(e);
+        if (off >= 0 && !a.wide_q)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float z = fabsf(v[u]);
-          bad |= !(z < INFINITY);
-          top = fmaxf(top, z);
-        }
-      }
-      const int ex = bad ? 0 : max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
-      const float down = exp2i(14 - ex);   // the largest to [2^14, 2^15)
-      rowf = exp2i(ex - 14) * a.scale_log2;
-#pragma unroll 4
-      for (int e = 0; e < D; e += 8) {
-        load8(e);
-        uint32_t w[C::NT][4];
+          for (int u = 0; u < N / 4; ++u)
 #pragma unroll
-        for (int u = 0; u < 8; u += 2) {
-          float y0 = bad ? __int_as_float(0x7fffffff) : v[u] * down, y1 = bad ? y0 : v[u + 1] * down;
+            for (int e = 0; e < V; ++e) reinterpret_cast<T*>(&raw[u])[e] = src[u * 4 * V + e];
+        float top = 0.f;
+#pragma unroll
+        for (int u = 0; u < N / 4; ++u)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float z = fabsf(Ty<T>::to_f(reinterpret_cast<const T*>(&raw[u])[e]));
+            top = fmaxf(top, z < INFINITY ? z : INFINITY);   // (NaN, too)
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const bool bad = !(top < INFINITY);   // an entry that is not finite: the row is NaN
+        const int ex = bad ? 0 : max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+        const float down = exp2i(14 - ex);    // the largest to [2^14, 2^15)
+        const float f = __shfl_sync(0xffffffffu, exp2i(ex - 14) * a.scale_log2, lane & 7);
+        if (lane >> 3 == g) rowf = f;
+        unsigned char* dst = qbuf + (Two ? x : 0) * C::QT + (wq * 32 + row_of(g)) * 16;
+#pragma unroll
+        for (int u = 0; u < N / 4; ++u) {
+          // a piece of fp32 is half a piece of the operand
+          const int at = (u * 4 + (lane >> 3)) * V;   // its first element
+          uint32_t w[C::NT][V / 2];
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            float y0 = Ty<T>::to_f(reinterpret_cast<const T*>(&raw[u])[e]) * down;
+            float y1 = Ty<T>::to_f(reinterpret_cast<const T*>(&raw[u])[e + 1]) * down;
+            if (bad) y0 = y1 = __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n) {
+              const __half2 z = __floats2half2_rn(y0, y1);
+              w[n][e / 2] = *reinterpret_cast<const uint32_t*>(&z);
+              y0 -= __low2float(z);
+              y1 -= __high2float(z);
+            }
+          }
 #pragma unroll
           for (int n = 0; n < C::NT; ++n) {
-            const __half2 z = __floats2half2_rn(y0, y1);
-            w[n][u / 2] = *reinterpret_cast<const uint32_t*>(&z);
-            y0 -= __low2float(z);
-            y1 -= __high2float(z);
+            unsigned char* d = dst + n * C::QT + (at >> 3) * 2048 + (at & 7) * 2;
+            if constexpr (V == 8) *reinterpret_cast<uint4*>(d) = make_uint4(w[n][0], w[n][1], w[n][2], w[n][3]);
+            else *reinterpret_cast<uint2*>(d) = make_uint2(w[n][0], w[n][1]);
           }
         }
-#pragma unroll
-        for (int n = 0; n < C::NT; ++n)
-          *reinterpret_cast<uint4*>(qbuf + (Two ? x : n) * C::QT + e * 256 + row * 16) = make_uint4(w[n][0], w[n][1], w[n][2], w[n][3]);
       }
       if (!Two) sqs[row] = rowf;
       tc::fence_proxy_async_smem();
@@ -618,28 +674,31 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       if (lane == 0) tc::mbar_arrive(&qfull[Two ? x : 0]);
     };
 
-    // S of one tile to P over its columns.  General: tokens the row does not see, scales of any kind.
+    // S of one tile to P over its columns, 32 columns at a time (the loops are short on purpose: unrolled over
+    // the tile, instruction fetch bound them).  General: tokens the row does not see, scales of any kind.
+    constexpr int W = kCtT / Copies;            // columns of this warp
+    const int col0 = Copies > 1 ? wq * W : 0;
     auto softmax = [&](const TileInfo& in, bool first, auto general) {
       constexpr bool General = decltype(general)::value;
-      const int rem = lim - in.tile * kCtT;
-      float f[8], mt = -INFINITY;
-#pragma unroll
-      for (int g = 0; g < 8; ++g) f[g] = rowf * in.ks[g];
-#pragma unroll
-      for (int c = 0; c < kCtT; c += 32) {
+      const int rem = lim - in.tile * kCtT - col0;
+      const float2* ksp = reinterpret_cast<const float2*>(in.ks + col0 / 16);
+      const float2* vsp = reinterpret_cast<const float2*>(in.vs + col0 / 16);
+      float mt = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < W; c += 32) {
         float s[32];
-        tc::tmem_ld32(tS + c, s);
+        tc::tmem_ld32(tS + col0 + c, s);
+        const float2 k2 = ksp[c / 32];
+        const float f0 = rowf * k2.x, f1 = rowf * k2.y;
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float top = General ? -INFINITY : s[16 * g];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float z = s[16 * g + e];
-            if (General) top = fmaxf(top, c + 16 * g + e < rem ? z * f[c / 16 + g] : -INFINITY);
-            else top = fmaxf(top, z);
-          }
-          mt = fmaxf(mt, General ? top : top * f[c / 16 + g]);
+        for (int e = 0; e < 16; ++e) {
+          top[e & 1] = fmaxf(top[e & 1], !General ? s[e] : c + e < rem ? s[e] * f0 : -INFINITY);
+          top[2 + (e & 1)] = fmaxf(top[2 + (e & 1)], !General ? s[16 + e] : c + 16 + e < rem ? s[16 + e] * f1 : -INFINITY);
         }
+        top[0] = fmaxf(top[0], top[1]);
+        top[2] = fmaxf(top[2], top[3]);
+        mt = fmaxf(mt, General ? fmaxf(top[0], top[2]) : fmaxf(top[0] * f0, top[2] * f1));
       }
       const int v2 = first ? in.vexp : max(vexp, in.vexp);
       if (first) {
@@ -661,60 +720,96 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       }
       vexp = v2;
       const float ref = m == -INFINITY ? 0.f : m, up = exp2i(11 - vexp);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      [[maybe_unused]] uint32_t low[C::NT > 1 ? 64 : 1];
-#pragma unroll
-      for (int c = 0; c < kCtT; c += 32) {
+      float2 sum[2] = {};
+      // (fp32's second terms go where S is still to be read: they wait in registers)
+      [[maybe_unused]] uint32_t low[C::NT > 1 ? W / 2 : 1];
+#pragma unroll(C::NT > 1 ? 4 : 1)
+      for (int c = 0; c < W; c += 32) {
         float s[32];
-        tc::tmem_ld32(tS + c, s);
+        tc::tmem_ld32(tS + col0 + c, s);
+        const float2 k2 = ksp[c / 32], u2 = vsp[c / 32];
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float fg = f[(c + e) / 16], fv = in.vs[(c + e) / 16] * up;
-          float p0 = ex2(fmaf(s[e], fg, -ref)), p1 = ex2(fmaf(s[e + 1], fg, -ref));
+          const float fg = rowf * (e < 16 ? k2.x : k2.y), fv = (e < 16 ? u2.x : u2.y) * up;
+          const float2 y = __ffma2_rn(make_float2(s[e], s[e + 1]), make_float2(fg, fg), make_float2(-ref, -ref));
+          float2 p = make_float2(ex2(y.x), ex2(y.y));
           if (General) {
-            p0 = c + e < rem ? p0 : 0.f;
-            p1 = c + e + 1 < rem ? p1 : 0.f;
+            p.x = c + e < rem ? p.x : 0.f;
+            p.y = c + e + 1 < rem ? p.y : 0.f;
           }
-          sum[e / 2 & 3] += p0 + p1;
-          p0 = !General || c + e < rem ? p0 * fv : 0.f;
-          p1 = !General || c + e + 1 < rem ? p1 * fv : 0.f;
-          const __half2 z = __floats2half2_rn(p0, p1);
+          sum[e / 2 & 1] = __fadd2_rn(sum[e / 2 & 1], p);
+          p = __fmul2_rn(p, make_float2(fv, fv));
+          if (General) {   // (a scale that is no number under a hidden token)
+            p.x = c + e < rem ? p.x : 0.f;
+            p.y = c + e + 1 < rem ? p.y : 0.f;
+          }
+          const __half2 z = __floats2half2_rn(p.x, p.y);
           w[e / 2] = *reinterpret_cast<const uint32_t*>(&z);
           if constexpr (C::NT > 1) {
-            const __half2 y = __floats2half2_rn(p0 - __low2float(z), p1 - __high2float(z));
-            low[(c + e) / 2] = *reinterpret_cast<const uint32_t*>(&y);
+            const __half2 y2 = __floats2half2_rn(p.x - __low2float(z), p.y - __high2float(z));
+            low[(c + e) / 2] = *reinterpret_cast<const uint32_t*>(&y2);
           }
         }
-        // (columns c / 2 .. c / 2 + 16 of S have been read)
-        tmem_st16(tS + c / 2, w);
+        tmem_st16(tS + (col0 + c) / 2, w);   // (columns below c + 32 of S have been read)
       }
       if constexpr (C::NT > 1) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 16) tmem_st16(tS + 64 + c, low + c);
+        for (int c = 0; c < W; c += 32) tmem_st16(tS + 64 + (col0 + c) / 2, low + c / 2);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if constexpr (Copies > 1) {   // the other warps' columns
+        const uint32_t zero[16] = {};
+#pragma unroll
+        for (int c = 0; c < Copies; ++c)
+          if (c != wq) {
+            tmem_st16(tS + c * 16, zero);
+            if constexpr (C::NT > 1) tmem_st16(tS + 64 + c * 16, zero);
+          }
+      }
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       tmem_wait_st();
     };
 
-    // The finished row (o times 2^(vexp - 11) / l), or this CTA's part of it.
-    auto store = [&](const float* o, int c, float r, bool whole, size_t part) {   // 16 columns from c
-      if (!whole) {
-        float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c);
+    // The warp's finished rows (fin), or this CTA's part of them, 16 columns at a time from o(c, v): 64 bytes of eight
+    // rows to a store, by way of the warp's own queries' place, which is free by now (no other warp's next
+    // queries go there).
+    auto store_rows = [&](bool fin, size_t part, auto&& o) {
+      unsigned char* buf = qbuf + (Two ? x : 0) * C::QT + wq * 512;   // pieces of 32 rows, 2048 bytes apart
+      const long long mine = !valid ? -1 : fin ? seq * a.ob + h * a.oh + j * a.os : static_cast<long long>(part * D);
+      const int E = fin ? static_cast<int>(sizeof(T)) : 4;
+      unsigned char* base = fin ? static_cast<unsigned char*>(a.out) : reinterpret_cast<unsigned char*>(a.part_o);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float v[16];
+        o(c, v);
+        __syncwarp();
+        if (fin && sizeof(T) == 2) {
+          T y[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e] * r, o[4 * e + 1] * r, o[4 * e + 2] * r, o[4 * e + 3] * r);
-        return;
-      }
-      T* dst = static_cast<T*>(a.out) + seq * a.ob + h * a.oh + j * a.os + c;
-      T v[16];
+          for (int e = 0; e < 16; ++e) y[e] = Ty<T>::from_f(v[e]);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = Ty<T>::from_f(lim > 0 ? o[e] * r : 0.f);
-      if (a.wide_o) {
+          for (int e = 0; e < 2; ++e) *reinterpret_cast<uint4*>(buf + e * 2048 + lane * 16) = reinterpret_cast<const uint4*>(y)[e];
+        } else {
 #pragma unroll
-        for (int e = 0; e < static_cast<int>(sizeof(v) / 16); ++e) reinterpret_cast<uint4*>(dst)[e] = reinterpret_cast<const uint4*>(v)[e];
-      } else {
+          for (int e = 0; e < 4; ++e) *reinterpret_cast<float4*>(buf + e * 2048 + lane * 16) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+        __syncwarp();
+        // 16 columns are 32 or 64 bytes: two or four lanes to a row
+        const int per = E, rows = 32 / per;   // lanes to a row (E == 2: 2, 4: 4), rows at a time
+#pragma unroll 1
+        for (int g = 0; g < 32; g += rows) {
+          const int r = g + lane % rows, piece = lane / rows;
+          const long long off = __shfl_sync(0xffffffffu, mine, r);
+          const uint4 z = *reinterpret_cast<const uint4*>(buf + piece * 2048 + r * 16);
+          if (off < 0) continue;
+          unsigned char* dst = base + (off + c) * E + piece * 16;
+          if (!fin || a.wide_o) {
+            *reinterpret_cast<uint4*>(dst) = z;
+          } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) dst[e] = v[e];
+            for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) reinterpret_cast<T*>(dst)[e] = reinterpret_cast<const T*>(&z)[e];
+          }
+        }
       }
     };
 
@@ -722,8 +817,9 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       if (!warp_wait(&ifull[i % kCtInfo], i / kCtInfo)) break;
       const TileInfo& in = infos[i % kCtInfo];
       const int flags = in.flags, turn = in.turn;
+      [[maybe_unused]] const int in_q = in.q, in_n = in.n, in_len = in.len, in_kvh = in.pair % a.c.h_kv;
       if (flags & kTFirst) {
-        const int r = in.q * Rows + (Two ? x * kCtT : 0) + row, kvh = in.pair % a.c.h_kv;
+        const int r = in.q * Rows + (Two ? x * kCtT : 0) + row % (kCtT / Copies), kvh = in.pair % a.c.h_kv;
         seq = in.pair / a.c.h_kv;
         valid = r < in.len * a.G;
         j = valid ? r / a.G : 0;
@@ -749,7 +845,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         if (!Two && x == 1 && !wait_joined(turn)) break;   // O is free
         if (active) {
           const int rem = lim - in.tile * kCtT;
-          if (__any_sync(0xffffffffu, rem < kCtT && valid) || (flags & kOdd))
+          if (__any_sync(0xffffffffu, rem < col0 + W && valid) || (flags & kOdd))
             softmax(in, !used, std::true_type{});
           else
             softmax(in, !used, std::false_type{});
@@ -815,12 +911,10 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         const float sum = (used ? l * r0 : 0.f) + (vexp1 != INT_MIN ? l1 * r1 : 0.f);
         r0 *= exp2i(used ? vexp - 11 : 0);
         r1 *= exp2i(vexp1 != INT_MIN ? vexp1 - 11 : 0);
-        const bool whole = flags & kWhole;
+        const bool whole = Copies == 1 && (flags & kWhole);   // (copies are joined below)
         const float inv = whole ? 1.f / sum : 1.f;
-        const size_t part = static_cast<size_t>(2 * cta + (turn > 0)) * Rows + (Two ? x * kCtT : 0) + row;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16], z[16];
+        const size_t part = static_cast<size_t>(2 * cta + (turn > 0)) * C::PartRows + (Two ? x * kCtT : 0) + row;
+        store_rows(whole, part, [&](int c, float* o) {
           if (used) {
             tc::tmem_ld16(tO + c, o);
 #pragma unroll
@@ -830,6 +924,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
             for (int e = 0; e < 16; ++e) o[e] = 0.f;
           }
           if (!Two && vexp1 != INT_MIN) {
+            float z[16];
             tc::tmem_ld16(tO0 + D + c, z);
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = fmaf(z[e], r1, o[e]);
@@ -842,11 +937,25 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
             for (int e = 0; e < 16; ++e)
               if (bits >> ((c & 31) + e) & 1) o[e] = __int_as_float(0x7fffffff);
           }
-          if (valid) store(o, c, inv, whole, part);
-        }
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = lim > 0 ? o[e] * inv : 0.f;
+          }
+        });
         if (valid && !whole) a.part_ml[part] = make_float2(mm, sum);
         if (valid && whole && a.lse)
           a.lse[(static_cast<size_t>(seq) * a.h_q + h) * a.s + j] = lim > 0 ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      }
+      if (Copies > 1 && (flags & kWhole)) {
+        // (the next parts are written after jdone)
+        if (!tc::named_sync_and(2, 128, true)) break;
+        const size_t part = static_cast<size_t>(2 * cta + (turn > 0)) * C::PartRows;
+        const int q = in_q, n = in_n, len = in_len;
+        for (int u = wq; u < Rows && q * Rows + u < len * a.G; u += 4) {
+          const int r = q * Rows + u, jr = r / a.G;
+          join_row<T, D, Copies>(a, seq, in_kvh * a.G + r - jr * a.G, jr, tokens_seen(a, n, len, jr) > 0, 1, Rows,
+                                 [&](int) { return part + u; });
+        }
       }
       tc::fence_before();
       if (!Two) {
@@ -868,11 +977,12 @@ constexpr int kCgThreads = 256, kCgRows = 8;
 
 // Row (x) = boundary between two CTAs' runs: the first one inside a row tile joins its
 // parts, in order; kCgRows rows to a CTA, a warp to a row.
-template <typename T, int D, int Rows>
+template <typename T, int D, bool Two, int Copies>
 __global__ void __launch_bounds__(kCgThreads) k_tokens_merge(const __grid_constant__ TokensArgs a, int ncta) {
-  constexpr int E = D / 32;
+  using C = Ct<T, D, Two, Copies>;
+  constexpr int Rows = C::Rows;
   tc::grid_dep_wait();
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  const int c = blockIdx.x + 1;
   const int4 rec = a.rec[c];
   if (rec.x < 0) return;
   const int total = rec.w, n = min(ncta, total), first = rec.z;
@@ -883,34 +993,13 @@ __global__ void __launch_bounds__(kCgThreads) k_tokens_merge(const __grid_consta
   const int slot0 = 2 * (c - 1) + (run_begin(c - 1, n, total) < first);   // CTA c - 1's last part; the others' first
   for (int u = threadIdx.x >> 5; u < kCgRows; u += kCgThreads / 32) {
     const int row = blockIdx.y * kCgRows + u, r = rec.y * Rows + row;
-    if (r >= len * a.G) return;
-    const int j = r / a.G, h = kvh * a.G + r - j * a.G;
-    auto at = [&](int v) { return static_cast<size_t>(v == c - 1 ? slot0 : 2 * v) * Rows + row; };
-    float M = -INFINITY;
-    for (int v = c - 1 + lane; v <= c1; v += 32) M = fmaxf(M, a.part_ml[at(v)].x);
-    M = warp_max(M);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f, o[E] = {};
-    for (int v = c - 1; v <= c1; ++v) {
-      const float2 ml = a.part_ml[at(v)];
-      const float w = ex2(ml.x - ref);
-      L = fmaf(ml.y, w, L);
-      const float* src = a.part_o + at(v) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], w, o[e]);
-    }
-    const bool sees = tokens_seen(a, tok, len, j) > 0;
-    T* dst = static_cast<T*>(a.out) + seq * a.ob + h * a.oh + j * a.os + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) dst[e] = Ty<T>::from_f(sees ? o[e] / L : 0.f);
-    if (a.lse && lane == 0)
-      a.lse[(static_cast<size_t>(seq) * a.h_q + h) * a.s + j] = sees ? (ref + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    if (row >= Rows || r >= len * a.G) return;
+    const int j = r / a.G;
+    join_row<T, D, Copies>(a, seq, kvh * a.G + r - j * a.G, j, tokens_seen(a, tok, len, j) > 0, c1 - c + 2, Rows, [&](int v) {
+      return static_cast<size_t>(v == 0 ? slot0 : 2 * (c - 1 + v)) * C::PartRows + row;
+    });
   }
 }
-
-// Two row tiles at a time where a sequence's rows fill more than one (bf16; an fp32 row's terms take the
-// room of the second).
-static bool tokens_two(int dtype, int rows) { return dtype == SKV_DTYPE_BF16 && rows > kCtT; }
 
 static int tokens_ctas(const shadowkv_cache& c, int rows, int per, int nsm) {
   const long long tiles = (static_cast<long long>(c.max_blocks) * c.block + kCtT - 1) / kCtT;
@@ -938,22 +1027,28 @@ static size_t tokens_layout(const shadowkv_cache& c, int nsm, char* base, Tokens
   return off;
 }
 
-template <typename T, int D, bool Two>
+template <typename T, int D, bool Two, int Copies>
 static cudaError_t attend_tokens_t(const TokensArgs& a, const shadowkv_cache& c, int nsm, cudaStream_t st) {
-  using C = Ct<T, D, Two>;
+  using C = Ct<T, D, Two, Copies>;
   const int ncta = tokens_ctas(c, a.s * a.G, C::Rows, nsm);
-  const auto kern = k_attend_tokens<T, D, Two>;
+  const auto kern = k_attend_tokens<T, D, Two, Copies>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), C::Smem);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ncta), dim3(kCtThreads), C::Smem, st, a);
   if (e != cudaSuccess || ncta == 1) return e;
   const int rows = a.s * a.G < C::Rows ? a.s * a.G : C::Rows;
-  return launch_pdl(k_tokens_merge<T, D, C::Rows>, dim3(ncta - 1, (rows + kCgRows - 1) / kCgRows), dim3(kCgThreads), 0, st, a, ncta);
+  return launch_pdl(k_tokens_merge<T, D, Two, Copies>, dim3(ncta - 1, (rows + kCgRows - 1) / kCgRows), dim3(kCgThreads), 0, st, a, ncta);
 }
 
+// Rows of a sequence and KV head: up to 32 stand four times in one tile; bf16's take two tiles at a time from
+// 129 on (an fp32 row's terms take the room of the second).
 template <int D>
 static cudaError_t attend_tokens_d(const TokensArgs& a, const shadowkv_cache& c, int dtype, int nsm, cudaStream_t st) {
-  if (dtype != SKV_DTYPE_BF16) return attend_tokens_t<float, D, false>(a, c, nsm, st);
-  return tokens_two(dtype, a.s * a.G) ? attend_tokens_t<bf16, D, true>(a, c, nsm, st) : attend_tokens_t<bf16, D, false>(a, c, nsm, st);
+  const int rows = a.s * a.G;
+  if (dtype != SKV_DTYPE_BF16)
+    return rows <= 32 ? attend_tokens_t<float, D, false, 4>(a, c, nsm, st) : attend_tokens_t<float, D, false, 1>(a, c, nsm, st);
+  return rows <= 32    ? attend_tokens_t<bf16, D, false, 4>(a, c, nsm, st)
+         : rows <= kCtT ? attend_tokens_t<bf16, D, false, 1>(a, c, nsm, st)
+                        : attend_tokens_t<bf16, D, true, 1>(a, c, nsm, st);
 }
 
 static const char* tokens_fault(const shadowkv_cache& c, int h_q, int s, skv_status* st) {
