@@ -31,7 +31,7 @@
 namespace skv {
 
 constexpr int kCtT = 128;       // tokens of a tile, rows of an MMA
-constexpr int kCtThreads = 448; // warps 0-3 and 4-7: softmax of stream 0 and 1; 8-11: conversion; 12: copies; 13: tcgen05.mma
+constexpr int kCtThreads = 576; // warps 0-3 and 4-7: softmax of stream 0 and 1; 8-11 and 12-15: conversion of K and of V; 16: copies; 17: tcgen05.mma
 constexpr int kCtInfo = 8;      // tiles described ahead
 
 struct TokensArgs {
@@ -72,7 +72,7 @@ struct Ct {
   static constexpr int QT = kCtT * D * 2;                   // an operand tile in fp16
   static constexpr int QB = (Two ? 2 : NT) * QT;
   static constexpr int KB = kCtT * D;                       // codes of K or of V: a stage
-  static constexpr int Misc = 2816;
+  static constexpr int Misc = 2912;
   static constexpr int Most = 227 * 1024 - 128 - Misc;
   static constexpr int NST0 = (Most - QB - 4 * QT) / KB, NST = NST0 > 8 ? 8 : NST0;
   static constexpr int Smem = 128 + QB + 4 * QT + NST * KB + Misc;
@@ -218,8 +218,6 @@ __device__ __forceinline__ void run_find(const TokensArgs& a, int cta, int ncta,
 
 // of a tile, beside its tokens (at most 128)
 enum : int {
-  kTFirst = 256,    // first of its row tile in this CTA
-  kTLast = 512,     // last
   kSFirst = 1024,   // first that its stream has of the row tile
   kSLast = 2048,
   kMixed = 4096,    // some rows do not see some of its tokens
@@ -229,6 +227,7 @@ enum : int {
 struct TileInfo {
   int pair, q, tile, flags, n, len, turn, vexp;   // turn: number of the row tile in this CTA; V scales are below 2^vexp
   float ks[8], vs[8];                             // of every 16 tokens
+  int end, pad[3];                                // number of the row tile's last tile in this CTA
 };
 
 // One row of a row tile from its parts (numbers u of n; a part's Copies sub-rows lie `step` apart): a warp's work.
@@ -293,10 +292,10 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
   volatile int* s_nan = reinterpret_cast<volatile int*>(misc + 360);   // [2]: V's tile has NaN
   int* s_scan = reinterpret_cast<int*>(misc + 448);      // [32], before the tiles are described
   TileInfo* infos = reinterpret_cast<TileInfo*>(misc + 448);
-  float* sqs = reinterpret_cast<float*>(misc + 1216);    // [128] rows' factors (one row tile)
-  float2* s_ml = reinterpret_cast<float2*>(misc + 1728); // [128] stream 1's maxima and sums
-  int2* s_join = reinterpret_cast<int2*>(misc + 2752);   // [4 warps] its vexp, and whether NaN is recorded
-  static_assert(sizeof(TileInfo) == 96, "misc");
+  float* sqs = reinterpret_cast<float*>(misc + 1344);    // [128] rows' factors (one row tile)
+  float2* s_ml = reinterpret_cast<float2*>(misc + 1856); // [128] stream 1's maxima and sums
+  int2* s_join = reinterpret_cast<int2*>(misc + 2880);   // [4 warps] its vexp, and whether NaN is recorded
+  static_assert(sizeof(TileInfo) == 112, "misc");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   if (gridDim.x > 1) tc::grid_dep_launch();   // (a call's last kernel lets nothing start early)
 
@@ -321,7 +320,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     tc::fence_mbar_init();
     *s_abort = 0;
   }
-  if (warp == 13) {
+  if (warp == 17) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
   }
@@ -352,7 +351,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     return ok;
   };
 
-  if (ntile > 0 && warp == 12) {
+  if (ntile > 0 && warp == 16) {
     // ------------------------------------------------------------ copies
     // Block ids are loaded two tiles ahead, scales one.
     Walk cur;
@@ -403,11 +402,12 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         in->pair = cur.pair;
         in->q = cur.q;
         in->tile = cur.tile;
-        in->flags = cnt | (k == 0 ? kTFirst : 0) | (it == seg_end - 1 ? kTLast : 0) | (k < stride ? kSFirst : 0) |
+        in->flags = cnt | (k < stride ? kSFirst : 0) |
                     (it >= seg_end - stride ? kSLast : 0) | (cur.tile * kCtT + cnt > cur.seen0 ? kMixed : 0) | (odd ? kOdd : 0) | whole;
         in->n = cur.n;
         in->len = cur.len;
         in->turn = turn;
+        in->end = seg_end - 1;
         in->vexp = max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -110);
       }
       __syncwarp();
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     if (lane == 0 && *s_abort)
       for (int u = max(0, copied - NST); u < copied; ++u) tc::mbar_wait(&full[u % NST], (u / NST) & 1, kWaitLimit);
     __syncwarp();
-  } else if (ntile > 0 && warp == 13) {
+  } else if (ntile > 0 && warp == 17) {
     // ------------------------------------------------------------ tensor core
     if (lane == 0) {
       // Per stream: S(i), then (once P(i) is there, over S's columns) O += P(i) V(i), then the next S.  While one stream's softmax
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
               for (int t = 0; t < C::NT; ++t)
 #pragma unroll
                 for (int k = 0; k < kCtT / 16; ++k)
-                  mma_f16_ts(tO, tS + t * 64 + k * 8, dv + ((i & 1) * C::QT + k * (2 * D * 16)) / 16,
+                  mma_f16_ts(tO, tS + k / 2 * 32 + k % 2 * 8 + t * 16, dv + ((i & 1) * C::QT + k * (2 * D * 16)) / 16,
                              idesc_f16(D), !(flags & kSFirst) || t + k > 0);
               if (!Two || (vdone ^= 1u << (i & 1), !(vdone >> (i & 1) & 1))) tc::mma_commit(&vempty[i & 1]);
               if (flags & kSLast) tc::mma_commit(&ofin[x]);
@@ -514,9 +514,10 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       }
     }
     __syncwarp();
-  } else if (ntile > 0 && warp >= 8 && warp < 12) {
+  } else if (ntile > 0 && warp >= 8 && warp < 16) {
     // ------------------------------------------------------------ conversion
-    const int t = tid - 256;
+    const int t = tid & 127;
+    const bool v = warp >= 12;
     auto to_half = [](const uint4& w, uint4* lo, uint4* hi) {
       const uint32_t c[4] = {w.x, w.y, w.z, w.w};
       uint32_t h[8];
@@ -532,48 +533,56 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     };
     constexpr int U = D / 16;   // 16-byte pieces of a thread
     // (one code for K and V: the kernel's instructions should stay in the instruction cache)
-    const int src_k = (t >> 3) * (8 * D) + (t & 7) * 16, dst_v = t / D * (2 * D * 16) + t % D * 16;
-    for (int i = 0; i < 2 * ntile; ++i) {
-      const bool v = i & 1;
-      const int b = (i >> 1) & 1, st = i % NST;
-      if (!warp_wait(&full[st], i / NST)) break;
-      if (!warp_wait(v ? &vempty[b] : &kempty[b], (i >> 2) ^ 1)) break;
-      const int flags = infos[(i >> 1) % kCtInfo].flags, cnt = flags & 255;
-      unsigned char* src = stages + st * C::KB + (v ? t * 16 : src_k);
-      // (keys past the tokens are whatever was there: their logits are not used)
-      if (v && (flags & kMixed || cnt < kCtT)) {
-        // V past the tokens counts as zero.  NaN that not all rows see is taken out and noted: bit e
-        // of a half word: token e of the 16
-        bool nan = false;
-#pragma unroll 1
-        for (int u = 0; u < U; ++u) {
-          const int x = u * 128 + t, g = x / D, j = x % D;   // 16 tokens, dimension
-          uint32_t* ww = reinterpret_cast<uint32_t*>(src + u * 2048);
-          uint32_t bits = 0;
-#pragma unroll 1
-          for (int e = 0; e < 16; e += 4) {
-            uint32_t w = ww[e / 4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const bool held = g * 16 + e + k < cnt, bad = held && (w >> (8 * k) & 0x7f) == 0x7f && (flags & kMixed);
-              if (!held || bad) w &= ~(0xffu << (8 * k));
-              bits |= (bad ? 1u : 0u) << (e + k);
-            }
-            ww[e / 4] = w;
-          }
-          if (flags & kMixed) reinterpret_cast<uint16_t*>(nan_masks)[(b * 128 + j) * 8 + g] = static_cast<uint16_t>(bits);
-          nan |= bits != 0;
-        }
-        if (flags & kMixed) {
-          const bool any = !tc::named_sync_and(1, 128, !nan);
-          if (t == 0) s_nan[b] = any;
-        }
-      }
-      const int sstep = v ? 2048 : 128, dhalf = v ? D * 16 : 2048;
-      unsigned char* dst = (v ? vbuf + dst_v : kbuf + t * 16) + b * C::QT;
+    const int sstep = v ? 2048 : 128, dhalf = v ? D * 16 : 2048;
+    const int src = v ? t * 16 : (t >> 3) * (8 * D) + (t & 7) * 16;
+    unsigned char* dst0 = v ? vbuf + t / D * (2 * D * 16) + t % D * 16 : kbuf + t * 16;
+    uint64_t* done = v ? vfull : kfull;
+    uint64_t* room = v ? vempty : kempty;
+    for (int i = 0; i < ntile; ++i) {
+      const int b = i & 1, n = 2 * i + v, st = n % NST;
+      if (!warp_wait(&full[st], n / NST)) break;
       uint4 w[U], lo, hi;
 #pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const uint4*>(src + u * sstep);
+      for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const uint4*>(stages + st * C::KB + src + u * sstep);
+      if (!warp_wait(&room[b], (i >> 1) ^ 1)) break;
+      const int flags = infos[i % kCtInfo].flags, cnt = flags & 255;
+      // (keys past the tokens are whatever was there: their logits are not used)
+      if (v && (flags & kMixed || cnt < kCtT)) {
+        // V past the tokens counts as zero.  NaN that not all rows see is taken out and noted
+        uint32_t nan = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int keep = cnt - (u * 128 + t) / D * 16;   // of the piece's 16 tokens
+          uint32_t* ww = reinterpret_cast<uint32_t*>(&w[u]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = keep - 4 * e;
+            ww[e] = k >= 4 ? ww[e] : k <= 0 ? 0u : ww[e] & ((1u << (8 * k)) - 1u);
+            nan |= (ww[e] & 0x7f7f7f7fu) + 0x01010101u;    // a NaN's byte carries into its sign
+          }
+        }
+        if (flags & kMixed) {
+          const bool any = !tc::named_sync_and(1, 128, !(nan & 0x80808080u));
+          if (t == 0) s_nan[b] = any;
+          if (any) {
+            // bit e of a half word: token e of the piece
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              uint32_t* ww = reinterpret_cast<uint32_t*>(&w[u]);
+              uint32_t bits = 0;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if ((ww[e / 4] >> (8 * (e & 3)) & 0x7f) == 0x7f) {
+                  ww[e / 4] &= ~(0xffu << (8 * (e & 3)));
+                  bits |= 1u << e;
+                }
+              const int x = u * 128 + t;
+              reinterpret_cast<uint16_t*>(nan_masks)[(b * 128 + x % D) * 8 + x / D] = static_cast<uint16_t>(bits);
+            }
+          }
+        }
+      }
+      unsigned char* dst = dst0 + b * C::QT;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         to_half(w[u], &lo, &hi);
@@ -583,7 +592,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tc::mbar_arrive(v ? &vfull[b] : &kfull[b]);
+        tc::mbar_arrive(&done[b]);
         tc::mbar_arrive(&sempty[st]);
       }
     }
@@ -611,21 +620,27 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     auto row_of = [&](int g) { return g * 8 + (lane & 7); };   // of the warp's
     auto lay_q = [&]() {
       const long long mine = valid ? seq * a.qb + h * a.qh + j * a.qs : -1;
-#pragma unroll 1
+      constexpr int R = V == 8 ? 2 : 1;   // groups of rows whose pieces wait in registers
+      uint4 all[R][N / 4];
+#pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const long long off = __shfl_sync(0xffffffffu, mine, row_of(g));
-        const T* src = static_cast<const T*>(a.q) + off + (lane >> 3) * V;
-        uint4 raw[N / 4];
+        if (g % R == 0)
 #pragma unroll
-        for (int u = 0; u < N / 4; ++u) {
-          raw[u] = make_uint4(0, 0, 0, 0);
-          if (off >= 0 && a.wide_q) raw[u] = *reinterpret_cast<const uint4*>(src + u * 4 * V);
-        }
-        if (off >= 0 && !a.wide_q)
+          for (int k = 0; k < R; ++k) {
+            const long long off = __shfl_sync(0xffffffffu, mine, row_of(g + k));
+            const T* src = static_cast<const T*>(a.q) + off + (lane >> 3) * V;
 #pragma unroll
-          for (int u = 0; u < N / 4; ++u)
+            for (int u = 0; u < N / 4; ++u) {
+              all[k][u] = make_uint4(0, 0, 0, 0);
+              if (off >= 0 && a.wide_q) all[k][u] = *reinterpret_cast<const uint4*>(src + u * 4 * V);
+            }
+            if (off >= 0 && !a.wide_q)
 #pragma unroll
-            for (int e = 0; e < V; ++e) reinterpret_cast<T*>(&raw[u])[e] = src[u * 4 * V + e];
+              for (int u = 0; u < N / 4; ++u)
+#pragma unroll
+                for (int e = 0; e < V; ++e) reinterpret_cast<T*>(&all[k][u])[e] = src[u * 4 * V + e];
+          }
+        const uint4* raw = all[g % R];
         float top = 0.f;
 #pragma unroll
         for (int u = 0; u < N / 4; ++u)
@@ -721,14 +736,12 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       vexp = v2;
       const float ref = m == -INFINITY ? 0.f : m, up = exp2i(11 - vexp);
       float2 sum[2] = {};
-      // (fp32's second terms go where S is still to be read: they wait in registers)
-      [[maybe_unused]] uint32_t low[C::NT > 1 ? W / 2 : 1];
-#pragma unroll(C::NT > 1 ? 4 : 1)
+#pragma unroll 1
       for (int c = 0; c < W; c += 32) {
         float s[32];
         tc::tmem_ld32(tS + col0 + c, s);
         const float2 k2 = ksp[c / 32], u2 = vsp[c / 32];
-        uint32_t w[16];
+        uint32_t w[C::NT][16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const float fg = rowf * (e < 16 ? k2.x : k2.y), fv = (e < 16 ? u2.x : u2.y) * up;
@@ -744,27 +757,25 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
             p.x = c + e < rem ? p.x : 0.f;
             p.y = c + e + 1 < rem ? p.y : 0.f;
           }
-          const __half2 z = __floats2half2_rn(p.x, p.y);
-          w[e / 2] = *reinterpret_cast<const uint32_t*>(&z);
-          if constexpr (C::NT > 1) {
-            const __half2 y2 = __floats2half2_rn(p.x - __low2float(z), p.y - __high2float(z));
-            low[(c + e) / 2] = *reinterpret_cast<const uint32_t*>(&y2);
+#pragma unroll
+          for (int n = 0; n < C::NT; ++n) {
+            const __half2 z = __floats2half2_rn(p.x, p.y);
+            w[n][e / 2] = *reinterpret_cast<const uint32_t*>(&z);
+            p.x -= __low2float(z);
+            p.y -= __high2float(z);
           }
         }
-        tmem_st16(tS + (col0 + c) / 2, w);   // (columns below c + 32 of S have been read)
-      }
-      if constexpr (C::NT > 1) {
+        // P of 32 tokens over their own columns of S: 16 columns a term
 #pragma unroll
-        for (int c = 0; c < W; c += 32) tmem_st16(tS + 64 + (col0 + c) / 2, low + c / 2);
+        for (int n = 0; n < C::NT; ++n) tmem_st16(tS + col0 + c + 16 * n, w[n]);
       }
       if constexpr (Copies > 1) {   // the other warps' columns
         const uint32_t zero[16] = {};
 #pragma unroll
-        for (int c = 0; c < Copies; ++c)
-          if (c != wq) {
-            tmem_st16(tS + c * 16, zero);
-            if constexpr (C::NT > 1) tmem_st16(tS + 64 + c * 16, zero);
-          }
+        for (int c = 0; c < kCtT; c += W)
+#pragma unroll
+          for (int n = 0; n < C::NT; ++n)
+            if (c != col0) tmem_st16(tS + c + 16 * n, zero);
       }
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       tmem_wait_st();
@@ -813,51 +824,58 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       }
     };
 
-    for (int i = 0; i < ntile; ++i) {
+    for (int i = 0, end; i < ntile; i = end + 1) {
       if (!warp_wait(&ifull[i % kCtInfo], i / kCtInfo)) break;
-      const TileInfo& in = infos[i % kCtInfo];
-      const int flags = in.flags, turn = in.turn;
-      [[maybe_unused]] const int in_q = in.q, in_n = in.n, in_len = in.len, in_kvh = in.pair % a.c.h_kv;
-      if (flags & kTFirst) {
-        const int r = in.q * Rows + (Two ? x * kCtT : 0) + row % (kCtT / Copies), kvh = in.pair % a.c.h_kv;
-        seq = in.pair / a.c.h_kv;
-        valid = r < in.len * a.G;
+      const TileInfo& head = infos[i % kCtInfo];
+      const int flags = head.flags, turn = head.turn, head_n = head.n, head_len = head.len, head_q = head.q;
+      const int kvh = head.pair % a.c.h_kv;
+      end = head.end;
+      {
+        const int r = head_q * Rows + (Two ? x * kCtT : 0) + row % (kCtT / Copies);
+        seq = head.pair / a.c.h_kv;
+        valid = r < head_len * a.G;
         j = valid ? r / a.G : 0;
         h = kvh * a.G + (valid ? r - j * a.G : 0);
-        lim = valid ? tokens_seen(a, in.n, in.len, j) : 0;
+        lim = valid ? tokens_seen(a, head_n, head_len, j) : 0;
         active = __any_sync(0xffffffffu, valid);
         m = -INFINITY;
         l = 0.f;
         used = false;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) nanrow[e] = 0;
-        if (Two || x == 0) {
-          lay_q();
-        } else {
-          if (!warp_wait(&qfull[0], turn)) break;
-          rowf = sqs[row];
-        }
       }
-      if (Two || (i & 1) == x) {
-        if (!warp_wait(&sfull[x], use)) break;
+      if (Two || x == 0) {
+        lay_q();
+      } else {
+        if (!warp_wait(&qfull[0], turn)) break;
+        rowf = sqs[row];
+      }
+      // this stream's tiles
+      int t = Two ? i : i + ((i ^ x) & 1);
+      bool ok = true;
+      for (; t <= end; t += Two ? 1 : 2) {
+        ok = warp_wait(&ifull[t % kCtInfo], t / kCtInfo) && warp_wait(&sfull[x], use);
+        if (!ok) break;
+        const TileInfo& in = infos[t % kCtInfo];
         ++use;
         tc::fence_after();
-        if (!Two && x == 1 && !wait_joined(turn)) break;   // O is free
+        if (!Two && x == 1 && !(ok = wait_joined(turn))) break;   // O is free
         if (active) {
-          const int rem = lim - in.tile * kCtT;
-          if (__any_sync(0xffffffffu, rem < col0 + W && valid) || (flags & kOdd))
+          const int rem = lim - in.tile * kCtT, tf = in.flags;
+          if (__any_sync(0xffffffffu, rem < col0 + W && valid) || (tf & kOdd))
             softmax(in, !used, std::true_type{});
           else
             softmax(in, !used, std::false_type{});
-          if (flags & kMixed) {
-            if (!warp_wait(&vfull[i & 1], i >> 1)) break;
-            if (s_nan[i & 1])
+          if (tf & kMixed) {
+            if (!(ok = warp_wait(&vfull[t & 1], t >> 1))) break;
+            if (s_nan[t & 1])
+#pragma unroll 1
               for (int d = 0; d < D; ++d)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const int k = rem - 32 * e;   // tokens of this word that the row sees
                   const uint32_t see = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
-                  const uint32_t hit = nan_masks[((i & 1) * 128 + d) * 4 + e] & see ? 1u << (d & 31) : 0u;
+                  const uint32_t hit = nan_masks[((t & 1) * 128 + d) * 4 + e] & see ? 1u << (d & 31) : 0u;
 #pragma unroll
                   for (int u = 0; u < D / 32; ++u) nanrow[u] |= d / 32 == u ? hit : 0u;
                 }
@@ -868,7 +886,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&pfull[x]);
       }
-      if (!(flags & kTLast)) continue;
+      if (!ok) break;
       // ---- the row tile's end
       bool nan_any = false;
 #pragma unroll
@@ -950,10 +968,9 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         // (the next parts are written after jdone)
         if (!tc::named_sync_and(2, 128, true)) break;
         const size_t part = static_cast<size_t>(2 * cta + (turn > 0)) * C::PartRows;
-        const int q = in_q, n = in_n, len = in_len;
-        for (int u = wq; u < Rows && q * Rows + u < len * a.G; u += 4) {
-          const int r = q * Rows + u, jr = r / a.G;
-          join_row<T, D, Copies>(a, seq, in_kvh * a.G + r - jr * a.G, jr, tokens_seen(a, n, len, jr) > 0, 1, Rows,
+        for (int u = wq; u < Rows && head_q * Rows + u < head_len * a.G; u += 4) {
+          const int r = head_q * Rows + u, jr = r / a.G;
+          join_row<T, D, Copies>(a, seq, kvh * a.G + r - jr * a.G, jr, tokens_seen(a, head_n, head_len, jr) > 0, 1, Rows,
                                  [&](int) { return part + u; });
         }
       }
@@ -966,7 +983,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == 17) {
     tc::fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
