@@ -92,6 +92,17 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 // kind::f16, fp16 A and B (format 0), fp32 D, both K-major, M = 128
 constexpr uint32_t idesc_f16(int N) { return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24); }
 
+// One lane of the warp (the compiler knows that one thread runs what depends on it, and keeps
+// descriptors in uniform registers: the eight products of a tile are issued in half the time of `lane == 0`)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     __syncwarp();
   } else if (ntile > 0 && warp == 17) {
     // ------------------------------------------------------------ tensor core
-    if (lane == 0) {
+    if (elect_one()) {
       // Per stream: S(i), then (once P(i) is there, over S's columns) O += P(i) V(i), then the next S.  While one stream's softmax
       // runs the other's products do.
       constexpr int stride = Two ? 1 : 2;
