@@ -33,6 +33,7 @@ namespace skv {
 constexpr int kCtT = 128;       // tokens of a tile, rows of an MMA
 constexpr int kCtThreads = 576; // warps 0-3 and 4-7: softmax of stream 0 and 1; 8-11 and 12-15: conversion of K and of V; 16: copies; 17: tcgen05.mma
 constexpr int kCtInfo = 8;      // tiles described ahead
+constexpr int kCtBatch = 8;
 
 struct TokensArgs {
   CacheDev c;
@@ -72,7 +73,7 @@ struct Ct {
   static constexpr int QT = kCtT * D * 2;                   // an operand tile in fp16
   static constexpr int QB = (Two ? 2 : NT) * QT;
   static constexpr int KB = kCtT * D;                       // codes of K or of V: a stage
-  static constexpr int Misc = 2912;
+  static constexpr int Misc = 2928;
   static constexpr int Most = 227 * 1024 - 128 - Misc;
   static constexpr int NST0 = (Most - QB - 4 * QT) / KB, NST = NST0 > 8 ? 8 : NST0;
   static constexpr int Smem = 128 + QB + 4 * QT + NST * KB + Misc;
@@ -115,6 +116,16 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ float ex2(float x) {   // 2^-22 relative; results below 2^-126 are 0
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {   // of a normal number: within 2^-22
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
@@ -232,13 +243,14 @@ enum : int {
   kSFirst = 1024,   // first that its stream has of the row tile
   kSLast = 2048,
   kMixed = 4096,    // some rows do not see some of its tokens
-  kOdd = 8192,      // a scale that is negative or no number
+  kOdd = 8192,      // a K scale that is negative, a V scale that is not positive, or one that is no number
   kWhole = 16384    // this CTA has all of the row tile
 };
 struct TileInfo {
-  int pair, q, tile, flags, n, len, turn, vexp;   // turn: number of the row tile in this CTA; V scales are below 2^vexp
-  float ks[8], vs[8];                             // of every 16 tokens
-  int end, pad[3];                                // number of the row tile's last tile in this CTA
+  int tile, flags, vexp, vlow;   // V scales are below 2^vexp, and 2^vlow or more
+  float ks[8], vs[8];            // of every 16 tokens
+  int pair, q, n, len;
+  int turn, end, pad[2];         // number of the row tile in this CTA; of its last tile here
 };
 
 // One row of a row tile from its parts (numbers u of n; a part's Copies sub-rows lie `step` apart): a warp's work.
@@ -306,6 +318,10 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
   float* sqs = reinterpret_cast<float*>(misc + 1344);    // [128] rows' factors (one row tile)
   float2* s_ml = reinterpret_cast<float2*>(misc + 1856); // [128] stream 1's maxima and sums
   int2* s_join = reinterpret_cast<int2*>(misc + 2880);   // [4 warps] its vexp, and whether NaN is recorded
+  // (the warps wait for one another at these, never at named barriers: a wait that gives up must not leave others behind)
+  uint64_t* vote_bar = reinterpret_cast<uint64_t*>(misc + 2912);             // the conversion of V
+  uint64_t* parts_bar = vote_bar + 1;                                        // stream 0, its copies' parts
+  volatile int* s_vote = reinterpret_cast<volatile int*>(misc + 368);        // [2][4]
   static_assert(sizeof(TileInfo) == 112, "misc");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   if (gridDim.x > 1) tc::grid_dep_launch();   // (a call's last kernel lets nothing start early)
@@ -328,6 +344,8 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     tc::mbar_init(jfull, 4);
     tc::mbar_init(jdone, 4);
     for (int i = 0; i < kCtInfo; ++i) tc::mbar_init(&ifull[i], 1);
+    tc::mbar_init(vote_bar, 4);
+    tc::mbar_init(parts_bar, 4);
     tc::fence_mbar_init();
     *s_abort = 0;
   }
@@ -400,7 +418,8 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       TileInfo* in = infos + it % kCtInfo;
       if (lane >= nb) ks = vs = 0.f;
       // largest finite V scale, as an exponent above it
-      const bool odd = __any_sync(0xffffffffu, !(ks * a.scale_log2 >= 0.f));
+      const bool odd = __any_sync(0xffffffffu, lane < nb && !(ks * a.scale_log2 >= 0.f && vs > 0.f && vs < INFINITY));
+      const float least = -warp_max(lane < nb ? -fabsf(vs) : -INFINITY);
       const float top = warp_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.f);
       const int g16 = lane << 4 >> shift;   // block of 16-token group `lane`
       const float ksg = __shfl_sync(0xffffffffu, ks, g16 & 7), vsg = __shfl_sync(0xffffffffu, vs, g16 & 7);
@@ -419,6 +438,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         in->len = cur.len;
         in->turn = turn;
         in->end = seg_end - 1;
+        in->vlow = static_cast<int>(__float_as_uint(least) >> 23) - 127;
         in->vexp = max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -110);
       }
       __syncwarp();
@@ -462,67 +482,65 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
   } else if (ntile > 0 && warp == 17) {
     // ------------------------------------------------------------ tensor core
     if (elect_one()) {
-      // Per stream: S(i), then (once P(i) is there, over S's columns) O += P(i) V(i), then the next S.  While one stream's softmax
-      // runs the other's products do.
-      constexpr int stride = Two ? 1 : 2;
-      int nS[2] = {0, Two ? 0 : 1}, nP[2] = {0, Two ? 0 : 1};
-      uint32_t useP[2] = {0, 0}, kdone = 0, vdone = 0;
-      uint64_t t_last = 0;
-      int idle = 0;
+      // Steps v in a fixed order: tile and stream in turn.  S two steps ahead of O += P V, so that one stream's
+      // softmax runs while the other's products do; not past the end of a row tile, though, whose last O has to come
+      // before the next one's queries can (the thread waits for what it needs next, and for nothing else).
+      const int steps = Two ? 2 * ntile : ntile;
       // (a descriptor's low bits are its address / 16)
       const uint64_t dq = tc::desc_k_none(tc::smem_u32(qbuf), 2048, 128), dk = tc::desc_k_none(tc::smem_u32(kbuf), 2048, 128),
                      dv = tc::desc_k_none(tc::smem_u32(vbuf), D * 16, 128);
-      while (nP[0] < ntile || nP[1] < ntile) {
-        bool did = false;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t tS = tmem + x * kCtT, tO = tmem + 2 * kCtT + x * D;
-          if (nP[x] < nS[x]) {
-            const int i = nP[x];
-            if (tc::mbar_test(&pfull[x], useP[x] & 1) && tc::mbar_test(&vfull[i & 1], (i >> 1) & 1)) {
-              tc::fence_after();
-              const int flags = infos[i % kCtInfo].flags;
-#pragma unroll
-              for (int t = 0; t < C::NT; ++t)
-#pragma unroll
-                for (int k = 0; k < kCtT / 16; ++k)
-                  mma_f16_ts(tO, tS + k / 2 * 32 + k % 2 * 8 + t * 16, dv + ((i & 1) * C::QT + k * (2 * D * 16)) / 16,
-                             idesc_f16(D), !(flags & kSFirst) || t + k > 0);
-              if (!Two || (vdone ^= 1u << (i & 1), !(vdone >> (i & 1) & 1))) tc::mma_commit(&vempty[i & 1]);
-              if (flags & kSLast) tc::mma_commit(&ofin[x]);
-              nP[x] += stride;
-              ++useP[x];
-              did = true;
-            }
+      // (what a wait has shown is not asked for again: a wait costs its 100 to 300 cycles also when it need not wait)
+      int next = 0, turn_p = 0, turn_s = 0;   // next S; row tiles of the next product with V and of the next S
+      int flags_s = 0, flags_p[2] = {0, 0};   // of the next S's tile, of the streams' next products with V
+      int asked = -1, laid[2] = {-1, -1};     // last tile whose K is known to be there; row tiles whose queries are
+      bool ok = true;
+      for (int v = 0; ok && v < steps; ++v) {
+        while (next < steps && next < v + 2) {
+          const int i = Two ? next >> 1 : next, x = next & 1;
+          if (asked != i) {
+            ok = tc::mbar_wait(&kfull[i & 1], (i >> 1) & 1, kWaitLimit);
+            if (!ok) break;
+            asked = i;
+            flags_s = infos[i % kCtInfo].flags;
+            turn_s = infos[i % kCtInfo].turn;
           }
-          if (nS[x] == nP[x] && nS[x] < ntile) {
-            const int i = nS[x];
-            if (tc::mbar_test(&kfull[i & 1], (i >> 1) & 1) && tc::mbar_test(&qfull[Two ? x : 0], infos[i % kCtInfo].turn & 1)) {
-              tc::fence_after();
-#pragma unroll
-              for (int t = 0; t < C::NT; ++t)
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                  tc::mma_bf16(tS, dq + ((Two ? x : t) * C::QT + k * 4096) / 16, dk + ((i & 1) * C::QT + k * 4096) / 16,
-                               idesc_f16(kCtT), t + k > 0);
-              tc::mma_commit(&sfull[x]);
-              if (!Two || (kdone ^= 1u << (i & 1), !(kdone >> (i & 1) & 1))) tc::mma_commit(&kempty[i & 1]);
-              nS[x] += stride;
-              did = true;
-            }
+          if (next == v) turn_p = turn_s;
+          if (turn_s != turn_p) break;
+          if (laid[Two ? x : 0] != turn_s) {
+            ok = tc::mbar_wait(&qfull[Two ? x : 0], turn_s & 1, kWaitLimit);
+            if (!ok) break;
+            laid[Two ? x : 0] = turn_s;
           }
+          tc::fence_after();
+          const uint64_t d0 = dk + (i & 1) * (C::QT / 16), q0 = dq + (Two ? x : 0) * (C::QT / 16);
+          const uint32_t tS = tmem + x * kCtT;
+#pragma unroll
+          for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              tc::mma_bf16(tS, q0 + t * (C::QT / 16) + k * 256, d0 + k * 256, idesc_f16(kCtT), t + k > 0);
+          tc::mma_commit(&sfull[x]);
+          if (!Two || x == 1) tc::mma_commit(&kempty[i & 1]);
+          flags_p[x] = flags_s;
+          ++next;
         }
-        if (did) {
-          idle = 0;
-          continue;
-        }
-        // nothing ready: look at the clock now and then
-        if (idle == 0) t_last = tc::globaltimer_ns();
-        if ((++idle & 63) == 0 && (*s_abort || tc::globaltimer_ns() - t_last > kWaitLimit)) {
-          abort_now();
-          break;
-        }
+        if (!ok) break;
+        const int i = Two ? v >> 1 : v, x = v & 1, flags = flags_p[x];
+        if (!Two || x == 0) ok = tc::mbar_wait(&vfull[i & 1], (i >> 1) & 1, kWaitLimit);
+        ok = ok && tc::mbar_wait(&pfull[x], (Two ? i : i >> 1) & 1, kWaitLimit);
+        if (!ok) break;
+        tc::fence_after();
+        const uint64_t d0 = dv + (i & 1) * (C::QT / 16);
+        const uint32_t tS = tmem + x * kCtT, tO = tmem + 2 * kCtT + x * D;
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+          for (int k = 0; k < kCtT / 16; ++k)
+            mma_f16_ts(tO, tS + k / 2 * 32 + k % 2 * 8 + t * 16, d0 + k * (2 * D), idesc_f16(D), !(flags & kSFirst) || t + k > 0);
+        if (!Two || x == 1) tc::mma_commit(&vempty[i & 1]);
+        if (flags & kSLast) tc::mma_commit(&ofin[x]);
       }
+      if (!ok) abort_now();
     }
     __syncwarp();
   } else if (ntile > 0 && warp >= 8 && warp < 16) {
@@ -530,17 +548,18 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     const int t = tid & 127;
     const bool v = warp >= 12;
     auto to_half = [](const uint4& w, uint4* lo, uint4* hi) {
-      const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-      uint32_t h[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c[e] >> (16 * u)), __NV_E4M3);
-          h[2 * e + u] = r.x | static_cast<uint32_t>(r.y) << 16;
-        }
-      *lo = make_uint4(h[0], h[1], h[2], h[3]);
-      *hi = make_uint4(h[4], h[5], h[6], h[7]);
+      auto four = [](uint32_t c, uint32_t* a, uint32_t* b) {
+        asm("{\n\t.reg .b16 x, y;\n\t"
+            "mov.b32 {x, y}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, x;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+            : "=r"(*a), "=r"(*b)
+            : "r"(c));
+      };
+      four(w.x, &lo->x, &lo->y);
+      four(w.y, &lo->z, &lo->w);
+      four(w.z, &hi->x, &hi->y);
+      four(w.w, &hi->z, &hi->w);
     };
     constexpr int U = D / 16;   // 16-byte pieces of a thread
     // (one code for K and V: the kernel's instructions should stay in the instruction cache)
@@ -549,56 +568,69 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     unsigned char* dst0 = v ? vbuf + t / D * (2 * D * 16) + t % D * 16 : kbuf + t * 16;
     uint64_t* done = v ? vfull : kfull;
     uint64_t* room = v ? vempty : kempty;
+    uint32_t votes = 0;
+    constexpr int Batch = kCtBatch < U ? kCtBatch : U;
     for (int i = 0; i < ntile; ++i) {
       const int b = i & 1, n = 2 * i + v, st = n % NST;
       if (!warp_wait(&full[st], n / NST)) break;
-      uint4 w[U], lo, hi;
-#pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const uint4*>(stages + st * C::KB + src + u * sstep);
-      if (!warp_wait(&room[b], (i >> 1) ^ 1)) break;
+      unsigned char* codes = stages + st * C::KB + src;
       const int flags = infos[i % kCtInfo].flags, cnt = flags & 255;
+      if (!warp_wait(&room[b], (i >> 1) ^ 1)) break;
       // (keys past the tokens are whatever was there: their logits are not used)
       if (v && (flags & kMixed || cnt < kCtT)) {
-        // V past the tokens counts as zero.  NaN that not all rows see is taken out and noted
+        // V past the tokens counts as zero.  NaN that not all rows see is taken out and noted.  (In the codes,
+        // of which each thread changes those that it converts)
         uint32_t nan = 0;
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < U; ++u) {
           const int keep = cnt - (u * 128 + t) / D * 16;   // of the piece's 16 tokens
-          uint32_t* ww = reinterpret_cast<uint32_t*>(&w[u]);
-#pragma unroll
+          uint32_t* ww = reinterpret_cast<uint32_t*>(codes + u * sstep);
+#pragma unroll 1
           for (int e = 0; e < 4; ++e) {
             const int k = keep - 4 * e;
-            ww[e] = k >= 4 ? ww[e] : k <= 0 ? 0u : ww[e] & ((1u << (8 * k)) - 1u);
-            nan |= (ww[e] & 0x7f7f7f7fu) + 0x01010101u;    // a NaN's byte carries into its sign
+            uint32_t w = ww[e];
+            if (k < 4) ww[e] = w = k <= 0 ? 0u : w & ((1u << (8 * k)) - 1u);
+            nan |= (w & 0x7f7f7f7fu) + 0x01010101u;        // a NaN's byte carries into its sign
           }
         }
         if (flags & kMixed) {
-          const bool any = !tc::named_sync_and(1, 128, !(nan & 0x80808080u));
+          const int mine = __any_sync(0xffffffffu, nan & 0x80808080u);
+          if (lane == 0) {
+            s_vote[(votes & 1) * 4 + (warp & 3)] = mine;
+            tc::mbar_arrive(vote_bar);
+          }
+          if (!warp_wait(vote_bar, votes)) break;
+          const volatile int* all = s_vote + (votes & 1) * 4;
+          const bool any = all[0] | all[1] | all[2] | all[3];
+          ++votes;
           if (t == 0) s_nan[b] = any;
-          if (any) {
-            // bit e of a half word: token e of the piece
-#pragma unroll
+          if (any)
+#pragma unroll 1
             for (int u = 0; u < U; ++u) {
-              uint32_t* ww = reinterpret_cast<uint32_t*>(&w[u]);
-              uint32_t bits = 0;
-#pragma unroll
+              uint32_t bits = 0;   // bit e: token e of the piece
+#pragma unroll 1
               for (int e = 0; e < 16; ++e)
-                if ((ww[e / 4] >> (8 * (e & 3)) & 0x7f) == 0x7f) {
-                  ww[e / 4] &= ~(0xffu << (8 * (e & 3)));
+                if ((codes[u * sstep + e] & 0x7f) == 0x7f) {
+                  codes[u * sstep + e] = 0;
                   bits |= 1u << e;
                 }
               const int x = u * 128 + t;
               reinterpret_cast<uint16_t*>(nan_masks)[(b * 128 + x % D) * 8 + x / D] = static_cast<uint16_t>(bits);
             }
-          }
         }
       }
       unsigned char* dst = dst0 + b * C::QT;
+#pragma unroll 1
+      for (int h = 0; h < U; h += Batch) {
+        uint4 w[Batch], lo, hi;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        to_half(w[u], &lo, &hi);
-        *reinterpret_cast<uint4*>(dst + u * 4096) = lo;
-        *reinterpret_cast<uint4*>(dst + u * 4096 + dhalf) = hi;
+        for (int u = 0; u < Batch; ++u) w[u] = *reinterpret_cast<const uint4*>(codes + (h + u) * sstep);
+#pragma unroll
+        for (int u = 0; u < Batch; ++u) {
+          to_half(w[u], &lo, &hi);
+          *reinterpret_cast<uint4*>(dst + (h + u) * 4096) = lo;
+          *reinterpret_cast<uint4*>(dst + (h + u) * 4096 + dhalf) = hi;
+        }
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
@@ -617,6 +649,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     bool valid = false, active = false, used = false;
     uint32_t nanrow[D / 32];
     uint32_t use = 0, fin0 = 0, fin1 = 0;
+    [[maybe_unused]] uint32_t whole_parts = 0;
     int joined = 0;   // stream 1: row tiles that stream 0 is known to have joined
     auto wait_joined = [&](int turn) {
       if (joined >= turn) return true;
@@ -704,28 +737,8 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     // the tile, instruction fetch bound them).  General: tokens the row does not see, scales of any kind.
     constexpr int W = kCtT / Copies;            // columns of this warp
     const int col0 = Copies > 1 ? wq * W : 0;
-    auto softmax = [&](const TileInfo& in, bool first, auto general) {
-      constexpr bool General = decltype(general)::value;
-      const int rem = lim - in.tile * kCtT - col0;
-      const float2* ksp = reinterpret_cast<const float2*>(in.ks + col0 / 16);
-      const float2* vsp = reinterpret_cast<const float2*>(in.vs + col0 / 16);
-      float mt = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < W; c += 32) {
-        float s[32];
-        tc::tmem_ld32(tS + col0 + c, s);
-        const float2 k2 = ksp[c / 32];
-        const float f0 = rowf * k2.x, f1 = rowf * k2.y;
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          top[e & 1] = fmaxf(top[e & 1], !General ? s[e] : c + e < rem ? s[e] * f0 : -INFINITY);
-          top[2 + (e & 1)] = fmaxf(top[2 + (e & 1)], !General ? s[16 + e] : c + 16 + e < rem ? s[16 + e] * f1 : -INFINITY);
-        }
-        top[0] = fmaxf(top[0], top[1]);
-        top[2] = fmaxf(top[2], top[3]);
-        mt = fmaxf(mt, General ? fmaxf(top[0], top[2]) : fmaxf(top[0] * f0, top[2] * f1));
-      }
+    // The references m and 2^vexp of a tile whose largest logit is mt; O and l follow.
+    auto raise = [&](const TileInfo& in, bool first, float mt) {
       const int v2 = first ? in.vexp : max(vexp, in.vexp);
       if (first) {
         m = mt;
@@ -745,50 +758,113 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         }
       }
       vexp = v2;
-      const float ref = m == -INFINITY ? 0.f : m, up = exp2i(11 - vexp);
-      float2 sum[2] = {};
+    };
+    auto zero_others = [&]() {   // P in the other warps' columns
+      const uint32_t zero[16] = {};
+#pragma unroll
+      for (int c = 0; c < kCtT; c += W)
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+          if (c != col0) tmem_st16(tS + c + 16 * n, zero);
+    };
+    // All tokens seen, scales positive and not too far apart: the V scale v goes into the exponent, w = 2^(x - m + log2 v), and comes
+    // out of the sum of 16 tokens' w again; two and a half instructions an element.
+    auto softmax_plain = [&](const TileInfo& in, bool first) {
+      float mt = -INFINITY;
 #pragma unroll 1
       for (int c = 0; c < W; c += 32) {
         float s[32];
         tc::tmem_ld32(tS + col0 + c, s);
-        const float2 k2 = ksp[c / 32], u2 = vsp[c / 32];
+        const float2 k2 = *reinterpret_cast<const float2*>(in.ks + (col0 + c) / 16);
+        float t0 = s[0], t1 = s[16];
+#pragma unroll
+        for (int e = 1; e < 15; e += 2) {
+          t0 = max3(t0, s[e], s[e + 1]);
+          t1 = max3(t1, s[16 + e], s[17 + e]);
+        }
+        mt = max3(mt, fmaxf(t0, s[15]) * (rowf * k2.x), fmaxf(t1, s[31]) * (rowf * k2.y));
+      }
+      raise(in, first, mt);
+      const float ref = m == -INFINITY ? 0.f : m, up = exp2i(11 - vexp);
+#pragma unroll 1
+      for (int c = 0; c < W; c += 32) {
+        float s[32];
+        tc::tmem_ld32(tS + col0 + c, s);
+        const float2 k2 = *reinterpret_cast<const float2*>(in.ks + (col0 + c) / 16);
+        const float2 v2 = *reinterpret_cast<const float2*>(in.vs + (col0 + c) / 16);
         uint32_t w[C::NT][16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float fg = rowf * (e < 16 ? k2.x : k2.y), fv = (e < 16 ? u2.x : u2.y) * up;
-          const float2 y = __ffma2_rn(make_float2(s[e], s[e + 1]), make_float2(fg, fg), make_float2(-ref, -ref));
-          float2 p = make_float2(ex2(y.x), ex2(y.y));
-          if (General) {
-            p.x = c + e < rem ? p.x : 0.f;
-            p.y = c + e + 1 < rem ? p.y : 0.f;
-          }
-          sum[e / 2 & 1] = __fadd2_rn(sum[e / 2 & 1], p);
-          p = __fmul2_rn(p, make_float2(fv, fv));
-          if (General) {   // (a scale that is no number under a hidden token)
-            p.x = c + e < rem ? p.x : 0.f;
-            p.y = c + e + 1 < rem ? p.y : 0.f;
-          }
+        for (int g = 0; g < 2; ++g) {
+          const float fg = rowf * (g ? k2.y : k2.x), fv = (g ? v2.y : v2.x) * up, off = lg2(fv) - ref;
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int n = 0; n < C::NT; ++n) {
-            const __half2 z = __floats2half2_rn(p.x, p.y);
-            w[n][e / 2] = *reinterpret_cast<const uint32_t*>(&z);
-            p.x -= __low2float(z);
-            p.y -= __high2float(z);
+          for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+            float2 p = make_float2(ex2(fmaf(s[e], fg, off)), ex2(fmaf(s[e + 1], fg, off)));
+            sum.x += p.x;
+            sum.y += p.y;
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n) {
+              const __half2 z = __floats2half2_rn(p.x, p.y);
+              w[n][e / 2] = *reinterpret_cast<const uint32_t*>(&z);
+              p.x -= __low2float(z);
+              p.y -= __high2float(z);
+            }
           }
+          l = fmaf(sum.x + sum.y, __fdividef(1.f, fv), l);
         }
         // P of 32 tokens over their own columns of S: 16 columns a term
 #pragma unroll
         for (int n = 0; n < C::NT; ++n) tmem_st16(tS + col0 + c + 16 * n, w[n]);
       }
-      if constexpr (Copies > 1) {   // the other warps' columns
-        const uint32_t zero[16] = {};
+      if constexpr (Copies > 1) zero_others();
+      tmem_wait_st();
+    };
+    // Any tokens, any scales.
+    auto softmax_any = [&](const TileInfo& in, bool first) {
+      const int rem = lim - in.tile * kCtT - col0;
+      float mt = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < W; c += 16) {
+        float s[16];
+        tc::tmem_ld16(tS + col0 + c, s);
+        const float fg = rowf * in.ks[(col0 + c) / 16];
 #pragma unroll
-        for (int c = 0; c < kCtT; c += W)
-#pragma unroll
-          for (int n = 0; n < C::NT; ++n)
-            if (c != col0) tmem_st16(tS + c + 16 * n, zero);
+        for (int e = 0; e < 16; ++e) mt = fmaxf(mt, c + e < rem ? s[e] * fg : -INFINITY);
       }
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      raise(in, first, mt);
+      const float ref = m == -INFINITY ? 0.f : m, up = exp2i(11 - vexp);
+      float sum = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < W; c += 32) {
+        float s[32];
+        tc::tmem_ld32(tS + col0 + c, s);
+        const float2 k2 = *reinterpret_cast<const float2*>(in.ks + (col0 + c) / 16);
+        const float2 v2 = *reinterpret_cast<const float2*>(in.vs + (col0 + c) / 16);
+        uint32_t w[C::NT][16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float fg = rowf * (e < 16 ? k2.x : k2.y), fv = (e < 16 ? v2.x : v2.y) * up;
+          float p[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const bool seen = c + e + u < rem;
+            p[u] = seen ? ex2(fmaf(s[e + u], fg, -ref)) : 0.f;
+            sum += p[u];
+            p[u] = seen ? p[u] * fv : 0.f;   // (a scale that is no number under a hidden token)
+          }
+#pragma unroll
+          for (int n = 0; n < C::NT; ++n) {
+            const __half2 z = __floats2half2_rn(p[0], p[1]);
+            w[n][e / 2] = *reinterpret_cast<const uint32_t*>(&z);
+            p[0] -= __low2float(z);
+            p[1] -= __high2float(z);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n) tmem_st16(tS + col0 + c + 16 * n, w[n]);
+      }
+      if constexpr (Copies > 1) zero_others();
+      l += sum;
       tmem_wait_st();
     };
 
@@ -872,11 +948,13 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         tc::fence_after();
         if (!Two && x == 1 && !(ok = wait_joined(turn))) break;   // O is free
         if (active) {
-          const int rem = lim - in.tile * kCtT, tf = in.flags;
-          if (__any_sync(0xffffffffu, rem < col0 + W && valid) || (tf & kOdd))
-            softmax(in, !used, std::true_type{});
+          const int4 what = *reinterpret_cast<const int4*>(&in);   // tile, flags, vexp, vlow
+          const int rem = lim - what.x * kCtT, tf = what.y;
+          if ((tf & (kMixed | kOdd)) || (tf & 255) < kCtT ||
+              what.w + 71 < (used ? max(vexp, what.z) : what.z))   // (below 2^-60 of the largest, w could vanish before p does)
+            softmax_any(in, !used);
           else
-            softmax(in, !used, std::false_type{});
+            softmax_plain(in, !used);
           if (tf & kMixed) {
             if (!(ok = warp_wait(&vfull[t & 1], t >> 1))) break;
             if (s_nan[t & 1])
@@ -977,7 +1055,9 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       }
       if (Copies > 1 && (flags & kWhole)) {
         // (the next parts are written after jdone)
-        if (!tc::named_sync_and(2, 128, true)) break;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(parts_bar);
+        if (!warp_wait(parts_bar, whole_parts++)) break;
         const size_t part = static_cast<size_t>(2 * cta + (turn > 0)) * C::PartRows;
         for (int u = wq; u < Rows && head_q * Rows + u < head_len * a.G; u += 4) {
           const int r = head_q * Rows + u, jr = r / a.G;
