@@ -411,6 +411,13 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         ph ^= 1;
       }
     };
+    // (one row tile per pair: the codes are read once and evicted first from L2)
+    const bool once = row_tiles<Rows>(a, a.s) == 1;
+    const uint64_t policy = tc::l2_evict_first_policy();
+    auto load = [&](void* dst, const uint8_t* src) {
+      if (once) tc::bulk_load_hint(dst, src, B * D, &full[st], policy);
+      else tc::bulk_load(dst, src, B * D, &full[st]);
+    };
     for (;; ++it) {
       const int nb = blocks(cur), cnt = tokens(cur);
       if (!warp_wait(&sempty[st], ph)) break;
@@ -448,13 +455,13 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       }
       __syncwarp();
       const size_t src = static_cast<size_t>(id) * (B * D);
-      if (lane < nb) tc::bulk_load(stages + st * C::KB + lane * (B * D), a.c.kc + src, B * D, &full[st]);
+      if (lane < nb) load(stages + st * C::KB + lane * (B * D), a.c.kc + src);
       ++copied;
       next_stage();
       if (!warp_wait(&sempty[st], ph)) break;
       if (lane == 0) tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb * B * D));
       __syncwarp();
-      if (lane < nb) tc::bulk_load(stages + st * C::KB + lane * (B * D), a.c.vc + src, B * D, &full[st]);
+      if (lane < nb) load(stages + st * C::KB + lane * (B * D), a.c.vc + src);
       ++copied;
       next_stage();
       Walk nx2 = nx;
