@@ -578,7 +578,7 @@ size_t shadowkv_verify_workspace(const shadowkv_verify_params* p);
  *   accept, sample : device f32, b x s and b: random numbers in [0, 1).  An accept that is NaN
  *            does not stand; a sample below 0 or NaN counts as 0, one of 1 or more as the largest below 1.
  *   lens   : device int32, b: drafts of each sequence (clamped to 0..s; nothing is read past them); NULL: s each.
- *   temperatures : device f32, b, or NULL.  One below 1e-30 or NaN counts as 0.
+ *   temperatures : device f32, b, or NULL.  One below 1e-30 or NaN counts as 0, one above 1e30 as that.
  *   tokens : device int32, b x (s + 1): the drafts that stand, the next token, then -1.  A row without a
  *            logit above -inf accepts nothing and gives -1.
  *   accepted : device int32, b: drafts that stand.

@@ -36,16 +36,41 @@ struct VerifyArgs {
   float4* part;        // [b (s + 1)][splits]: maximum, its index, sum
   long long lb, ls, pb, ps;
   double temperature;
-  int b, s, vocab, splits, per;   // per: elements of a split
+  int b, s, vocab, splits;
+  int held;            // elements of a CTA of k_verify_pick whose weights it keeps, or 0
 };
 
-// Logits are taken as finite: NaN counts as -inf, +inf as the largest float.
-__device__ __forceinline__ float logit(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f); }
+// Logits are taken as finite: NaN counts as -inf (the maximum's other operand), +inf as the largest float.
+__device__ __forceinline__ float logit(float x) { return fminf(fmaxf(x, -INFINITY), 3.402823466e38f); }
+
+// Eight logits from element v on (those past the vocabulary: -inf), in 16-byte pieces where
+// the row's address allows and the piece ends within the row.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int v, int vocab, bool wide, float* x) {
+  constexpr int V = Ty<T>::kVec;
+#pragma unroll
+  for (int e = 0; e < 8; e += V) {
+    if (wide && v + e + V <= vocab) {
+      Ty<T>::load16(row + v + e, x + e);
+#pragma unroll
+      for (int u = 0; u < V; ++u) x[e + u] = logit(x[e + u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < V; ++u) x[e + u] = v + e + u < vocab ? logit(Ty<T>::to_f(row[v + e + u])) : -INFINITY;
+    }
+  }
+}
+__device__ __forceinline__ bool wide_row(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+__device__ __forceinline__ float ex2(float x) {   // 2^-22 relative
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // The temperature's factor of the logits, log2(e) / T; 0: greedy.
 __device__ __forceinline__ double log2_factor(const VerifyArgs& a, int seq) {
   const double t = a.temperatures ? static_cast<double>(a.temperatures[seq]) : a.temperature;
-  return t >= 1e-30 ? 1.4426950408889634 / t : 0.0;
+  return t >= 1e-30 ? 1.4426950408889634 / fmin(t, 1e30) : 0.0;
 }
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int seq) {
   return a.lens ? min(max(a.lens[seq], 0), a.s) : a.s;
@@ -72,9 +97,9 @@ __device__ __forceinline__ Best warp_best(Best x) {
   return x;
 }
 
-// CTA = (split of the vocabulary, row): its largest logit, the first index of it, and
-// the sum of 2^(c (l - max)).
-template <typename T>
+// CTA = (split of the vocabulary: 2048 N logits, row): its largest logit, the first index of it (greedy
+// sequences), and the sum of 2^(c (l - max)).  The logits stay in registers between the two.
+template <typename T, int N>
 __global__ void __launch_bounds__(kVrThreads)
 k_verify_rows(const __grid_constant__ VerifyArgs a) {
   __shared__ Best s_best[kVrThreads / 32];
@@ -84,19 +109,36 @@ k_verify_rows(const __grid_constant__ VerifyArgs a) {
   const int row = blockIdx.y, seq = row / (a.s + 1), j = row - seq * (a.s + 1), tid = threadIdx.x;
   if (j > drafts_of(a, seq)) return;
   const T* l = static_cast<const T*>(a.logits) + seq * a.lb + j * a.ls;
-  const int v0 = blockIdx.x * a.per, v1 = min(a.vocab, v0 + a.per);
-  Best mine{-INFINITY, a.vocab};
-  for (int v = v0 + tid; v < v1; v += kVrThreads) mine = better(mine, Best{logit(Ty<T>::to_f(l[v])), v});
-  mine = warp_best(mine);
-  if ((tid & 31) == 0) s_best[tid >> 5] = mine;
+  const bool wide = wide_row(l);
+  float x[N][8], top = -INFINITY;
+  const int v0 = blockIdx.x * (kVrThreads * 8 * N) + tid * 8;
+#pragma unroll
+  for (int n = 0; n < N; ++n) load8(l, v0 + n * (kVrThreads * 8), a.vocab, wide, x[n]);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, x[n][e]);
+  const double factor = log2_factor(a, seq);
+  Best best{top, a.vocab};
+  if (factor == 0.0)
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n)
+#pragma unroll
+      for (int e = 7; e >= 0; --e)
+        if (x[n][e] == top) best.at = v0 + n * (kVrThreads * 8) + e;
+  best = warp_best(best);
+  if ((tid & 31) == 0) s_best[tid >> 5] = best;
   __syncthreads();
-  Best best = s_best[0];
+  best = s_best[0];
 #pragma unroll
   for (int w = 1; w < kVrThreads / 32; ++w) best = better(best, s_best[w]);
-  const float c = static_cast<float>(log2_factor(a, seq));
+  const float c = static_cast<float>(factor);
   float z = 0.f;
   if (best.m > -INFINITY)
-    for (int v = v0 + tid; v < v1; v += kVrThreads) z += exp2f((logit(Ty<T>::to_f(l[v])) - best.m) * c);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z += ex2((x[n][e] - best.m) * c);
   z = warp_sum(z);
   if ((tid & 31) == 0) s_sum[tid >> 5] = z;
   __syncthreads();
@@ -155,8 +197,8 @@ __device__ __forceinline__ unsigned long long times(float f, unsigned long long 
 }
 
 // ------------------------------------------------------------------ pick
-constexpr int kVpCtas = 8, kVpThreads = 512, kVpWarps = kVpThreads / 32;
-constexpr int kVpChunk = 512;   // elements whose sum is kept, one warp's work
+constexpr int kVpCtas = 8, kVpThreads = 1024, kVpWarps = kVpThreads / 32;
+constexpr int kVpChunk = 256;   // elements whose sum is kept, one warp's work: eight adjacent ones a lane
 
 struct PickShared {
   ulonglong2 table[64];
@@ -197,7 +239,7 @@ __device__ __forceinline__ unsigned long long cluster_add(cg::cluster_group& cl,
 template <typename T>
 __global__ void __cluster_dims__(kVpCtas, 1, 1) __launch_bounds__(kVpThreads)
 k_verify_pick(const __grid_constant__ VerifyArgs a) {
-  extern __shared__ unsigned long long s_chunk[];   // sums of this CTA's chunks
+  extern __shared__ unsigned long long s_chunk[];   // sums of this CTA's chunks, then (held) its weights
   __shared__ PickShared sh;
   __shared__ float s_max;
   __shared__ int s_arg, s_yes;
@@ -220,6 +262,8 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
   const int chunks = (a.vocab + kVpChunk - 1) / kVpChunk, c0 = static_cast<int>(static_cast<long long>(chunks) * rank / kVpCtas),
             c1 = static_cast<int>(static_cast<long long>(chunks) * (rank + 1) / kVpCtas);
   const T* rows = static_cast<const T*>(a.logits) + seq * a.lb;
+  unsigned long long* weights = s_chunk + c1 - c0;   // element 8 lane + e of a chunk at 32 e + lane
+  const bool held = a.held > 0;
   int turn = 0;
 
   // The row's maximum and fp32 sum from its splits (warp 0, to shared memory).
@@ -231,7 +275,7 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
       best = warp_best(best);
       double z = 0.0;
       for (int u = lane; u < a.splits; u += 32)
-        if (p[u].x > -INFINITY) z += static_cast<double>(p[u].z * exp2f((p[u].x - best.m) * ch));
+        if (p[u].x > -INFINITY) z += static_cast<double>(p[u].z * ex2((p[u].x - best.m) * ch));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
       if (lane == 0) {
@@ -246,13 +290,17 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
   auto row_sum = [&](int j, unsigned long long* ahead) {
     const Exp e{s_max, ch, cl_, sh.table};
     const T* l = rows + j * a.ls;
+    const bool wide = wide_row(l);
     unsigned long long sum = 0;
     for (int c = c0 + warp; c < c1; c += kVpWarps) {
       unsigned long long x = 0;
-#pragma unroll 4
-      for (int u = 0; u < kVpChunk / 32; ++u) {
-        const int v = c * kVpChunk + u * 32 + lane;
-        if (v < a.vocab) x += weight_of(e, logit(Ty<T>::to_f(l[v])));
+      float y[8];
+      load8(l, c * kVpChunk + lane * 8, a.vocab, wide, y);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const unsigned long long w = weight_of(e, y[u]);
+        if (held) weights[(c - c0) * kVpChunk + u * 32 + lane] = w;
+        x += w;
       }
       x = warp_add(x);
       if (lane == 0) s_chunk[c - c0] = x;
@@ -313,24 +361,41 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
   const float* q = j < n && a.probs ? a.probs + seq * a.pb + j * a.ps : nullptr;
   const int out = j < n && !a.probs ? a.drafts[static_cast<size_t>(seq) * a.s + j] : -1;   // the token left out
   const unsigned long long z = total;
-  // what is left of token v's weight
+  // what is left of a lane's eight weights of chunk c
   bool plain = j == n;
-  auto left = [&](int v) {
-    const unsigned long long w = weight_of(e, logit(Ty<T>::to_f(l[v])));
-    if (plain) return w;
-    if (!q) return v == out ? 0ull : w;
-    const unsigned long long t = times(q[v], z);
-    return w > t ? w - t : 0ull;
+  const bool wide_l = wide_row(l), wide_q = q && wide_row(q);
+  auto left = [&](int c, unsigned long long* w) {
+    const int v = c * kVpChunk + lane * 8;
+    if (held) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) w[u] = weights[(c - c0) * kVpChunk + u * 32 + lane];
+    } else {
+      float y[8];
+      load8(l, v, a.vocab, wide_l, y);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) w[u] = weight_of(e, y[u]);
+    }
+    if (plain) return;
+    if (!q) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) w[u] = v + u == out ? 0ull : w[u];
+      return;
+    }
+    float y[8];
+    load8(q, v, a.vocab, wide_q, y);   // (what is past the vocabulary has no weight)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const unsigned long long t = times(y[u], z);
+      w[u] = w[u] > t ? w[u] - t : 0ull;
+    }
   };
   auto left_sum = [&](unsigned long long* before) {
     unsigned long long sum = 0;
     for (int c = c0 + warp; c < c1; c += kVpWarps) {
-      unsigned long long x = 0;
-#pragma unroll 4
-      for (int u = 0; u < kVpChunk / 32; ++u) {
-        const int v = c * kVpChunk + u * 32 + lane;
-        if (v < a.vocab) x += left(v);
-      }
+      unsigned long long w[8], x = 0;
+      left(c, w);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x += w[u];
       x = warp_add(x);
       if (lane == 0) s_chunk[c - c0] = x;
       sum += x;
@@ -372,43 +437,59 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
       }
     }
     if (found >= 0 && ahead <= at) {
-      for (int u = 0; u < kVpChunk / 32; ++u) {
-        const int v = found * kVpChunk + u * 32 + lane;
-        unsigned long long x = v < a.vocab ? left(v) : 0;
+      unsigned long long w[8], mine = 0;
+      left(found, w);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, run + x > at);
-        if (past) {
-          if (lane == 0) *next = found * kVpChunk + u * 32 + __ffs(past) - 1;
-          break;
-        }
-        run += __shfl_sync(0xffffffffu, x, 31);
+      for (int u = 0; u < 8; ++u) mine += w[u];
+      unsigned long long x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, run + x > at);
+      if (past && lane == __ffs(past) - 1) {
+        run += x - mine;
+        int u = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (run + w[k] <= at && u == k) {
+            run += w[k];
+            ++u;
+          }
+        *next = found * kVpChunk + lane * 8 + u;
       }
     }
   }
 }
 
-static int verify_splits(const shadowkv_verify_params& p, int* per) {
-  // 8 KB of logits or more to a CTA, four CTAs per SM or more
-  const int least = 4096;
+// Logits per CTA of k_verify_rows / 2048: four, where that still gives every SM two CTAs.
+static int verify_vectors(const shadowkv_verify_params& p) {
   const long long rows = static_cast<long long>(p.b) * (p.s + 1);
-  long long n = (4 * 152 + rows - 1) / rows;
-  const long long most = (p.vocab + least - 1) / least;
-  n = n < most ? n : most;
-  *per = static_cast<int>(((p.vocab + n - 1) / n + 7) / 8 * 8);
-  return (p.vocab + *per - 1) / *per;
+  for (int n = 4; n > 1; n /= 2)
+    if (rows * ((p.vocab + 2048 * n - 1) / (2048 * n)) >= 2 * 152) return n;
+  return 1;
+}
+static int verify_splits(const shadowkv_verify_params& p) {
+  const int per = 2048 * verify_vectors(p);
+  return (p.vocab + per - 1) / per;
 }
 
 template <typename T>
-static cudaError_t verify_t(const VerifyArgs& a, cudaStream_t st) {
-  cudaError_t e = launch_pdl(k_verify_rows<T>, dim3(a.splits, a.b * (a.s + 1)), dim3(kVrThreads), 0, st, a);
-  const int chunks = (a.vocab + kVpChunk - 1) / kVpChunk, mine = (chunks + kVpCtas - 1) / kVpCtas + 1;
-  if (e == cudaSuccess)
-    e = launch_pdl(k_verify_pick<T>, dim3(a.b * kVpCtas), dim3(kVpThreads), mine * sizeof(unsigned long long), st, a);
-  return e;
+static cudaError_t verify_t(VerifyArgs a, int n, cudaStream_t st) {
+  const dim3 grid(a.splits, a.b * (a.s + 1)), block(kVrThreads);
+  cudaError_t e = n == 4   ? launch_pdl(k_verify_rows<T, 4>, grid, block, 0, st, a)
+                  : n == 2 ? launch_pdl(k_verify_rows<T, 2>, grid, block, 0, st, a)
+                           : launch_pdl(k_verify_rows<T, 1>, grid, block, 0, st, a);
+  if (e != cudaSuccess) return e;
+  // a CTA keeps the weights of its share of the row in shared memory where they fit (224,000 tokens)
+  const int chunks = (a.vocab + kVpChunk - 1) / kVpChunk, mine = (chunks + kVpCtas - 1) / kVpCtas;
+  constexpr int kMost = 220 * 1024;
+  size_t smem = mine * sizeof(unsigned long long);
+  a.held = smem + static_cast<size_t>(mine) * kVpChunk * 8 <= kMost ? mine * kVpChunk : 0;
+  smem += static_cast<size_t>(a.held) * 8;
+  e = set_smem_once(reinterpret_cast<const void*>(k_verify_pick<T>), kMost);
+  return e == cudaSuccess ? launch_pdl(k_verify_pick<T>, dim3(a.b * kVpCtas), dim3(kVpThreads), smem, st, a) : e;
 }
 
 static const char* verify_fault(const shadowkv_verify_params* p, skv_status* st) {
@@ -437,8 +518,7 @@ size_t shadowkv_verify_workspace(const shadowkv_verify_params* p) try {
     return 0;
   }
   if (p->b == 0) return 256;
-  int per;
-  return static_cast<size_t>(p->b) * (p->s + 1) * skv::verify_splits(*p, &per) * sizeof(float4);
+  return static_cast<size_t>(p->b) * (p->s + 1) * skv::verify_splits(*p) * sizeof(float4);
 } catch (...) {   // host memory for an error text ran out
   return 0;
 }
@@ -462,7 +542,7 @@ skv_status shadowkv_verify_drafts(const shadowkv_verify_params* p, const void* l
   if (!work || reinterpret_cast<uintptr_t>(work) % 256)
     return set_error(SKV_ERR_INVALID_ARG, "the workspace must be non-NULL and 256-byte aligned");
   skv::VerifyArgs a;
-  a.splits = skv::verify_splits(*p, &a.per);
+  a.splits = skv::verify_splits(*p);
   if (work_bytes < static_cast<size_t>(p->b) * (p->s + 1) * a.splits * sizeof(float4))
     return set_error(SKV_ERR_INVALID_ARG, "the workspace is smaller than shadowkv_verify_workspace");
   a.logits = logits;
@@ -481,7 +561,8 @@ skv_status shadowkv_verify_drafts(const shadowkv_verify_params* p, const void* l
   a.b = p->b; a.s = p->s; a.vocab = p->vocab;
   cudaStream_t q = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> together(skv::cache_enqueue());
-  const cudaError_t e = p->dtype == SKV_DTYPE_BF16 ? skv::verify_t<skv::bf16>(a, q) : skv::verify_t<float>(a, q);
+  const int n = skv::verify_vectors(*p);
+  const cudaError_t e = p->dtype == SKV_DTYPE_BF16 ? skv::verify_t<skv::bf16>(a, n, q) : skv::verify_t<float>(a, n, q);
   return e == cudaSuccess ? SKV_OK : set_error(SKV_ERR_CUDA, cudaGetErrorString(e));
 } catch (...) {   // host memory for an error text ran out
   return SKV_ERR_OOM;
