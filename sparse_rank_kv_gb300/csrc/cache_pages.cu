@@ -236,10 +236,21 @@ __device__ __forceinline__ void copy_codes(const CacheDev& from, int id, const C
   const uint4* v0 = reinterpret_cast<const uint4*>(from.vc) + static_cast<size_t>(id) * n16;
   uint4* k1 = reinterpret_cast<uint4*>(to.kc) + static_cast<size_t>(id2) * n16;
   uint4* v1 = reinterpret_cast<uint4*>(to.vc) + static_cast<size_t>(id2) * n16;
-#pragma unroll 4
-  for (int i = tid; i < n16; i += nt) {
-    k1[i] = k0[i];
-    v1[i] = v0[i];
+  // four pieces of each in flight, read once and not kept
+  for (int i = tid; i < n16; i += 4 * nt) {
+    uint4 k[4], v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * nt < n16) {
+        k[u] = __ldcs(k0 + i + u * nt);
+        v[u] = __ldcs(v0 + i + u * nt);
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * nt < n16) {
+        __stcs(k1 + i + u * nt, k[u]);
+        __stcs(v1 + i + u * nt, v[u]);
+      }
   }
   if (tid == 0) {
     to.ks[id2] = from.ks[id];
@@ -297,7 +308,13 @@ __global__ void __launch_bounds__(kPgThreads)
 k_compact_move(const __grid_constant__ CompactArgs a) {
   tc::grid_dep_wait();
   const int n = *a.count;
-  for (int i = blockIdx.x; i < n; i += gridDim.x) copy_codes(a.c, a.list[i], a.to, i, a.d, threadIdx.x, kPgThreads);
+  // (the next block's id is on its way while one is copied)
+  int id = blockIdx.x < n ? a.list[blockIdx.x] : 0;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int next = i + static_cast<int>(gridDim.x) < n ? a.list[i + gridDim.x] : 0;
+    copy_codes(a.c, id, a.to, i, a.d, threadIdx.x, kPgThreads);
+    id = next;
+  }
   const size_t entries = static_cast<size_t>(a.c.pairs) * a.c.max_blocks, step = static_cast<size_t>(gridDim.x) * kPgThreads;
   for (size_t e = static_cast<size_t>(blockIdx.x) * kPgThreads + threadIdx.x; e < entries; e += step) {
     const int id = a.c.table[e];

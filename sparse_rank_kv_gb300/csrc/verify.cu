@@ -7,8 +7,8 @@
 // whole numbers: 2^43 w_v, each within 2^-37 of itself, by a table of 2^(j/64) and a
 // short polynomial (Tang, "Table-driven implementation of the exponential function",
 // 1989) on pairs of floats.  Their sums are exact and do not depend on the order.  The rows'
-// sums for the acceptance tests are fp32 and good to 2^-14; a test that close to its
-// border (one in 10,000) is decided again with the row's whole-number sum.
+// sums for the acceptance tests are fp32 and good to 2^-13; a test that close to its
+// border (one in 5,000) is decided again with the row's whole-number sum.
 //
 // Memory bounds it: the logits are read once by k_verify_rows, one row per sequence (from L2) and
 // the draft's distribution again by k_verify_pick.
@@ -35,7 +35,7 @@ struct VerifyArgs {
   int32_t *tokens, *accepted;
   float4* part;        // [b (s + 1)][splits]: maximum, its index, sum
   long long lb, ls, pb, ps;
-  double temperature;
+  float ch, cl;        // log2(e) / T as two floats, where no temperatures are given; 0: greedy
   int b, s, vocab, splits;
   int held;            // elements of a CTA of k_verify_pick whose weights it keeps, or 0
 };
@@ -67,10 +67,12 @@ __device__ __forceinline__ float ex2(float x) {   // 2^-22 relative
   return r;
 }
 
-// The temperature's factor of the logits, log2(e) / T; 0: greedy.
-__device__ __forceinline__ double log2_factor(const VerifyArgs& a, int seq) {
-  const double t = a.temperatures ? static_cast<double>(a.temperatures[seq]) : a.temperature;
-  return t >= 1e-30 ? 1.4426950408889634 / fmin(t, 1e30) : 0.0;
+// The temperature's factor of the logits, log2(e) / T, as two floats; 0: greedy.  (64-bit arithmetic runs at a hundredth of
+// the fp32 rate: one thread, or the host, does what there is of it.)
+__host__ __device__ inline void log2_factor(double t, float* ch, float* cl) {
+  const double f = t >= 1e-30 ? 1.4426950408889634 / (t < 1e30 ? t : 1e30) : 0.0;
+  *ch = static_cast<float>(f);
+  *cl = static_cast<float>(f - *ch);
 }
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int seq) {
   return a.lens ? min(max(a.lens[seq], 0), a.s) : a.s;
@@ -118,9 +120,10 @@ k_verify_rows(const __grid_constant__ VerifyArgs a) {
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = fmaxf(top, x[n][e]);
-  const double factor = log2_factor(a, seq);
+  const float t = a.temperatures ? a.temperatures[seq] : 1.f;
+  const float c = !a.temperatures ? a.ch : t >= 1e-30f ? __fdividef(1.44269504f, fminf(t, 1e30f)) : 0.f;
   Best best{top, a.vocab};
-  if (factor == 0.0)
+  if (c == 0.f)
 #pragma unroll
     for (int n = N - 1; n >= 0; --n)
 #pragma unroll
@@ -132,7 +135,6 @@ k_verify_rows(const __grid_constant__ VerifyArgs a) {
   best = s_best[0];
 #pragma unroll
   for (int w = 1; w < kVrThreads / 32; ++w) best = better(best, s_best[w]);
-  const float c = static_cast<float>(factor);
   float z = 0.f;
   if (best.m > -INFINITY)
 #pragma unroll
@@ -235,15 +237,14 @@ __device__ __forceinline__ unsigned long long cluster_add(cg::cluster_group& cl,
 }
 
 // Cluster = sequence.  Every CTA decides the acceptance tests by itself (on the same
-// numbers); the sampled row is dealt in chunks, a run of them to each CTA.
+// numbers), a warp to a draft; the sampled row is dealt in chunks, a run of them to each CTA.
 template <typename T>
 __global__ void __cluster_dims__(kVpCtas, 1, 1) __launch_bounds__(kVpThreads)
 k_verify_pick(const __grid_constant__ VerifyArgs a) {
   extern __shared__ unsigned long long s_chunk[];   // sums of this CTA's chunks, then (held) its weights
   __shared__ PickShared sh;
-  __shared__ float s_max;
-  __shared__ int s_arg, s_yes;
-  __shared__ double s_z;
+  __shared__ float s_top[kVpWarps], s_ch, s_cl;   // largest logits of the rows looked at, the factor
+  __shared__ int s_at[kVpWarps], s_state[kVpWarps], s_yes;
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < 64) {
@@ -255,10 +256,14 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
                       static_cast<unsigned long long>(__float_as_uint(static_cast<float>(x - tf))) << 32;
   }
   tc::grid_dep_wait();
-  cl.sync();   // every CTA's shared memory is there
   const int seq = blockIdx.x / kVpCtas, n = drafts_of(a, seq), rank = cl.block_rank();
-  const double factor = log2_factor(a, seq);
-  const float ch = static_cast<float>(factor), cl_ = static_cast<float>(factor - ch);
+  if (tid == 0) {
+    s_ch = a.ch;
+    s_cl = a.cl;
+    if (a.temperatures) log2_factor(a.temperatures[seq], &s_ch, &s_cl);
+  }
+  cl.sync();   // every CTA's shared memory is there
+  const float ch = s_ch, cl_ = s_cl;
   const int chunks = (a.vocab + kVpChunk - 1) / kVpChunk, c0 = static_cast<int>(static_cast<long long>(chunks) * rank / kVpCtas),
             c1 = static_cast<int>(static_cast<long long>(chunks) * (rank + 1) / kVpCtas);
   const T* rows = static_cast<const T*>(a.logits) + seq * a.lb;
@@ -266,29 +271,21 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
   const bool held = a.held > 0;
   int turn = 0;
 
-  // The row's maximum and fp32 sum from its splits (warp 0, to shared memory).
-  auto row_stats = [&](int j) {
-    if (warp == 0) {
-      const float4* p = a.part + (static_cast<size_t>(seq) * (a.s + 1) + j) * a.splits;
-      Best best{-INFINITY, a.vocab};
-      for (int u = lane; u < a.splits; u += 32) best = better(best, Best{p[u].x, __float_as_int(p[u].y)});
-      best = warp_best(best);
-      double z = 0.0;
-      for (int u = lane; u < a.splits; u += 32)
-        if (p[u].x > -INFINITY) z += static_cast<double>(p[u].z * ex2((p[u].x - best.m) * ch));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-      if (lane == 0) {
-        s_max = best.m;
-        s_arg = best.at;
-        s_z = z;
-      }
-    }
-    __syncthreads();
+  // The row's maximum, its index and its fp32 sum, from its splits (by one warp).
+  auto row_stats = [&](int j, float* z_out) {
+    const float4* p = a.part + (static_cast<size_t>(seq) * (a.s + 1) + j) * a.splits;
+    Best best{-INFINITY, a.vocab};
+    for (int u = lane; u < a.splits; u += 32) best = better(best, Best{p[u].x, __float_as_int(p[u].y)});
+    best = warp_best(best);
+    float z = 0.f;
+    for (int u = lane; u < a.splits; u += 32)
+      if (p[u].x > -INFINITY) z = fmaf(p[u].z, ex2((p[u].x - best.m) * ch), z);
+    *z_out = warp_sum(z);
+    return best;
   };
   // Whole-number sum of row j's weights, and of each of this CTA's chunks.
-  auto row_sum = [&](int j, unsigned long long* ahead) {
-    const Exp e{s_max, ch, cl_, sh.table};
+  auto row_sum = [&](int j, float top, unsigned long long* ahead) {
+    const Exp e{top, ch, cl_, sh.table};
     const T* l = rows + j * a.ls;
     const bool wide = wide_row(l);
     unsigned long long sum = 0;
@@ -312,36 +309,51 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
   };
 
   int j = 0;
-  for (; j < n; ++j) {
-    row_stats(j);
-    const int y = a.drafts[static_cast<size_t>(seq) * a.s + j];
-    const bool real = static_cast<unsigned>(y) < static_cast<unsigned>(a.vocab) && s_max > -INFINITY;
-    bool yes = false;
-    if (real && factor == 0.0) {
-      yes = y == s_arg && static_cast<double>(a.accept[static_cast<size_t>(seq) * a.s + j]) *
-                                  (a.probs ? a.probs[seq * a.pb + j * a.ps + y] : 1.f) < 1.0;
-    } else if (real) {
-      int v = 0;   // 0, 1: decided; 2: too near
-      double u = 0.0, w = 0.0;
-      if (tid == 0) {
-        const float q = a.probs ? a.probs[seq * a.pb + j * a.ps + y] : 1.f;
-        u = static_cast<double>(a.accept[static_cast<size_t>(seq) * a.s + j]) * q;   // exact
-        w = exp2((static_cast<double>(logit(Ty<T>::to_f(rows[j * a.ls + y]))) - s_max) * factor);
-        const double uz = u * s_z;
-        s_yes = fabs(uz - w) <= 0x1p-14 * w && w > 0.0 ? 2 : uz < w;
+  for (bool all = true; all && j < n;) {
+    const int j0 = j, k = j0 + warp;
+    if (k < n) {
+      float z;
+      const Best best = row_stats(k, &z);
+      if (lane == 0) {
+        const size_t at = static_cast<size_t>(seq) * a.s + k;
+        const int y = a.drafts[at];
+        int state = 0;   // 1: it stands; 2: too near to say
+        if (static_cast<unsigned>(y) < static_cast<unsigned>(a.vocab) && best.m > -INFINITY) {
+          const float q = a.probs ? a.probs[seq * a.pb + k * a.ps + y] : 1.f, u = a.accept[at];
+          if (ch == 0.f) {
+            state = y == best.at && static_cast<double>(u) * q < 1.0;
+          } else {
+            const float w = ex2((logit(Ty<T>::to_f(rows[k * a.ls + y])) - best.m) * ch), uz = u * q * z;
+            // (below 2^-100 the products' roundings are not relative any more)
+            state = !(fabsf(uz - w) > 0x1p-13f * w && (uz > 0x1p-100f || w > 0x1p-100f)) ? 2 : uz < w;
+          }
+        }
+        s_top[warp] = best.m;
+        s_state[warp] = state;
       }
-      __syncthreads();
-      v = s_yes;
-      if (v == 2) {
-        const unsigned long long z = row_sum(j, nullptr);
-        if (tid == 0) s_yes = u * (static_cast<double>(z) * 0x1p-43) < w;
-        __syncthreads();
-        v = s_yes;
-      }
-      yes = v == 1;
     }
-    __syncthreads();   // the row's numbers are written again
-    if (!yes) break;
+    __syncthreads();
+    for (; j < min(n, j0 + kVpWarps); ++j) {
+      int state = s_state[j - j0];
+      if (state == 2) {
+        const float top = s_top[j - j0];
+        const unsigned long long z = row_sum(j, top, nullptr);
+        if (tid == 0) {
+          const size_t at = static_cast<size_t>(seq) * a.s + j;
+          const int y = a.drafts[at];
+          const double u = static_cast<double>(a.accept[at]) * (a.probs ? a.probs[seq * a.pb + j * a.ps + y] : 1.f);   // exact
+          const double d = static_cast<double>(logit(Ty<T>::to_f(rows[j * a.ls + y]))) - top;
+          s_yes = u * (static_cast<double>(z) * 0x1p-43) < exp2(d * (static_cast<double>(ch) + cl_));
+        }
+        __syncthreads();
+        state = s_yes;
+      }
+      if (state != 1) {
+        all = false;
+        break;
+      }
+    }
+    __syncthreads();   // the states are written again
   }
   // the drafts that stand, and what follows them
   if (rank == 0) {
@@ -350,13 +362,22 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
     if (tid == 0) a.accepted[seq] = j;
   }
   int32_t* next = a.tokens + static_cast<size_t>(seq) * (a.s + 1) + j;
-  row_stats(j);
-  if (factor == 0.0 || s_max == -INFINITY) {
-    if (rank == 0 && tid == 0) *next = s_max == -INFINITY ? -1 : s_arg;
+  if (warp == 0) {
+    float z;
+    const Best best = row_stats(j, &z);
+    if (lane == 0) {
+      s_top[0] = best.m;
+      s_at[0] = best.at;
+    }
+  }
+  __syncthreads();
+  const float top = s_top[0];
+  if (ch == 0.f || top == -INFINITY) {
+    if (rank == 0 && tid == 0) *next = top == -INFINITY ? -1 : s_at[0];
     return;
   }
-  unsigned long long ahead, total = row_sum(j, &ahead);
-  const Exp e{s_max, ch, cl_, sh.table};
+  unsigned long long ahead, total = row_sum(j, top, &ahead);
+  const Exp e{top, ch, cl_, sh.table};
   const T* l = rows + j * a.ls;
   const float* q = j < n && a.probs ? a.probs + seq * a.pb + j * a.ps : nullptr;
   const int out = j < n && !a.probs ? a.drafts[static_cast<size_t>(seq) * a.s + j] : -1;   // the token left out
@@ -557,7 +578,7 @@ skv_status shadowkv_verify_drafts(const shadowkv_verify_params* p, const void* l
   a.part = static_cast<float4*>(work);
   a.lb = p->logits_sb; a.ls = p->logits_ss;
   a.pb = p->probs_sb; a.ps = p->probs_ss;
-  a.temperature = p->temperature;
+  skv::log2_factor(p->temperature, &a.ch, &a.cl);
   a.b = p->b; a.s = p->s; a.vocab = p->vocab;
   cudaStream_t q = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> together(skv::cache_enqueue());
