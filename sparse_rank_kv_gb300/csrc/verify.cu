@@ -16,6 +16,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <mutex>
 
 #include "common.cuh"
@@ -199,8 +200,30 @@ __device__ __forceinline__ unsigned long long times(float f, unsigned long long 
 }
 
 // ------------------------------------------------------------------ pick
-constexpr int kVpCtas = 8, kVpThreads = 1024, kVpWarps = kVpThreads / 32;
+constexpr int kVpCtas = 8, kVpThreads = 512, kVpWarps = kVpThreads / 32;
 constexpr int kVpChunk = 256;   // elements whose sum is kept, one warp's work: eight adjacent ones a lane
+
+// 2^(43 + j/64), rounded; its leading 24 bits and the rest as floats.  (Made on the host once: 64-bit exponentials
+// took the kernel 1.4 us.)
+struct VerifyTable {
+  ulonglong2 e[64];
+};
+static const VerifyTable& verify_table() {
+  static const VerifyTable t = [] {
+    VerifyTable v;
+    for (int j = 0; j < 64; ++j) {
+      const double x = std::exp2(j / 64.0);
+      const float lead = static_cast<float>(x), rest = static_cast<float>(x - lead);
+      uint32_t a, b;
+      std::memcpy(&a, &lead, 4);
+      std::memcpy(&b, &rest, 4);
+      v.e[j].x = static_cast<unsigned long long>(std::llrint(x * 0x1p43));
+      v.e[j].y = a | static_cast<unsigned long long>(b) << 32;
+    }
+    return v;
+  }();
+  return t;
+}
 
 struct PickShared {
   ulonglong2 table[64];
@@ -239,22 +262,15 @@ __device__ __forceinline__ unsigned long long cluster_add(cg::cluster_group& cl,
 // Cluster = sequence.  Every CTA decides the acceptance tests by itself (on the same
 // numbers), a warp to a draft; the sampled row is dealt in chunks, a run of them to each CTA.
 template <typename T>
-__global__ void __cluster_dims__(kVpCtas, 1, 1) __launch_bounds__(kVpThreads)
-k_verify_pick(const __grid_constant__ VerifyArgs a) {
+__global__ void __cluster_dims__(kVpCtas, 1, 1) __launch_bounds__(kVpThreads, 2)
+k_verify_pick(const __grid_constant__ VerifyArgs a, const __grid_constant__ VerifyTable table) {
   extern __shared__ unsigned long long s_chunk[];   // sums of this CTA's chunks, then (held) its weights
   __shared__ PickShared sh;
   __shared__ float s_top[kVpWarps], s_ch, s_cl;   // largest logits of the rows looked at, the factor
   __shared__ int s_at[kVpWarps], s_state[kVpWarps], s_yes;
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < 64) {
-    const double x = exp2(tid / 64.0);
-    const unsigned long long t = static_cast<unsigned long long>(__double2ll_rn(x * 0x1p43));
-    const float tf = static_cast<float>(x);
-    sh.table[tid].x = t;
-    sh.table[tid].y = __float_as_uint(tf) |
-                      static_cast<unsigned long long>(__float_as_uint(static_cast<float>(x - tf))) << 32;
-  }
+  if (tid < 64) sh.table[tid] = table.e[tid];
   tc::grid_dep_wait();
   const int seq = blockIdx.x / kVpCtas, n = drafts_of(a, seq), rank = cl.block_rank();
   if (tid == 0) {
@@ -309,12 +325,18 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
   };
 
   int j = 0;
-  for (bool all = true; all && j < n;) {
-    const int j0 = j, k = j0 + warp;
-    if (k < n) {
+  int j0 = 0;
+  for (bool all = true; all;) {
+    j0 = j;
+    const int k = j0 + warp;
+    if (k <= n) {
       float z;
       const Best best = row_stats(k, &z);
       if (lane == 0) {
+        s_top[warp] = best.m;
+        s_at[warp] = best.at;
+      }
+      if (lane == 0 && k < n) {
         const size_t at = static_cast<size_t>(seq) * a.s + k;
         const int y = a.drafts[at];
         int state = 0;   // 1: it stands; 2: too near to say
@@ -328,7 +350,6 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
             state = !(fabsf(uz - w) > 0x1p-13f * w && (uz > 0x1p-100f || w > 0x1p-100f)) ? 2 : uz < w;
           }
         }
-        s_top[warp] = best.m;
         s_state[warp] = state;
       }
     }
@@ -353,7 +374,8 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
         break;
       }
     }
-    __syncthreads();   // the states are written again
+    if (j == n && n < j0 + kVpWarps) all = false;
+    if (all) __syncthreads();   // the states are written again
   }
   // the drafts that stand, and what follows them
   if (rank == 0) {
@@ -362,18 +384,9 @@ k_verify_pick(const __grid_constant__ VerifyArgs a) {
     if (tid == 0) a.accepted[seq] = j;
   }
   int32_t* next = a.tokens + static_cast<size_t>(seq) * (a.s + 1) + j;
-  if (warp == 0) {
-    float z;
-    const Best best = row_stats(j, &z);
-    if (lane == 0) {
-      s_top[0] = best.m;
-      s_at[0] = best.at;
-    }
-  }
-  __syncthreads();
-  const float top = s_top[0];
+  const float top = s_top[j - j0];
   if (ch == 0.f || top == -INFINITY) {
-    if (rank == 0 && tid == 0) *next = top == -INFINITY ? -1 : s_at[0];
+    if (rank == 0 && tid == 0) *next = top == -INFINITY ? -1 : s_at[j - j0];
     return;
   }
   unsigned long long ahead, total = row_sum(j, top, &ahead);
@@ -503,14 +516,15 @@ static cudaError_t verify_t(VerifyArgs a, int n, cudaStream_t st) {
                   : n == 2 ? launch_pdl(k_verify_rows<T, 2>, grid, block, 0, st, a)
                            : launch_pdl(k_verify_rows<T, 1>, grid, block, 0, st, a);
   if (e != cudaSuccess) return e;
-  // a CTA keeps the weights of its share of the row in shared memory where they fit (224,000 tokens)
+  // a CTA keeps the weights of its share of the row in shared memory where two CTAs still fit on an SM (104,000
+  // tokens); else it forms them twice
   const int chunks = (a.vocab + kVpChunk - 1) / kVpChunk, mine = (chunks + kVpCtas - 1) / kVpCtas;
-  constexpr int kMost = 220 * 1024;
+  constexpr int kMost = 104 * 1024;
   size_t smem = mine * sizeof(unsigned long long);
   a.held = smem + static_cast<size_t>(mine) * kVpChunk * 8 <= kMost ? mine * kVpChunk : 0;
   smem += static_cast<size_t>(a.held) * 8;
   e = set_smem_once(reinterpret_cast<const void*>(k_verify_pick<T>), kMost);
-  return e == cudaSuccess ? launch_pdl(k_verify_pick<T>, dim3(a.b * kVpCtas), dim3(kVpThreads), smem, st, a) : e;
+  return e == cudaSuccess ? launch_pdl(k_verify_pick<T>, dim3(a.b * kVpCtas), dim3(kVpThreads), smem, st, a, verify_table()) : e;
 }
 
 static const char* verify_fault(const shadowkv_verify_params* p, skv_status* st) {
