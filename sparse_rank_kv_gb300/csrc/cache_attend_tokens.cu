@@ -41,7 +41,7 @@ struct TokensArgs {
   void* out;
   float* lse;
   const int32_t* lens;
-  int4* rec;          // [ctas]: row tile in which the CTA's run begins (pair, tile, its first number, its tiles), pair -1: none
+  int4* rec;          // [ctas]: row tile in whose midst the CTA's run begins (pair, tile, its first unit, all units), pair -1: none
   float* part_o;      // [2 ctas][Rows][d]
   float2* part_ml;    // [2 ctas][Rows]
   uint32_t* nan;      // [ctas][3][128][4]
@@ -182,59 +182,85 @@ __device__ __forceinline__ int run_owner(int x, int n, int total) {
   return static_cast<int>(((static_cast<long long>(x) + 1) * n - 1) / total);
 }
 
-// Where this CTA's run begins: s_where = {pair, row tile, tile, total of all tiles}; s_first: its row tile's first
-// number.  Groups of 2^lg lanes take runs of pairs, a lane every 2^lg-th row tile.
+// The runs are dealt in units: a row tile has kCtCost units for its start and end (queries laid, outputs stored:
+// about as long as five tiles take), then one for each of its tiles.  Measured against tiles alone: a prompt of 2048
+// 127.7 -> 88 us, of 8192 845 -> 629, of 16,384 2645 -> 2215; four pieces of up to 2048 over up to 20,001 1391 -> 1210.
+//
+// Where this CTA's run begins: s_where = {pair, row tile, its first tile here, all units}, s_run = {the row tile's
+// first unit, tiles before the run, tiles before the next CTA's}.  Groups of 2^lg lanes take runs of pairs, a lane every
+// 2^lg-th row tile.
+constexpr int kCtCost = 5;
 template <int Rows>
-__device__ __forceinline__ void run_find(const TokensArgs& a, int cta, int ncta, int* s_where, int* s_scan) {
+__device__ __forceinline__ void run_find(const TokensArgs& a, int cta, int ncta, int* s_where, int* s_run, int* s_scan) {
   const int tid = threadIdx.x, P = a.c.pairs, most = row_tiles<Rows>(a, a.s);
   const int lg = most <= 2 ? 0 : most <= 8 ? 2 : 5, gs = 1 << lg, sub = tid & (gs - 1);
   const int ng = kCtThreads >> lg, per = (P + ng - 1) / ng, p0 = min(P, (tid >> lg) * per), p1 = min(P, p0 + per);
-  auto pair_sum = [&](int p) {   // this lane's part
+  auto pair_sum = [&](int p, int* items) {   // this lane's part
     const int n = cache_tokens(a.c, p), len = tokens_len(a, p / a.c.h_kv), nq = row_tiles<Rows>(a, len);
     int x = 0;
-    for (int q = sub; q < nq; q += gs) x += lim_tiles(tile_lim<Rows>(a, n, len, q));
+    for (int q = sub; q < nq; q += gs) x += kCtCost + lim_tiles(tile_lim<Rows>(a, n, len, q));
+    *items = sub == 0 ? nq : 0;
     return x;
   };
   auto group_sum = [&](int x) {
     for (int o = gs >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
   };
-  int sum = 0;
-  for (int i = 0; i < per; ++i) sum += p0 + i < p1 ? pair_sum(p0 + i) : 0;
+  int sum = 0, items = 0;
+  for (int i = 0; i < per; ++i)
+    if (p0 + i < p1) {
+      int k;
+      sum += pair_sum(p0 + i, &k);
+      items += k;
+    }
   sum = group_sum(sum);
   if (tid < 4) s_where[tid] = tid == 0 ? -1 : 0;
-  int total;
+  if (tid < 3) s_run[tid] = 0;
+  int total, all_items;
   const int scan = block_exclusive_scan(sub == 0 ? sum : 0, s_scan, &total);
-  int before = __shfl_sync(0xffffffffu, scan, tid & 31 & ~(gs - 1));
+  const int scan_items = block_exclusive_scan(items, s_scan, &all_items);
+  const int lead = tid & 31 & ~(gs - 1);
+  int before = __shfl_sync(0xffffffffu, scan, lead), items_before = __shfl_sync(0xffffffffu, scan_items, lead);
   const int n = min(ncta, total);
-  const int t0 = cta < n ? run_begin(cta, n, total) : -1;
+  const int t0 = cta < n ? run_begin(cta, n, total) : -1, t1 = cta < n ? run_begin(cta + 1, n, total) : -1;
+  if (tid == 0) {
+    s_where[3] = total;
+    if (t1 == total) s_run[2] = total - kCtCost * all_items;
+  }
   // the groups walk their pairs once more, in step within the warp
   for (int i = 0; i < per; ++i) {
-    const int p = p0 + i, mine = p < p1 ? pair_sum(p) : 0, all = group_sum(mine);
-    const bool here = before <= t0 && t0 < before + all;
+    const int p = p0 + i;
+    int nq = 0;
+    const int mine = p < p1 ? pair_sum(p, &nq) : 0, all = group_sum(mine);
+    nq = __shfl_sync(0xffffffffu, nq, lead);
+    const bool here = (before <= t0 && t0 < before + all) || (before <= t1 && t1 < before + all);
     if (__any_sync(0xffffffffu, here)) {
       const int cn = p < p1 ? cache_tokens(a.c, p) : 0, len = p < p1 ? tokens_len(a, p / a.c.h_kv) : 0;
-      const int nq = here ? row_tiles<Rows>(a, len) : 0;
       int run = before;
-      for (int q0 = 0; __any_sync(0xffffffffu, q0 < nq); q0 += gs) {
-        const int q = q0 + sub, x = q < nq ? lim_tiles(tile_lim<Rows>(a, cn, len, q)) : 0;
+      for (int q0 = 0; __any_sync(0xffffffffu, here && q0 < nq); q0 += gs) {
+        const int q = q0 + sub, x = here && q < nq ? kCtCost + lim_tiles(tile_lim<Rows>(a, cn, len, q)) : 0;
         int inc = x;
         for (int o = 1; o < gs; o <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, inc, o);
           if (sub >= o) inc += y;
         }
-        const int at = run + inc - x;
+        const int at = run + inc - x;   // the row tile's first unit
+        const int tiles = at - kCtCost * (items_before + q);
         if (x > 0 && at <= t0 && t0 < at + x) {
+          const int first = max(t0 - at - kCtCost, 0);
           s_where[0] = p;
           s_where[1] = q;
-          s_where[2] = t0 - at;
+          s_where[2] = first;
+          s_run[0] = at;
+          s_run[1] = tiles + first;
         }
+        if (x > 0 && at <= t1 && t1 < at + x) s_run[2] = tiles + max(t1 - at - kCtCost, 0);
         run += __shfl_sync(0xffffffffu, inc, tid & 31 | (gs - 1));
       }
     }
     before += all;
+    items_before += nq;
   }
-  if (tid == 0) s_where[3] = total;
   __syncthreads();
 }
 
@@ -312,6 +338,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 336);
   volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 340);
   int* s_where = reinterpret_cast<int*>(misc + 344);     // [4]
+  int* s_run = reinterpret_cast<int*>(misc + 400);       // [3]
   volatile int* s_nan = reinterpret_cast<volatile int*>(misc + 360);   // [2]: V's tile has NaN
   int* s_scan = reinterpret_cast<int*>(misc + 448);      // [32], before the tiles are described
   TileInfo* infos = reinterpret_cast<TileInfo*>(misc + 448);
@@ -358,15 +385,10 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
-  run_find<Rows>(a, cta, gridDim.x, s_where, s_scan);
-  int ntile = 0;
-  {
-    const int total = s_where[3], n = min(static_cast<int>(gridDim.x), total);
-    if (cta < n && s_where[0] >= 0) ntile = run_begin(cta + 1, n, total) - run_begin(cta, n, total);
-    if (tid == 0)
-      a.rec[cta] = ntile > 0 && s_where[2] > 0 ? make_int4(s_where[0], s_where[1], run_begin(cta, n, total) - s_where[2], total)
-                                               : make_int4(-1, 0, 0, total);
-  }
+  run_find<Rows>(a, cta, gridDim.x, s_where, s_run, s_scan);
+  const int ntile = s_where[0] >= 0 ? s_run[2] - s_run[1] : 0;
+  if (tid == 0)
+    a.rec[cta] = ntile > 0 && s_where[2] > 0 ? make_int4(s_where[0], s_where[1], s_run[0], s_where[3]) : make_int4(-1, 0, 0, s_where[3]);
   const int shift = a.c.shift, B = 1 << shift;
   uint32_t* nan_masks = a.nan + static_cast<size_t>(cta) * 3 * 128 * 4;
   auto abort_now = [&]() {
@@ -671,27 +693,30 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     auto row_of = [&](int g) { return g * 8 + (lane & 7); };   // of the warp's
     auto lay_q = [&]() {
       const long long mine = valid ? seq * a.qb + h * a.qh + j * a.qs : -1;
-      constexpr int R = V == 8 ? 2 : 1;   // groups of rows whose pieces wait in registers
-      uint4 all[R][N / 4];
+      auto load = [&](int g, uint4* r) {
+        const long long off = __shfl_sync(0xffffffffu, mine, row_of(g & 3));
+        const T* src = static_cast<const T*>(a.q) + off + (lane >> 3) * V;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (g % R == 0)
+        for (int u = 0; u < N / 4; ++u) {
+          r[u] = make_uint4(0, 0, 0, 0);
+          if (off < 0 || g > 3) continue;
+          if (a.wide_q) {
+            r[u] = *reinterpret_cast<const uint4*>(src + u * 4 * V);
+          } else {
 #pragma unroll
-          for (int k = 0; k < R; ++k) {
-            const long long off = __shfl_sync(0xffffffffu, mine, row_of(g + k));
-            const T* src = static_cast<const T*>(a.q) + off + (lane >> 3) * V;
-#pragma unroll
-            for (int u = 0; u < N / 4; ++u) {
-              all[k][u] = make_uint4(0, 0, 0, 0);
-              if (off >= 0 && a.wide_q) all[k][u] = *reinterpret_cast<const uint4*>(src + u * 4 * V);
-            }
-            if (off >= 0 && !a.wide_q)
-#pragma unroll
-              for (int u = 0; u < N / 4; ++u)
-#pragma unroll
-                for (int e = 0; e < V; ++e) reinterpret_cast<T*>(&all[k][u])[e] = src[u * 4 * V + e];
+            for (int e = 0; e < V; ++e) reinterpret_cast<T*>(&r[u])[e] = src[u * 4 * V + e];
           }
-        const uint4* raw = all[g % R];
+        }
+      };
+      // (rolled, the next group's pieces on their way: unrolled, the code of a row tile's start and end was fetched
+      // anew each time, and a prompt of 2048 took 128 us)
+      uint4 raw[N / 4], ahead[N / 4];
+      load(0, ahead);
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+#pragma unroll
+        for (int u = 0; u < N / 4; ++u) raw[u] = ahead[u];
+        load(g + 1, ahead);
         float top = 0.f;
 #pragma unroll
         for (int u = 0; u < N / 4; ++u)
@@ -843,28 +868,29 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       float sum = 0.f;
 #pragma unroll 1
       for (int c = 0; c < W; c += 32) {
-        float s[32];
-        tc::tmem_ld32(tS + col0 + c, s);
-        const float2 k2 = *reinterpret_cast<const float2*>(in.ks + (col0 + c) / 16);
-        const float2 v2 = *reinterpret_cast<const float2*>(in.vs + (col0 + c) / 16);
         uint32_t w[C::NT][16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float fg = rowf * (e < 16 ? k2.x : k2.y), fv = (e < 16 ? v2.x : v2.y) * up;
-          float p[2];
+        for (int g = 0; g < 2; ++g) {
+          float s[16];
+          tc::tmem_ld16(tS + col0 + c + 16 * g, s);
+          const float fg = rowf * in.ks[(col0 + c) / 16 + g], fv = in.vs[(col0 + c) / 16 + g] * up;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const bool seen = c + e + u < rem;
-            p[u] = seen ? ex2(fmaf(s[e + u], fg, -ref)) : 0.f;
-            sum += p[u];
-            p[u] = seen ? p[u] * fv : 0.f;   // (a scale that is no number under a hidden token)
-          }
+          for (int e = 0; e < 16; e += 2) {
+            float p[2];
 #pragma unroll
-          for (int n = 0; n < C::NT; ++n) {
-            const __half2 z = __floats2half2_rn(p[0], p[1]);
-            w[n][e / 2] = *reinterpret_cast<const uint32_t*>(&z);
-            p[0] -= __low2float(z);
-            p[1] -= __high2float(z);
+            for (int u = 0; u < 2; ++u) {
+              const bool seen = c + 16 * g + e + u < rem;
+              p[u] = seen ? ex2(fmaf(s[e + u], fg, -ref)) : 0.f;
+              sum += p[u];
+              p[u] = seen ? p[u] * fv : 0.f;   // (a scale that is no number under a hidden token)
+            }
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n) {
+              const __half2 z = __floats2half2_rn(p[0], p[1]);
+              w[n][8 * g + e / 2] = *reinterpret_cast<const uint32_t*>(&z);
+              p[0] -= __low2float(z);
+              p[1] -= __high2float(z);
+            }
           }
         }
 #pragma unroll
@@ -1101,10 +1127,10 @@ __global__ void __launch_bounds__(kCgThreads) k_tokens_merge(const __grid_consta
   const int4 rec = a.rec[c];
   if (rec.x < 0) return;
   const int total = rec.w, n = min(ncta, total), first = rec.z;
-  if (run_begin(c - 1, n, total) > first) return;
+  if (run_begin(c - 1, n, total) > first + kCtCost) return;
   const int seq = rec.x / a.c.h_kv, kvh = rec.x - seq * a.c.h_kv, len = tokens_len(a, seq), tok = cache_tokens(a.c, rec.x);
   const int nt = lim_tiles(tile_lim<Rows>(a, tok, len, rec.y));
-  const int c1 = run_owner(min(first + nt, total) - 1, n, total);
+  const int c1 = run_owner(min(first + kCtCost + nt, total) - 1, n, total);
   const int slot0 = 2 * (c - 1) + (run_begin(c - 1, n, total) < first);   // CTA c - 1's last part; the others' first
   for (int u = threadIdx.x >> 5; u < kCgRows; u += kCgThreads / 32) {
     const int row = blockIdx.y * kCgRows + u, r = rec.y * Rows + row;
@@ -1118,7 +1144,7 @@ __global__ void __launch_bounds__(kCgThreads) k_tokens_merge(const __grid_consta
 
 static int tokens_ctas(const shadowkv_cache& c, int rows, int per, int nsm) {
   const long long tiles = (static_cast<long long>(c.max_blocks) * c.block + kCtT - 1) / kCtT;
-  const long long all = tiles * ((rows + per - 1) / per) * c.b * c.h_kv;
+  const long long all = (tiles + kCtCost) * ((rows + per - 1) / per) * c.b * c.h_kv;
   return static_cast<int>(all < nsm ? all : nsm);
 }
 
@@ -1173,7 +1199,7 @@ static const char* tokens_fault(const shadowkv_cache& c, int h_q, int s, skv_sta
   if (h_q < 1 || h_q % c.h_kv || h_q / c.h_kv > 128) return "h_q must be a multiple of h_kv, of at most 128";
   const long long rows = static_cast<long long>(s) * (h_q / c.h_kv);
   if (rows > 1 << 24) return "s h_q / h_kv must be at most 2^24";
-  if (((rows + 127) / 128) * ((static_cast<long long>(c.max_blocks) * c.block + 127) / 128) >= (1LL << 31) / (static_cast<long long>(c.b) * c.h_kv))
+  if (((rows + 127) / 128) * ((static_cast<long long>(c.max_blocks) * c.block + 127) / 128 + kCtCost) >= (1LL << 31) / (static_cast<long long>(c.b) * c.h_kv))
     return "too many queries and tokens for one call";
   *st = SKV_OK;
   return nullptr;
