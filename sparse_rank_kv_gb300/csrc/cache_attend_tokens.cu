@@ -46,7 +46,7 @@ struct TokensArgs {
   float2* part_ml;    // [2 ctas][Rows]
   uint32_t* nan;      // [ctas][3][128][4]
   long long qb, qh, qs, ob, oh, os;
-  float scale_log2;   // scale log2(e)
+  float scale_log2, scale_rest;   // scale log2(e), and what its rounding leaves over it
   int s, h_q, G, causal, wide_q, wide_o;   // wide: rows in 16-byte pieces
 };
 
@@ -544,10 +544,10 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
           const uint64_t d0 = dk + (i & 1) * (C::QT / 16), q0 = dq + (Two ? x : 0) * (C::QT / 16);
           const uint32_t tS = tmem + x * kCtT;
 #pragma unroll
-          for (int t = 0; t < C::NT; ++t)
+          for (int t = C::NT - 1; t >= 0; --t)   // (the small terms first)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              tc::mma_bf16(tS, q0 + t * (C::QT / 16) + k * 256, d0 + k * 256, idesc_f16(kCtT), t + k > 0);
+              tc::mma_bf16(tS, q0 + t * (C::QT / 16) + k * 256, d0 + k * 256, idesc_f16(kCtT), t < C::NT - 1 || k > 0);
           tc::mma_commit(&sfull[x]);
           if (!Two || x == 1) tc::mma_commit(&kempty[i & 1]);
           flags_p[x] = flags_s;
@@ -769,13 +769,14 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     // the tile, instruction fetch bound them).  General: tokens the row does not see, scales of any kind.
     constexpr int W = kCtT / Copies;            // columns of this warp
     const int col0 = Copies > 1 ? wq * W : 0;
-    // The references m and 2^vexp of a tile whose largest logit is mt; O and l follow.
+    // The references m and 2^vexp of a tile whose largest logit is mt; O and l follow.  m is a whole number, so that what
+    // was formed by one reference is brought to another's exactly, here and where parts are joined.
     auto raise = [&](const TileInfo& in, bool first, float mt) {
       const int v2 = first ? in.vexp : max(vexp, in.vexp);
       if (first) {
-        m = mt;
+        m = floorf(mt);
       } else if (__any_sync(0xffffffffu, mt > m + 4.f) || v2 > vexp) {
-        const float m2 = fmaxf(m, mt), al = m2 == -INFINITY ? 1.f : ex2(m - m2);
+        const float m2 = fmaxf(m, floorf(mt)), al = m2 == -INFINITY ? 1.f : exp2i(static_cast<int>(fmaxf(m - m2, -126.f)));
         m = m2;
         l *= al;
         const float r = al * exp2i(max(vexp - v2, -126));
@@ -799,8 +800,13 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         for (int n = 0; n < C::NT; ++n)
           if (c != col0) tmem_st16(tS + c + 16 * n, zero);
     };
-    // All tokens seen, scales positive and not too far apart: the V scale v goes into the exponent, w = 2^(x - m + log2 v), and comes
-    // out of the sum of 16 tokens' w again; two and a half instructions an element.
+    // x f + off; beside fp32 with what f's rounding leaves (one relative error of all logits otherwise, 3e-7 of p)
+    auto exponent = [&](float x, float f, float off) {
+      const float y = fmaf(x, f, off);
+      return C::NT > 1 ? fmaf(x * f, a.scale_rest, y) : y;
+    };
+    // All tokens seen, scales positive and not too far apart: bf16's V scale v goes into the exponent, w = 2^(x - m + log2 v), and
+    // comes out of the sum of 16 tokens' w again; two and a half instructions an element.
     auto softmax_plain = [&](const TileInfo& in, bool first) {
       float mt = -INFINITY;
 #pragma unroll 1
@@ -827,13 +833,16 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         uint32_t w[C::NT][16];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const float fg = rowf * (g ? k2.y : k2.x), fv = (g ? v2.y : v2.x) * up, off = lg2(fv) - ref;
+          // (not beside fp32: with the scale's 11 binades the exponent's own rounding would show)
+          constexpr bool Fold = C::NT == 1;
+          const float fg = rowf * (g ? k2.y : k2.x), fv = (g ? v2.y : v2.x) * up, off = Fold ? lg2(fv) - ref : -ref;
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-            float2 p = make_float2(ex2(fmaf(s[e], fg, off)), ex2(fmaf(s[e + 1], fg, off)));
+            float2 p = make_float2(ex2(exponent(s[e], fg, off)), ex2(exponent(s[e + 1], fg, off)));
             sum.x += p.x;
             sum.y += p.y;
+            if (!Fold) p = make_float2(p.x * fv, p.y * fv);
 #pragma unroll
             for (int n = 0; n < C::NT; ++n) {
               const __half2 z = __floats2half2_rn(p.x, p.y);
@@ -842,7 +851,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
               p.y -= __high2float(z);
             }
           }
-          l = fmaf(sum.x + sum.y, __fdividef(1.f, fv), l);
+          l = Fold ? fmaf(sum.x + sum.y, __fdividef(1.f, fv), l) : l + (sum.x + sum.y);
         }
         // P of 32 tokens over their own columns of S: 16 columns a term
 #pragma unroll
@@ -880,7 +889,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const bool seen = c + 16 * g + e + u < rem;
-              p[u] = seen ? ex2(fmaf(s[e + u], fg, -ref)) : 0.f;
+              p[u] = seen ? ex2(exponent(s[e + u], fg, -ref)) : 0.f;
               sum += p[u];
               p[u] = seen ? p[u] * fv : 0.f;   // (a scale that is no number under a hidden token)
             }
@@ -1268,7 +1277,9 @@ skv_status shadowkv_cache_attend_tokens(const shadowkv_cache* c, int dtype, int 
   // the stride of an extent of 1 is not used
   a.qb = c->b > 1 ? q->sb : 0; a.qh = h_q > 1 ? q->sh : 0; a.qs = s > 1 ? q->ss : 0;
   a.ob = c->b > 1 ? out->sb : 0; a.oh = h_q > 1 ? out->sh : 0; a.os = s > 1 ? out->ss : 0;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  const double scale_log2 = static_cast<double>(scale) * 1.4426950408889634;
+  a.scale_log2 = static_cast<float>(scale_log2);
+  a.scale_rest = a.scale_log2 != 0.f ? static_cast<float>((scale_log2 - a.scale_log2) / a.scale_log2) : 0.f;
   a.s = s;
   a.h_q = h_q;
   a.G = h_q / c->h_kv;
