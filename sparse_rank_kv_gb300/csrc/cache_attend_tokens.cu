@@ -283,27 +283,38 @@ struct TileInfo {
 template <typename T, int D, int Copies, typename At>
 __device__ __forceinline__ void join_row(const TokensArgs& a, int seq, int h, int j, bool sees, int n, int step, At&& at) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, parts = n * Copies;
+  auto row_of = [&](int u) { return at(u / Copies) + u % Copies * step; };
   float M = -INFINITY;
-  for (int u = lane; u < n * Copies; u += 32) M = fmaxf(M, __ldcg(&a.part_ml[at(u / Copies) + u % Copies * step].x));
+  for (int u = lane; u < parts; u += 32) M = fmaxf(M, __ldcg(&a.part_ml[row_of(u)].x));
   M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f, o[E] = {};
-#pragma unroll 4
-  for (int u = 0; u < n * Copies; ++u) {
-    const size_t row = at(u / Copies) + u % Copies * step;
-    const float2 ml = __ldcg(&a.part_ml[row]);
-    const float w = ex2(ml.x - ref);
-    L = fmaf(ml.y, w, L);
-    const float* src = a.part_o + row * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-      o[0] = fmaf(v.x, w, o[0]); o[1] = fmaf(v.y, w, o[1]); o[2] = fmaf(v.z, w, o[2]); o[3] = fmaf(v.w, w, o[3]);
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-      o[0] = fmaf(v.x, w, o[0]); o[1] = fmaf(v.y, w, o[1]);
+  constexpr int B = Copies > 1 ? 8 : 2;   // (without copies a row has two or three parts as a rule)
+  // 32 parts at a time: a lane forms one's weight, then the parts' values, B loads in flight
+  for (int u0 = 0; u0 < parts; u0 += 32) {
+    const float2 ml = u0 + lane < parts ? __ldcg(&a.part_ml[row_of(u0 + lane)]) : make_float2(-INFINITY, 0.f);
+    const float mine = ex2(ml.x - ref);
+    L = fmaf(ml.y, mine, L);
+    const int k = min(32, parts - u0);
+    for (int v = 0; v < k; v += B) {
+      float x[B][E];
+#pragma unroll
+      for (int e = 0; e < B; ++e) {
+        const float* src = a.part_o + row_of(u0 + min(v + e, k - 1)) * D + lane * E;
+        if constexpr (E == 4) *reinterpret_cast<float4*>(x[e]) = __ldcg(reinterpret_cast<const float4*>(src));
+        else *reinterpret_cast<float2*>(x[e]) = __ldcg(reinterpret_cast<const float2*>(src));
+      }
+#pragma unroll
+      for (int e = 0; e < B; ++e) {
+        const float w = __shfl_sync(0xffffffffu, mine, min(v + e, 31));
+        if (v + e < k)
+#pragma unroll
+          for (int c = 0; c < E; ++c) o[c] = fmaf(x[e][c], w, o[c]);
+      }
     }
   }
+  L = warp_sum(L);
   T* dst = static_cast<T*>(a.out) + seq * a.ob + h * a.oh + j * a.os + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) dst[e] = Ty<T>::from_f(sees ? o[e] / L : 0.f);
