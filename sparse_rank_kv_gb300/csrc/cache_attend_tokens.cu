@@ -83,7 +83,7 @@ struct Ct {
   static constexpr int Most = 227 * 1024 - 128 - Misc;
   static constexpr int NST0 = (Most - QB - 4 * QT) / KB, NST = NST0 > 8 ? 8 : NST0;
   static constexpr int Smem = 128 + QB + 4 * QT + NST * KB + Misc;
-  static_assert(NST >= 2 && !(Two && (NT > 1 || Copies > 1)), "tile");
+  static_assert(NST >= 2 && NST % 2 == 0 && !(Two && (NT > 1 || Copies > 1)), "tile");
 };
 
 // ------------------------------------------------------------ tensor core
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&full[i], i & 1 ? 1 : 2);   // K's also waits for the tile's description
       tc::mbar_init(&sempty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -460,6 +460,11 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     for (;; ++it) {
       const int nb = blocks(cur), cnt = tokens(cur);
       if (!warp_wait(&sempty[st], ph)) break;
+      if (lane == 0) tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb * B * D));
+      __syncwarp();
+      const size_t src = static_cast<size_t>(id) * (B * D);
+      if (lane < nb) load(stages + st * C::KB + lane * (B * D), a.c.kc + src);
+      ++copied;
       // (the stage is free: the tile kCtInfo before this one has been described to all and used)
       TileInfo* in = infos + it % kCtInfo;
       if (lane >= nb) ks = vs = 0.f;
@@ -490,12 +495,9 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       __syncwarp();
       if (lane == 0) {
         tc::mbar_arrive(&ifull[it % kCtInfo]);
-        tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb * B * D));
+        tc::mbar_arrive(&full[st]);
       }
       __syncwarp();
-      const size_t src = static_cast<size_t>(id) * (B * D);
-      if (lane < nb) load(stages + st * C::KB + lane * (B * D), a.c.kc + src);
-      ++copied;
       next_stage();
       if (!warp_wait(&sempty[st], ph)) break;
       if (lane == 0) tc::mbar_expect_tx(&full[st], static_cast<uint32_t>(nb * B * D));

@@ -412,3 +412,56 @@ def test_a_speculative_decode_loop():
     assert torch.equal(named.int(), c.refs)
     c.check()
     ref.check()
+
+
+@pytest.mark.parametrize("dtype,d,G,s", [("bf16", 128, 4, 6), ("bf16", 64, 1, 32), ("bf16", 128, 4, 25), ("bf16", 64, 3, 40), ("bf16", 128, 4, 70),
+                                         ("bf16", 64, 8, 33), ("f32", 128, 4, 5), ("f32", 64, 2, 60), ("f32", 128, 1, 300)])
+def test_rings_turned_many_times(dtype, d, G, s):
+    """More than 40 tiles to a CTA, its run over several pairs of different lengths: every ring's turn, parts that several
+    CTAs hold, whole row tiles, in each of the kernel's forms."""
+    lens = [9000, 1, 130, 8704, 4097, 77, 12000, 300]
+    c = cache(8, 8, d, 64, lens, 31)
+    q = queries(8, 8 * G, s, d, dtype, 32)
+    n = [min(s, x) for x in lens]
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+    c.attend_tokens(q, lens=ints(n), out=out, lse=lse)
+    close(out, lse, c, q, n)
+    c.check()
+
+
+def test_threads_on_their_own_streams():
+    """Four host threads at a time, one cache: each call's kernels and workspace are its own."""
+    import threading
+    c = cache(4, 2, 128, 64, [700, 3000, 64, 1500], 33)
+    qs = [queries(4, 8, s, 128, "bf16", 34 + s) for s in (1, 7, 40, 150)]
+    want = [c.attend_tokens(q) for q in qs]
+    torch.cuda.synchronize()
+    got, faults = [None] * 4, []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            for _ in range(20):
+                got[i] = c.attend_tokens(qs[i], stream=st)
+            st.synchronize()
+        except Exception as e:      # noqa: BLE001 (shown below)
+            faults.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not faults
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("s", [4, 40, 200])
+def test_v_scales_far_apart(dtype, s):
+    """Blocks of all-zero values (a scale of 2^-100) and scales over 40 binades beside ordinary ones."""
+    c = cache(1, 2, 64, 16, [640], 35, wide=20, top=0x40)
+    c.v_codes.view(torch.uint8)[c.table[0, :, 5].long()] = 0
+    c.v_scale[c.table[0, :, 5].long()] = 2.0 ** -100
+    run(c, queries(1, 4, s, 64, dtype, 36), scale=0.002)
