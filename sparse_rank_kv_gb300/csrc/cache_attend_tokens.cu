@@ -17,9 +17,9 @@
 // CTA takes an equal run of them: one prompt, ragged batches and few rows over a long cache fill the
 // GPU alike.  A row tile that several CTAs work on is joined by k_tokens_merge.
 //
-// Measured, 32 query and 8 KV heads of 128 in bf16: a prompt of 16,384 tokens 2.21 ms, 995 TFLOP/s (0.51 of a
+// Measured, 32 query and 8 KV heads of 128 in bf16: a prompt of 16,384 tokens 2.23 ms, 986 TFLOP/s (0.51 of a
 // cuBLAS product's rate; the tensor pipe is busy a third of the time at 4096 tokens); 6 tokens over 8 x 131,072
-// 549 us, 3.9 TB/s of codes.  What bounds it: the chain S -> softmax -> P -> O of a stream, 2300 cycles of softmax and 500 of
+// 531 us, 4.05 TB/s of codes.  What bounds it: the chain S -> softmax -> P -> O of a stream, 2300 cycles of softmax and 500 of
 // waits between warps beside 2200 of products for two streams; the shared memory, which the products' operands,
 // the codes and their fp16 forms share; and at a row tile's start and end about 20,000 cycles.
 #include <cuda_fp16.h>
