@@ -309,11 +309,12 @@ k_compact_number(const __grid_constant__ CompactArgs a) {
 __global__ void __launch_bounds__(kPgThreads)
 k_compact_move(const __grid_constant__ CompactArgs a) {
   tc::grid_dep_wait();
-  const int n = *a.count;
+  // (n = -1 where the new pool has too few blocks: all of these are compared as signed numbers)
+  const int n = *a.count, first = blockIdx.x, ctas = gridDim.x;
   // (the next block's id is on its way while one is copied)
-  int id = blockIdx.x < n ? a.list[blockIdx.x] : 0;
-  for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const int next = i + static_cast<int>(gridDim.x) < n ? a.list[i + gridDim.x] : 0;
+  int id = first < n ? a.list[first] : 0;
+  for (int i = first; i < n; i += ctas) {
+    const int next = i + ctas < n ? a.list[i + ctas] : 0;
     copy_codes(a.c, id, a.to, i, a.d, threadIdx.x, kPgThreads);
     id = next;
   }
