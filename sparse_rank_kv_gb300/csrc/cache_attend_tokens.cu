@@ -8,20 +8,20 @@
 // their way (exact: e4m3 has 4 bits and fp16 more range), their scales go to the
 // logits and to p in fp32.  A bf16 query row is exact in fp16 after division by the power
 // of two of its largest entry (entries down to 2^-31 of it, the others to 2^-39 of it); an fp32
-// row, and p beside it, are sums of two fp16 terms (2^-22 of themselves).  p times its V scale, relative to
-// the largest scale so far, has fp16's 11 bits (2^-11 of itself) down to 2^-25 of the largest and is good to 2^-36 of
-// that below: p is at most 2^4 (the running maximum is only raised where a tile
-// passes it by more than 4 in base 2, so that O is rarely rescaled).
+// row, and p times its V scale beside both, are sums of two fp16 terms (2^-22 of themselves).  p's are relative to
+// the largest scale so far and good to 2^-36 of the largest: p is at most 2^4 (the running maximum is only raised where
+// a tile passes it by more than 4 in base 2, so that O is rarely rescaled).  One term of p, 2^-11 of itself, would
+// show in bf16 where values cancel, and took a prompt of 16,384 tokens 2.23 ms in place of 2.44.
 //
 // All tiles (of 128 tokens) that all row tiles see are numbered through, and every
 // CTA takes an equal run of them: one prompt, ragged batches and few rows over a long cache fill the
 // GPU alike.  A row tile that several CTAs work on is joined by k_tokens_merge.
 //
-// Measured, 32 query and 8 KV heads of 128 in bf16: a prompt of 16,384 tokens 2.23 ms, 986 TFLOP/s (0.51 of a
-// cuBLAS product's rate; the tensor pipe is busy a third of the time at 4096 tokens); 6 tokens over 8 x 131,072
-// 531 us, 4.05 TB/s of codes.  What bounds it: the chain S -> softmax -> P -> O of a stream, 2300 cycles of softmax and 500 of
-// waits between warps beside 2200 of products for two streams; the shared memory, which the products' operands,
-// the codes and their fp16 forms share; and at a row tile's start and end about 20,000 cycles.
+// Measured, 32 query and 8 KV heads of 128 in bf16: a prompt of 16,384 tokens 2.44 ms, 903 TFLOP/s (0.46 of a
+// cuBLAS product's rate; the products with V run once for each term of p, and that is counted once); 6 tokens over
+// 8 x 131,072 537 us, 4.0 TB/s of codes.  What bounds it: the chain S -> softmax -> P -> O of a stream (with one term of p 2300
+// cycles of softmax and 500 of waits between warps beside 2200 of products for two streams); the shared memory, which
+// the products' operands, the codes and their fp16 forms share; and at a row tile's start and end about 20,000 cycles.
 #include <cuda_fp16.h>
 
 #include <climits>
@@ -73,17 +73,18 @@ __device__ __forceinline__ int tokens_seen(const TokensArgs& a, int n, int len, 
 // P is zero elsewhere) and has sums of its own.
 template <typename T, int D, bool Two, int Copies>
 struct Ct {
-  static constexpr int NT = sizeof(T) == 2 ? 1 : 2;        // fp16 terms of q and p
+  static constexpr int NQ = sizeof(T) == 2 ? 1 : 2;        // fp16 terms of q
+  static constexpr int NP = 2;                             // and of p
   static constexpr int Rows = (Two ? 256 : 128) / Copies;
   static constexpr int PartRows = Two ? 256 : 128;          // rows of a part, copies and all
   static constexpr int QT = kCtT * D * 2;                   // an operand tile in fp16
-  static constexpr int QB = (Two ? 2 : NT) * QT;
+  static constexpr int QB = (Two ? 2 : NQ) * QT;
   static constexpr int KB = kCtT * D;                       // codes of K or of V: a stage
   static constexpr int Misc = 2928;
   static constexpr int Most = 227 * 1024 - 128 - Misc;
   static constexpr int NST0 = (Most - QB - 4 * QT) / KB, NST = NST0 > 8 ? 8 : NST0;
   static constexpr int Smem = 128 + QB + 4 * QT + NST * KB + Misc;
-  static_assert(NST >= 2 && NST % 2 == 0 && !(Two && (NT > 1 || Copies > 1)), "tile");
+  static_assert(NST >= 2 && NST % 2 == 0 && !(Two && (NQ > 1 || Copies > 1)), "tile");
 };
 
 // ------------------------------------------------------------ tensor core
@@ -117,6 +118,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {   // 2^-22 relative; results below 2^-126 are 0
@@ -133,6 +139,43 @@ __device__ __forceinline__ float lg2(float x) {   // of a normal number: within 
   float r;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// Two numbers as a pair, each rounded as by itself
+__device__ __forceinline__ unsigned long long pair_of(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 of_pair(unsigned long long a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)), "l"(pair_of(c)));
+  return of_pair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)));
+  return of_pair(r);
+}
+// The two fp16 terms of two numbers: each to the nearest, then what it leaves over (exact in fp32; -1 times the fp16
+// number as it is, in place of two conversions back and two sums: a prompt of 16,384 2.63 -> 2.44 ms).
+__device__ __forceinline__ void terms2(float2 p, uint32_t* first, uint32_t* rest) {
+  const __half2 z = __floats2half2_rn(p.x, p.y);
+  *first = *reinterpret_cast<const uint32_t*>(&z);
+  float x, y;
+  asm("{\n\t.reg .b16 l, h, m;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "mov.b16 m, 0xBC00;\n\t"
+      "fma.rn.f32.f16 %0, l, m, %3;\n\t"
+      "fma.rn.f32.f16 %1, h, m, %4;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "r"(*first), "f"(p.x), "f"(p.y));
+  const __half2 w = __floats2half2_rn(x, y);
+  *rest = *reinterpret_cast<const uint32_t*>(&w);
 }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
@@ -563,10 +606,10 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
           const uint64_t d0 = dk + (i & 1) * (C::QT / 16), q0 = dq + (Two ? x : 0) * (C::QT / 16);
           const uint32_t tS = tmem + x * kCtT;
 #pragma unroll
-          for (int t = C::NT - 1; t >= 0; --t)   // (the small terms first)
+          for (int t = C::NQ - 1; t >= 0; --t)   // (the small terms first)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              tc::mma_bf16(tS, q0 + t * (C::QT / 16) + k * 256, d0 + k * 256, idesc_f16(kCtT), t < C::NT - 1 || k > 0);
+              tc::mma_bf16(tS, q0 + t * (C::QT / 16) + k * 256, d0 + k * 256, idesc_f16(kCtT), t < C::NQ - 1 || k > 0);
           tc::mma_commit(&sfull[x]);
           if (!Two || x == 1) tc::mma_commit(&kempty[i & 1]);
           flags_p[x] = flags_s;
@@ -581,7 +624,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         const uint64_t d0 = dv + (i & 1) * (C::QT / 16);
         const uint32_t tS = tmem + x * kCtT, tO = tmem + 2 * kCtT + x * D;
 #pragma unroll
-        for (int t = 0; t < C::NT; ++t)
+        for (int t = 0; t < C::NP; ++t)
 #pragma unroll
           for (int k = 0; k < kCtT / 16; ++k)
             mma_f16_ts(tO, tS + k / 2 * 32 + k % 2 * 8 + t * 16, d0 + k * (2 * D), idesc_f16(D), !(flags & kSFirst) || t + k > 0);
@@ -756,14 +799,14 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         for (int u = 0; u < N / 4; ++u) {
           // a piece of fp32 is half a piece of the operand
           const int at = (u * 4 + (lane >> 3)) * V;   // its first element
-          uint32_t w[C::NT][V / 2];
+          uint32_t w[C::NQ][V / 2];
 #pragma unroll
           for (int e = 0; e < V; e += 2) {
             float y0 = Ty<T>::to_f(reinterpret_cast<const T*>(&raw[u])[e]) * down;
             float y1 = Ty<T>::to_f(reinterpret_cast<const T*>(&raw[u])[e + 1]) * down;
             if (bad) y0 = y1 = __int_as_float(0x7fffffff);
 #pragma unroll
-            for (int n = 0; n < C::NT; ++n) {
+            for (int n = 0; n < C::NQ; ++n) {
               const __half2 z = __floats2half2_rn(y0, y1);
               w[n][e / 2] = *reinterpret_cast<const uint32_t*>(&z);
               y0 -= __low2float(z);
@@ -771,7 +814,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
             }
           }
 #pragma unroll
-          for (int n = 0; n < C::NT; ++n) {
+          for (int n = 0; n < C::NQ; ++n) {
             unsigned char* d = dst + n * C::QT + (at >> 3) * 2048 + (at & 7) * 2;
             if constexpr (V == 8) *reinterpret_cast<uint4*>(d) = make_uint4(w[n][0], w[n][1], w[n][2], w[n][3]);
             else *reinterpret_cast<uint2*>(d) = make_uint2(w[n][0], w[n][1]);
@@ -816,16 +859,16 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
 #pragma unroll
       for (int c = 0; c < kCtT; c += W)
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n)
+        for (int n = 0; n < C::NP; ++n)
           if (c != col0) tmem_st16(tS + c + 16 * n, zero);
     };
     // x f + off; beside fp32 with what f's rounding leaves (one relative error of all logits otherwise, 3e-7 of p)
     auto exponent = [&](float x, float f, float off) {
       const float y = fmaf(x, f, off);
-      return C::NT > 1 ? fmaf(x * f, a.scale_rest, y) : y;
+      return C::NQ > 1 ? fmaf(x * f, a.scale_rest, y) : y;
     };
     // All tokens seen, scales positive and not too far apart: bf16's V scale v goes into the exponent, w = 2^(x - m + log2 v), and
-    // comes out of the sum of 16 tokens' w again; two and a half instructions an element.
+    // comes out of the sum of 16 tokens' w again; four and a half instructions an element, two of them w's second term.
     auto softmax_plain = [&](const TileInfo& in, bool first) {
       float mt = -INFINITY;
 #pragma unroll 1
@@ -845,36 +888,32 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       const float ref = m == -INFINITY ? 0.f : m, up = exp2i(11 - vexp);
 #pragma unroll 1
       for (int c = 0; c < W; c += 32) {
-        float s[32];
-        tc::tmem_ld32(tS + col0 + c, s);
         const float2 k2 = *reinterpret_cast<const float2*>(in.ks + (col0 + c) / 16);
         const float2 v2 = *reinterpret_cast<const float2*>(in.vs + (col0 + c) / 16);
-        uint32_t w[C::NT][16];
+        float s[32];
+        tc::tmem_ld32(tS + col0 + c, s);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           // (not beside fp32: with the scale's 11 binades the exponent's own rounding would show)
-          constexpr bool Fold = C::NT == 1;
+          constexpr bool Fold = C::NQ == 1;
           const float fg = rowf * (g ? k2.y : k2.x), fv = (g ? v2.y : v2.x) * up, off = Fold ? lg2(fv) - ref : -ref;
           float2 sum = make_float2(0.f, 0.f);
+          uint32_t w[C::NP][8];
 #pragma unroll
-          for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-            float2 p = make_float2(ex2(exponent(s[e], fg, off)), ex2(exponent(s[e + 1], fg, off)));
-            sum.x += p.x;
-            sum.y += p.y;
+          for (int e = 0; e < 16; e += 2) {
+            const float s0 = s[16 * g + e], s1 = s[16 * g + e + 1];
+            const float2 x = Fold ? fma2(make_float2(s0, s1), make_float2(fg, fg), make_float2(off, off))
+                                  : make_float2(exponent(s0, fg, off), exponent(s1, fg, off));
+            float2 p = make_float2(ex2(x.x), ex2(x.y));
+            sum = add2(sum, p);
             if (!Fold) p = make_float2(p.x * fv, p.y * fv);
-#pragma unroll
-            for (int n = 0; n < C::NT; ++n) {
-              const __half2 z = __floats2half2_rn(p.x, p.y);
-              w[n][e / 2] = *reinterpret_cast<const uint32_t*>(&z);
-              p.x -= __low2float(z);
-              p.y -= __high2float(z);
-            }
+            terms2(p, &w[0][e / 2], &w[1][e / 2]);
           }
           l = Fold ? fmaf(sum.x + sum.y, __fdividef(1.f, fv), l) : l + (sum.x + sum.y);
-        }
-        // P of 32 tokens over their own columns of S: 16 columns a term
+          // P of 32 tokens over their own columns of S: 16 columns a term
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n) tmem_st16(tS + col0 + c + 16 * n, w[n]);
+          for (int n = 0; n < C::NP; ++n) tmem_st8(tS + col0 + c + 16 * n + 8 * g, w[n]);
+        }
       }
       if constexpr (Copies > 1) zero_others();
       tmem_wait_st();
@@ -896,7 +935,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       float sum = 0.f;
 #pragma unroll 1
       for (int c = 0; c < W; c += 32) {
-        uint32_t w[C::NT][16];
+        uint32_t w[C::NP][16];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           float s[16];
@@ -912,17 +951,14 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
               sum += p[u];
               p[u] = seen ? p[u] * fv : 0.f;   // (a scale that is no number under a hidden token)
             }
-#pragma unroll
-            for (int n = 0; n < C::NT; ++n) {
-              const __half2 z = __floats2half2_rn(p[0], p[1]);
-              w[n][8 * g + e / 2] = *reinterpret_cast<const uint32_t*>(&z);
-              p[0] -= __low2float(z);
-              p[1] -= __high2float(z);
-            }
+            terms2(make_float2(p[0], p[1]), &w[0][8 * g + e / 2], &w[1][8 * g + e / 2]);
           }
+          if (!(fabsf(fv) < INFINITY))   // an infinite scale's p is its first term
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[1][8 * g + e] = 0;
         }
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n) tmem_st16(tS + col0 + c + 16 * n, w[n]);
+        for (int n = 0; n < C::NP; ++n) tmem_st16(tS + col0 + c + 16 * n, w[n]);
       }
       if constexpr (Copies > 1) zero_others();
       l += sum;

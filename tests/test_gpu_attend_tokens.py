@@ -465,3 +465,48 @@ def test_v_scales_far_apart(dtype, s):
     c.v_codes.view(torch.uint8)[c.table[0, :, 5].long()] = 0
     c.v_scale[c.table[0, :, 5].long()] = 2.0 ** -100
     run(c, queries(1, 4, s, 64, dtype, 36), scale=0.002)
+
+
+@pytest.mark.parametrize("s,G", [(1, 1), (5, 4), (40, 1), (30, 4), (300, 1), (70, 8)])
+@pytest.mark.parametrize("wide", [0, 3])
+def test_values_that_cancel(s, G, wide):
+    """bf16, one row for all queries, and values chosen for its p so that sum p v is next to nothing beside
+    M = sum p |v|: p's own error shows, whatever bf16 keeps of the result.
+
+    The allowance is the one above with p (and its V scale) held to 2^-20 in place of 2^-11, and 2^-19 for its exponent,
+    which the scale's 11 binades take to 32 (two roundings of 2^-24 32, log2 of the scale 2^-22): 2^-15.7 M in
+    all at the logits here (at most 6).  2^-12, as one fp16 of p is off by, is 10 times that."""
+    d, block, n = 128, 16, 200
+    c = cache(1, 1, d, block, [n], 50, wide=wide)
+    r = gen(51)
+    ids = c.table[0, 0, :-(-n // block)].long()
+    # keys: one code in all dimensions, so that |q . k| is the sum of its magnitudes, too; logits over +-6
+    row = torch.randint(0x28, 0x40, (len(ids), 1, 1, block, 1), generator=r, device="cuda", dtype=torch.uint8)
+    row |= torch.randint(0, 2, row.shape, generator=r, device="cuda", dtype=torch.uint8) << 7
+    c.k_codes.view(torch.uint8)[ids] = row.view(len(ids), block // 8, 1, 8, 1).expand(-1, -1, d // 16, 8, 16)
+    c.k_scale[ids] = 1.0
+    q = torch.full((1, 1, 1, d), 0.75, device="cuda").bfloat16()
+    scale = 6 / (0.75 * d * 1.875)
+    k, v, vs = values(c, 0, 0)
+    x = scale * (q[0, 0].double() @ k.T)[0]
+    p = torch.softmax(x, 0)
+    # values of random magnitude, each of the sign that takes the sum so far towards 0, the largest p first
+    code = torch.randint(0x30, 0x40, (n, d), generator=r, device="cuda", dtype=torch.uint8)
+    size = code.view(torch.float8_e4m3fn).double() * vs[:, None]
+    total, sign = torch.zeros(d, dtype=torch.float64, device="cuda"), torch.zeros(n, d, dtype=torch.uint8, device="cuda")
+    for t in (p[:, None] * size).amax(1).argsort(descending=True).tolist():
+        sign[t] = (total > 0).to(torch.uint8)
+        total += torch.where(total > 0, -1.0, 1.0) * p[t] * size[t]
+    full = torch.zeros(len(ids) * block, d, dtype=torch.uint8, device="cuda")
+    full[:n] = code | sign << 7
+    c.v_codes.view(torch.uint8)[ids] = full.view(len(ids), block // 16, 16, d).transpose(2, 3)
+    k, v, vs = values(c, 0, 0)
+    ref, mag = p @ v, p @ v.abs()
+    assert float((ref.abs() / mag).max()) < 2.0 ** -8
+    got = c.attend_tokens(q.expand(1, G, s, d), causal=False, scale=scale)
+    dp = (2.0 ** -21 + 3 * U + 2 * U * 1.45) * 6 + 2.0 ** -22 + 2 * U * 6 * 1.45 + 66 * U
+    floor = n * 2.0 ** -36 * 448 * p.max() * vs.max()
+    tol = 2.0 ** -8 * ref.abs() + (2 * (dp + 2.0 ** -20 + 2.0 ** -19) + 2.0 ** -21 + 2 * U) * mag + floor
+    err = (got.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    c.check()
