@@ -451,7 +451,8 @@ size_t shadowkv_cache_attend_tokens_workspace(const shadowkv_cache* c, int h_q, 
  * queries that see it and no others; a query with an entry that is not finite gives NaN.
  * The products run on fp16 operands, accumulated in fp32: codes exactly; a bf16 query exactly from 2^-31 of its row's
  * largest entry on and to 2^-39 of that below, p times its V scale to 2^-20 of itself (beside its logit's own rounding to 24
- * bits) and 2^-36 of the largest p times the largest V scale; f32: q and p to 2^-22 of themselves, with the same floors.
+ * bits) and 2^-36 of the largest p times the largest V scale among the tokens that the query sees (each the largest by itself);
+ * f32: q and p to 2^-22 of themselves, with the same floors.
  * Results do not depend on timing.
  * s h_q / h_kv <= 2^24 (SKV_ERR_UNSUPPORTED).  s = 0 does nothing.
  * Asynchronous on `stream`; runs on the current device.

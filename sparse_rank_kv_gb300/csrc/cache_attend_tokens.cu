@@ -24,7 +24,6 @@
 // the products' operands, the codes and their fp16 forms share; and at a row tile's start and end about 20,000 cycles.
 #include <cuda_fp16.h>
 
-#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -177,6 +176,8 @@ __device__ __forceinline__ void terms2(float2 p, uint32_t* first, uint32_t* rest
   const __half2 w = __floats2half2_rn(x, y);
   *rest = *reinterpret_cast<const uint32_t*>(&w);
 }
+// e >= -110 with x < 2^e, of a largest V scale
+__device__ __forceinline__ int scale_exp(float x) { return max(static_cast<int>(__float_as_uint(x) >> 23) - 126, -110); }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
 // ------------------------------------------------------------ the tiles in order
@@ -322,7 +323,7 @@ enum : int {
   kWhole = 16384    // this CTA has all of the row tile
 };
 struct TileInfo {
-  int tile, flags, vexp, vlow;   // V scales are below 2^vexp, and 2^vlow or more
+  int tile, flags, vexp, vlow;   // all V scales are below 2^vexp, and 2^vlow or more
   float ks[8], vs[8];            // of every 16 tokens
   int pair, q, n, len;
   int turn, end, pad[2];         // number of the row tile in this CTA; of its last tile here
@@ -402,9 +403,9 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
   volatile int* s_nan = reinterpret_cast<volatile int*>(misc + 360);   // [2]: V's tile has NaN
   int* s_scan = reinterpret_cast<int*>(misc + 448);      // [32], before the tiles are described
   TileInfo* infos = reinterpret_cast<TileInfo*>(misc + 448);
-  float* sqs = reinterpret_cast<float*>(misc + 1344);    // [128] rows' factors (one row tile)
+  float* sqs = reinterpret_cast<float*>(misc + 1344);    // [128] rows' factors (one row tile), then stream 1's vexp
   float2* s_ml = reinterpret_cast<float2*>(misc + 1856); // [128] stream 1's maxima and sums
-  int2* s_join = reinterpret_cast<int2*>(misc + 2880);   // [4 warps] its vexp, and whether NaN is recorded
+  int2* s_join = reinterpret_cast<int2*>(misc + 2880);   // [4 warps] whether it had tiles, and whether NaN is recorded
   // (the warps wait for one another at these, never at named barriers: a wait that gives up must not leave others behind)
   uint64_t* vote_bar = reinterpret_cast<uint64_t*>(misc + 2912);             // the conversion of V
   uint64_t* parts_bar = vote_bar + 1;                                        // stream 0, its copies' parts
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         in->turn = turn;
         in->end = seg_end - 1;
         in->vlow = static_cast<int>(__float_as_uint(least) >> 23) - 127;
-        in->vexp = max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -110);
+        in->vexp = scale_exp(top);
       }
       __syncwarp();
       if (lane == 0) {
@@ -831,13 +832,15 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
     // the tile, instruction fetch bound them).  General: tokens the row does not see, scales of any kind.
     constexpr int W = kCtT / Copies;            // columns of this warp
     const int col0 = Copies > 1 ? wq * W : 0;
-    // The references m and 2^vexp of a tile whose largest logit is mt; O and l follow.  m is a whole number, so that what
-    // was formed by one reference is brought to another's exactly, here and where parts are joined.
-    auto raise = [&](const TileInfo& in, bool first, float mt) {
-      const int v2 = first ? in.vexp : max(vexp, in.vexp);
+    // The references m and 2^vexp of a tile whose largest logit is mt and whose V scales that the row sees are below 2^vt; O and
+    // l follow.  m is a whole number, so that what was formed by one reference is brought to another's exactly, here
+    // and where parts are joined.  (Rows that do not see all of a tile have vt's of their own: by a hidden token's scale
+    // theirs would lose bits.  Such tiles are a row tile's last ones.)
+    auto raise = [&](int vt, bool first, float mt) {
+      const int v2 = first ? vt : max(vexp, vt);
       if (first) {
         m = floorf(mt);
-      } else if (__any_sync(0xffffffffu, mt > m + 4.f) || v2 > vexp) {
+      } else if (__any_sync(0xffffffffu, mt > m + 4.f || v2 > vexp)) {
         const float m2 = fmaxf(m, floorf(mt)), al = m2 == -INFINITY ? 1.f : exp2i(static_cast<int>(fmaxf(m - m2, -126.f)));
         m = m2;
         l *= al;
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         }
         mt = max3(mt, fmaxf(t0, s[15]) * (rowf * k2.x), fmaxf(t1, s[31]) * (rowf * k2.y));
       }
-      raise(in, first, mt);
+      raise(in.vexp, first, mt);
       const float ref = m == -INFINITY ? 0.f : m, up = exp2i(11 - vexp);
 #pragma unroll 1
       for (int c = 0; c < W; c += 32) {
@@ -930,7 +933,17 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
 #pragma unroll
         for (int e = 0; e < 16; ++e) mt = fmaxf(mt, c + e < rem ? s[e] * fg : -INFINITY);
       }
-      raise(in, first, mt);
+      int vt = in.vexp;
+      if (in.flags & kMixed) {   // of the scales that the row sees
+        float top = 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float v = fabsf(in.vs[g]);
+          if (16 * g < rem + col0 && v < INFINITY) top = fmaxf(top, v);
+        }
+        vt = scale_exp(top);
+      }
+      raise(vt, first, mt);
       const float ref = m == -INFINITY ? 0.f : m, up = exp2i(11 - vexp);
       float sum = 0.f;
 #pragma unroll 1
@@ -1084,19 +1097,22 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         if (nan_any)
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) nan_masks[(2 * 128 + row) * 4 + e] = nanrow[e];
-        if (lane == 0) s_join[wq] = make_int2(used ? vexp : INT_MIN, nan_any);
+        sqs[row] = __int_as_float(vexp);   // (this row's factor has been read, and is written anew after jfull)
+        if (lane == 0) s_join[wq] = make_int2(used, nan_any);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(jfull);
         continue;
       }
       float m1 = -INFINITY, l1 = 0.f;
-      int vexp1 = INT_MIN;
+      int vexp1 = 0;
+      bool had1 = false;   // stream 1 had tiles of it
       if (!Two) {
         if (!warp_wait(jfull, turn)) break;
         const float2 ml = s_ml[row];
         const int2 sj = s_join[wq];
-        vexp1 = sj.x;
-        if (vexp1 != INT_MIN) {
+        had1 = sj.x;
+        if (had1) {
+          vexp1 = __float_as_int(sqs[row]);
           m1 = ml.x;
           l1 = ml.y;
           if (!warp_wait(&ofin[1], fin1++)) break;
@@ -1111,10 +1127,10 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       tc::fence_after();
       if (active) {
         const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
-        float r0 = used ? ex2(m - ref) : 0.f, r1 = vexp1 != INT_MIN ? ex2(m1 - ref) : 0.f;
-        const float sum = (used ? l * r0 : 0.f) + (vexp1 != INT_MIN ? l1 * r1 : 0.f);
+        float r0 = used ? ex2(m - ref) : 0.f, r1 = had1 ? ex2(m1 - ref) : 0.f;
+        const float sum = (used ? l * r0 : 0.f) + (had1 ? l1 * r1 : 0.f);
         r0 *= exp2i(used ? vexp - 11 : 0);
-        r1 *= exp2i(vexp1 != INT_MIN ? vexp1 - 11 : 0);
+        r1 *= exp2i(had1 ? vexp1 - 11 : 0);
         const bool whole = Copies == 1 && (flags & kWhole);   // (copies are joined below)
         const float inv = whole ? 1.f / sum : 1.f;
         const size_t part = static_cast<size_t>(2 * cta + (turn > 0)) * C::PartRows + (Two ? x * kCtT : 0) + row;
@@ -1127,7 +1143,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = 0.f;
           }
-          if (!Two && vexp1 != INT_MIN) {
+          if (!Two && had1) {
             float z[16];
             tc::tmem_ld16(tO0 + D + c, z);
 #pragma unroll

@@ -510,3 +510,24 @@ def test_values_that_cancel(s, G, wide):
     err = (got.double() - ref).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
     c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("s,G", [(20, 1), (20, 4), (20, 8), (100, 4), (300, 1)])
+@pytest.mark.parametrize("up", [30, 40, 100])
+def test_a_hidden_block_of_large_values_leaves_earlier_queries_alone(dtype, s, G, up):
+    """The last block's V scale is 2^up times the others'.  The queries that do not see it are those of a cache without it:
+    the same definition, with the allowance of the scales that they see (`close` knows no others there)."""
+    n, block = 330 + s, 16
+    c = cache(2, 2, 128, block, [n, n], 60)
+    last = c.table[:, :, (n - 1) // block].long().flatten()
+    c.v_scale[last] = 2.0 ** (up - 7)
+    m = s - ((n - 1) % block + 1)                                     # queries before the last block's first token
+    assert 0 < m < s
+    q = queries(2, 2 * G, s, 128, dtype, 61)
+    lse = torch.empty(2, 2 * G, s, device="cuda")
+    got = c.attend_tokens(q, lse=lse)
+    short = binding.BlockCache(c.k_codes, c.v_codes, c.k_scale, c.v_scale, c.table, c.n_tok - (s - m))
+    close(got[:, :, :m], lse[:, :, :m], short, q[:, :, :m])
+    close(got, lse, c, q)                                              # and those that see it
+    c.check()
