@@ -347,7 +347,8 @@ skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, const shado
  * (the tensor core's K-major operand order for K, and for V transposed).  The
  * value of a code is the e4m3 number times the block's k_scale or v_scale.
  * A scale written by the library is 2^e with the smallest e >= -100 for which
- * max |x| <= 448 2^e over the block's finite entries.
+ * max |x| <= 448 2^e over the block's finite entries, those that shadowkv_cache_truncate has taken off
+ * since the block's first token among them.
  *
  * A kernel that meets a table entry outside the pool or a token count outside
  * 0..max_blocks block records it in *status (see shadowkv_cache_check).  Attention reads
@@ -531,6 +532,10 @@ skv_status shadowkv_cache_reserve(const shadowkv_cache* c, int32_t* refs, int s,
  *   refs  : NULL for a cache whose pool is not shared: its tables stay as they are.
  *   drop  : device int32, b (a negative one counts as 0 and is recorded); NULL: none, which
  *           gives back what eviction and unused reservations hold.
+ * A block that keeps some of its tokens stays as the others left it: with the scales that a large one of them has
+ * raised (its tokens' entries are then off by up to 2^-10 of the new scale, and later tokens are held by it), and with the weight that it
+ * gathered.  Drafts come off without a trace where the sequence was forked before their append: shadowkv_cache_share to a spare
+ * sequence, whose partly filled block shadowkv_cache_reserve then copies, and back.
  * Asynchronous on `stream`; runs on the current device.
  */
 skv_status shadowkv_cache_truncate(const shadowkv_cache* c, int32_t* refs, const int32_t* drop, void* stream);

@@ -772,7 +772,8 @@ class BlockCache:
 
     def truncate(self, drop: Optional[torch.Tensor] = None, stream=None) -> None:
         """Takes drop[i] tokens (drop (b,) int32, default none) off the end of every sequence i; blocks past the
-        tokens go back to a shared pool."""
+        tokens go back to a shared pool.  A block that keeps some of its tokens keeps the scales and the
+        weight that the others gave it; share() to a spare sequence before their append, and back, leaves no trace."""
         dp = _dense(drop, "drop", (self.b,), torch.int32, self.device)
         _call((_step or _step_calls())["cache_truncate"], self.n_tok, stream, self._desc,
               None if self.refs is None else self.refs.data_ptr(), dp)

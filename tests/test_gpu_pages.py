@@ -310,3 +310,59 @@ def test_refusals():
     plain.truncate(ints([3, 30]))                            # a cache of its own pool: counts and weights alone
     assert plain.n_tok.tolist() == [[17], [0]] and torch.equal(plain.table, table)
     plain.check()
+
+
+def held(c, i):
+    """Keys and values of sequence i in 64 bits, each (h, n, d), and the scale of each token's block (h, n, 1)."""
+    n, out = int(c.n_tok[i, 0]), []
+    ids = c.table[i, :, :-(-n // c.block)].long()
+    for codes, scale, shape in ((c.k_codes, c.k_scale, (0, 1, 2, 4, 3, 5)), (c.v_codes, c.v_scale, (0, 1, 2, 4, 3))):
+        x = codes.view(torch.uint8)[ids].view(torch.float8_e4m3fn).double().permute(*shape)
+        x = x.reshape(c.h_kv, -1, c.d)[:, :n]
+        s = scale[ids].double().repeat_interleave(c.block, 1)[:, :n, None]
+        out += [x * s, s]
+    return out
+
+
+def test_a_rejected_draft_leaves_no_more_than_its_scale():
+    """A draft 2^12 times as large as the tokens beside it in a block, taken off again.  The scale stays: the smallest power
+    of two with which 448 covers the draft; the other entries are off by half a step of e4m3 below its normal range, 2^-10
+    of that scale, at most, and exact where the block was not touched.  Then the same with a fork before the
+    drafts: every bit is as it was."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    h, d, block = 2, 128, 16
+    tok = lambda n, up=1.0: (up * torch.randn(2, h, n, d, generator=g, device="cuda")).bfloat16()  # noqa: E731
+    c = binding.BlockCache.pooled(2, h, d, 6, 30, block=block)
+    only = lambda n: ints([n, 0])  # noqa: E731
+    c.append(tok(21), tok(21), c.reserve(21, only(21)))
+    c.weight[0, :, :2] = 0.5
+    before = [x.clone() for x in held(c, 0)]
+    k, v = tok(2, 4096.0), tok(2, 4096.0)
+    start = {n: getattr(c, n).clone() for n in ("table", "n_tok", "weight", "refs", "k_codes", "v_codes", "k_scale", "v_scale")}
+
+    c.append(k, v, c.reserve(2, only(2)))
+    c.truncate(only(2))
+    after = held(c, 0)
+    for x, new, s_old, s_new, big in ((before[0], after[0], before[1], after[1], k), (before[2], after[2], before[3], after[3], v)):
+        assert torch.equal(x[:, :block], new[:, :block]) and torch.equal(s_old[:, :block], s_new[:, :block])
+        most = big[0].double().abs().amax((1, 2))[:, None, None]
+        s = s_new[:, block:]
+        assert bool((s > s_old[:, block:]).all()) and bool((most <= 448 * s).all()) and bool((most > 224 * s).all())
+        err = (new[:, block:] - x[:, block:]).abs()
+        assert bool((err <= 2.0 ** -10 * s).all()) and bool((err > 0).any())
+    c.append(k * 0 + 1, v * 0 + 1, c.reserve(2, only(2)))          # later tokens are held by that scale
+    assert bool((held(c, 0)[1][:, -1] == after[1][:, -1]).all())
+
+    for n, t in start.items():
+        getattr(c, n).copy_(t)
+    there, back = ints([0]), ints([1])
+    c.share(there, back)
+    c.append(k, v, c.reserve(2, only(2)))
+    c.share(back, there)                                           # the drafts are rejected
+    c.truncate(ints([0, 21]))
+    for x, y in zip(before, held(c, 0)):
+        assert torch.equal(x, y)
+    assert torch.equal(c.weight[0], start["weight"][0]) and c.n_tok.tolist() == [[21, 21], [0, 0]]
+    same(c, model(c))
+    c.check()
