@@ -452,7 +452,7 @@ k_verify_pick(const __grid_constant__ VerifyArgs a, const __grid_constant__ Veri
   }
   // the first token whose running sum passes sample times the total
   const float r = a.sample[seq];
-  const unsigned long long at = min(times(r, total), total - 1);
+  const unsigned long long at = times(r >= 1.f ? 0x1.fffffep-1f : r, total);   // below the total
   __syncthreads();
   // the chunk (warp 0 of the CTA that has it), then the token in it
   if (warp == 0) {

@@ -200,3 +200,15 @@ def test_verify_refusals():
     empty = made(0, 2, 64, "f32", 1)
     t, a = binding.verify_drafts(*empty)
     assert t.shape == (0, 3) and a.shape == (0,)
+
+
+@pytest.mark.parametrize("sampled", [True, False])
+def test_a_sample_of_one_or_more_is_the_largest_below(sampled):
+    """A last token of weight e^-20, 2^-28.9: past 1 - 2^-24 of the total, where no number in [0, 1) falls."""
+    l = torch.zeros(5, 2, 3, device="cuda")
+    l[:, :, 0], l[:, :, 2] = -30.0, -20.0
+    r = torch.tensor([1.0, 2.5, float("inf"), 1 - 2.0 ** -24, 0.0], device="cuda")
+    d, u = ints([[0]] * 5), torch.full((5, 1), 0.5, device="cuda")
+    q = torch.tensor([1.0, 0.0, 0.0], device="cuda").expand(5, 1, 3) if sampled else None
+    tokens, acc = binding.verify_drafts(l, d, q, u, r)
+    assert acc.tolist() == [0] * 5 and tokens[:, 0].tolist() == [1] * 5
