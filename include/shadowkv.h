@@ -595,7 +595,8 @@ size_t shadowkv_verify_workspace(const shadowkv_verify_params* p);
  *   work   : device, 256-byte aligned, at least shadowkv_verify_workspace bytes; its contents before
  *            and after mean nothing.
  * The sampled row's weights exp((l - max) / T) are whole numbers of 2^-43, each within 2^-37 of
- * itself, and their sums exact; acceptance is decided to 2^-36 of its border.  Results do not depend on
+ * itself and 2^-44 (half a unit: a token less likely than 2^-44 times the likeliest has no weight), and their sums exact.
+ * Acceptance is decided to 2^-36 + vocab 2^-44 of its border, the sampled token to as much of the total.  Results do not depend on
  * timing.  b (s + 1) <= 65535 (SKV_ERR_UNSUPPORTED).
  * b = 0 does nothing.  Asynchronous on `stream`; runs on the current device.
  */

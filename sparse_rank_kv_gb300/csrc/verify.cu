@@ -4,9 +4,10 @@
 //
 // Which token a number falls on is decided next to borders (a vocabulary of 2^17 has as
 // many), so the weights w_v = exp((l_v - max) / T) of the row that is sampled from are
-// whole numbers: 2^43 w_v, each within 2^-37 of itself, by a table of 2^(j/64) and a
+// whole numbers: 2^43 w_v, each within 2^-37 of itself and half a unit, by a table of 2^(j/64) and a
 // short polynomial (Tang, "Table-driven implementation of the exponential function",
-// 1989) on pairs of floats.  Their sums are exact and do not depend on the order.  The rows'
+// 1989) on pairs of floats.  Their sums are exact and do not depend on the order; the half units of a long flat tail add
+// up to vocab 2^-44 of a total at most (2^-27 of 131,072 tokens).  The rows'
 // sums for the acceptance tests are fp32 and good to 2^-13; a test that close to its
 // border (one in 5,000) is decided again with the row's whole-number sum.
 //

@@ -212,3 +212,45 @@ def test_a_sample_of_one_or_more_is_the_largest_below(sampled):
     q = torch.tensor([1.0, 0.0, 0.0], device="cuda").expand(5, 1, 3) if sampled else None
     tokens, acc = binding.verify_drafts(l, d, q, u, r)
     assert acc.tolist() == [0] * 5 and tokens[:, 0].tolist() == [1] * 5
+
+
+@pytest.mark.parametrize("v", [5000, 1 << 17, 1 << 19])
+@pytest.mark.parametrize("tail", [27.3, 28.0, 30.2, 30.6])
+def test_verify_of_a_peak_over_a_flat_tail(v, tail):
+    """Two likely tokens and v - 2 equal ones e^-tail as likely: weights of few units, or none, whose errors all have one
+    sign.  A weight is off by 2^-37 of itself and by 2^-44, the total (at least 1) by 2^-37 of itself and v 2^-44: u q z < p
+    is decided right where u q and p are farther apart than B = 2^-36 + v 2^-44 of them, and the sampled token's
+    place is right to B of the total, twice (its own sum and the total)."""
+    bound = 2.0 ** -36 + v * 2.0 ** -44
+    b = 16
+    l = torch.full((b, 2, v), -tail, device="cuda")
+    at = 1234
+    l[:, :, at] = l[:, :, at + 7] = 0.0
+    z = 2 + (v - 2) * float(np.exp(-np.float64(np.float32(tail))))
+    p = 1 / z
+    # u q next to p, from both sides: products of two floats, whose last bits are as fine as 2^-48
+    g = np.random.default_rng(7)
+    uq = []
+    while len(uq) < b:
+        q = np.float32(g.uniform(0.6, 0.95))
+        u = np.float32(p / float(q))
+        if 1.01 * bound < abs(float(u) * float(q) - p) / p < 16 * bound:
+            uq.append((u, q))
+    u, q = torch.tensor([[x[0]] for x in uq], device="cuda"), torch.zeros(b, 1, v, device="cuda")
+    q[:, 0, at] = torch.tensor([x[1] for x in uq], device="cuda")
+    r = torch.tensor(1 - g.integers(1, 9, b) * 2.0 ** -24, dtype=torch.float32, device="cuda")
+    r[::3] = torch.rand(len(r[::3]), device="cuda")
+    d = torch.full((b, 1), at, dtype=torch.int32, device="cuda")
+    want = [float(x) * float(y) < p for x, y in uq]
+    tokens, acc = binding.verify_drafts(l, d, q, u, r)
+    assert acc.tolist() == [int(x) for x in want] and 0 < sum(want) < b
+    w = np.full(v, np.exp(-np.float64(np.float32(tail))))
+    for i in range(b):
+        rest = w.copy()
+        rest[at] = rest[at + 7] = 1.0
+        rest /= z
+        if not want[i]:
+            rest = np.maximum(rest - q[i, 0].double().cpu().numpy(), 0)
+        cum = np.cumsum(rest)
+        k, place = int(tokens[i, int(acc[i])]), float(r[i]) * cum[-1]
+        assert (cum[k - 1] if k else 0.0) - 2 * bound <= place <= cum[k] + 2 * bound
