@@ -755,6 +755,8 @@ class BlockCache:
         writes to, and partly filled ones in any case, become the pairs' own, free ones or copies.  Returns granted (b,) int32: lens
         where the pool had the blocks, else 0, to append with."""
         refs = self._counts()
+        if s >= 1 << 31:    # (it goes on as 32 bits)
+            raise ValueError(f"s must be below 2^31, got {s}")
         lp = _dense(lens, "lens", (self.b,), torch.int32, self.device)
         if self.device.type != "cuda":
             raise ValueError(f"tensors must be on a CUDA device, got {self.device}")

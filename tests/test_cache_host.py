@@ -305,3 +305,9 @@ def test_attend_tokens_of_nothing_is_no_call(lib):
     assert lib.shadowkv_cache_attend_tokens_workspace(desc(d=96), 32, 4) == 0
     assert lib.shadowkv_cache_attend_tokens_workspace(desc(), 12, 4) == 0
     assert lib.shadowkv_cache_attend_tokens_workspace(desc(), 32, -1) == 0
+
+
+def test_reserve_of_more_than_32_bits_is_refused():
+    c = binding.BlockCache.pooled(1, 2, 64, 3, 6, block=16, device="cpu")
+    with pytest.raises(ValueError, match="2\\^31"):
+        c.reserve((1 << 32) + 5)
