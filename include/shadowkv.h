@@ -338,7 +338,8 @@ skv_status shadowkv_qk_norm_rope(const shadowkv_norm_rope_params* p, const shado
  *
  * Blocks live in a pool.  Pair (i, g) = sequence i, KV head g holds
  * n_tok[i, g] tokens: token t is row t % block of the pool block
- * table[i, g, t / block].  Every table entry, also past the tokens held, must
+ * table[i, g, t / block].  Every table entry, also past the tokens held (there, in a pool that
+ * sequences share, it may be -1: see below), must
  * name a pool block (0 <= id < n_pool) and no pool block that a pair appends to may be
  * named twice; entry c of pair p = p max_blocks + c does for a pool of
  * b h_kv max_blocks blocks.  Codes inside a pool block:

@@ -13,9 +13,9 @@
 // a tile passes it by more than 4 in base 2, so that O is rarely rescaled).  One term of p, 2^-11 of itself, would
 // show in bf16 where values cancel, and took a prompt of 16,384 tokens 2.23 ms in place of 2.44.
 //
-// All tiles (of 128 tokens) that all row tiles see are numbered through, and every
-// CTA takes an equal run of them: one prompt, ragged batches and few rows over a long cache fill the
-// GPU alike.  A row tile that several CTAs work on is joined by k_tokens_merge.
+// All row tiles and the tiles (of 128 tokens) that each sees are numbered through in units, five for a row tile's start
+// and end and one for each of its tiles, and every CTA takes an equal run of units: one prompt, ragged batches and few rows over
+// a long cache fill the GPU alike.  A row tile that several CTAs work on is joined by k_tokens_merge.
 //
 // Measured, 32 query and 8 KV heads of 128 in bf16: a prompt of 16,384 tokens 2.44 ms, 903 TFLOP/s (0.46 of a
 // cuBLAS product's rate; the products with V run once for each term of p, and that is counted once); 6 tokens over

@@ -503,11 +503,13 @@ k_verify_pick(const __grid_constant__ VerifyArgs a, const __grid_constant__ Veri
   }
 }
 
-// Logits per CTA of k_verify_rows / 2048: four, where that still gives every SM two CTAs.
+// Logits per CTA of k_verify_rows / 2048: four, where that still gives every SM of a GB300 two CTAs.  (Not asked of the device: the
+// workspace's size goes by it, which is known without one.)
+constexpr int kGbSms = 152;
 static int verify_vectors(const shadowkv_verify_params& p) {
   const long long rows = static_cast<long long>(p.b) * (p.s + 1);
   for (int n = 4; n > 1; n /= 2)
-    if (rows * ((p.vocab + 2048 * n - 1) / (2048 * n)) >= 2 * 152) return n;
+    if (rows * ((p.vocab + 2048 * n - 1) / (2048 * n)) >= 2 * kGbSms) return n;
   return 1;
 }
 static int verify_splits(const shadowkv_verify_params& p) {

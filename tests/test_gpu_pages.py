@@ -366,3 +366,18 @@ def test_a_rejected_draft_leaves_no_more_than_its_scale():
     assert torch.equal(c.weight[0], start["weight"][0]) and c.n_tok.tolist() == [[21, 21], [0, 0]]
     same(c, model(c))
     c.check()
+
+
+def test_reserve_may_write_what_it_grants_over_the_lengths():
+    """granted is lens itself: what one of its own gets, sequences without room, past the table and clamped ones among them."""
+    for n_pool in (20, 23, 80):
+        lens = [20, 300, 3, 16, 40]
+        got = []
+        for own in (False, True):
+            c = pooled(5, 2, 64, 16, 6, n_pool, [16, 32, 40, 16, 8], 3)
+            x = ints(lens)
+            got.append((c.reserve(200, x, granted=None if own else x).tolist(), c.table.tolist(), c.refs.tolist()))
+            with pytest.raises(binding.ShadowKVError, match="DEVICE_CHECK"):
+                c.check()
+        assert got[0] == got[1]
+        assert got[0][0][1] == 0 and got[0][0][2] == 3
