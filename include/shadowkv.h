@@ -449,7 +449,7 @@ size_t shadowkv_cache_attend_tokens_workspace(const shadowkv_cache* c, int h_q, 
  *   work  : device, 256-byte aligned, at least shadowkv_cache_attend_tokens_workspace bytes; its
  *           contents before and after mean nothing.  Calls that may run at the same time need
  *           workspaces of their own.
- * A query that sees no token gives zeros and an lse of -inf.  A key or value that is NaN reaches the
+ * No block weights are gathered.  A query that sees no token gives zeros and an lse of -inf.  A key or value that is NaN reaches the
  * queries that see it and no others; a query with an entry that is not finite gives NaN.
  * The products run on fp16 operands, accumulated in fp32: codes exactly; a bf16 query exactly from 2^-31 of its row's
  * largest entry on and to 2^-39 of that below, p times its V scale to 2^-20 of itself (beside its logit's own rounding to 24

@@ -11,13 +11,13 @@
 // row, and p times its V scale beside both, are sums of two fp16 terms (2^-22 of themselves).  p's are relative to
 // the largest scale so far and good to 2^-36 of the largest: p is at most 2^4 (the running maximum is only raised where
 // a tile passes it by more than 4 in base 2, so that O is rarely rescaled).  One term of p, 2^-11 of itself, would
-// show in bf16 where values cancel, and took a prompt of 16,384 tokens 2.23 ms in place of 2.44.
+// show in bf16 where values cancel, and took a prompt of 16,384 tokens 2.23 ms in place of 2.45.
 //
 // All row tiles and the tiles (of 128 tokens) that each sees are numbered through in units, five for a row tile's start
 // and end and one for each of its tiles, and every CTA takes an equal run of units: one prompt, ragged batches and few rows over
 // a long cache fill the GPU alike.  A row tile that several CTAs work on is joined by k_tokens_merge.
 //
-// Measured, 32 query and 8 KV heads of 128 in bf16: a prompt of 16,384 tokens 2.44 ms, 903 TFLOP/s (0.46 of a
+// Measured, 32 query and 8 KV heads of 128 in bf16: a prompt of 16,384 tokens 2.45 ms, 899 TFLOP/s (0.46 of a
 // cuBLAS product's rate; the products with V run once for each term of p, and that is counted once); 6 tokens over
 // 8 x 131,072 537 us, 4.0 TB/s of codes.  What bounds it: the chain S -> softmax -> P -> O of a stream (with one term of p 2300
 // cycles of softmax and 500 of waits between warps beside 2200 of products for two streams); the shared memory, which
