@@ -320,8 +320,13 @@ enum : int {
   kSLast = 2048,
   kMixed = 4096,    // some rows do not see some of its tokens
   kOdd = 8192,      // a K scale that is negative, a V scale that is not positive, or one that is no number
-  kWhole = 16384    // this CTA has all of the row tile
+  kWhole = 16384,   // this CTA has all of the row tile
+  kKexp = 16        // (a shift) the exponent of its largest K scale, as a float holds it
 };
+// Logits up to this much (a row's factor times the largest K scale, by the sum of their exponents as floats hold them: with
+// 2^15 448 128 of S, below 2^23) are sure to be resolved to a half: more than that is rounded before it is compared and
+// subtracted, since what is left between a logit and its rounding could be any power of two.
+constexpr int kLargeSum = 2 * 127 - 10;
 struct TileInfo {
   int tile, flags, vexp, vlow;   // all V scales are below 2^vexp, and 2^vlow or more
   float ks[8], vs[8];            // of every 16 tokens
@@ -516,6 +521,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       const bool odd = __any_sync(0xffffffffu, lane < nb && !(ks * a.scale_log2 >= 0.f && vs > 0.f && vs < INFINITY));
       const float least = -warp_max(lane < nb ? -fabsf(vs) : -INFINITY);
       const float top = warp_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.f);
+      const uint32_t kexp = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(ks))) >> 23;   // (NaN above all)
       const int g16 = lane << 4 >> shift;   // block of 16-token group `lane`
       const float ksg = __shfl_sync(0xffffffffu, ks, g16 & 7), vsg = __shfl_sync(0xffffffffu, vs, g16 & 7);
       if (lane < 8) {
@@ -528,7 +534,8 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         in->q = cur.q;
         in->tile = cur.tile;
         in->flags = cnt | (k < stride ? kSFirst : 0) |
-                    (it >= seg_end - stride ? kSLast : 0) | (cur.tile * kCtT + cnt > cur.seen0 ? kMixed : 0) | (odd ? kOdd : 0) | whole;
+                    (it >= seg_end - stride ? kSLast : 0) | (cur.tile * kCtT + cnt > cur.seen0 ? kMixed : 0) | (odd ? kOdd : 0) | whole |
+                    static_cast<int>(kexp) << kKexp;
         in->n = cur.n;
         in->len = cur.len;
         in->turn = turn;
@@ -866,9 +873,9 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
           if (c != col0) tmem_st16(tS + c + 16 * n, zero);
     };
     // x f + off; beside fp32 with what f's rounding leaves (one relative error of all logits otherwise, 3e-7 of p)
-    auto exponent = [&](float x, float f, float off) {
+    auto exponent = [&](float x, float f, float off, float rest) {
       const float y = fmaf(x, f, off);
-      return C::NQ > 1 ? fmaf(x * f, a.scale_rest, y) : y;
+      return C::NQ > 1 ? fmaf(x * f, rest, y) : y;
     };
     // All tokens seen, scales positive and not too far apart: bf16's V scale v goes into the exponent, w = 2^(x - m + log2 v), and
     // comes out of the sum of 16 tokens' w again; four and a half instructions an element, two of them w's second term.
@@ -906,7 +913,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
           for (int e = 0; e < 16; e += 2) {
             const float s0 = s[16 * g + e], s1 = s[16 * g + e + 1];
             const float2 x = Fold ? fma2(make_float2(s0, s1), make_float2(fg, fg), make_float2(off, off))
-                                  : make_float2(exponent(s0, fg, off), exponent(s1, fg, off));
+                                  : make_float2(exponent(s0, fg, off, a.scale_rest), exponent(s1, fg, off, a.scale_rest));
             float2 p = make_float2(ex2(x.x), ex2(x.y));
             sum = add2(sum, p);
             if (!Fold) p = make_float2(p.x * fv, p.y * fv);
@@ -921,15 +928,29 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
       if constexpr (Copies > 1) zero_others();
       tmem_wait_st();
     };
-    // Any tokens, any scales.
-    auto softmax_any = [&](const TileInfo& in, bool first) {
+    // Any tokens, any scales; large: logits of any size, S is replaced by them, rounded.
+    auto softmax_any = [&](const TileInfo& in, bool first, bool large) {
       const int rem = lim - in.tile * kCtT - col0;
+      const float rest = large ? 0.f : a.scale_rest;
+      if (large) {
+#pragma unroll 1
+        for (int c = 0; c < W; c += 16) {
+          float s[16];
+          tc::tmem_ld16(tS + col0 + c, s);
+          const float fg = rowf * in.ks[(col0 + c) / 16];
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(s[e] * fg);
+          tmem_st16(tS + col0 + c, w);
+        }
+        tmem_wait_st();
+      }
       float mt = -INFINITY;
 #pragma unroll 1
       for (int c = 0; c < W; c += 16) {
         float s[16];
         tc::tmem_ld16(tS + col0 + c, s);
-        const float fg = rowf * in.ks[(col0 + c) / 16];
+        const float fg = large ? 1.f : rowf * in.ks[(col0 + c) / 16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) mt = fmaxf(mt, c + e < rem ? s[e] * fg : -INFINITY);
       }
@@ -953,14 +974,14 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         for (int g = 0; g < 2; ++g) {
           float s[16];
           tc::tmem_ld16(tS + col0 + c + 16 * g, s);
-          const float fg = rowf * in.ks[(col0 + c) / 16 + g], fv = in.vs[(col0 + c) / 16 + g] * up;
+          const float fg = large ? 1.f : rowf * in.ks[(col0 + c) / 16 + g], fv = in.vs[(col0 + c) / 16 + g] * up;
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             float p[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const bool seen = c + 16 * g + e + u < rem;
-              p[u] = seen ? ex2(exponent(s[e + u], fg, -ref)) : 0.f;
+              p[u] = seen ? ex2(exponent(s[e + u], fg, -ref, rest)) : 0.f;
               sum += p[u];
               p[u] = seen ? p[u] * fv : 0.f;   // (a scale that is no number under a hidden token)
             }
@@ -1047,6 +1068,7 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         if (!warp_wait(&qfull[0], turn)) break;
         rowf = sqs[row];
       }
+      const int rexp = static_cast<int>(__float_as_uint(warp_max(fabsf(rowf))) >> 23);   // of the warp's largest factor
       // this stream's tiles
       int t = Two ? i : i + ((i ^ x) & 1);
       bool ok = true;
@@ -1060,9 +1082,10 @@ __global__ void __launch_bounds__(kCtThreads, 1) k_attend_tokens(const __grid_co
         if (active) {
           const int4 what = *reinterpret_cast<const int4*>(&in);   // tile, flags, vexp, vlow
           const int rem = lim - what.x * kCtT, tf = what.y;
-          if ((tf & (kMixed | kOdd)) || (tf & 255) < kCtT ||
+          const bool large = (tf >> kKexp) + rexp > kLargeSum;
+          if (large || (tf & (kMixed | kOdd)) || (tf & 255) < kCtT ||
               what.w + 71 < (used ? max(vexp, what.z) : what.z))   // (below 2^-60 of the largest, w could vanish before p does)
-            softmax_any(in, !used);
+            softmax_any(in, !used, large);
           else
             softmax_plain(in, !used);
           if (tf & kMixed) {

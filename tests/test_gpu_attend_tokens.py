@@ -531,3 +531,38 @@ def test_a_hidden_block_of_large_values_leaves_earlier_queries_alone(dtype, s, G
     close(got[:, :, :m], lse[:, :, :m], short, q[:, :, :m])
     close(got, lse, c, q)                                              # and those that see it
     c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("s,G", [(1, 1), (7, 4), (30, 4), (300, 1)])
+@pytest.mark.parametrize("kexp,qexp", [(6, 0), (14, 6), (16, 8), (30, 0), (0, 40), (60, 50), (-90, 100)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_logits_of_any_size(dtype, s, G, kexp, qexp, causal):
+    """Finite logits from 2^8 to 2^112, the largest ones of a row apart by a sixteenth of themselves or the same: the
+    softmax is the mean over the same ones (e^-16 beside it at the smallest), which products of e4m3 and powers of two
+    give exactly; the tolerance is that of the other tests with a logit's error 0."""
+    d, block, n = 64, 16, 700
+    c = cache(2, 1, d, block, [n, n - 30], 70)
+    g = gen(71)
+    row = torch.randint(0x20, 0x40, (len(c.k_scale), 1, 1, block, 1), generator=g, device="cuda", dtype=torch.uint8)
+    row |= torch.randint(0, 2, row.shape, generator=g, device="cuda", dtype=torch.uint8) << 7
+    c.k_codes.view(torch.uint8).copy_(row.view(len(c.k_scale), block // 8, 1, 8, 1).expand(-1, -1, d // 16, 8, 16))
+    c.k_scale.fill_(2.0 ** kexp)
+    c.v_scale.fill_(2.0 ** -7)                                         # (scales without tokens, too: there they are not read)
+    sign = torch.where(torch.arange(s, device="cuda") % 3 == 1, -1.0, 1.0)
+    q = (sign[:, None] * 2.0 ** qexp).expand(2, G, s, d).to(DT[dtype]).contiguous()
+    lse = torch.empty(2, G, s, device="cuda")
+    got = c.attend_tokens(q, causal=causal, scale=0.125, lse=lse)
+    for i in range(2):
+        k, v, _ = values(c, i, 0)
+        y = 0.125 * (q[i].double() @ k.T)
+        m = len(k)
+        if causal:
+            y.masked_fill_(torch.arange(m, device="cuda") >= (m - s + torch.arange(s, device="cuda") + 1)[:, None], -math.inf)
+        p = torch.softmax(y, -1)
+        ref, mag = p @ v, p @ v.abs()
+        e = 2.0 ** -20 + 2.0 ** -19 + 2.0 ** -22 + 70 * U              # p's terms and exponent, 2^x, the sums
+        assert bool(((got[i].double() - ref).abs() <= (2.0 ** -8 if dtype == "bf16" else U) * ref.abs() + (2 * e + 2.0 ** -21) * mag).all())
+        want = torch.logsumexp(y, -1)
+        assert bool(((lse[i].double() - want).abs() <= 6 * U * want.abs() + 2.0 ** -19).all())
+    c.check()
