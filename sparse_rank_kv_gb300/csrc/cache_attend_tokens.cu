@@ -19,7 +19,7 @@
 //
 // Measured, 32 query and 8 KV heads of 128 in bf16: a prompt of 16,384 tokens 2.45 ms, 899 TFLOP/s (0.46 of a
 // cuBLAS product's rate; the products with V run once for each term of p, and that is counted once); 6 tokens over
-// 8 x 131,072 537 us, 4.0 TB/s of codes.  What bounds it: the chain S -> softmax -> P -> O of a stream (with one term of p 2300
+// 8 x 131,072 538 us, 4.0 TB/s of codes.  What bounds it: the chain S -> softmax -> P -> O of a stream (with one term of p 2300
 // cycles of softmax and 500 of waits between warps beside 2200 of products for two streams); the shared memory, which
 // the products' operands, the codes and their fp16 forms share; and at a row tile's start and end about 20,000 cycles.
 #include <cuda_fp16.h>
