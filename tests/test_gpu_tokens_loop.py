@@ -1,4 +1,4 @@
-"""The step of several tokens as README.md writes it, run: drafts of different lengths, sequences that get no
+"""The step of several tokens as the front page writes it, run: drafts of different lengths, sequences that get no
 room, one that ends and makes room for others."""
 import os
 import re
@@ -9,7 +9,7 @@ import torch
 from sparse_rank_kv_gb300 import binding, build
 
 pytestmark = pytest.mark.gpu
-README = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+PAGE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -19,18 +19,18 @@ def _built():
 
 
 def the_step():
-    """The cache and the step of README.md's block on several tokens, as two pieces of code."""
-    with open(README) as f:
+    """The cache and the step of its block on several tokens, as two pieces of code."""
+    with open(PAGE) as f:
         blocks = re.findall(r"```(?:python)?\n(.*?)```", f.read(), flags=re.S)
     made, step = [x for x in blocks if "BlockCache.pooled" in x and "verify_drafts" in x][0].split("\n", 1)
-    return compile(made, README, "exec"), compile(step, README, "exec")
+    return compile(made, PAGE, "exec"), compile(step, PAGE, "exec")
 
 
 def ints(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def test_the_readme_step_keeps_what_stood():
+def test_the_front_pages_step_keeps_what_stood():
     """After every step the cache holds what one that was only ever given the tokens that stood holds (values share
     a scale, so that rejected ones leave no trace), whatever the drafts' lengths and the room."""
     g = torch.Generator(device="cuda")
